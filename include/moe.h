@@ -393,6 +393,48 @@ int moe_forward(const moe_config *cfg, const moe_weights *w, const void *x,
 int moe_forward_noalloc(const moe_config *cfg, const moe_weights *w, const void *x,
                         const int32_t *token_ids, int64_t T, void *y, void *stream);
 
+/* moe_forward for a few tokens (T of 1 .. MOE_FEW_MAX_TOKENS): the decode step
+ * of a handful of sequences.  The same layer -- every routing, expert type,
+ * activation encoding and weight layout moe_forward takes -- in three launches
+ * and no permutation.  Results agree with moe_forward's to rounding (H keeps 16
+ * bits and the weighted expert outputs are summed in fp32, so this form rounds
+ * less); the routing follows the same rules.
+ *   x, token_ids, y, w, stream  as moe_forward; x, y and the matrices (not the
+ *       scales) 16-byte aligned
+ *   ws  device workspace of at least moe_few_workspace_size(cfg, T) bytes,
+ *       256-byte aligned.  Nothing in it needs to start at any value; after the
+ *       call it holds the routing and the device error flags at the offsets of
+ *       moe_few_layout
+ * Only kernels are enqueued: no allocation, memset or synchronisation, so the
+ * call can be captured in a HIP graph.  Calls that share a workspace must be
+ * ordered on one stream.  T == 0 is a no-op; T above MOE_FEW_MAX_TOKENS, or a
+ * dim or moe_inter_dim above MOE_FEW_MAX_DIM, is MOE_ERR_UNSUPPORTED. */
+#define MOE_FEW_MAX_TOKENS 16
+#define MOE_FEW_MAX_DIM (1 << 20)
+typedef struct {
+  size_t total_bytes;
+  size_t route_weights;        /* float [T, k]   gate values                     */
+  size_t route_indices;        /* int32 [T, k]   expert ids                      */
+  size_t flags;                /* uint32 [4]     device error flags; flags[0] as
+                                  moe_forward's: an expert id outside [0, E)
+                                  (MOE_FLAG_EXPERT_RANGE) adds nothing           */
+  size_t route_logits;         /* float          partial gate logits             */
+  size_t plan_slots;           /* int32 [1]      distinct chosen experts         */
+  size_t plan_experts;         /* int32 [T*k]    their ids, by first appearance  */
+  size_t plan_weights;         /* float [T*k, 16] gate value per (expert, token) */
+  size_t plan_rows;            /* int16 [T*k, 16] its row of h, -1: not chosen   */
+  size_t xq, xq_scales;        /* MXFP8 copy of x (act_quant)                    */
+  size_t hq, hq_scales;        /* MXFP8 SwiGLU rows [T*k, I] (act_quant)         */
+  size_t h, h_lo;              /* SwiGLU rows [T*k + T, I]: fp32, or the high and
+                                  low bf16 whose sum is the value (T*k .. : the
+                                  shared expert's; MXFP8 layers: those alone)    */
+} moe_few_layout;
+int moe_few_workspace_layout(const moe_config *cfg, int64_t T, moe_few_layout *layout);
+size_t moe_few_workspace_size(const moe_config *cfg, int64_t T); /* 0 if invalid */
+int moe_forward_few(const moe_config *cfg, const moe_weights *w, const void *x,
+                    const int32_t *token_ids, int64_t T, void *y,
+                    void *ws, size_t ws_bytes, void *stream);
+
 /* Stages of moe_forward in launch order (for moe_forward_profiled). */
 #define MOE_STAGE_ROUTE 0     /* router kernel (or hash gather)                  */
 #define MOE_STAGE_PERMUTE 1   /* permute kernel                                 */

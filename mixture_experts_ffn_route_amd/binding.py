@@ -26,12 +26,14 @@ MOE_ERR_HIP = -4
 MOE_FLAG_TOKEN_ID_RANGE = 1
 MOE_FLAG_EXPERT_RANGE = 2
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20
+MOE_FEW_MAX_TOKENS = 16
 
 EXPORTED_SYMBOLS = (
     "moe_status_string", "moe_validate_config", "moe_build_tid2eid", "moe_workspace_layout",
     "moe_workspace_size", "moe_route", "moe_permute", "moe_forward", "moe_forward_profiled",
     "moe_pack_weights", "moe_build_tid2eid_multistart", "moe_update_bias", "moe_probe_read",
     "moe_probe_mfma", "moe_redequant_fp8", "moe_forward_ex", "moe_forward_noalloc",
+    "moe_few_workspace_layout", "moe_few_workspace_size", "moe_forward_few",
 )
 MOE_STAGES = ("route", "permute", "gemm1", "gemm2", "combine")
 
@@ -64,6 +66,13 @@ class MoeWsLayoutC(ctypes.Structure):
         ("max_tiles", ctypes.c_int32), ("tile_rows", ctypes.c_int32)]
 
 
+class MoeFewLayoutC(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_size_t) for n in (
+        "total_bytes", "route_weights", "route_indices", "flags", "route_logits", "plan_slots",
+        "plan_experts", "plan_weights", "plan_rows", "xq", "xq_scales", "hq", "hq_scales", "h",
+        "h_lo")]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise RuntimeError(f"{LIB_PATH} is not built; run __graft_entry__.build() first")
@@ -91,6 +100,12 @@ def _load():
     lib.moe_forward_ex.argtypes = [cfgp, wp, vp, vp, i64, vp, vp, ctypes.c_size_t,
                                    ctypes.POINTER(ctypes.c_void_p), vp, vp]
     lib.moe_forward_noalloc.argtypes = [cfgp, wp, vp, vp, i64, vp, vp]
+    lib.moe_few_workspace_layout.argtypes = [cfgp, i64, ctypes.POINTER(MoeFewLayoutC)]
+    lib.moe_few_workspace_size.restype = ctypes.c_size_t
+    lib.moe_few_workspace_size.argtypes = [cfgp, i64]
+    lib.moe_forward_few.argtypes = lib.moe_forward.argtypes
+    for f in ("moe_few_workspace_layout", "moe_forward_few"):
+        getattr(lib, f).restype = ctypes.c_int
     for f in ("moe_validate_config", "moe_build_tid2eid", "moe_workspace_layout", "moe_route",
               "moe_permute", "moe_forward", "moe_forward_profiled", "moe_forward_ex",
               "moe_forward_noalloc",
@@ -324,6 +339,33 @@ def moe_forward_noalloc(cfg: MoEConfig, layer: dict, x, token_ids, T: int, y, st
            "moe_forward_noalloc")
 
 
+def _config_ref(cfg):
+    """byref of a configuration given as MoEConfig or as config_c of one."""
+    return ctypes.byref(cfg if isinstance(cfg, MoeConfigC) else config_c(cfg))
+
+
+def moe_few_workspace_layout(cfg, T: int) -> dict:
+    lay = MoeFewLayoutC()
+    _check(_lib.moe_few_workspace_layout(_config_ref(cfg), T, ctypes.byref(lay)),
+           "moe_few_workspace_layout")
+    return {name: getattr(lay, name) for name, _ in MoeFewLayoutC._fields_}
+
+
+def moe_few_workspace_size(cfg, T: int) -> int:
+    return _lib.moe_few_workspace_size(_config_ref(cfg), T)
+
+
+def moe_forward_few(cfg, layer, x, token_ids, T: int, y, ws, stream=None):
+    """moe_forward for T <= MOE_FEW_MAX_TOKENS tokens.  A decode loop may build
+    the C structs once and pass them: cfg a MoEConfig or config_c of it, layer
+    the weights' dict or weights_c of it.  ws: alloc_few_workspace."""
+    w = layer if isinstance(layer, MoeWeightsC) else weights_c(layer)
+    _check(_lib.moe_forward_few(_config_ref(cfg), ctypes.byref(w), _ptr(x), _ptr(token_ids), T,
+                                _ptr(y), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+                                _stream(stream)),
+           "moe_forward_few")
+
+
 class HipEvents:
     """Raw HIP timing events from the HIP runtime torch already loaded."""
 
@@ -397,3 +439,26 @@ def workspace_views(cfg: MoEConfig, T: int, ws):
         out["hq"] = view(lay["hq"], T * k * I, torch.uint8).view(T * k, I)
         out["hq_scales"] = view(lay["hq_scales"], T * k * I // 32, torch.uint8).view(T * k, -1)
     return out
+
+
+def alloc_few_workspace(cfg, T: int, device="cuda"):
+    """Workspace of moe_forward_few for T tokens (one that fits more fits fewer
+    tokens only of the same configuration)."""
+    lay = moe_few_workspace_layout(cfg, T)
+    return torch.empty(max(lay["total_bytes"], 1), dtype=torch.uint8, device=device)
+
+
+def few_views(cfg: MoEConfig, T: int, ws):
+    """Routing and flags a moe_forward_few call left in its workspace."""
+    lay = moe_few_workspace_layout(cfg, T)
+    k = cfg.n_activated_experts
+
+    def view(off, n, dtype):
+        return ws[off:off + 4 * n].view(dtype)
+
+    return {
+        "route_weights": view(lay["route_weights"], T * k, torch.float32).view(T, k),
+        "route_indices": view(lay["route_indices"], T * k, torch.int32).view(T, k),
+        "flags": view(lay["flags"], 4, torch.int32),
+        "layout": lay,
+    }

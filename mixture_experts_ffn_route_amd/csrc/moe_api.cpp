@@ -11,6 +11,7 @@
 #include <numeric>
 #include <vector>
 
+#include "few.h"
 #include "internal.h"
 #include "moe.h"
 
@@ -127,6 +128,47 @@ int make_layout(const moe_config *c, int64_t T, moe_ws_layout *out) {
   l.total_bytes = off;
   l.max_tiles = (int32_t)max_tiles;
   l.tile_rows = bm;
+  if (out) *out = l;
+  return MOE_OK;
+}
+
+int make_few_layout(const moe_config *c, int64_t T, moe_few_layout *out) {
+  const int st = validate(c);
+  if (st != MOE_OK) return st;
+  if (T < 0) return MOE_ERR_INVALID_ARG;
+  // the kernels address rows of x and H with 32-bit byte offsets
+  if (T > MOE_FEW_MAX_TOKENS || c->dim > MOE_FEW_MAX_DIM || c->moe_inter_dim > MOE_FEW_MAX_DIM)
+    return MOE_ERR_UNSUPPORTED;
+  const size_t k = c->n_activated_experts, E = c->n_routed_experts;
+  const size_t d = c->dim, I = c->moe_inter_dim, pairs = T * k;
+  const bool f32 = c->act_dtype == MOE_DTYPE_F32;
+  const bool mx = c->act_quant == MOE_ACT_QUANT_MXFP8;
+  const bool learned = c->route_mode == MOE_ROUTE_LEARNED;
+  moe_few_layout l;
+  std::memset(&l, 0, sizeof(l));
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = align_up(off + bytes);
+    return o;
+  };
+  l.route_weights = take(sizeof(float) * pairs);
+  l.route_indices = take(sizeof(int32_t) * pairs);
+  l.flags = take(sizeof(uint32_t) * 4);
+  l.route_logits =
+      take(learned ? sizeof(float) * moe::few_logit_parts((int)E, (int)d, f32) * T * E : 0);
+  l.plan_slots = take(sizeof(int32_t));
+  l.plan_experts = take(sizeof(int32_t) * pairs);
+  l.plan_weights = take(sizeof(float) * 16 * pairs);
+  l.plan_rows = take(sizeof(int16_t) * 16 * pairs);
+  l.xq = take(mx ? T * d : 0);
+  l.xq_scales = take(mx ? T * d / 32 : 0);
+  l.hq = take(mx ? pairs * I : 0);
+  l.hq_scales = take(mx ? pairs * I / 32 : 0);
+  const size_t rows = pairs + (c->n_shared_experts ? T : 0);
+  l.h = take((f32 ? 4 : 2) * rows * I);
+  l.h_lo = take(f32 ? 0 : 2 * rows * I);
+  l.total_bytes = off;
   if (out) *out = l;
   return MOE_OK;
 }
@@ -414,15 +456,10 @@ int moe_permute(const moe_config *cfg, const int32_t *indices, int64_t T, int32_
                                         inverse, flags, nullptr, false, (hipStream_t)stream));
 }
 
-static int forward_impl(const moe_config *cfg, const moe_weights *w, const void *x,
-                        const int32_t *token_ids, int64_t T, void *y, void *ws, size_t ws_bytes,
-                        hipEvent_t *events, void *stream, void *side_stream) {
-  moe_ws_layout L;
-  int st = make_layout(cfg, T, &L);
-  if (st != MOE_OK) return st;
-  if (!w) return MOE_ERR_INVALID_ARG;
-  if (T == 0) return MOE_OK;
-  if (!x || !y || x == y) return MOE_ERR_INVALID_ARG;
+// The pointers a forward call of this (valid) configuration needs.
+static int check_forward_args(const moe_config *cfg, const moe_weights *w, const void *x,
+                              const int32_t *token_ids, const void *y) {
+  if (!w || !x || !y || x == y) return MOE_ERR_INVALID_ARG;
   if (!w->w_gate || !w->w_up || !w->w_down) return MOE_ERR_INVALID_ARG;
   if ((cfg->expert_dtype == MOE_DTYPE_FP4_E2M1 || cfg->expert_dtype == MOE_DTYPE_FP8_E4M3_B128) &&
       (!w->s_gate || !w->s_up || !w->s_down))
@@ -436,6 +473,18 @@ static int forward_impl(const moe_config *cfg, const moe_weights *w, const void 
   } else if (!w->gate_w) {
     return MOE_ERR_INVALID_ARG;
   }
+  return MOE_OK;
+}
+
+static int forward_impl(const moe_config *cfg, const moe_weights *w, const void *x,
+                        const int32_t *token_ids, int64_t T, void *y, void *ws, size_t ws_bytes,
+                        hipEvent_t *events, void *stream, void *side_stream) {
+  moe_ws_layout L;
+  int st = make_layout(cfg, T, &L);
+  if (st != MOE_OK) return st;
+  if (!w) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if ((st = check_forward_args(cfg, w, x, token_ids, y)) != MOE_OK) return st;
   if (!ws || ((uintptr_t)ws % kAlign) != 0 || ws_bytes < L.total_bytes) return MOE_ERR_WORKSPACE;
 
   hipStream_t s = (hipStream_t)stream;
@@ -567,6 +616,70 @@ static int forward_impl(const moe_config *cfg, const moe_weights *w, const void 
   if (e != hipSuccess) return finish(MOE_ERR_HIP);
   if (moe::launch_experts(p, s) != hipSuccess) return finish(MOE_ERR_HIP);
   return MOE_OK;
+}
+
+int moe_few_workspace_layout(const moe_config *cfg, int64_t T, moe_few_layout *layout) {
+  return make_few_layout(cfg, T, layout);
+}
+
+size_t moe_few_workspace_size(const moe_config *cfg, int64_t T) {
+  moe_few_layout l;
+  return make_few_layout(cfg, T, &l) == MOE_OK ? l.total_bytes : 0;
+}
+
+int moe_forward_few(const moe_config *cfg, const moe_weights *w, const void *x,
+                    const int32_t *token_ids, int64_t T, void *y, void *ws, size_t ws_bytes,
+                    void *stream) {
+  moe_few_layout L;
+  int st = make_few_layout(cfg, T, &L);
+  if (st != MOE_OK) return st;
+  if (T == 0) return w ? MOE_OK : MOE_ERR_INVALID_ARG;
+  if ((st = check_forward_args(cfg, w, x, token_ids, y)) != MOE_OK) return st;
+  const bool low_precision = cfg->expert_dtype == MOE_DTYPE_FP4_E2M1 ||
+                             cfg->expert_dtype == MOE_DTYPE_FP8_E4M3_B128;
+  const bool learned = cfg->route_mode == MOE_ROUTE_LEARNED;
+  const bool shared = cfg->n_shared_experts == 1;
+  // 16-byte loads of x and of every matrix row
+  for (const void *p : {x, (const void *)y, w->w_gate, w->w_up, w->w_down,
+                        learned ? w->gate_w : nullptr, shared ? w->sh_gate : nullptr,
+                        shared ? w->sh_up : nullptr, shared ? w->sh_down : nullptr})
+    if ((uintptr_t)p % 16) return MOE_ERR_INVALID_ARG;
+  if (!ws || ((uintptr_t)ws % kAlign) != 0 || ws_bytes < L.total_bytes) return MOE_ERR_WORKSPACE;
+
+  char *base = (char *)ws;
+  const bool f32 = cfg->act_dtype == MOE_DTYPE_F32;
+  const bool mx = cfg->act_quant == MOE_ACT_QUANT_MXFP8;
+  moe::FewArgs a = {};
+  a.x = x; a.y = y;
+  a.T = (int)T; a.d = cfg->dim; a.E = cfg->n_routed_experts; a.k = cfg->n_activated_experts;
+  a.I = cfg->moe_inter_dim; a.G = cfg->n_expert_groups; a.kept = cfg->n_limited_groups;
+  a.score = cfg->score_func; a.route_mode = cfg->route_mode;
+  a.renorm = cfg->renormalize < 0 ? (cfg->score_func != MOE_SCORE_SOFTMAX)
+                                  : (cfg->renormalize != 0);
+  a.route_scale = cfg->route_scale; a.limit = cfg->swiglu_limit;
+  a.has_shared = shared ? 1 : 0;
+  a.gate_w = w->gate_w; a.bias = w->gate_bias;
+  a.token_ids = token_ids; a.tid2eid = w->tid2eid; a.vocab = cfg->vocab_size;
+  if (cfg->route_mode == MOE_ROUTE_NGRAM_HASH) primes_above(a.vocab, a.k, a.primes);
+  a.w_gate = w->w_gate; a.w_up = w->w_up; a.w_down = w->w_down;
+  if (low_precision) { a.s_gate = w->s_gate; a.s_up = w->s_up; a.s_down = w->s_down; }
+  a.sh_gate = w->sh_gate; a.sh_up = w->sh_up; a.sh_down = w->sh_down;
+  a.out_w = (float *)(base + L.route_weights);
+  a.out_e = (int32_t *)(base + L.route_indices);
+  a.flags = (uint32_t *)(base + L.flags);
+  a.zpart = (float *)(base + L.route_logits);
+  a.KS = moe::few_logit_parts(a.E, a.d, f32);
+  a.plan_slots = (int32_t *)(base + L.plan_slots);
+  a.plan_expert = (int32_t *)(base + L.plan_experts);
+  a.plan_w = (float *)(base + L.plan_weights);
+  a.plan_row = (int16_t *)(base + L.plan_rows);
+  a.xq = mx ? (uint8_t *)(base + L.xq) : nullptr;
+  a.xq_scales = (uint8_t *)(base + L.xq_scales);
+  a.hq = (uint8_t *)(base + L.hq);
+  a.hq_scales = (uint8_t *)(base + L.hq_scales);
+  a.h = base + L.h;
+  a.h_lo = base + L.h_lo;
+  return hip_status(moe::launch_few(a, *cfg, (hipStream_t)stream));
 }
 
 int moe_pack_weights(const moe_config *cfg, const moe_weights *src, const moe_weights *dst,
