@@ -477,6 +477,91 @@ int moe_forward_ex(const moe_config *cfg, const moe_weights *w, const void *x,
                    void *ws, size_t ws_bytes, void **events, void *stream,
                    void *side_stream);
 
+/* Dense products of the feed-forward layers that stand between MoE layers: a
+ * linear layer with bias, activation and residual in one call, and its
+ * gradient.  A dense SwiGLU layer is two of them, the gate|up product with
+ * MOE_ACTIVATION_SWIGLU and the down product with the residual stream.
+ *
+ *   z = x W^T + bias                     (swiglu: also zu = x W_up^T + bias_up)
+ *   y = cast(act(z) + residual)
+ *
+ * swiglu: act = SiLU(min(z, L)) * clamp(zu, -L, L) for limit L > 0, SiLU(z) zu
+ * for limit 0 ("From One Giant FFN to 384 Tiny Experts", Ch.1 and 11.4). */
+typedef enum {
+  MOE_ACTIVATION_NONE = 0,
+  MOE_ACTIVATION_RELU = 1,
+  MOE_ACTIVATION_SILU = 2,
+  MOE_ACTIVATION_GELU = 3,       /* z Phi(z), the exact form (erf)               */
+  MOE_ACTIVATION_GELU_TANH = 4,  /* its tanh form                                */
+  MOE_ACTIVATION_SWIGLU = 5      /* two products, see above                      */
+} moe_activation;
+
+typedef struct {
+  int64_t rows;                /* M (0 .. 2^31 - 1)                              */
+  int32_t in_dim;              /* K >= 1                                         */
+  int32_t out_dim;             /* N >= 1                                         */
+  int32_t dtype;               /* moe_dtype F32 or BF16, of every tensor         */
+  int32_t activation;          /* moe_activation                                 */
+  float limit;                 /* swiglu clamp L > 0; 0: none                    */
+  int64_t ld_x;                /* row strides in elements, 0 = contiguous: x and
+                                  dx (>= K), y and dy (>= N), residual (>= N);
+                                  up to MOE_LINEAR_MAX_LD                        */
+  int64_t ld_y;
+  int64_t ld_residual;
+} moe_linear_config;
+#define MOE_LINEAR_MAX_LD (1 << 20)
+
+typedef struct {               /* contiguous, dtype; w and w_up 16-byte aligned  */
+  const void *w;               /* [N, K]                                         */
+  const void *w_up;            /* [N, K] swiglu only, else NULL                  */
+  const void *bias;            /* [N], or NULL                                   */
+  const void *bias_up;         /* [N] swiglu only, or NULL                       */
+} moe_linear_weights;
+
+typedef struct {               /* contiguous except dx; NULL: not wanted         */
+  void *dx;                    /* [M, K], stride ld_x                            */
+  void *dw, *dw_up;            /* [N, K]                                         */
+  void *dbias, *dbias_up;      /* [N]                                            */
+} moe_linear_grads;
+
+/* Workspace of moe_linear (backward = 0) or moe_linear_backward (backward = 1,
+ * for every gradient).  Host-only; 0 for an invalid configuration, 256 at
+ * least for a valid one. */
+size_t moe_linear_workspace_size(const moe_linear_config *cfg, int32_t backward);
+
+/* The forward product.
+ *   x         [M, K] stride ld_x, 16-byte aligned
+ *   residual  [M, N] stride ld_residual, or NULL; may be y itself (same stride)
+ *   y         [M, N] stride ld_y out; not x
+ *   z, z_up   [M, N] contiguous out, or NULL: the pre-activations z (and zu),
+ *             which the gradient needs unless the activation is NONE.  Rounded
+ *             to dtype, but never across the clamp's border
+ *   ws        device workspace of at least moe_linear_workspace_size(cfg, 0)
+ *             bytes, 256-byte aligned; nothing in it needs to start at any value
+ * Products accumulate in fp32, the epilogue is fp32, y is rounded once.  All
+ * sizes and strides are taken; rows that are not whole 16-byte pieces are
+ * first copied to padded ones in the workspace.  Results do not depend on what
+ * else runs (no atomics).  Only kernels are enqueued on `stream`, so the call
+ * can be captured in a HIP graph.  rows == 0 is a no-op. */
+int moe_linear(const moe_linear_config *cfg, const moe_linear_weights *w, const void *x,
+               const void *residual, void *y, void *z, void *z_up,
+               void *ws, size_t ws_bytes, void *stream);
+
+/* The gradient of moe_linear for the output gradient dy:
+ *   dz = dy act'(z)          (swiglu: for both products; a clamped value has none)
+ *   dx = dz W,  dW = dz^T x,  dbias = sum over rows of dz;  dresidual is dy
+ *   dy        [M, N] stride ld_y, 16-byte aligned
+ *   z, z_up   as moe_linear wrote them (activation NONE: ignored)
+ *   x         needed for dw / dw_up; w->w, w->w_up for dx; else may be NULL
+ *             (biases are not read)
+ *   grads     at least one member; outputs are overwritten, not added to
+ * dz is rounded to dtype before the products (they run on the matrix cores);
+ * sums are fp32, outputs are rounded once.  rows == 0 writes zeros to the
+ * weight and bias gradients. */
+int moe_linear_backward(const moe_linear_config *cfg, const moe_linear_weights *w, const void *x,
+                        const void *dy, const void *z, const void *z_up,
+                        const moe_linear_grads *grads, void *ws, size_t ws_bytes, void *stream);
+
 /* Roofline probes: the achievable HBM read rate and bf16 / FP8 MFMA rates of
  * the GPU, measured with the instruction forms the layer kernels use (16-byte
  * nontemporal vector loads; v_mfma_f32_16x16x32_bf16, v_mfma_f32_32x32x16_bf16,

@@ -7,6 +7,6 @@ synthetic inputs.  Importing the package does not load the library; import
 ``mixture_experts_ffn_route_amd.binding`` for that.
 """
 
-from .config import MoEConfig, Workload, FULL_WORKLOADS, SMALL_WORKLOADS
+from .config import LinearConfig, MoEConfig, Workload, FULL_WORKLOADS, SMALL_WORKLOADS
 
-__all__ = ["MoEConfig", "Workload", "FULL_WORKLOADS", "SMALL_WORKLOADS"]
+__all__ = ["LinearConfig", "MoEConfig", "Workload", "FULL_WORKLOADS", "SMALL_WORKLOADS"]

@@ -14,7 +14,8 @@ import torch  # loaded first so the library binds to the same HIP runtime as tor
 
 from dataclasses import replace
 
-from .config import ACT_QUANT, DTYPE, LAYOUT, ROUTE, SCORE, MoEConfig
+from .config import (ACT_QUANT, ACTIVATION, DTYPE, LAYOUT, ROUTE, SCORE, LinearConfig,
+                     MoEConfig)
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_mi355x.so")
 
@@ -34,6 +35,7 @@ EXPORTED_SYMBOLS = (
     "moe_pack_weights", "moe_build_tid2eid_multistart", "moe_update_bias", "moe_probe_read",
     "moe_probe_mfma", "moe_redequant_fp8", "moe_forward_ex", "moe_forward_noalloc",
     "moe_few_workspace_layout", "moe_few_workspace_size", "moe_forward_few",
+    "moe_linear_workspace_size", "moe_linear", "moe_linear_backward",
 )
 MOE_STAGES = ("route", "permute", "gemm1", "gemm2", "combine")
 
@@ -73,6 +75,22 @@ class MoeFewLayoutC(ctypes.Structure):
         "h_lo")]
 
 
+class MoeLinearConfigC(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("in_dim", ctypes.c_int32), ("out_dim", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("activation", ctypes.c_int32), ("limit", ctypes.c_float),
+        ("ld_x", ctypes.c_int64), ("ld_y", ctypes.c_int64), ("ld_residual", ctypes.c_int64),
+    ]
+
+
+class MoeLinearWeightsC(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("w", "w_up", "bias", "bias_up")]
+
+
+class MoeLinearGradsC(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("dx", "dw", "dw_up", "dbias", "dbias_up")]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise RuntimeError(f"{LIB_PATH} is not built; run __graft_entry__.build() first")
@@ -104,7 +122,13 @@ def _load():
     lib.moe_few_workspace_size.restype = ctypes.c_size_t
     lib.moe_few_workspace_size.argtypes = [cfgp, i64]
     lib.moe_forward_few.argtypes = lib.moe_forward.argtypes
-    for f in ("moe_few_workspace_layout", "moe_forward_few"):
+    lcp, lwp = ctypes.POINTER(MoeLinearConfigC), ctypes.POINTER(MoeLinearWeightsC)
+    lib.moe_linear_workspace_size.restype = ctypes.c_size_t
+    lib.moe_linear_workspace_size.argtypes = [lcp, i32]
+    lib.moe_linear.argtypes = [lcp, lwp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
+    lib.moe_linear_backward.argtypes = [lcp, lwp, vp, vp, vp, vp, ctypes.POINTER(MoeLinearGradsC),
+                                        vp, ctypes.c_size_t, vp]
+    for f in ("moe_few_workspace_layout", "moe_forward_few", "moe_linear", "moe_linear_backward"):
         getattr(lib, f).restype = ctypes.c_int
     for f in ("moe_validate_config", "moe_build_tid2eid", "moe_workspace_layout", "moe_route",
               "moe_permute", "moe_forward", "moe_forward_profiled", "moe_forward_ex",
@@ -366,6 +390,82 @@ def moe_forward_few(cfg, layer, x, token_ids, T: int, y, ws, stream=None):
            "moe_forward_few")
 
 
+_LINEAR_DTYPE = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def _linear_config(cfg: LinearConfig, x, y, residual=None) -> MoeLinearConfigC:
+    """cfg with the row strides of x, y (or dy) and the residual."""
+    return MoeLinearConfigC(
+        cfg.rows, cfg.in_dim, cfg.out_dim, DTYPE[cfg.dtype], ACTIVATION[cfg.activation], cfg.limit,
+        0 if x is None else x.stride(0), 0 if y is None else y.stride(0),
+        0 if residual is None else residual.stride(0))
+
+
+def _linear_check(cfg: LinearConfig, where, matrices, contiguous):
+    """Types, shapes and strides of a call's tensors (None: not given): the
+    library sees addresses only."""
+    dt = _LINEAR_DTYPE[cfg.dtype]
+    for name, t, shape in matrices + contiguous:
+        if t is None:
+            continue
+        if t.dtype != dt or tuple(t.shape) != shape:
+            raise ValueError(f"{where}: {name} is {tuple(t.shape)} {t.dtype}, "
+                             f"expected {shape} {dt}")
+        if t.numel() and t.stride(-1) != 1:
+            raise ValueError(f"{where}: {name}'s rows are not contiguous")
+    for name, t, _ in contiguous:
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{where}: {name} is not contiguous")
+
+
+def _raw(t):
+    return None if t is None else t.data_ptr()
+
+
+def moe_linear_workspace_size(cfg: LinearConfig, backward=False, ld_x=0, ld_y=0,
+                              ld_residual=0) -> int:
+    """Bytes for calls whose tensors have these row strides (0: contiguous)."""
+    c = MoeLinearConfigC(cfg.rows, cfg.in_dim, cfg.out_dim, DTYPE[cfg.dtype],
+                         ACTIVATION[cfg.activation], cfg.limit, ld_x, ld_y, ld_residual)
+    return _lib.moe_linear_workspace_size(ctypes.byref(c), int(bool(backward)))
+
+
+def moe_linear(cfg: LinearConfig, x, w, y, *, bias=None, residual=None, w_up=None, bias_up=None,
+               z=None, z_up=None, ws=None, stream=None):
+    """y = act(x w^T + bias) + residual; z (and z_up) receive the
+    pre-activations that moe_linear_backward takes.  x, y and residual may be
+    rows of wider buffers.  ws: alloc_linear_workspace."""
+    M, K, N = cfg.rows, cfg.in_dim, cfg.out_dim
+    _linear_check(cfg, "moe_linear", [("x", x, (M, K)), ("y", y, (M, N)),
+                                      ("residual", residual, (M, N))],
+                  [("w", w, (N, K)), ("w_up", w_up, (N, K)), ("bias", bias, (N,)),
+                   ("bias_up", bias_up, (N,)), ("z", z, (M, N)), ("z_up", z_up, (M, N))])
+    weights = MoeLinearWeightsC(_raw(w), _raw(w_up), _raw(bias), _raw(bias_up))
+    _check(_lib.moe_linear(ctypes.byref(_linear_config(cfg, x, y, residual)),
+                           ctypes.byref(weights), _raw(x), _raw(residual), _raw(y), _raw(z),
+                           _raw(z_up), _raw(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+                           _stream(stream)), "moe_linear")
+
+
+def moe_linear_backward(cfg: LinearConfig, dy, x, w, *, w_up=None, z=None, z_up=None, dx=None,
+                        dw=None, dw_up=None, dbias=None, dbias_up=None, ws=None, stream=None):
+    """Gradients of moe_linear for dy, into the tensors given (the residual's
+    is dy itself).  dx has x's row stride where both are given."""
+    M, K, N = cfg.rows, cfg.in_dim, cfg.out_dim
+    _linear_check(cfg, "moe_linear_backward",
+                  [("dy", dy, (M, N)), ("x", x, (M, K)), ("dx", dx, (M, K))],
+                  [("w", w, (N, K)), ("w_up", w_up, (N, K)), ("z", z, (M, N)),
+                   ("z_up", z_up, (M, N)), ("dw", dw, (N, K)), ("dw_up", dw_up, (N, K)),
+                   ("dbias", dbias, (N,)), ("dbias_up", dbias_up, (N,))])
+    weights = MoeLinearWeightsC(_raw(w), _raw(w_up), None, None)
+    grads = MoeLinearGradsC(_raw(dx), _raw(dw), _raw(dw_up), _raw(dbias), _raw(dbias_up))
+    _check(_lib.moe_linear_backward(
+        ctypes.byref(_linear_config(cfg, x if x is not None else dx, dy)), ctypes.byref(weights),
+        _raw(x), _raw(dy), _raw(z), _raw(z_up), ctypes.byref(grads), _raw(ws),
+        0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)),
+        "moe_linear_backward")
+
+
 class HipEvents:
     """Raw HIP timing events from the HIP runtime torch already loaded."""
 
@@ -462,3 +562,12 @@ def few_views(cfg: MoEConfig, T: int, ws):
         "flags": view(lay["flags"], 4, torch.int32),
         "layout": lay,
     }
+
+
+def alloc_linear_workspace(cfg: LinearConfig, backward=False, device="cuda", **strides):
+    """Workspace of moe_linear, or with `backward` one that serves both it and
+    moe_linear_backward; strides: ld_x, ld_y, ld_residual where not contiguous."""
+    sizes = [moe_linear_workspace_size(cfg, b, **strides) for b in {False, bool(backward)}]
+    if 0 in sizes:
+        raise MoEError(MOE_ERR_INVALID_ARG, "moe_linear_workspace_size")
+    return torch.empty(max(sizes), dtype=torch.uint8, device=device)

@@ -12,6 +12,7 @@ ROUTE = {"learned": 0, "hash": 1, "ngram": 2}
 DTYPE = {"f32": 0, "bf16": 1, "fp4": 2, "fp8": 3}   # fp8: E4M3 in 128x128 blocks (re-dequantised FP4)
 LAYOUT = {"rows": 0, "tiled": 1}
 ACT_QUANT = {"none": 0, "mxfp8": 1}
+ACTIVATION = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, "swiglu": 5}
 
 
 @dataclass(frozen=True)
@@ -40,6 +41,18 @@ class MoEConfig:
         if self.renormalize < 0:
             return self.score_func != "softmax"
         return bool(self.renormalize)
+
+
+@dataclass(frozen=True)
+class LinearConfig:
+    """A dense product with its epilogue (moe_linear_config in moe.h; the row
+    strides come from the tensors of a call)."""
+    rows: int
+    in_dim: int
+    out_dim: int
+    dtype: str = "bf16"           # "f32" or "bf16", of every tensor
+    activation: str = "none"      # a key of ACTIVATION
+    limit: float = 0.0            # swiglu clamp, 0: none
 
 
 @dataclass(frozen=True)

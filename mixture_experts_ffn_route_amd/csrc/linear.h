@@ -1,0 +1,35 @@
+// Launch interface of the dense product (linear.hip): moe_linear and its
+// gradient.
+#pragma once
+
+#include "internal.h"
+
+namespace moe {
+
+// Sizes and workspace of one moe_linear (or moe_linear_backward) call; offsets
+// in bytes from the workspace base, 0-byte parts are not used.
+struct LinearSpace {
+  size_t total;
+  size_t x, w, w_up;           // copies with 16-byte rows, where a row has none
+  size_t dz, du;               // backward: gradient of the products' outputs
+  size_t colsum;               // backward: partial column sums of dz (and du)
+  size_t part;                 // partial products of split contractions
+};
+
+// Element counts of the padded forms: rows of a copy are padded with zeros to
+// whole 16-byte pieces.
+inline int64_t linear_pad(int64_t n, int dtype) {
+  const int64_t m = dtype == MOE_DTYPE_F32 ? 4 : 8;
+  return (n + m - 1) / m * m;
+}
+
+LinearSpace linear_space(const moe_linear_config &c, bool backward, bool dx, bool dw, bool db);
+
+hipError_t launch_linear(const moe_linear_config &c, const moe_linear_weights &w, const void *x,
+                         const void *residual, void *y, void *z, void *z_up, char *ws,
+                         hipStream_t s);
+hipError_t launch_linear_backward(const moe_linear_config &c, const moe_linear_weights &w,
+                                  const void *x, const void *dy, const void *z, const void *z_up,
+                                  const moe_linear_grads &g, char *ws, hipStream_t s);
+
+}  // namespace moe

@@ -1,0 +1,880 @@
+// Dense product with bias, activation and residual, and its gradient:
+//
+//   z = x W^T + b,  y = act(z) + r                 (swiglu: two products)
+//   dz = dy act'(z), dx = dz W, dW = dz^T x, db = sum over rows of dz
+//
+// One GEMM kernel serves the three products.  D[M, N] = A B with A and B given
+// either "by rows" (the contraction index is the contiguous one) or "by
+// columns" (it is the row index), so no operand is transposed in memory:
+//   forward  A = x  by rows,        B = W  by rows
+//   dx       A = dz by rows,        B = W  by columns (contraction over out)
+//   dW       A = dz by columns,     B = x  by columns (contraction over rows)
+//
+// A workgroup of four waves computes a (64 MI) x (64 NI) tile, each wave a
+// quarter of it as MI x NI blocks of v_mfma_f32_32x32x16_bf16 (fp32 layers:
+// four v_mfma_f32_32x32x2_f32 on the same bytes).  The contraction runs in
+// stages of 64 bytes per row (32 bf16 or 16 fp32) through a four-slot LDS ring
+// filled by asynchronous 16-byte copies; the fragments of the next step are
+// read from LDS while the MFMAs of this one run.  Column operands are read
+// back transposed by ds_read_b64_tr_b16 (fp32: one dword per lane).
+//
+// Copies are buffer loads into LDS: a piece past the end of a matrix or of the
+// contraction arrives as zeros without traffic, which covers every ragged
+// size.  Rows that are not whole 16-byte pieces (odd widths or strides) are
+// first copied to padded rows in the workspace.
+
+#include "gemm.h"
+#include "linear.h"
+
+namespace moe {
+namespace {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+constexpr uint32_t kOut = 0x80000000u;         // an offset past every resource here
+
+// ---------------------------------------------------------------------------
+// Epilogue, shared by the GEMM, the sum of split products and the few-row
+// kernel: eight consecutive columns of one row.
+struct Epilogue {
+  const void *bias, *bias_up, *residual;
+  void *y, *z, *z_up;
+  int64_t ld_y, ld_res, ld_z;
+  int N;                       // output columns
+  int act;                     // moe_activation
+  float limit;
+  int vec;                     // every row piece of 8 columns is 16-byte aligned
+};
+
+template <typename T>
+__device__ __forceinline__ void load8(float (&v)[8], const T *p, int n, bool vec) {
+  if (vec && n >= 8) {
+    if constexpr (sizeof(T) == 2) {
+      const bf16x8 w = *(const bf16x8 *)p;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = (float)w[j];
+    } else {
+      const f32x4 a = *(const f32x4 *)p, b = *(const f32x4 *)(p + 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) { v[j] = a[j]; v[4 + j] = b[j]; }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j < n ? (float)p[j] : 0.f;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store8(T *p, const float (&v)[8], int n, bool vec) {
+  if (vec && n >= 8) {
+    if constexpr (sizeof(T) == 2) {
+      bf16x8 w;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = (bf16)v[j];
+      *(bf16x8 *)p = w;
+    } else {
+      *(f32x4 *)p = f32x4{v[0], v[1], v[2], v[3]};
+      *(f32x4 *)(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) p[j] = (T)v[j];
+  }
+}
+
+// fp32 layers take the accurate exponential; before a rounding to bf16 the
+// hardware one (relative error below 2^-20 at the arguments that matter) does.
+template <typename T>
+__device__ __forceinline__ float exp_of(float v) {
+  return sizeof(T) == 4 ? expf(v) : __expf(v);
+}
+template <typename T>
+__device__ __forceinline__ float sigmoid(float v) {
+  return 1.f / (1.f + exp_of<T>(-v));
+}
+
+constexpr float kGeluA = 0.7978845608028654f;  // sqrt(2 / pi)
+constexpr float kGeluB = 0.044715f;
+
+template <typename T>
+__device__ __forceinline__ float activate(float z, int act) {
+  switch (act) {
+    case MOE_ACTIVATION_RELU: return z > 0.f ? z : (z != z ? z : 0.f);
+    case MOE_ACTIVATION_SILU: return z * sigmoid<T>(z);
+    case MOE_ACTIVATION_GELU: return 0.5f * z * erfcf(-z * 0.7071067811865476f);
+    case MOE_ACTIVATION_GELU_TANH:
+      // 0.5 z (1 + tanh q) = z sigmoid(2q), which keeps its relative accuracy
+      // for large negative z
+      return z * sigmoid<T>(2.f * kGeluA * (z + kGeluB * z * z * z));
+    default: return z;
+  }
+}
+
+// act'(z).
+template <typename T>
+__device__ __forceinline__ float slope(float z, int act) {
+  switch (act) {
+    case MOE_ACTIVATION_RELU: return z > 0.f ? 1.f : (z != z ? z : 0.f);
+    case MOE_ACTIVATION_SILU: {
+      const float s = sigmoid<T>(z);
+      return s * (1.f + z * (1.f - s));
+    }
+    case MOE_ACTIVATION_GELU:
+      return 0.5f * erfcf(-z * 0.7071067811865476f) + z * 0.3989422804014327f * exp_of<T>(-0.5f * z * z);
+    case MOE_ACTIVATION_GELU_TANH: {
+      const float s = sigmoid<T>(2.f * kGeluA * (z + kGeluB * z * z * z));
+      return s + z * s * (1.f - s) * 2.f * kGeluA * (1.f + 3.f * kGeluB * z * z);
+    }
+    default: return 1.f;
+  }
+}
+
+// The value of v in storage type T, kept on v's side of the clamp: the saved
+// pre-activation decides in the backward pass whether the clamp was active,
+// so rounding must not carry it across (v > L has to stay above L, v <= L at
+// or below it).  One step of the type towards the right side otherwise.
+template <typename T>
+__device__ __forceinline__ float saved(float v, float L) {
+  const float r = (float)(T)v;
+  if (sizeof(T) == 4 || !(L > 0.f)) return r;
+  const float a = fabsf(v), b = fabsf(r);
+  if ((a > L) == (b > L) || v != v) return r;
+  const uint32_t bits = __float_as_uint(r);
+  return __uint_as_float(a > L ? bits + 0x10000u : bits - 0x10000u);
+}
+
+// y (and z) of eight columns n .. of row m from the raw products v (and u).
+template <typename T, bool DUAL>
+__device__ __forceinline__ void finish8(const Epilogue &e, float (&v)[8], float (&u)[8], int64_t m,
+                                        int n) {
+  const int left = e.N - n;
+  const bool vec = e.vec != 0;
+  float b[8];
+  if (e.bias) {
+    load8<T>(b, (const T *)e.bias + n, left, vec);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += b[j];
+  }
+  if constexpr (DUAL) {
+    if (e.bias_up) {
+      load8<T>(b, (const T *)e.bias_up + n, left, vec);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[j] += b[j];
+    }
+  }
+  if (e.z) {
+    float k[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) k[j] = saved<T>(v[j], DUAL ? e.limit : 0.f);
+    store8<T>((T *)e.z + m * e.ld_z + n, k, left, vec);
+    if constexpr (DUAL) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) k[j] = saved<T>(u[j], e.limit);
+      store8<T>((T *)e.z_up + m * e.ld_z + n, k, left, vec);
+    }
+  }
+  if constexpr (DUAL) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float g = v[j], w = u[j];
+      if (e.limit > 0.f) {                     // NaN passes
+        g = g > e.limit ? e.limit : g;
+        w = w > e.limit ? e.limit : (w < -e.limit ? -e.limit : w);
+      }
+      v[j] = g * sigmoid<T>(g) * w;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = activate<T>(v[j], e.act);
+  }
+  if (e.residual) {
+    load8<T>(b, (const T *)e.residual + m * e.ld_res + n, left, vec);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += b[j];
+  }
+  store8<T>((T *)e.y + m * e.ld_y + n, v, left, vec);
+}
+
+// ---------------------------------------------------------------------------
+// The GEMM.
+struct Matrix {
+  const void *p;
+  int64_t ld, rows;            // as stored: rows of ld elements, cols used
+  int64_t cols;
+};
+struct GemmOp {
+  Matrix a[2], b[2], b_up;     // contraction segments added up; b_up: swiglu
+  int64_t kdim[2];             // contraction length of each segment
+  int segments;
+  int64_t M;                   // rows of D
+  int n_tiles, parts;
+  int64_t m_tiles;
+  float *part;                 // parts > 1: [parts][DUAL ? 2 : 1][M][ldp]
+  int64_t ldp;
+  Epilogue e;
+};
+
+template <typename T, bool COL, int TC>
+struct Operand {
+  static constexpr int ES = sizeof(T);
+  static constexpr int KB = 64 / ES;           // contraction elements per stage
+  static constexpr int RB = TC * ES;           // column operand: bytes of an LDS row
+  // 16-byte pieces of an LDS row are permuted so that a half-wave's reads take
+  // distinct banks: by rows, row r's piece c sits at c ^ (r / 8 % 4) (eight
+  // rows of 64 bytes cover address bits 6-8, the four pieces bits 4-5); by
+  // columns, the four rows of a transposed read sit 64 bytes apart modulo 256.
+  static __device__ __forceinline__ int swz(int k) { return ES == 2 && TC >= 128 ? (k & 3) << 2 : 0; }
+
+  // Byte offset, from the stage's origin, of what lane l copies to byte 16 l of
+  // unit u; kc: its first contraction index (row operands).
+  static __device__ __forceinline__ uint32_t source(int u, int lane, int64_t ld, int *kc) {
+    if constexpr (!COL) {
+      const int r = u * 16 + (lane >> 2);
+      const int c = (lane & 3) ^ ((r >> 3) & 3);
+      *kc = c * (16 / ES);
+      return (uint32_t)(r * ld * ES) + c * 16;
+    } else {
+      const int byte = u * 1024 + lane * 16;
+      const int k = byte / RB;
+      const int c = (byte % RB / 16) ^ swz(k);
+      *kc = 0;
+      return (uint32_t)(k * ld * ES) + c * 16;
+    }
+  }
+  static __device__ __forceinline__ rsrc_t origin(const Matrix &m, int64_t tile0, int64_t k0,
+                                                  bool there) {
+    const int64_t at = (COL ? k0 * m.ld + tile0 : tile0 * m.ld + k0) * ES;
+    int64_t left = ((m.rows - 1) * m.ld + m.cols) * ES - at;
+    left = left < 0 || !there ? 0 : left < (int64_t)kOut ? left : (int64_t)kOut;
+    const uint8_t *p = (const uint8_t *)m.p + (left > 0 ? at : 0);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, (uint32_t)left,
+                                             0x00027000);
+  }
+  // One lane's fragment of the 32 rows (columns of D) from `base`, step s.
+  static __device__ __forceinline__ u32x4 fragment(const uint8_t *lds, int base, int s, int lane) {
+    if constexpr (!COL) {
+      const int r = base + (lane & 31);
+      return *(const u32x4 *)(lds + r * 64 + ((2 * s + (lane >> 5)) ^ ((r >> 3) & 3)) * 16);
+    } else if constexpr (ES == 2) {
+      const int col = base + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+      const int k0 = 16 * s + 8 * (lane >> 5) + ((lane & 15) >> 2);
+      s16x4 v[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int k = k0 + 4 * i;
+        v[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (MOE_LDS s16x4 *)(lds + k * RB + ((col >> 3) ^ swz(k)) * 16 + (col & 7) * 2));
+      }
+      const u32x2 a = __builtin_bit_cast(u32x2, v[0]), b = __builtin_bit_cast(u32x2, v[1]);
+      return u32x4{a[0], a[1], b[0], b[1]};
+    } else {
+      const int col = base + (lane & 31);
+      u32x4 v;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v[j] = *(const uint32_t *)(lds + (8 * s + 4 * (lane >> 5) + j) * RB + col * 4);
+      return v;
+    }
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ void mma(f32x16 &acc, const u32x4 &a, const u32x4 &b) {
+  if constexpr (sizeof(T) == 2) {
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                  __builtin_bit_cast(bf16x8, b), acc, 0, 0, 0);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[i]), __uint_as_float(b[i]), acc,
+                                                 0, 0, 0);
+  }
+}
+
+// Work item of this workgroup: workgroups are dealt round-robin to the 8 XCDs,
+// each XCD takes a contiguous run of items; within a part, tiles run down
+// groups of 8 row tiles before the next column tile, so the tiles an XCD works
+// on at a time form a block that shares operand rows in its L2.
+__device__ __forceinline__ bool gemm_item(const GemmOp &g, int64_t *mt, int *nt, int *part) {
+  const int64_t tiles = g.m_tiles * g.n_tiles, items = tiles * g.parts;
+  const int64_t per = (items + 7) / 8;
+  const int64_t item = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if ((blockIdx.x >> 3) >= per || item >= items) return false;
+  *part = (int)(item / tiles);
+  const int64_t t = item - *part * tiles;
+  const int64_t group = t / (8 * g.n_tiles), first = group * 8;
+  const int64_t high = g.m_tiles - first < 8 ? g.m_tiles - first : 8;
+  const int64_t r = t - first * g.n_tiles;
+  *nt = (int)(r / high);
+  *mt = first + (r - *nt * high);
+  return true;
+}
+
+template <typename T, int MI, int NI, bool AC, bool BC, bool DUAL>
+__global__ __launch_bounds__(256, MI *NI >= 8 ? 1 : 2) void gemm_kernel(const GemmOp g) {
+  constexpr int ES = sizeof(T), KB = 64 / ES, NS = 4;
+  constexpr int TM = 64 * MI, TN = 64 * NI;
+  constexpr int UA = TM / 16, UB = TN / 16;    // 1 KB copy units per stage
+  constexpr int VM = (UA + UB) / 4;            // per wave
+  constexpr int SLOT = (TM + TN) * 64;
+  static_assert(!DUAL || (!AC && !BC), "the two-matrix product is the forward one");
+  static_assert(UA % 4 == 0 && UB % 4 == 0, "units split evenly");
+  using OA = Operand<T, AC, TM>;
+  using OB = Operand<T, BC, TN>;
+  // one LDS object per slot, so that a read of one does not wait for copies
+  // into another
+  __shared__ __attribute__((aligned(1024))) uint8_t L0[SLOT];
+  __shared__ __attribute__((aligned(1024))) uint8_t L1[SLOT];
+  __shared__ __attribute__((aligned(1024))) uint8_t L2[SLOT];
+  __shared__ __attribute__((aligned(1024))) uint8_t L3[SLOT];
+  uint8_t *const ring[4] = {L0, L1, L2, L3};
+  int64_t mt;
+  int nt, part;
+  if (!gemm_item(g, &mt, &nt, &part)) return;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  constexpr int TO = DUAL ? TN / 2 : TN;       // output columns of a tile
+  const int64_t m0 = mt * TM, n0 = (int64_t)nt * TO;
+
+  const int st_seg0 = (int)((g.kdim[0] + KB - 1) / KB);
+  const int st_all = st_seg0 + (g.segments > 1 ? (int)((g.kdim[1] + KB - 1) / KB) : 0);
+  const int st_first = (int)((int64_t)st_all * part / g.parts);
+  const int nst = (int)((int64_t)st_all * (part + 1) / g.parts) - st_first;
+
+  // the segments share strides (dz, du and W, W_up have the same shapes)
+  uint32_t off[VM];
+  int kc[VM];
+#pragma unroll
+  for (int q = 0; q < VM; ++q) {
+    const int u = wave + 4 * q;
+    if (q < UA / 4) {
+      off[q] = OA::source(u, lane, g.a[0].ld, &kc[q]);
+    } else {
+      int ub = u - UA;
+      if (DUAL && ub >= UB / 2) ub -= UB / 2;
+      off[q] = OB::source(ub, lane, g.b[0].ld, &kc[q]);
+    }
+  }
+  auto issue = [&](int slot, int st, int q) {
+    const bool there = st < nst;
+    const int abs_st = st_first + st;
+    const int seg = abs_st >= st_seg0 ? 1 : 0;
+    const int64_t k0 = (int64_t)(abs_st - (seg ? st_seg0 : 0)) * KB;
+    const int64_t kd = seg ? g.kdim[1] : g.kdim[0];
+    const int u = wave + 4 * q;
+    uint32_t o = off[q];
+    rsrc_t r;
+    if (q < UA / 4) {
+      const Matrix m = seg ? g.a[1] : g.a[0];
+      r = OA::origin(m, m0, k0, there);
+      if (!AC && k0 + kc[q] >= kd) o = kOut;
+    } else {
+      Matrix m = seg ? g.b[1] : g.b[0];
+      if (DUAL && u - UA >= UB / 2) m = g.b_up;
+      r = OB::origin(m, n0, k0, there);
+      if (!BC && k0 + kc[q] >= kd) o = kOut;
+    }
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (MOE_LDS void *)(ring[slot] + u * 1024), 16, o, 0,
+                                             0, 0);
+  };
+
+  f32x16 acc[MI][NI];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NI; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+
+  u32x4 fa[2][MI], fb[2][NI];
+  auto read = [&](int buf, int slot, int s) {
+    const uint8_t *A = ring[slot], *B = ring[slot] + UA * 1024;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) fa[buf][i] = OA::fragment(A, (wm * MI + i) * 32, s, lane);
+#pragma unroll
+    for (int j = 0; j < NI; ++j) fb[buf][j] = OB::fragment(B, (wn * NI + j) * 32, s, lane);
+  };
+  auto multiply = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NI; ++j) mma<T>(acc[i][j], fa[buf][i], fb[buf][j]);
+  };
+
+#pragma unroll
+  for (int p = 0; p < NS - 1; ++p)
+#pragma unroll
+    for (int q = 0; q < VM; ++q) issue(p, p, q);
+  __builtin_amdgcn_s_waitcnt(MOE_VMCNT(2 * VM));
+  __builtin_amdgcn_s_barrier();
+  read(0, 0, 0);
+  // Stage st from slot p.  Its second step's fragments are read while the
+  // first step multiplies; then, with every read of this slot done and the
+  // next stage landed (two younger stages may be in flight), one barrier, the
+  // next stage's first fragments, and the second step's MFMAs.  The slot the
+  // previous stage used (free since the previous barrier) is refilled during
+  // the first step.  Stages past the end copy nothing.
+  for (int st0 = 0; st0 < nst; st0 += NS) {
+#pragma unroll
+    for (int p = 0; p < NS; ++p) {
+      const int st = st0 + p;
+      read(1, p, 1);
+#pragma unroll
+      for (int q = 0; q < VM; ++q) issue((p + NS - 1) % NS, st + NS - 1, q);
+      multiply(0);
+      __builtin_amdgcn_s_waitcnt(MOE_VMCNT(2 * VM) & ~(15 << 8));    // and lgkmcnt(0)
+      __builtin_amdgcn_s_barrier();
+      read(0, (p + 1) % NS, 0);
+      multiply(1);
+    }
+  }
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+
+  // Epilogue: 32 rows of each wave row (64 rows of D) at a time go through LDS
+  // as fp32, so that a thread then holds eight consecutive columns of a row.
+  // Consecutive groups use the two halves of the ring in turn.
+  constexpr int PIECES = TO / 8;
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    float *h0 = (float *)((i & 1) ? L2 : L0), *h1 = (float *)((i & 1) ? L3 : L1);
+    float *half = wm ? h1 : h0;
+#pragma unroll
+    for (int j = 0; j < NI; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        half[(8 * (e >> 2) + 4 * (lane >> 5) + (e & 3)) * TN + (wn * NI + j) * 32 + (lane & 31)] =
+            acc[i][j][e];
+    __syncthreads();
+    for (int idx = threadIdx.x; idx < 64 * PIECES; idx += 256) {
+      const int r = idx / PIECES, c = (idx - r * PIECES) * 8;
+      const int64_t m = m0 + (r >> 5) * (32 * MI) + i * 32 + (r & 31);
+      const int64_t n = n0 + c;
+      if (m >= g.M || n >= g.e.N) continue;
+      const float *row = (r >> 5 ? h1 : h0) + (r & 31) * TN + c;
+      float v[8], u[8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const f32x4 w = *(const f32x4 *)(row + 4 * h);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[4 * h + j] = w[j];
+        if constexpr (DUAL) {
+          const f32x4 w2 = *(const f32x4 *)(row + TO + 4 * h);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) u[4 * h + j] = w2[j];
+        }
+      }
+      if (g.parts > 1) {
+        float *o = g.part + (((int64_t)part * (DUAL ? 2 : 1)) * g.M + m) * g.ldp + n;
+        store8<float>(o, v, 8, true);
+        if constexpr (DUAL) store8<float>(o + g.M * g.ldp, u, 8, true);
+      } else {
+        finish8<T, DUAL>(g.e, v, u, m, (int)n);
+      }
+    }
+  }
+}
+
+// Sum of the parts of a split product, in order, and the epilogue.
+template <typename T, bool DUAL>
+__global__ __launch_bounds__(256) void sum_parts_kernel(const GemmOp g) {
+  const int pieces = (g.e.N + 7) / 8;
+  const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (idx >= g.M * pieces) return;
+  const int64_t m = idx / pieces;
+  const int n = (int)(idx - m * pieces) * 8;
+  constexpr int D = DUAL ? 2 : 1;
+  float v[8] = {}, u[8] = {}, t[8];
+  for (int p = 0; p < g.parts; ++p) {
+    const float *o = g.part + ((int64_t)p * D * g.M + m) * g.ldp + n;
+    load8<float>(t, o, 8, true);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += t[j];
+    if constexpr (DUAL) {
+      load8<float>(t, o + g.M * g.ldp, 8, true);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[j] += t[j];
+    }
+  }
+  finish8<T, DUAL>(g.e, v, u, m, n);
+}
+
+// ---------------------------------------------------------------------------
+// Rows of `cols` elements at stride ld to padded rows of ldo, zeros behind.
+template <typename T>
+__global__ __launch_bounds__(256) void pad_rows_kernel(const T *src, int64_t ld, int64_t rows,
+                                                       int cols, T *dst, int64_t ldo) {
+  const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t pieces = ldo / (16 / sizeof(T));
+  if (idx >= rows * pieces) return;
+  const int64_t r = idx / pieces;
+  const int c = (int)(idx - r * pieces) * (int)(16 / sizeof(T));
+  alignas(16) T v[16 / sizeof(T)];
+#pragma unroll
+  for (int j = 0; j < (int)(16 / sizeof(T)); ++j)
+    v[j] = c + j < cols ? src[r * ld + c + j] : (T)0.f;
+  *(u32x4 *)(dst + r * ldo + c) = *(const u32x4 *)v;
+}
+
+// dz = dy act'(z) (swiglu: dz and du) in rows of ldz, zeros behind column N,
+// and the column sums of dz over this workgroup's rows.  A workgroup takes 64
+// columns and a share of the rows: thread (c8, r) eight columns of every 32nd row.
+struct SlopeArgs {
+  const void *dy, *z, *z_up;
+  void *dz, *du;               // null: column sums alone
+  float *sums;                 // [parts][DUAL ? 2 : 1][N], or null
+  int64_t M, ld_dy, ldz;
+  int N, act, parts, vec;
+  float limit;
+};
+template <typename T, bool DUAL>
+__global__ __launch_bounds__(256) void slope_kernel(const SlopeArgs a) {
+  constexpr int D = DUAL ? 2 : 1;
+  __shared__ float red[D][32][65];
+  const int c8 = threadIdx.x & 7, r0 = threadIdx.x >> 3;
+  const int n = blockIdx.x * 64 + c8 * 8;
+  const int part = blockIdx.y;
+  const int64_t lo = a.M * part / a.parts, hi = a.M * (part + 1) / a.parts;
+  const int left = a.N - n;
+  const bool vec = a.vec != 0;
+  float s[D][8] = {};
+  for (int64_t m = lo + r0; m < hi; m += 32) {
+    float g[8], z[8], u[8], dz[8], du[8];
+    if (left <= 0 && n >= a.ldz) break;
+    load8<T>(g, (const T *)a.dy + m * a.ld_dy + n, left, vec);
+    if (a.z) load8<T>(z, (const T *)a.z + m * a.N + n, left, vec);
+    if constexpr (DUAL) load8<T>(u, (const T *)a.z_up + m * a.N + n, left, vec);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if constexpr (DUAL) {
+        float gg = z[j], w = u[j];
+        bool on = j < left, on_up = on;        // clamped: no gradient, whatever dy holds
+        if (a.limit > 0.f) {
+          if (gg > a.limit) { gg = a.limit; on = false; }
+          if (w > a.limit) { w = a.limit; on_up = false; }
+          if (w < -a.limit) { w = -a.limit; on_up = false; }
+        }
+        const float sg = sigmoid<T>(gg);
+        dz[j] = on ? g[j] * w * sg * (1.f + gg * (1.f - sg)) : 0.f;
+        du[j] = on_up ? g[j] * gg * sg : 0.f;
+        s[0][j] += dz[j];
+        s[D - 1][j] += du[j];
+      } else {
+        const float sl = a.z ? slope<T>(z[j], a.act) : 1.f;
+        dz[j] = sl != 0.f && j < left ? g[j] * sl : 0.f;
+        s[0][j] += dz[j];
+      }
+    }
+    if (a.dz && n < a.ldz) {
+      store8<T>((T *)a.dz + m * a.ldz + n, dz, (int)(a.ldz - n < 8 ? a.ldz - n : 8), true);
+      if constexpr (DUAL)
+        store8<T>((T *)a.du + m * a.ldz + n, du, (int)(a.ldz - n < 8 ? a.ldz - n : 8), true);
+    }
+  }
+  if (!a.sums) return;
+#pragma unroll
+  for (int d = 0; d < D; ++d)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) red[d][r0][c8 * 8 + j] = s[d][j];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 64 * D; i += 256) {
+    const int d = i >> 6, c = i & 63;
+    if (blockIdx.x * 64 + c >= a.N) continue;
+    float v = 0.f;
+    for (int r = 0; r < 32; ++r) v += red[d][r][c];
+    a.sums[((int64_t)part * D + d) * a.N + blockIdx.x * 64 + c] = v;
+  }
+}
+
+// db: the parts' column sums added in order.
+template <typename T>
+__global__ __launch_bounds__(256) void bias_sum_kernel(const float *sums, int N, int parts, int d,
+                                                       T *db, T *db_up) {
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= N * d) return;
+  const int which = i / N, n = i - which * N;
+  T *out = which ? db_up : db;
+  if (!out) return;
+  float v = 0.f;
+  for (int p = 0; p < parts; ++p) v += sums[((int64_t)p * d + which) * N + n];
+  out[n] = (T)v;
+}
+
+// ---------------------------------------------------------------------------
+// Tile shape and parts of a product of `rows` x `cols` (cols of both matrices
+// for swiglu) over `stages` stages.
+struct Shape { int mi, ni, parts; };
+
+// Per-CU cost of a stage in cycles, from the MFMA cycles of the tile (each
+// 32 x 32 block and step 32 cycles on one of four SIMDs) and the share of them
+// the shapes reach on long contractions.
+Shape pick_shape(int64_t rows, int64_t cols, int64_t stages, bool f32) {
+  struct { int mi, ni; double eff; } shapes[] = {
+      {4, 4, 0.85}, {4, 2, 0.75}, {2, 2, 0.6}, {1, 1, 0.3}};
+  Shape best = {1, 1, 1};
+  double best_t = 1e300;
+  for (const auto &sh : shapes) {
+    const int64_t tiles = ((rows + 64 * sh.mi - 1) / (64 * sh.mi)) *
+                          ((cols + 64 * sh.ni - 1) / (64 * sh.ni));
+    const double stage = 64.0 * sh.mi * sh.ni * (f32 ? 8 : 1) / sh.eff;
+    for (int parts = 1; parts <= 16; parts *= 2) {
+      if (parts > 1 && (stages < 16 * parts || tiles * parts > 1024)) break;
+      const double rounds = (double)((tiles * parts + 255) / 256);
+      double t = rounds * ((double)((stages + parts - 1) / parts) * stage + 3000.0);
+      // partial sums: written, read and finished at about 1500 bytes a cycle
+      if (parts > 1) t += 8000.0 + (double)rows * cols * 8.0 * parts / 1500.0;
+      if (t < best_t) {
+        best_t = t;
+        best = {sh.mi, sh.ni, parts};
+      }
+    }
+  }
+  return best;
+}
+
+Shape shape_of(int64_t rows, int64_t cols, const int64_t *kdim, int segments, int dtype) {
+  const int64_t kb = dtype == MOE_DTYPE_F32 ? 16 : 32;
+  int64_t st = 0;
+  for (int i = 0; i < segments; ++i) st += (kdim[i] + kb - 1) / kb;
+  return pick_shape(rows, cols, st, dtype == MOE_DTYPE_F32);
+}
+
+size_t part_bytes(int64_t rows, int64_t cols, bool dual, const Shape &s) {
+  return s.parts > 1 ? (size_t)s.parts * (dual ? 2 : 1) * rows * ((cols + 7) / 8 * 8) * 4 : 0;
+}
+
+template <typename T, int MI, int NI, bool AC, bool BC, bool DUAL>
+hipError_t run_gemm_shape(GemmOp g, hipStream_t s) {
+  constexpr int TM = 64 * MI, TO = DUAL ? 32 * NI : 64 * NI;
+  g.m_tiles = (g.M + TM - 1) / TM;
+  g.n_tiles = (g.e.N + TO - 1) / TO;
+  const int64_t items = g.m_tiles * g.n_tiles * g.parts;
+  hipLaunchKernelGGL((gemm_kernel<T, MI, NI, AC, BC, DUAL>), dim3((unsigned)(8 * ((items + 7) / 8))),
+                     dim3(256), 0, s, g);
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess || g.parts == 1) return err;
+  const int64_t pieces = g.M * ((g.e.N + 7) / 8);
+  hipLaunchKernelGGL((sum_parts_kernel<T, DUAL>), dim3((unsigned)((pieces + 255) / 256)), dim3(256),
+                     0, s, g);
+  return hipGetLastError();
+}
+
+template <typename T, bool AC, bool BC, bool DUAL>
+hipError_t run_gemm(GemmOp g, const Shape &sh, void *part, hipStream_t s) {
+  g.parts = sh.parts;
+  g.part = (float *)part;
+  g.ldp = (g.e.N + 7) / 8 * 8;
+  if (sh.mi == 4 && sh.ni == 4) return run_gemm_shape<T, 4, 4, AC, BC, DUAL>(g, s);
+  if (sh.mi == 4) return run_gemm_shape<T, 4, 2, AC, BC, DUAL>(g, s);
+  if (sh.mi == 2) return run_gemm_shape<T, 2, 2, AC, BC, DUAL>(g, s);
+  return run_gemm_shape<T, 1, 1, AC, BC, DUAL>(g, s);
+}
+
+template <typename T>
+hipError_t pad_rows(const void *src, int64_t ld, int64_t rows, int cols, void *dst, int64_t ldo,
+                    hipStream_t s) {
+  const int64_t n = rows * (ldo / (16 / sizeof(T)));
+  if (n == 0) return hipSuccess;
+  hipLaunchKernelGGL((pad_rows_kernel<T>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s,
+                     (const T *)src, ld, rows, cols, (T *)dst, ldo);
+  return hipGetLastError();
+}
+
+bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
+
+// Row chunks of the column sums: enough workgroups to fill the GPU, each with
+// rows to add.
+int colsum_parts(int64_t M, int N) {
+  const int64_t across = (N + 63) / 64;
+  int64_t parts = (1024 + across - 1) / across;
+  const int64_t most = (M + 63) / 64;
+  return (int)(parts > most ? most : parts);
+}
+
+bool odd_rows(int64_t width, int64_t ld, int dtype) {
+  return width % linear_pad(1, dtype) || ld % linear_pad(1, dtype);
+}
+
+template <typename T>
+hipError_t linear_forward(const moe_linear_config &c, const moe_linear_weights &w, const void *x,
+                          const void *residual, void *y, void *z, void *z_up, char *ws,
+                          hipStream_t s) {
+  const LinearSpace L = linear_space(c, false, false, false, false);
+  const int64_t M = c.rows, K = c.in_dim, N = c.out_dim;
+  const bool dual = c.activation == MOE_ACTIVATION_SWIGLU;
+  hipError_t err;
+  Matrix mx = {x, c.ld_x, M, K}, mw = {w.w, K, N, K}, mu = {w.w_up, K, N, K};
+  const int64_t Kp = linear_pad(K, c.dtype);
+  if (odd_rows(K, c.ld_x, c.dtype)) {
+    if ((err = pad_rows<T>(x, c.ld_x, M, (int)K, ws + L.x, Kp, s)) != hipSuccess) return err;
+    mx = {ws + L.x, Kp, M, Kp};
+  }
+  if (odd_rows(K, K, c.dtype)) {
+    if ((err = pad_rows<T>(w.w, K, N, (int)K, ws + L.w, Kp, s)) != hipSuccess) return err;
+    mw = {ws + L.w, Kp, N, Kp};
+    if (dual) {
+      if ((err = pad_rows<T>(w.w_up, K, N, (int)K, ws + L.w_up, Kp, s)) != hipSuccess) return err;
+      mu = {ws + L.w_up, Kp, N, Kp};
+    }
+  }
+  GemmOp g = {};
+  g.a[0] = mx; g.b[0] = mw; g.b_up = mu;
+  g.kdim[0] = K;
+  g.segments = 1;
+  g.M = M;
+  Epilogue &e = g.e;
+  e.bias = w.bias; e.bias_up = w.bias_up; e.residual = residual;
+  e.y = y; e.z = z; e.z_up = z_up;
+  e.ld_y = c.ld_y; e.ld_res = c.ld_residual; e.ld_z = N;
+  e.N = (int)N; e.act = c.activation; e.limit = c.limit;
+  e.vec = !odd_rows(N, c.ld_y, c.dtype) && (!residual || !odd_rows(N, c.ld_residual, c.dtype)) &&
+          N % 8 == 0 && aligned16(y) && aligned16(z) && aligned16(z_up) && aligned16(residual) &&
+          aligned16(w.bias) && aligned16(w.bias_up);
+  const Shape sh = shape_of(M, dual ? 2 * N : N, g.kdim, 1, c.dtype);
+  return dual ? run_gemm<T, false, false, true>(g, sh, ws + L.part, s)
+              : run_gemm<T, false, false, false>(g, sh, ws + L.part, s);
+}
+
+template <typename T>
+hipError_t linear_backward(const moe_linear_config &c, const moe_linear_weights &w, const void *x,
+                           const void *dy, const void *z, const void *z_up,
+                           const moe_linear_grads &gr, char *ws, hipStream_t s) {
+  const bool dual = c.activation == MOE_ACTIVATION_SWIGLU;
+  const bool want_dw = gr.dw || gr.dw_up, want_db = gr.dbias || gr.dbias_up;
+  const LinearSpace L = linear_space(c, true, gr.dx != nullptr, want_dw, want_db);
+  const int64_t M = c.rows, K = c.in_dim, N = c.out_dim;
+  const int64_t Kp = linear_pad(K, c.dtype), Np = linear_pad(N, c.dtype);
+  hipError_t err;
+  // dz: dy itself where nothing changes it and its rows are whole pieces
+  const bool same = c.activation == MOE_ACTIVATION_NONE && !odd_rows(N, c.ld_y, c.dtype);
+  Matrix mz = {dy, c.ld_y, M, N}, mu = {};
+  if (!same) {
+    mz = {ws + L.dz, Np, M, Np};
+    if (dual) mu = {ws + L.du, Np, M, Np};
+  }
+  if (!same || want_db) {
+    SlopeArgs a = {};
+    a.dy = dy; a.z = c.activation == MOE_ACTIVATION_NONE ? nullptr : z; a.z_up = z_up;
+    a.dz = same || !(gr.dx || want_dw) ? nullptr : ws + L.dz;
+    a.du = ws + L.du;
+    a.sums = want_db ? (float *)(ws + L.colsum) : nullptr;
+    a.M = M; a.ld_dy = c.ld_y; a.ldz = Np; a.N = (int)N; a.act = c.activation;
+    a.limit = c.limit;
+    a.parts = colsum_parts(M, (int)N);
+    a.vec = !odd_rows(N, c.ld_y, c.dtype) && N % 8 == 0 && aligned16(z) && aligned16(z_up);
+    const dim3 grid((unsigned)((Np + 63) / 64), (unsigned)a.parts);
+    if (M > 0) {                               // no rows: the sums below are empty
+      if (dual) hipLaunchKernelGGL((slope_kernel<T, true>), grid, dim3(256), 0, s, a);
+      else hipLaunchKernelGGL((slope_kernel<T, false>), grid, dim3(256), 0, s, a);
+    }
+    if ((err = hipGetLastError()) != hipSuccess) return err;
+    if (want_db) {
+      const int d = dual ? 2 : 1;
+      hipLaunchKernelGGL((bias_sum_kernel<T>), dim3((unsigned)((N * d + 255) / 256)), dim3(256), 0,
+                         s, (const float *)(ws + L.colsum), (int)N, a.parts, d, (T *)gr.dbias,
+                         (T *)gr.dbias_up);
+      if ((err = hipGetLastError()) != hipSuccess) return err;
+    }
+  }
+  if (gr.dx && M > 0) {
+    Matrix mw = {w.w, K, N, K}, mwu = {w.w_up, K, N, K};
+    if (odd_rows(K, K, c.dtype)) {
+      if ((err = pad_rows<T>(w.w, K, N, (int)K, ws + L.w, Kp, s)) != hipSuccess) return err;
+      mw = {ws + L.w, Kp, N, Kp};
+      if (dual) {
+        if ((err = pad_rows<T>(w.w_up, K, N, (int)K, ws + L.w_up, Kp, s)) != hipSuccess) return err;
+        mwu = {ws + L.w_up, Kp, N, Kp};
+      }
+    }
+    GemmOp g = {};
+    g.a[0] = mz; g.b[0] = mw;
+    g.a[1] = mu; g.b[1] = mwu;
+    g.kdim[0] = N; g.kdim[1] = N;
+    g.segments = dual ? 2 : 1;
+    g.M = M;
+    g.e.y = gr.dx; g.e.ld_y = c.ld_x; g.e.N = (int)K; g.e.act = MOE_ACTIVATION_NONE;
+    g.e.vec = !odd_rows(K, c.ld_x, c.dtype) && K % 8 == 0 && aligned16(gr.dx);
+    const Shape sh = shape_of(M, K, g.kdim, g.segments, c.dtype);
+    if ((err = run_gemm<T, false, true, false>(g, sh, ws + L.part, s)) != hipSuccess) return err;
+  }
+  if (want_dw) {
+    Matrix mx = {x, c.ld_x, M, K};
+    if (odd_rows(K, c.ld_x, c.dtype)) {
+      if ((err = pad_rows<T>(x, c.ld_x, M, (int)K, ws + L.x, Kp, s)) != hipSuccess) return err;
+      mx = {ws + L.x, Kp, M, Kp};
+    }
+    for (int i = 0; i < (dual ? 2 : 1); ++i) {
+      void *out = i ? gr.dw_up : gr.dw;
+      if (!out) continue;
+      GemmOp g = {};
+      g.a[0] = i ? mu : mz; g.b[0] = mx;
+      g.kdim[0] = M;
+      g.segments = 1;
+      g.M = N;
+      g.e.y = out; g.e.ld_y = K; g.e.N = (int)K; g.e.act = MOE_ACTIVATION_NONE;
+      g.e.vec = K % 8 == 0 && aligned16(out);
+      const Shape sh = shape_of(N, K, g.kdim, 1, c.dtype);
+      if ((err = run_gemm<T, true, true, false>(g, sh, ws + L.part, s)) != hipSuccess) return err;
+    }
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+LinearSpace linear_space(const moe_linear_config &c, bool backward, bool dx, bool dw, bool db) {
+  const int64_t M = c.rows, K = c.in_dim, N = c.out_dim;
+  const int64_t Kp = linear_pad(K, c.dtype), Np = linear_pad(N, c.dtype);
+  const size_t es = c.dtype == MOE_DTYPE_F32 ? 4 : 2;
+  const bool dual = c.activation == MOE_ACTIVATION_SWIGLU;
+  LinearSpace l = {};
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = (off + bytes + 255) / 256 * 256;
+    return o;
+  };
+  const bool use_x = !backward || dw, use_w = !backward || dx;
+  l.x = take(use_x && odd_rows(K, c.ld_x, c.dtype) ? es * M * Kp : 0);
+  l.w = take(use_w && odd_rows(K, K, c.dtype) ? es * N * Kp : 0);
+  l.w_up = take(use_w && dual && odd_rows(K, K, c.dtype) ? es * N * Kp : 0);
+  size_t part = 0;
+  auto need = [&](int64_t rows, int64_t cols, int64_t k, int segments, bool two) {
+    const int64_t kd[2] = {k, k};
+    const Shape s = shape_of(rows, two ? 2 * cols : cols, kd, segments, c.dtype);
+    const size_t b = part_bytes(rows, cols, two, s);
+    if (b > part) part = b;
+  };
+  if (backward) {
+    const bool same = c.activation == MOE_ACTIVATION_NONE && !odd_rows(N, c.ld_y, c.dtype);
+    l.dz = take(!same && (dx || dw) ? es * M * Np : 0);
+    l.du = take(dual && (dx || dw) ? es * M * Np : 0);
+    l.colsum = take(db ? sizeof(float) * colsum_parts(M, (int)N) * (dual ? 2 : 1) * N : 0);
+    if (dx) need(M, K, N, dual ? 2 : 1, false);
+    if (dw) need(N, K, M, 1, false);
+  } else {
+    need(M, N, K, 1, dual);
+  }
+  l.part = take(part);
+  l.total = off;
+  return l;
+}
+
+hipError_t launch_linear(const moe_linear_config &c, const moe_linear_weights &w, const void *x,
+                         const void *residual, void *y, void *z, void *z_up, char *ws,
+                         hipStream_t s) {
+  return c.dtype == MOE_DTYPE_F32
+             ? linear_forward<float>(c, w, x, residual, y, z, z_up, ws, s)
+             : linear_forward<bf16>(c, w, x, residual, y, z, z_up, ws, s);
+}
+
+hipError_t launch_linear_backward(const moe_linear_config &c, const moe_linear_weights &w,
+                                  const void *x, const void *dy, const void *z, const void *z_up,
+                                  const moe_linear_grads &g, char *ws, hipStream_t s) {
+  return c.dtype == MOE_DTYPE_F32 ? linear_backward<float>(c, w, x, dy, z, z_up, g, ws, s)
+                                  : linear_backward<bf16>(c, w, x, dy, z, z_up, g, ws, s);
+}
+
+}  // namespace moe

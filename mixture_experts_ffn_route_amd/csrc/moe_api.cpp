@@ -13,6 +13,7 @@
 
 #include "few.h"
 #include "internal.h"
+#include "linear.h"
 #include "moe.h"
 
 namespace {
@@ -172,6 +173,30 @@ int make_few_layout(const moe_config *c, int64_t T, moe_few_layout *out) {
   if (out) *out = l;
   return MOE_OK;
 }
+
+// Checks a linear layer and fills in the strides given as 0.
+int check_linear(const moe_linear_config *c, moe_linear_config *out) {
+  if (!c) return MOE_ERR_INVALID_ARG;
+  *out = *c;
+  if (c->rows < 0 || c->in_dim < 1 || c->out_dim < 1) return MOE_ERR_INVALID_ARG;
+  if (c->dtype != MOE_DTYPE_F32 && c->dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
+  if (c->activation < MOE_ACTIVATION_NONE || c->activation > MOE_ACTIVATION_SWIGLU)
+    return MOE_ERR_INVALID_ARG;
+  if (!(c->limit >= 0.f) || std::isinf(c->limit)) return MOE_ERR_INVALID_ARG;
+  if (c->limit > 0.f && c->activation != MOE_ACTIVATION_SWIGLU) return MOE_ERR_INVALID_ARG;
+  if (out->ld_x == 0) out->ld_x = c->in_dim;
+  if (out->ld_y == 0) out->ld_y = c->out_dim;
+  if (out->ld_residual == 0) out->ld_residual = c->out_dim;
+  if (out->ld_x < c->in_dim || out->ld_y < c->out_dim || out->ld_residual < c->out_dim)
+    return MOE_ERR_INVALID_ARG;
+  // the kernels address a tile's rows with 32-bit byte offsets
+  if (out->ld_x > MOE_LINEAR_MAX_LD || out->ld_y > MOE_LINEAR_MAX_LD ||
+      out->ld_residual > MOE_LINEAR_MAX_LD || c->rows > INT32_MAX)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+bool misaligned(const void *p, size_t n) { return (uintptr_t)p % n != 0; }
 
 int hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
@@ -765,6 +790,70 @@ int moe_forward_ex(const moe_config *cfg, const moe_weights *w, const void *x,
   if (side_stream && side_stream == stream) return MOE_ERR_INVALID_ARG;
   return forward_impl(cfg, w, x, token_ids, T, y, ws, ws_bytes, (hipEvent_t *)events, stream,
                       side_stream);
+}
+
+size_t moe_linear_workspace_size(const moe_linear_config *cfg, int32_t backward) {
+  moe_linear_config c;
+  if (check_linear(cfg, &c) != MOE_OK) return 0;
+  const size_t n = moe::linear_space(c, backward != 0, true, true, true).total;
+  return n < kAlign ? kAlign : n;
+}
+
+int moe_linear(const moe_linear_config *cfg, const moe_linear_weights *w, const void *x,
+               const void *residual, void *y, void *z, void *z_up, void *ws, size_t ws_bytes,
+               void *stream) {
+  moe_linear_config c;
+  const int st = check_linear(cfg, &c);
+  if (st != MOE_OK) return st;
+  const bool dual = c.activation == MOE_ACTIVATION_SWIGLU;
+  const size_t es = c.dtype == MOE_DTYPE_F32 ? 4 : 2;
+  if (!w || !w->w || (dual != (w->w_up != nullptr)) || (!dual && w->bias_up))
+    return MOE_ERR_INVALID_ARG;
+  if ((z && dual && !z_up) || (z_up && (!z || !dual))) return MOE_ERR_INVALID_ARG;
+  if (c.rows == 0) return MOE_OK;
+  if (!x || !y || x == y || y == z || y == z_up || (residual == y && c.ld_residual != c.ld_y))
+    return MOE_ERR_INVALID_ARG;
+  if (misaligned(x, 16) || misaligned(w->w, 16) || misaligned(w->w_up, 16))
+    return MOE_ERR_INVALID_ARG;
+  for (const void *p : {(const void *)y, residual, (const void *)z, (const void *)z_up, w->bias,
+                        w->bias_up})
+    if (misaligned(p, es)) return MOE_ERR_INVALID_ARG;
+  const size_t need = moe::linear_space(c, false, true, true, true).total;
+  if (need > 0 && (!ws || misaligned(ws, kAlign) || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  return hip_status(moe::launch_linear(c, *w, x, residual, y, z, z_up, (char *)ws,
+                                       (hipStream_t)stream));
+}
+
+int moe_linear_backward(const moe_linear_config *cfg, const moe_linear_weights *w, const void *x,
+                        const void *dy, const void *z, const void *z_up,
+                        const moe_linear_grads *grads, void *ws, size_t ws_bytes, void *stream) {
+  moe_linear_config c;
+  const int st = check_linear(cfg, &c);
+  if (st != MOE_OK) return st;
+  const bool dual = c.activation == MOE_ACTIVATION_SWIGLU;
+  const size_t es = c.dtype == MOE_DTYPE_F32 ? 4 : 2;
+  if (!w || !grads) return MOE_ERR_INVALID_ARG;
+  const bool want_dw = grads->dw || grads->dw_up, want_db = grads->dbias || grads->dbias_up;
+  if (!grads->dx && !want_dw && !want_db) return MOE_ERR_INVALID_ARG;
+  if (!dual && (grads->dw_up || grads->dbias_up)) return MOE_ERR_INVALID_ARG;
+  if (c.rows > 0) {
+    if (!dy || misaligned(dy, 16)) return MOE_ERR_INVALID_ARG;
+    if (c.activation != MOE_ACTIVATION_NONE && (!z || (dual && !z_up))) return MOE_ERR_INVALID_ARG;
+    if (grads->dx && (!w->w || (dual && !w->w_up))) return MOE_ERR_INVALID_ARG;
+    if (want_dw && !x) return MOE_ERR_INVALID_ARG;
+    if (misaligned(x, 16) || misaligned(w->w, 16) || misaligned(w->w_up, 16))
+      return MOE_ERR_INVALID_ARG;
+    if (grads->dx && (grads->dx == dy || grads->dx == x)) return MOE_ERR_INVALID_ARG;
+  }
+  for (const void *p : {z, z_up, (const void *)grads->dx, (const void *)grads->dw,
+                        (const void *)grads->dw_up, (const void *)grads->dbias,
+                        (const void *)grads->dbias_up})
+    if (misaligned(p, es)) return MOE_ERR_INVALID_ARG;
+  const size_t need =
+      moe::linear_space(c, true, grads->dx != nullptr, want_dw, want_db).total;
+  if (need > 0 && (!ws || misaligned(ws, kAlign) || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  return hip_status(moe::launch_linear_backward(c, *w, x, dy, z, z_up, *grads, (char *)ws,
+                                                (hipStream_t)stream));
 }
 
 int moe_probe_read(const void *buf, int64_t bytes, void *out, void *stream) {
