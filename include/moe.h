@@ -395,8 +395,8 @@ int moe_forward_noalloc(const moe_config *cfg, const moe_weights *w, const void 
 
 /* moe_forward for a few tokens (T of 1 .. MOE_FEW_MAX_TOKENS): the decode step
  * of a handful of sequences.  The same layer -- every routing, expert type,
- * activation encoding and weight layout moe_forward takes -- in three launches
- * and no permutation.  Results agree with moe_forward's to rounding (H keeps 16
+ * activation encoding and weight layout moe_forward takes -- without the
+ * permutation and with the inputs of a weight stream in mind.  Results agree with moe_forward's to rounding (H keeps 16
  * bits and the weighted expert outputs are summed in fp32, so this form rounds
  * less); the routing follows the same rules.
  *   x, token_ids, y, w, stream  as moe_forward; x, y and the matrices (not the
@@ -418,16 +418,18 @@ typedef struct {
   size_t flags;                /* uint32 [4]     device error flags; flags[0] as
                                   moe_forward's: an expert id outside [0, E)
                                   (MOE_FLAG_EXPERT_RANGE) adds nothing           */
-  size_t route_logits;         /* float          partial gate logits             */
+  size_t scores;               /* float [T, E]   affinities (softmax: logits)    */
   size_t plan_slots;           /* int32 [1]      distinct chosen experts         */
   size_t plan_experts;         /* int32 [T*k]    their ids, by first appearance  */
   size_t plan_weights;         /* float [T*k, 16] gate value per (expert, token) */
   size_t plan_rows;            /* int16 [T*k, 16] its row of h, -1: not chosen   */
+  size_t plan_masks;           /* int32 [T]      choices that hold a row         */
   size_t xq, xq_scales;        /* MXFP8 copy of x (act_quant)                    */
   size_t hq, hq_scales;        /* MXFP8 SwiGLU rows [T*k, I] (act_quant)         */
   size_t h, h_lo;              /* SwiGLU rows [T*k + T, I]: fp32, or the high and
                                   low bf16 whose sum is the value (T*k .. : the
                                   shared expert's; MXFP8 layers: those alone)    */
+  size_t yrows;                /* float [T*k + T, d] weighted expert outputs     */
 } moe_few_layout;
 int moe_few_workspace_layout(const moe_config *cfg, int64_t T, moe_few_layout *layout);
 size_t moe_few_workspace_size(const moe_config *cfg, int64_t T); /* 0 if invalid */

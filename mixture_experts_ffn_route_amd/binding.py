@@ -70,9 +70,9 @@ class MoeWsLayoutC(ctypes.Structure):
 
 class MoeFewLayoutC(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in (
-        "total_bytes", "route_weights", "route_indices", "flags", "route_logits", "plan_slots",
-        "plan_experts", "plan_weights", "plan_rows", "xq", "xq_scales", "hq", "hq_scales", "h",
-        "h_lo")]
+        "total_bytes", "route_weights", "route_indices", "flags", "scores", "plan_slots",
+        "plan_experts", "plan_weights", "plan_rows", "plan_masks", "xq", "xq_scales", "hq",
+        "hq_scales", "h", "h_lo", "yrows")]
 
 
 class MoeLinearConfigC(ctypes.Structure):

@@ -22,19 +22,19 @@ struct FewArgs {
   float *out_w;                                // [T, k] gate values
   int32_t *out_e;                              // [T, k] expert ids
   uint32_t *flags;                             // [4]
-  float *zpart;                                // [KS, T, E] partial logits
-  int KS;
+  float *scores;                               // [T, E] affinities (softmax: logits)
   uint8_t *xq, *xq_scales;                     // MXFP8 layers, else null
   void *h, *h_lo;                              // [T*k + T, I] SwiGLU output
   uint8_t *hq, *hq_scales;                     // [T*k, I] MXFP8 layers
   int32_t *plan_slots, *plan_expert;           // the distinct chosen experts
   float *plan_w;                               // [slots, 16]
   int16_t *plan_row;                           // [slots, 16]
+  int32_t *plan_mask;                          // [T] choices that hold a row
+  float *yrows;                                // [T*k + T, d] weighted expert outputs
   void *y;
-  int logit_items, shared_items;               // set by launch_few
+  int score_items;                             // set by launch_few
 };
 
-int few_logit_parts(int E, int d, bool f32);
 hipError_t launch_few(FewArgs a, const moe_config &cfg, hipStream_t s);
 
 }  // namespace moe

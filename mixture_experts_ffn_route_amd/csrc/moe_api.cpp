@@ -156,12 +156,12 @@ int make_few_layout(const moe_config *c, int64_t T, moe_few_layout *out) {
   l.route_weights = take(sizeof(float) * pairs);
   l.route_indices = take(sizeof(int32_t) * pairs);
   l.flags = take(sizeof(uint32_t) * 4);
-  l.route_logits =
-      take(learned ? sizeof(float) * moe::few_logit_parts((int)E, (int)d, f32) * T * E : 0);
+  l.scores = take(learned ? sizeof(float) * T * E : 0);
   l.plan_slots = take(sizeof(int32_t));
   l.plan_experts = take(sizeof(int32_t) * pairs);
   l.plan_weights = take(sizeof(float) * 16 * pairs);
   l.plan_rows = take(sizeof(int16_t) * 16 * pairs);
+  l.plan_masks = take(sizeof(int32_t) * T);
   l.xq = take(mx ? T * d : 0);
   l.xq_scales = take(mx ? T * d / 32 : 0);
   l.hq = take(mx ? pairs * I : 0);
@@ -169,6 +169,7 @@ int make_few_layout(const moe_config *c, int64_t T, moe_few_layout *out) {
   const size_t rows = pairs + (c->n_shared_experts ? T : 0);
   l.h = take((f32 ? 4 : 2) * rows * I);
   l.h_lo = take(f32 ? 0 : 2 * rows * I);
+  l.yrows = take(sizeof(float) * rows * d);
   l.total_bytes = off;
   if (out) *out = l;
   return MOE_OK;
@@ -672,7 +673,6 @@ int moe_forward_few(const moe_config *cfg, const moe_weights *w, const void *x,
   if (!ws || ((uintptr_t)ws % kAlign) != 0 || ws_bytes < L.total_bytes) return MOE_ERR_WORKSPACE;
 
   char *base = (char *)ws;
-  const bool f32 = cfg->act_dtype == MOE_DTYPE_F32;
   const bool mx = cfg->act_quant == MOE_ACT_QUANT_MXFP8;
   moe::FewArgs a = {};
   a.x = x; a.y = y;
@@ -692,12 +692,13 @@ int moe_forward_few(const moe_config *cfg, const moe_weights *w, const void *x,
   a.out_w = (float *)(base + L.route_weights);
   a.out_e = (int32_t *)(base + L.route_indices);
   a.flags = (uint32_t *)(base + L.flags);
-  a.zpart = (float *)(base + L.route_logits);
-  a.KS = moe::few_logit_parts(a.E, a.d, f32);
+  a.scores = (float *)(base + L.scores);
   a.plan_slots = (int32_t *)(base + L.plan_slots);
   a.plan_expert = (int32_t *)(base + L.plan_experts);
   a.plan_w = (float *)(base + L.plan_weights);
   a.plan_row = (int16_t *)(base + L.plan_rows);
+  a.plan_mask = (int32_t *)(base + L.plan_masks);
+  a.yrows = (float *)(base + L.yrows);
   a.xq = mx ? (uint8_t *)(base + L.xq) : nullptr;
   a.xq_scales = (uint8_t *)(base + L.xq_scales);
   a.hq = (uint8_t *)(base + L.hq);
