@@ -418,7 +418,7 @@ typedef struct {
   size_t flags;                /* uint32 [4]     device error flags; flags[0] as
                                   moe_forward's: an expert id outside [0, E)
                                   (MOE_FLAG_EXPERT_RANGE) adds nothing           */
-  size_t scores;               /* float [T, E]   affinities (softmax: logits)    */
+  size_t scores;               /* float          partial gate logits             */
   size_t plan_slots;           /* int32 [1]      distinct chosen experts         */
   size_t plan_experts;         /* int32 [T*k]    their ids, by first appearance  */
   size_t plan_weights;         /* float [T*k, 16] gate value per (expert, token) */

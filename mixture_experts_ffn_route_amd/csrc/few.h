@@ -22,7 +22,8 @@ struct FewArgs {
   float *out_w;                                // [T, k] gate values
   int32_t *out_e;                              // [T, k] expert ids
   uint32_t *flags;                             // [4]
-  float *scores;                               // [T, E] affinities (softmax: logits)
+  float *scores;                               // [KS, T, E] partial gate logits
+  int KS;
   uint8_t *xq, *xq_scales;                     // MXFP8 layers, else null
   void *h, *h_lo;                              // [T*k + T, I] SwiGLU output
   uint8_t *hq, *hq_scales;                     // [T*k, I] MXFP8 layers
@@ -35,6 +36,7 @@ struct FewArgs {
   int score_items;                             // set by launch_few
 };
 
+int few_logit_parts(int d, bool f32);
 hipError_t launch_few(FewArgs a, const moe_config &cfg, hipStream_t s);
 
 }  // namespace moe

@@ -43,6 +43,7 @@ typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
 
 constexpr int kRows = MOE_FEW_MAX_TOKENS;      // MFMA rows = tokens
+constexpr int kLogitParts = 8;
 constexpr uint32_t kOut = 0x80000000u;         // an offset no resource here reaches: reads 0
 
 // Weight formats of a product.
@@ -64,6 +65,9 @@ __device__ __forceinline__ rsrc_t resource(const void *p, int64_t bytes) {
 }
 __device__ __forceinline__ u32x4 load16(rsrc_t r, uint32_t off) {
   return __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
+}
+__device__ __forceinline__ u32x2 load8(rsrc_t r, uint32_t off) {
+  return __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0);
 }
 __device__ __forceinline__ uint32_t load4(rsrc_t r, uint32_t off) {
   return __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
@@ -142,29 +146,43 @@ __device__ __forceinline__ u32x4 w_operand(const uint8_t *lds, int b, int f, int
 }
 
 // Scale bytes of a stage: per row block and half (FP4), one (MX8: the block's).
-template <int F, int NB> struct Scales {
-  uint32_t s[F == F_FP4 || F == F_MX4 ? 2 * NB : 1];
-  static constexpr int kLoads = F == F_FP4 || F == F_MX4 ? 2 * NB : F == F_MX8 ? 1 : 0;
+// Row layout: the row's eight bytes of the stage in one load where rows of
+// scales start at multiples of four (K % 128 == 0; ROWS), a quarter of the
+// loads that single bytes take (ROWS_ODD).
+enum { ROWS, ROWS_ODD, TILES };
+template <int F, int L, int NB> struct Scales {
+  static constexpr bool kFp4 = F == F_FP4 || F == F_MX4;
+  uint32_t s[kFp4 ? 2 * NB : 1];
+  static constexpr int kLoads = kFp4 ? (L == ROWS ? NB : 2 * NB) : F == F_MX8 ? 1 : 0;
+  // the scale byte of row block b, half h
+  __device__ __forceinline__ uint32_t get(int b, int h, int lane) const {
+    return L == ROWS ? (s[2 * b + h] >> (8 * (lane >> 4))) & 0xFFu : s[2 * b + h];
+  }
 };
-template <int F, bool TILED, int NB>
-__device__ __forceinline__ void load_scales(Scales<F, NB> &x, const WSrc &w, int K, int lane,
+template <int F, int L, int NB>
+__device__ __forceinline__ void load_scales(Scales<F, L, NB> &x, const WSrc &w, int K, int lane,
                                             int st) {
   const uint32_t r = lane & 15, q = lane >> 4;
   if constexpr (F == F_MX8) {
     x.s[0] = load1(w.rs, st);
   } else if constexpr (F == F_FP4 || F == F_MX4) {
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
+    for (int b = 0; b < NB; ++b) {
+      if constexpr (L == ROWS) {
+        // what follows a row's last scale goes with weights that read as zeros
+        const u32x2 v = load8(w.rs, (b * 16 + r) * (K / 32) + st * 8);
+        x.s[2 * b] = v[0];
+        x.s[2 * b + 1] = v[1];
+      } else {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int half = 2 * st + h;
-        uint32_t off;
-        if constexpr (TILED)
-          off = b * 16 * (K / 32) + (2 * half + (q >> 1)) * 32 + r * 2 + (q & 1);
-        else
-          off = (b * 16 + r) * (K / 32) + half * 4 + q;
-        x.s[2 * b + h] = load1(w.rs, half * 128 + (int)q * 32 < K ? off : kOut);
+        for (int h = 0; h < 2; ++h) {
+          const int half = 2 * st + h;
+          const uint32_t off = L == TILES ? b * 16 * (K / 32) + (2 * half + (q >> 1)) * 32 + r * 2 + (q & 1)
+                                          : (b * 16 + r) * (K / 32) + half * 4 + q;
+          x.s[2 * b + h] = load1(w.rs, half * 128 + (int)q * 32 < K ? off : kOut);
+        }
       }
+    }
   }
 }
 
@@ -238,22 +256,22 @@ __device__ __forceinline__ i32x8 wide(const u32x4 &a, const u32x4 &b) {
 }
 
 // acc += tokens x the 16 rows of row block b over one stage.
-template <int F, bool TILED, bool HILO, int NB>
+template <int F, int L, bool HILO, int NB>
 __device__ __forceinline__ void stage_mma(f32x4 &acc, const Tokens<F, HILO> &a,
-                                          const Scales<F, NB> &sc, const uint8_t *lds, int b,
+                                          const Scales<F, L, NB> &sc, const uint8_t *lds, int b,
                                           int lane) {
   if constexpr (F == F_BF16) {
 #pragma unroll
     for (int f = 0; f < 2; ++f) {
-      const u32x4 w = w_operand<F, TILED>(lds, b, f, lane);
+      const u32x4 w = w_operand<F, L == TILES>(lds, b, f, lane);
       acc = mma16(a.v[f], w, acc);
       if constexpr (HILO) acc = mma16(a.v[2 + f], w, acc);
     }
   } else if constexpr (F == F_FP4) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const u32x4 codes = w_operand<F, TILED>(lds, b, h, lane);
-      const float scale = __uint_as_float(sc.s[2 * b + h] << 23);
+      const u32x4 codes = w_operand<F, L == TILES>(lds, b, h, lane);
+      const float scale = __uint_as_float(sc.get(b, h, lane) << 23);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const bf16x2 v0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[i], scale, 0);
@@ -270,12 +288,12 @@ __device__ __forceinline__ void stage_mma(f32x4 &acc, const Tokens<F, HILO> &a,
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-          wide(a.v[2 * h], a.v[2 * h + 1]), wide(w_operand<F, TILED>(lds, b, h, lane), u32x4{}),
-          acc, 0, 4, 0, (int)a.s[h], 0, (int)sc.s[2 * b + h]);
+          wide(a.v[2 * h], a.v[2 * h + 1]), wide(w_operand<F, L == TILES>(lds, b, h, lane), u32x4{}),
+          acc, 0, 4, 0, (int)a.s[h], 0, (int)sc.get(b, h, lane));
   } else {
     acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
         wide(a.v[0], a.v[1]),
-        wide(w_operand<F, TILED>(lds, b, 0, lane), w_operand<F, TILED>(lds, b, 1, lane)), acc, 0, 0,
+        wide(w_operand<F, L == TILES>(lds, b, 0, lane), w_operand<F, L == TILES>(lds, b, 1, lane)), acc, 0, 0,
         0, (int)a.s[0], 0, (int)sc.s[0]);
   }
 }
@@ -293,7 +311,7 @@ __device__ __forceinline__ u32x4 w_direct(const WSrc &w, int K, int lane, int b,
 // The wave's tile of products: acc[s][b] = tokens x row block b of source s,
 // over stages first, first + step, ... below end, two stages in flight.
 // ring0 / ring1: the wave's two slots of 4 NB KB.
-template <int F, bool TILED, bool HILO, int NB>
+template <int F, int L, bool HILO, int NB>
 __device__ __forceinline__ void tile_dot(f32x4 (&acc)[2][NB], const TSrc &ts, const WSrc (&ws)[2],
                                          int K, int lane, uint32_t row, bool there, int first,
                                          int step, int end, uint8_t *ring0, uint8_t *ring1) {
@@ -315,17 +333,17 @@ __device__ __forceinline__ void tile_dot(f32x4 (&acc)[2][NB], const TSrc &ts, co
         }
     }
   } else {
-    constexpr int VM = 4 * NB + Tokens<F, HILO>::kLoads + 2 * Scales<F, NB>::kLoads;
+    constexpr int VM = 4 * NB + Tokens<F, HILO>::kLoads + 2 * Scales<F, L, NB>::kLoads;
     static_assert(VM <= 63, "vmcnt holds 6 bits");
     Tokens<F, HILO> a[2];
-    Scales<F, NB> sc[2][2];
+    Scales<F, L, NB> sc[2][2];
     auto issue = [&](int p, int st) {
       uint8_t *lds = p ? ring1 : ring0;
       load_tokens<F, HILO>(a[p], ts, K, lane, row, st, out);
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        load_scales<F, TILED, NB>(sc[p][s], ws[s], K, lane, st);
-        copy_stage<F, TILED, NB>(ws[s], K, lane, st, lds + s * NB * 2048);
+        load_scales<F, L, NB>(sc[p][s], ws[s], K, lane, st);
+        copy_stage<F, L == TILES, NB>(ws[s], K, lane, st, lds + s * NB * 2048);
       }
       // keep the loads here: the scheduler otherwise moves them behind the
       // next products
@@ -337,7 +355,7 @@ __device__ __forceinline__ void tile_dot(f32x4 (&acc)[2][NB], const TSrc &ts, co
       for (int s = 0; s < 2; ++s)
 #pragma unroll
         for (int b = 0; b < NB; ++b)
-          stage_mma<F, TILED, HILO, NB>(acc[s][b], a[p], sc[p][s], lds + s * NB * 2048, b, lane);
+          stage_mma<F, L, HILO, NB>(acc[s][b], a[p], sc[p][s], lds + s * NB * 2048, b, lane);
       // the slot's reads are done before a copy may land in it again
       __builtin_amdgcn_s_waitcnt(0xC07F);      // lgkmcnt(0)
       __builtin_amdgcn_sched_barrier(0);
@@ -412,13 +430,13 @@ __device__ __forceinline__ float mx_element(float v, int X) {
 }
 
 // ---------------------------------------------------------------------------
-// few_scores: affinities s[t, e] (softmax: the logits) and, for MXFP8 layers,
-// the codes of x.  A workgroup of 16 waves takes 16 experts, its waves
-// splitting the inputs: one burst of loads per wave, since latency and not
-// bandwidth is what the gate matrix (a few MB) costs.
+// few_scores: partial gate logits and, for MXFP8 layers, the codes of x.  A
+// workgroup takes 16 experts and one of KS parts of the inputs, its four waves
+// splitting those, each with one burst of loads: latency, not bandwidth, is
+// what the gate matrix (a few MB) costs.
 template <int F>
-__global__ __launch_bounds__(1024) void few_scores(const FewArgs a) {
-  __shared__ float red[16 * 256];
+__global__ __launch_bounds__(256) void few_scores(const FewArgs a) {
+  __shared__ float red[4 * 256];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int d = a.d, T = a.T;
@@ -426,7 +444,8 @@ __global__ __launch_bounds__(1024) void few_scores(const FewArgs a) {
   if (item < a.score_items) {
     constexpr int KST = stage_inputs<F>(), DEPTH = 4;
     constexpr int es = F == F_F32 ? 4 : 2;
-    const int n0 = item * 16, nst = (d + KST - 1) / KST;
+    const int part = item % a.KS, n0 = item / a.KS * 16, nst = (d + KST - 1) / KST;
+    const int end = (int)((int64_t)nst * (part + 1) / a.KS);
     const int r = lane & 15, q = lane >> 4;
     const TSrc ts = {resource(a.x, (int64_t)T * d * es), resource(a.x, 0)};
     const int have = a.E - n0 < 16 ? a.E - n0 : 16;
@@ -436,27 +455,28 @@ __global__ __launch_bounds__(1024) void few_scores(const FewArgs a) {
     Tokens<F, false> tk[DEPTH];
     u32x4 wv[DEPTH][2];
     auto load = [&](int p, int st) {
-      load_tokens<F, false>(tk[p], ts, d, lane, r, st, st < nst && r < T ? 0u : kOut);
+      load_tokens<F, false>(tk[p], ts, d, lane, r, st, st < end && r < T ? 0u : kOut);
       if constexpr (F == F_F32) {
         wv[p][0] = w_direct(w, d, lane, 0, st);
       } else {
         const uint32_t off = ((uint32_t)r * d + st * 64 + q * 8) * 2;
-        wv[p][0] = load16(w.r, st < nst ? off : kOut);
-        wv[p][1] = load16(w.r, st < nst ? off + 64 : kOut);
+        wv[p][0] = load16(w.r, st < end ? off : kOut);
+        wv[p][1] = load16(w.r, st < end ? off + 64 : kOut);
       }
       __builtin_amdgcn_sched_barrier(0);
     };
-    // whole bursts of DEPTH stages a wave; what is past the end reads zeros
-    for (int st = wave; st < nst; st += 16 * DEPTH) {
+    // whole bursts of DEPTH stages a wave; tokens past the end read as zeros
+    for (int st = (int)((int64_t)nst * part / a.KS) + wave; st < end; st += 4 * DEPTH) {
 #pragma unroll
-      for (int p = 0; p < DEPTH; ++p) load(p, st + 16 * p);
+      for (int p = 0; p < DEPTH; ++p) load(p, st + 4 * p);
 #pragma unroll
       for (int p = 0; p < DEPTH; ++p) {
         if constexpr (F == F_F32) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(tk[p].v[0][i]),
-                                                       __uint_as_float(wv[p][0][i]), acc, 0, 0, 0);
+            acc = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                __uint_as_float(tk[p].v[0][i]),
+                st + 4 * p < end ? __uint_as_float(wv[p][0][i]) : 0.f, acc, 0, 0, 0);
         } else {
           acc = mma16(tk[p].v[0], wv[p][0], acc);
           acc = mma16(tk[p].v[1], wv[p][1], acc);
@@ -466,19 +486,11 @@ __global__ __launch_bounds__(1024) void few_scores(const FewArgs a) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) red[wave * 256 + (q * 4 + i) * 16 + r] = acc[i];
     __syncthreads();
-    if (threadIdx.x < 256) {
-      const int t = threadIdx.x >> 4, e = n0 + (threadIdx.x & 15);
-      if (t < T && e < a.E) {
-        float z = 0.f;
-#pragma unroll
-        for (int wv2 = 0; wv2 < 16; ++wv2) z += red[wv2 * 256 + threadIdx.x];
-        float s = z;
-        if (a.score == MOE_SCORE_SIGMOID) s = 1.f / (1.f + expf(-z));
-        else if (a.score == MOE_SCORE_SQRTSOFTPLUS)
-          s = sqrtf(fmaxf(z, 0.f) + log1pf(expf(-fabsf(z))));
-        a.scores[(int64_t)t * a.E + e] = s;
-      }
-    }
+    const int t = threadIdx.x >> 4, e = n0 + (threadIdx.x & 15);
+    if (t < T && e < a.E)
+      a.scores[((int64_t)part * T + t) * a.E + e] =
+          ((red[threadIdx.x] + red[256 + threadIdx.x]) + red[512 + threadIdx.x]) +
+          red[768 + threadIdx.x];
     return;
   }
   item -= a.score_items;
@@ -536,17 +548,15 @@ __device__ __forceinline__ float wave_max_dpp(float v) {
 
 template <int EPL>
 __device__ __forceinline__ void select_few(const FewArgs &a, int t, int lane, float *out_w,
-                                           int32_t *out_e) {
+                                           int32_t *out_e, const float *scores) {
   const int E = a.E;
   float s[EPL], key[EPL], bias[EPL];
-  const rsrc_t sr = resource(a.scores, (int64_t)a.T * E * 4);
   const rsrc_t br = resource(a.bias, a.bias ? (int64_t)E * 4 : 0);
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
     const int e = lane * EPL + j;
-    const uint32_t out = e < E ? 0u : kOut;
-    s[j] = __uint_as_float(load4(sr, (((uint32_t)t * E + e) * 4) | out));
-    bias[j] = __uint_as_float(load4(br, ((uint32_t)e * 4) | out));
+    s[j] = e < E ? scores[t * E + e] : 0.f;
+    bias[j] = __uint_as_float(load4(br, e < E ? (uint32_t)e * 4 : kOut));
   }
   if (a.score == MOE_SCORE_SOFTMAX) {
     float m = -INFINITY;
@@ -629,17 +639,17 @@ __device__ __forceinline__ void select_few(const FewArgs &a, int t, int lane, fl
   }
 }
 
-__device__ __forceinline__ void select_any(const FewArgs &a, int t, int lane, float *w,
-                                           int32_t *e) {
+__device__ __forceinline__ void select_any(const FewArgs &a, int t, int lane, float *w, int32_t *e,
+                                           const float *scores) {
   switch ((a.E + 63) / 64) {
-    case 1: return select_few<1>(a, t, lane, w, e);
-    case 2: return select_few<2>(a, t, lane, w, e);
-    case 3: return select_few<3>(a, t, lane, w, e);
-    case 4: return select_few<4>(a, t, lane, w, e);
-    case 5: return select_few<5>(a, t, lane, w, e);
-    case 6: return select_few<6>(a, t, lane, w, e);
-    case 7: return select_few<7>(a, t, lane, w, e);
-    default: return select_few<8>(a, t, lane, w, e);
+    case 1: return select_few<1>(a, t, lane, w, e, scores);
+    case 2: return select_few<2>(a, t, lane, w, e, scores);
+    case 3: return select_few<3>(a, t, lane, w, e, scores);
+    case 4: return select_few<4>(a, t, lane, w, e, scores);
+    case 5: return select_few<5>(a, t, lane, w, e, scores);
+    case 6: return select_few<6>(a, t, lane, w, e, scores);
+    case 7: return select_few<7>(a, t, lane, w, e, scores);
+    default: return select_few<8>(a, t, lane, w, e, scores);
   }
 }
 
@@ -647,19 +657,43 @@ __device__ __forceinline__ void select_any(const FewArgs &a, int t, int lane, fl
 // by first appearance in (token, choice) order), for each slot and token the H
 // row (the pair's number t*k + j; -1: not chosen) and the gate value (summed
 // where a token has the expert twice), and for each token the choices that
-// hold a row.  One workgroup of 8 waves; lead: [E] scratch.
+// hold a row.  One workgroup of 8 waves; a thread per pair.
 struct PlanScratch {
   float w[256];
   int32_t e[256];
-  int32_t lead[1024];
+  int32_t lead[1024];                          // per expert: its first pair, then its slot
   int32_t misc[8];
+  uint32_t mask[kRows];
+  float cell_w[256 * kRows];
+  int16_t cell_row[256 * kRows];
 };
-__device__ __forceinline__ void make_plan(const FewArgs &a, PlanScratch &p) {
+__device__ __forceinline__ void make_plan(const FewArgs &a, PlanScratch &p, float *scores) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int T = a.T, k = a.k, E = a.E, pairs = T * k;
   if (tid == 0) p.misc[0] = 0;
+  if (tid < kRows) p.mask[tid] = 0;
+  for (int i = tid; i < pairs * kRows; i += 512) {
+    p.cell_w[i] = 0.f;
+    p.cell_row[i] = -1;
+  }
   if (a.route_mode == MOE_ROUTE_LEARNED) {
-    for (int t = wave; t < T; t += 8) select_any(a, t, lane, p.w, p.e);
+    // affinities of all tokens by all threads (softmax: the logits), the parts
+    // of a logit added in order; then a wave per token
+    const int n = T * E;
+    for (int i = tid; i < n; i += 512) {
+      float part[kLogitParts];
+#pragma unroll
+      for (int q = 0; q < kLogitParts; ++q) part[q] = q < a.KS ? a.scores[(int64_t)q * n + i] : 0.f;
+      float z = part[0];
+#pragma unroll
+      for (int q = 1; q < kLogitParts; ++q) z += part[q];
+      if (a.score == MOE_SCORE_SIGMOID) z = 1.f / (1.f + expf(-z));
+      else if (a.score == MOE_SCORE_SQRTSOFTPLUS)
+        z = sqrtf(fmaxf(z, 0.f) + log1pf(expf(-fabsf(z))));
+      scores[i] = z;
+    }
+    __syncthreads();
+    for (int t = wave; t < T; t += 8) select_any(a, t, lane, p.w, p.e, scores);
     __syncthreads();
   } else {
     __syncthreads();
@@ -707,46 +741,41 @@ __device__ __forceinline__ void make_plan(const FewArgs &a, PlanScratch &p) {
   }
   if (tid < pairs) {
     a.out_w[tid] = p.w[tid];
-    a.out_e[tid] = p.e[tid];
+    a.out_e[tid] = e;
   }
-  if (tid < T) a.plan_mask[tid] = 0;
   if (tid == 0) {
     a.plan_slots[0] = slots;
     a.flags[0] = (uint32_t)p.misc[0];
   }
   __syncthreads();
-  // every (slot, token) cell by one thread: its row, or -1
-  for (int i = tid; i < slots * kRows; i += 512) {
-    const int s = i >> 4, t = i & 15;
+  if (in) {
+    const int t = tid / k, j = tid - t * k;
     float w = 0.f;
-    int row = -1;
-    if (t < T)
-      for (int j = k - 1; j >= 0; --j) {
-        const int ej = p.e[t * k + j];
-        if (ej >= 0 && ej < E && p.lead[ej] == s) {
-          w += p.w[t * k + j];
-          row = t * k + j;                     // the first choice of it
-        }
+    bool mine = true;                          // the token's first choice of this expert
+    for (int i = 0; i < k; ++i)
+      if (p.e[t * k + i] == e) {
+        mine = mine && i >= j;
+        w += p.w[t * k + i];
       }
-    a.plan_w[i] = w;
-    a.plan_row[i] = (int16_t)row;
-  }
-  if (tid < T) {
-    uint32_t mask = 0;
-    for (int j = 0; j < k; ++j) {
-      const int ej = p.e[tid * k + j];
-      bool keep = ej >= 0 && ej < E;
-      for (int i = 0; i < j && keep; ++i) keep = p.e[tid * k + i] != ej;
-      mask |= keep ? 1u << j : 0u;
+    if (mine) {
+      const int cell = p.lead[e] * kRows + t;
+      p.cell_w[cell] = w;
+      p.cell_row[cell] = (int16_t)tid;
+      atomicOr(&p.mask[t], 1u << j);
     }
-    a.plan_mask[tid] = (int32_t)mask;
   }
+  __syncthreads();
+  for (int i = tid; i < slots * kRows; i += 512) {
+    a.plan_w[i] = p.cell_w[i];
+    a.plan_row[i] = p.cell_row[i];
+  }
+  if (tid < T) a.plan_mask[tid] = (int32_t)p.mask[tid];
 }
 
 // ---------------------------------------------------------------------------
 // Tile of gate|up: 16 NB columns of H.  `waves` of the workgroup split the
 // inputs, this one taking stages gw, gw + waves, ...
-template <int F, bool TILED, int NB>
+template <int F, int L, int NB>
 __device__ __forceinline__ void up_tile(const FewArgs &a, const TSrc &xs, const void *wg,
                                         const void *wu, const uint8_t *sg, const uint8_t *su,
                                         int n0, uint32_t row, bool there, int gw, int waves,
@@ -760,20 +789,21 @@ __device__ __forceinline__ void up_tile(const FewArgs &a, const TSrc &xs, const 
   for (int s = 0; s < 2; ++s)
 #pragma unroll
     for (int b = 0; b < NB; ++b) acc[s][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-  tile_dot<F, TILED, false, NB>(acc, xs, ws, a.d, lane, row, there, gw, waves, nst, ring0, ring1);
+  tile_dot<F, L, false, NB>(acc, xs, ws, a.d, lane, row, there, gw, waves, nst, ring0, ring1);
   put_partial<NB>(mine, acc, lane);
 }
 
 // few_plan: workgroup 0 routes; the others stream the shared expert's gate|up,
 // 16 columns each, 8 waves splitting the inputs.
-template <int F, bool TILED>
+template <int F, int L>
 __global__ __launch_bounds__(512, 2) void few_plan(const FewArgs a) {
   constexpr int SLOT = F == F_F32 ? 2048 : 4096;
-  __shared__ __attribute__((aligned(1024))) uint8_t R0[8 * SLOT];
-  __shared__ __attribute__((aligned(1024))) uint8_t R1[F == F_F32 ? 16 : 8 * SLOT];
+  constexpr int PLAN = (int)sizeof(PlanScratch);
+  __shared__ __attribute__((aligned(1024))) uint8_t R0[8 * SLOT > PLAN ? 8 * SLOT : PLAN];
+  __shared__ __attribute__((aligned(1024))) uint8_t R1[kRows * 512 * 4];
+  static_assert(sizeof(R1) >= 8 * SLOT, "ring slots");
   if (blockIdx.x == 0) {
-    static_assert(sizeof(PlanScratch) <= sizeof(R0), "routing scratch");
-    make_plan(a, *(PlanScratch *)R0);
+    make_plan(a, *(PlanScratch *)R0, (float *)R1);
     return;
   }
   const int lane = threadIdx.x & 63;
@@ -782,7 +812,7 @@ __global__ __launch_bounds__(512, 2) void few_plan(const FewArgs a) {
   const int n0 = (blockIdx.x - 1) * 16, t0 = lane & 15;
   const TSrc xs = {resource(a.x, (int64_t)a.T * a.d * es), resource(a.x, 0)};
   float *red = (float *)R0;
-  up_tile<F, TILED, 1>(a, xs, a.sh_gate, a.sh_up, nullptr, nullptr, n0, t0, t0 < a.T, wave, 8, lane,
+  up_tile<F, L, 1>(a, xs, a.sh_gate, a.sh_up, nullptr, nullptr, n0, t0, t0 < a.T, wave, 8, lane,
                        R0 + wave * SLOT, F == F_F32 ? R0 : R1 + wave * SLOT,
                        red + wave * (SLOT / 4));
   __syncthreads();
@@ -812,7 +842,7 @@ __device__ __forceinline__ int waves_per_tile(int tiles, int resident) {
 }
 
 // few_up: 32 columns of H of one slot per tile (an MXFP8 scale block).
-template <int F, bool TILED>
+template <int F, int L>
 __global__ __launch_bounds__(256, 2) void few_up(const FewArgs a) {
   constexpr bool MX = F == F_MX4 || F == F_MX8;
   constexpr int NB = 2, SLOT = F == F_F32 ? 4096 : 8192;
@@ -844,7 +874,7 @@ __global__ __launch_bounds__(256, 2) void few_up(const FewArgs a) {
       const int e = __builtin_amdgcn_readfirstlane(a.plan_expert[slot]);
       const int64_t at = e * ((int64_t)I * row_bytes<F>(d));
       const int64_t sat = e * ((int64_t)I * d / (F == F_MX8 ? 16384 : 32));
-      up_tile<F, TILED, NB>(a, xs, (const uint8_t *)a.w_gate + at, (const uint8_t *)a.w_up + at,
+      up_tile<F, L, NB>(a, xs, (const uint8_t *)a.w_gate + at, (const uint8_t *)a.w_up + at,
                             a.s_gate + sat, a.s_up + sat, n0, lane & 15, rows[lane & 15] >= 0, gw, G,
                             lane, R0 + wave * SLOT, F == F_F32 ? R0 : R1 + wave * SLOT,
                             red + wave * (SLOT / 4));
@@ -887,7 +917,7 @@ __global__ __launch_bounds__(256, 2) void few_up(const FewArgs a) {
 }
 
 // Tile of W_down: 64 output columns of one slot; the wave's partial to `mine`.
-template <int F, bool TILED, bool HILO>
+template <int F, int L, bool HILO>
 __device__ __forceinline__ void down_tile(const FewArgs &a, const TSrc &hs, const void *w,
                                           const uint8_t *sc, int n0, int row, int gw, int waves,
                                           int lane, uint8_t *ring0, uint8_t *ring1, float *mine) {
@@ -899,18 +929,22 @@ __device__ __forceinline__ void down_tile(const FewArgs &a, const TSrc &hs, cons
   for (int s = 0; s < 2; ++s)
 #pragma unroll
     for (int b = 0; b < NB; ++b) acc[s][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-  tile_dot<F, TILED, HILO, NB>(acc, hs, ws, a.I, lane, row < 0 ? 0 : row, row >= 0, gw, waves, nst,
+  tile_dot<F, L, HILO, NB>(acc, hs, ws, a.I, lane, row < 0 ? 0 : row, row >= 0, gw, waves, nst,
                                ring0, ring1);
   put_partial<NB>(mine, acc, lane);
 }
 
 // few_down: yrows[pair] = w (H[pair] W_down^T) in fp32, rows T*k .. the shared
 // expert's.  The shared tiles (longer, in bf16) come first, four waves each.
-template <int F, bool TILED>
+// PACK (T <= 8): the two halves of H ride in one operand, MFMA row t the high
+// half of token t and row 8 + t the low one, whose products are added at the
+// end; more tokens take a second operand.
+template <int F, int L, bool PACK>
 __global__ __launch_bounds__(256, 2) void few_down(const FewArgs a) {
   constexpr bool MX = F == F_MX4 || F == F_MX8;
   constexpr bool F32 = F == F_F32;
   constexpr int SLOT = F32 ? 4096 : 8192;
+  constexpr int kLow = 8 * 16;                 // the low half's products in a 16 x 16 block
   __shared__ __attribute__((aligned(1024))) uint8_t R0[4 * SLOT];
   __shared__ __attribute__((aligned(1024))) uint8_t R1[F32 ? 16 : 4 * SLOT];
   const int lane = threadIdx.x & 63;
@@ -919,8 +953,10 @@ __global__ __launch_bounds__(256, 2) void few_down(const FewArgs a) {
   const int blocks = (d + 63) / 64;
   const int shared = a.has_shared ? blocks : 0;
   const int tiles = a.plan_slots[0] * blocks;
-  const int64_t hbytes = (int64_t)(pairs + (a.has_shared ? T : 0)) * I * (F32 ? 4 : 2);
-  const TSrc hs = {resource(a.h, hbytes), resource(F32 ? a.h : a.h_lo, hbytes)};
+  const int hrows = pairs + (a.has_shared ? T : 0);
+  const int64_t hbytes = (int64_t)hrows * I * (F32 ? 4 : 2);
+  // the low halves follow the high ones
+  const TSrc hs = {resource(a.h, F32 ? hbytes : 2 * hbytes), resource(F32 ? a.h : a.h_lo, hbytes)};
   const TSrc qs = {resource(a.hq, MX ? (int64_t)pairs * I : 0),
                    resource(a.hq_scales, MX ? (int64_t)pairs * (I / 32) : 0)};
   float *red = (float *)R0;
@@ -938,29 +974,35 @@ __global__ __launch_bounds__(256, 2) void few_down(const FewArgs a) {
     const int slot = sh || !live ? 0 : tile / blocks;
     const int n0 = (live ? tile - slot * blocks : 0) * 64;
     const int16_t *rows = a.plan_row + slot * kRows;
+    const bool packed = PACK && (sh || !MX);
+    const int t = packed ? lane & 7 : lane & 15;
+    const int low = packed && (lane & 8) ? hrows : 0;
     if (sh) {
-      const int t = lane & 15;
-      down_tile<F32 ? F_F32 : F_BF16, TILED && !F32, !F32>(
-          a, hs, a.sh_down, nullptr, n0, t < T ? pairs + t : -1, gw, 4, lane, ring0, ring1,
+      down_tile<F32 ? F_F32 : F_BF16, L, !F32 && !PACK>(
+          a, hs, a.sh_down, nullptr, n0, t < T ? pairs + t + low : -1, gw, 4, lane, ring0, ring1,
           red + wave * (SLOT / 4));
     } else if (live) {
       const int e = __builtin_amdgcn_readfirstlane(a.plan_expert[slot]);
       const int64_t at = e * ((int64_t)d * row_bytes<F>(I));
       const int64_t sat = e * ((int64_t)d * I / (F == F_MX8 ? 16384 : 32));
-      down_tile<F, TILED, !F32 && !MX>(a, MX ? qs : hs, (const uint8_t *)a.w_down + at,
-                                       a.s_down + sat, n0, rows[lane & 15], gw, g, lane, ring0,
-                                       ring1, red + wave * (SLOT / 4));
+      const int row = rows[t];
+      down_tile<F, L, !F32 && !MX && !PACK>(a, MX ? qs : hs, (const uint8_t *)a.w_down + at,
+                                            a.s_down + sat, n0, row < 0 ? row : row + low, gw, g,
+                                            lane, ring0, ring1, red + wave * (SLOT / 4));
     }
     __syncthreads();
     if (live) {
       const float *part = red + (wave - gw) * (SLOT / 4);
-      for (int t = gw; t < T; t += g) {
-        const int pair = sh ? pairs + t : rows[t], n = n0 + lane;
+      for (int tt = gw; tt < T; tt += g) {
+        const int pair = sh ? pairs + tt : rows[tt], n = n0 + lane;
         if (pair < 0 || n >= d) continue;
-        const int el = (lane >> 4) * 256 + t * 16 + (lane & 15);
+        const int el = (lane >> 4) * 256 + tt * 16 + (lane & 15);
         float v = 0.f;
-        for (int w = 0; w < g; ++w) v += part[w * (SLOT / 4) + el];
-        a.yrows[(int64_t)pair * d + n] = sh ? v : a.plan_w[slot * kRows + t] * v;
+        for (int w = 0; w < g; ++w) {
+          v += part[w * (SLOT / 4) + el];
+          if (packed) v += part[w * (SLOT / 4) + el + kLow];
+        }
+        a.yrows[(int64_t)pair * d + n] = sh ? v : a.plan_w[slot * kRows + tt] * v;
       }
     }
     __syncthreads();
@@ -1000,23 +1042,36 @@ template <int F, bool TILED>
 hipError_t run_few(FewArgs a, hipStream_t s) {
   constexpr bool MX = F == F_MX4 || F == F_MX8;
   constexpr int FS = F == F_F32 ? F_F32 : F_BF16;
+  constexpr bool FP4 = F == F_FP4;             // MXFP8 layers have K % 128 == 0
+  constexpr int L = TILED ? TILES : ROWS, L_ODD = FP4 && !TILED ? ROWS_ODD : L;
   hipError_t err;
   const int pairs = a.T * a.k;
-  const int quant = MX ? (a.T * a.d / 32 + 1023) / 1024 : 0;
+  const int quant = MX ? (a.T * a.d / 32 + 255) / 256 : 0;
   if (a.score_items + quant > 0) {
-    hipLaunchKernelGGL((few_scores<FS>), dim3(a.score_items + quant), dim3(1024), 0, s, a);
+    hipLaunchKernelGGL((few_scores<FS>), dim3(a.score_items + quant), dim3(256), 0, s, a);
     if ((err = hipGetLastError()) != hipSuccess) return err;
   }
   const int shared = a.has_shared ? (a.I + 15) / 16 : 0;
-  hipLaunchKernelGGL((few_plan<FS, TILED && F != F_F32>), dim3(1 + shared), dim3(512), 0, s, a);
+  hipLaunchKernelGGL((few_plan<FS, TILED ? TILES : ROWS>), dim3(1 + shared), dim3(512), 0, s, a);
   if ((err = hipGetLastError()) != hipSuccess) return err;
   const int64_t up = (int64_t)pairs * ((a.I + 31) / 32);
-  hipLaunchKernelGGL((few_up<F, TILED>), dim3(up < kGroups ? (unsigned)up : kGroups), dim3(256), 0,
-                     s, a);
+  const dim3 up_grid(up < kGroups ? (unsigned)up : kGroups);
+  if (TILED || !FP4 || a.d % 128 == 0)
+    hipLaunchKernelGGL((few_up<F, L>), up_grid, dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((few_up<F, L_ODD>), up_grid, dim3(256), 0, s, a);
   if ((err = hipGetLastError()) != hipSuccess) return err;
   const int64_t down = (int64_t)(pairs + (a.has_shared ? 1 : 0)) * ((a.d + 63) / 64);
-  hipLaunchKernelGGL((few_down<F, TILED>), dim3(down < kGroups ? (unsigned)down : kGroups),
-                     dim3(256), 0, s, a);
+  const dim3 down_grid(down < kGroups ? (unsigned)down : kGroups);
+  const bool odd = !TILED && FP4 && a.I % 128 != 0;
+  if (F == F_F32 || a.T > 8) {
+    if (odd) hipLaunchKernelGGL((few_down<F, L_ODD, false>), down_grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((few_down<F, L, false>), down_grid, dim3(256), 0, s, a);
+  } else {
+    constexpr bool P = F != F_F32;
+    if (odd) hipLaunchKernelGGL((few_down<F, L_ODD, P>), down_grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((few_down<F, L, P>), down_grid, dim3(256), 0, s, a);
+  }
   if ((err = hipGetLastError()) != hipSuccess) return err;
   const dim3 grid((unsigned)((a.d + 1023) / 1024), (unsigned)a.T);
   if (F == F_F32) hipLaunchKernelGGL((few_combine<float>), grid, dim3(256), 0, s, a);
@@ -1026,9 +1081,16 @@ hipError_t run_few(FewArgs a, hipStream_t s) {
 
 }  // namespace
 
+// Parts of the inputs of the gate logits: workgroups for half the GPU, each
+// wave still with stages to load.
+int few_logit_parts(int d, bool f32) {
+  const int nst = (d + (f32 ? 15 : 63)) / (f32 ? 16 : 64), parts = nst / 8;
+  return parts < 1 ? 1 : parts > kLogitParts ? kLogitParts : parts;
+}
+
 hipError_t launch_few(FewArgs a, const moe_config &cfg, hipStream_t s) {
   const bool tiled = cfg.weight_layout == MOE_LAYOUT_TILED;
-  a.score_items = cfg.route_mode == MOE_ROUTE_LEARNED ? (a.E + 15) / 16 : 0;
+  a.score_items = cfg.route_mode == MOE_ROUTE_LEARNED ? (a.E + 15) / 16 * a.KS : 0;
   if (cfg.act_dtype == MOE_DTYPE_F32) return run_few<F_F32, false>(a, s);
   if (cfg.expert_dtype == MOE_DTYPE_FP8_E4M3_B128) return run_few<F_MX8, true>(a, s);
   if (cfg.expert_dtype == MOE_DTYPE_BF16)

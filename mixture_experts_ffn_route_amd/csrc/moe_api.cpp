@@ -156,7 +156,7 @@ int make_few_layout(const moe_config *c, int64_t T, moe_few_layout *out) {
   l.route_weights = take(sizeof(float) * pairs);
   l.route_indices = take(sizeof(int32_t) * pairs);
   l.flags = take(sizeof(uint32_t) * 4);
-  l.scores = take(learned ? sizeof(float) * T * E : 0);
+  l.scores = take(learned ? sizeof(float) * moe::few_logit_parts((int)d, f32) * T * E : 0);
   l.plan_slots = take(sizeof(int32_t));
   l.plan_experts = take(sizeof(int32_t) * pairs);
   l.plan_weights = take(sizeof(float) * 16 * pairs);
@@ -167,8 +167,8 @@ int make_few_layout(const moe_config *c, int64_t T, moe_few_layout *out) {
   l.hq = take(mx ? pairs * I : 0);
   l.hq_scales = take(mx ? pairs * I / 32 : 0);
   const size_t rows = pairs + (c->n_shared_experts ? T : 0);
-  l.h = take((f32 ? 4 : 2) * rows * I);
-  l.h_lo = take(f32 ? 0 : 2 * rows * I);
+  l.h = take(4 * rows * I);
+  l.h_lo = f32 ? l.h : l.h + 2 * rows * I;
   l.yrows = take(sizeof(float) * rows * d);
   l.total_bytes = off;
   if (out) *out = l;
@@ -693,6 +693,7 @@ int moe_forward_few(const moe_config *cfg, const moe_weights *w, const void *x,
   a.out_e = (int32_t *)(base + L.route_indices);
   a.flags = (uint32_t *)(base + L.flags);
   a.scores = (float *)(base + L.scores);
+  a.KS = moe::few_logit_parts(a.d, cfg->act_dtype == MOE_DTYPE_F32);
   a.plan_slots = (int32_t *)(base + L.plan_slots);
   a.plan_expert = (int32_t *)(base + L.plan_experts);
   a.plan_w = (float *)(base + L.plan_weights);
