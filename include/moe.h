@@ -399,8 +399,8 @@ int moe_forward_noalloc(const moe_config *cfg, const moe_weights *w, const void 
  * permutation and with the inputs of a weight stream in mind.  Results agree with moe_forward's to rounding (H keeps 16
  * bits and the weighted expert outputs are summed in fp32, so this form rounds
  * less); the routing follows the same rules.
- *   x, token_ids, y, w, stream  as moe_forward; x, y and the matrices (not the
- *       scales) 16-byte aligned
+ *   x, token_ids, y, w, stream  as moe_forward; x, y, the matrices and the FP4
+ *       scales 16-byte aligned
  *   ws  device workspace of at least moe_few_workspace_size(cfg, T) bytes,
  *       256-byte aligned.  Nothing in it needs to start at any value; after the
  *       call it holds the routing and the device error flags at the offsets of

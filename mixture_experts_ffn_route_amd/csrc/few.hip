@@ -66,9 +66,6 @@ __device__ __forceinline__ rsrc_t resource(const void *p, int64_t bytes) {
 __device__ __forceinline__ u32x4 load16(rsrc_t r, uint32_t off) {
   return __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
 }
-__device__ __forceinline__ u32x2 load8(rsrc_t r, uint32_t off) {
-  return __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0);
-}
 __device__ __forceinline__ uint32_t load4(rsrc_t r, uint32_t off) {
   return __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
 }
@@ -145,45 +142,43 @@ __device__ __forceinline__ u32x4 w_operand(const uint8_t *lds, int b, int f, int
   }
 }
 
-// Scale bytes of a stage: per row block and half (FP4), one (MX8: the block's).
-// Row layout: the row's eight bytes of the stage in one load where rows of
-// scales start at multiples of four (K % 128 == 0; ROWS), a quarter of the
-// loads that single bytes take (ROWS_ODD).
-enum { ROWS, ROWS_ODD, TILES };
-template <int F, int L, int NB> struct Scales {
-  static constexpr bool kFp4 = F == F_FP4 || F == F_MX4;
-  uint32_t s[kFp4 ? 2 * NB : 1];
-  static constexpr int kLoads = kFp4 ? (L == ROWS ? NB : 2 * NB) : F == F_MX8 ? 1 : 0;
-  // the scale byte of row block b, half h
-  __device__ __forceinline__ uint32_t get(int b, int h, int lane) const {
-    return L == ROWS ? (s[2 * b + h] >> (8 * (lane >> 4))) & 0xFFu : s[2 * b + h];
-  }
-};
-template <int F, int L, int NB>
-__device__ __forceinline__ void load_scales(Scales<F, L, NB> &x, const WSrc &w, int K, int lane,
-                                            int st) {
-  const uint32_t r = lane & 15, q = lane >> 4;
-  if constexpr (F == F_MX8) {
-    x.s[0] = load1(w.rs, st);
-  } else if constexpr (F == F_FP4 || F == F_MX4) {
+// FP4 scales.  Eight scale bytes of a row go with a stage of it; loaded stage
+// by stage they touch as many cache lines as the weights and cost 20 % of the
+// stream, so the workgroup, which works on one tile, first copies the scales of
+// the tile's rows for up to kScaleSpan inputs (31 stages, 248 bytes a row): per
+// source 8 KB of LDS, row layout 256 bytes a row, from the row's first byte
+// rounded down to four; tiled layout as the row blocks lie, 4 KB each.
+constexpr int kScaleSpan = 31 * 256;           // inputs
+template <int F> constexpr bool is_fp4() { return F == F_FP4 || F == F_MX4; }
+
+// This wave's (of four) share of the 32 rows' scales for inputs k0 ...
+template <bool TILED>
+__device__ __forceinline__ void copy_scales(const WSrc &w, int K, int k0, int wave, int lane,
+                                            uint8_t *lds) {
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      if constexpr (L == ROWS) {
-        // what follows a row's last scale goes with weights that read as zeros
-        const u32x2 v = load8(w.rs, (b * 16 + r) * (K / 32) + st * 8);
-        x.s[2 * b] = v[0];
-        x.s[2 * b + 1] = v[1];
-      } else {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int half = 2 * st + h;
-          const uint32_t off = L == TILES ? b * 16 * (K / 32) + (2 * half + (q >> 1)) * 32 + r * 2 + (q & 1)
-                                          : (b * 16 + r) * (K / 32) + half * 4 + q;
-          x.s[2 * b + h] = load1(w.rs, half * 128 + (int)q * 32 < K ? off : kOut);
-        }
-      }
+  for (int i = 0; i < 2; ++i) {
+    const int u = wave + 4 * i;                // 1 KB unit
+    uint32_t off;
+    if constexpr (TILED) {
+      const uint32_t in = (uint32_t)k0 / 2 + (u & 3) * 1024 + lane * 16;
+      off = in < (uint32_t)K / 2 ? (u >> 2) * (K / 2) + in : kOut;
+    } else {
+      const uint32_t row = (4 * u + (lane >> 4)) * (K / 32);
+      const uint32_t at = ((row + k0 / 32) & ~3u) + (lane & 15) * 16;
+      off = at < row + K / 32 ? at : kOut;
     }
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(w.rs, (MOE_LDS void *)(lds + u * 1024), 16, off, 0, 0,
+                                             0);
   }
+}
+// The scale byte of row block b's row l % 16 for its 32 inputs of half `half`
+// (of 128 inputs, from the span's start k0).
+template <bool TILED>
+__device__ __forceinline__ uint32_t scale_byte(const uint8_t *lds, int K, int k0, int b, int half,
+                                               int lane) {
+  const int r = 16 * b + (lane & 15), q = lane >> 4;
+  return TILED ? lds[b * 4096 + (2 * half + (q >> 1)) * 32 + (lane & 15) * 2 + (q & 1)]
+               : lds[r * 256 + ((r * (K / 32) + k0 / 32) & 3) + half * 4 + q];
 }
 
 // ---------------------------------------------------------------------------
@@ -255,23 +250,24 @@ __device__ __forceinline__ i32x8 wide(const u32x4 &a, const u32x4 &b) {
                (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
 }
 
-// acc += tokens x the 16 rows of row block b over one stage.
-template <int F, int L, bool HILO, int NB>
-__device__ __forceinline__ void stage_mma(f32x4 &acc, const Tokens<F, HILO> &a,
-                                          const Scales<F, L, NB> &sc, const uint8_t *lds, int b,
-                                          int lane) {
+// acc += tokens x the 16 rows of row block b over one stage; scl: the source's
+// FP4 scales in LDS, `half` the stage's first half in them; s8: the FP8 scale.
+template <int F, bool TILED, bool HILO>
+__device__ __forceinline__ void stage_mma(f32x4 &acc, const Tokens<F, HILO> &a, uint32_t s8,
+                                          const uint8_t *scl, int K, int k0, int half,
+                                          const uint8_t *lds, int b, int lane) {
   if constexpr (F == F_BF16) {
 #pragma unroll
     for (int f = 0; f < 2; ++f) {
-      const u32x4 w = w_operand<F, L == TILES>(lds, b, f, lane);
+      const u32x4 w = w_operand<F, TILED>(lds, b, f, lane);
       acc = mma16(a.v[f], w, acc);
       if constexpr (HILO) acc = mma16(a.v[2 + f], w, acc);
     }
   } else if constexpr (F == F_FP4) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const u32x4 codes = w_operand<F, L == TILES>(lds, b, h, lane);
-      const float scale = __uint_as_float(sc.get(b, h, lane) << 23);
+      const u32x4 codes = w_operand<F, TILED>(lds, b, h, lane);
+      const float scale = __uint_as_float(scale_byte<TILED>(scl, K, k0, b, half + h, lane) << 23);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const bf16x2 v0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[i], scale, 0);
@@ -288,13 +284,13 @@ __device__ __forceinline__ void stage_mma(f32x4 &acc, const Tokens<F, HILO> &a,
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-          wide(a.v[2 * h], a.v[2 * h + 1]), wide(w_operand<F, L == TILES>(lds, b, h, lane), u32x4{}),
-          acc, 0, 4, 0, (int)a.s[h], 0, (int)sc.get(b, h, lane));
+          wide(a.v[2 * h], a.v[2 * h + 1]), wide(w_operand<F, TILED>(lds, b, h, lane), u32x4{}),
+          acc, 0, 4, 0, (int)a.s[h], 0, (int)scale_byte<TILED>(scl, K, k0, b, half + h, lane));
   } else {
     acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
         wide(a.v[0], a.v[1]),
-        wide(w_operand<F, L == TILES>(lds, b, 0, lane), w_operand<F, L == TILES>(lds, b, 1, lane)), acc, 0, 0,
-        0, (int)a.s[0], 0, (int)sc.s[0]);
+        wide(w_operand<F, TILED>(lds, b, 0, lane), w_operand<F, TILED>(lds, b, 1, lane)), acc, 0, 0,
+        0, (int)a.s[0], 0, (int)s8);
   }
 }
 
@@ -309,16 +305,20 @@ __device__ __forceinline__ u32x4 w_direct(const WSrc &w, int K, int lane, int b,
 }
 
 // The wave's tile of products: acc[s][b] = tokens x row block b of source s,
-// over stages first, first + step, ... below end, two stages in flight.
-// ring0 / ring1: the wave's two slots of 4 NB KB.
-template <int F, int L, bool HILO, int NB>
+// over stages wave, wave + waves, ..., two stages in flight.  ring0 / ring1: the
+// wave's two slots of 4 NB KB; scales: the workgroup's 16 KB (FP4; four waves,
+// NB = 2, every wave calls).
+template <int F, bool TILED, bool HILO, int NB>
 __device__ __forceinline__ void tile_dot(f32x4 (&acc)[2][NB], const TSrc &ts, const WSrc (&ws)[2],
-                                         int K, int lane, uint32_t row, bool there, int first,
-                                         int step, int end, uint8_t *ring0, uint8_t *ring1) {
+                                         int K, int lane, uint32_t row, bool there, int wave,
+                                         int waves, uint8_t *ring0, uint8_t *ring1,
+                                         uint8_t *scales) {
   const uint32_t out = there ? 0u : kOut;
+  constexpr int KST = stage_inputs<F>();
+  const int nst = (K + KST - 1) / KST;
   if constexpr (F == F_F32) {
-    (void)ring0; (void)ring1;
-    for (int st = first; st < end; st += step) {
+    (void)ring0; (void)ring1; (void)scales;
+    for (int st = wave; st < nst; st += waves) {
       Tokens<F, HILO> a;
       load_tokens<F, HILO>(a, ts, K, lane, row, st, out);
 #pragma unroll
@@ -333,64 +333,83 @@ __device__ __forceinline__ void tile_dot(f32x4 (&acc)[2][NB], const TSrc &ts, co
         }
     }
   } else {
-    constexpr int VM = 4 * NB + Tokens<F, HILO>::kLoads + 2 * Scales<F, L, NB>::kLoads;
-    static_assert(VM <= 63, "vmcnt holds 6 bits");
+    constexpr int VM = 4 * NB + Tokens<F, HILO>::kLoads + (F == F_MX8 ? 2 : 0);
+    static_assert(2 * VM <= 63, "vmcnt holds 6 bits");
+    static_assert(!is_fp4<F>() || NB == 2, "32 rows of scales a source");
+    constexpr int SPAN = is_fp4<F>() ? kScaleSpan / KST : 1 << 30;
     Tokens<F, HILO> a[2];
-    Scales<F, L, NB> sc[2][2];
-    auto issue = [&](int p, int st) {
-      uint8_t *lds = p ? ring1 : ring0;
-      load_tokens<F, HILO>(a[p], ts, K, lane, row, st, out);
+    uint32_t s8[2][2];
+    // stages lo .. hi - 1 (whose scales are in LDS)
+    for (int lo = 0; lo < nst; lo += SPAN) {
+      const int hi = nst - lo > SPAN ? lo + SPAN : nst;
+      if constexpr (is_fp4<F>()) {
+        if (lo > 0) __syncthreads();           // every wave is done with the last scales
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        load_scales<F, L, NB>(sc[p][s], ws[s], K, lane, st);
-        copy_stage<F, L == TILES, NB>(ws[s], K, lane, st, lds + s * NB * 2048);
+        for (int s = 0; s < 2; ++s)
+          copy_scales<TILED>(ws[s], K, lo * KST, wave, lane, scales + s * 8192);
       }
-      // keep the loads here: the scheduler otherwise moves them behind the
-      // next products
-      __builtin_amdgcn_sched_barrier(0);
-    };
-    auto compute = [&](int p) {
-      const uint8_t *lds = p ? ring1 : ring0;
+      auto issue = [&](int p, int st) {
+        uint8_t *lds = p ? ring1 : ring0;
+        load_tokens<F, HILO>(a[p], ts, K, lane, row, st, out);
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+        for (int s = 0; s < 2; ++s) {
+          if constexpr (F == F_MX8) s8[p][s] = load1(ws[s].rs, st);
+          copy_stage<F, TILED, NB>(ws[s], K, lane, st, lds + s * NB * 2048);
+        }
+        // keep the loads here: the scheduler otherwise moves them behind the
+        // next products
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      auto compute = [&](int p, int st) {
+        const uint8_t *lds = p ? ring1 : ring0;
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
-          stage_mma<F, L, HILO, NB>(acc[s][b], a[p], sc[p][s], lds + s * NB * 2048, b, lane);
-      // the slot's reads are done before a copy may land in it again
-      __builtin_amdgcn_s_waitcnt(0xC07F);      // lgkmcnt(0)
-      __builtin_amdgcn_sched_barrier(0);
-    };
-    // stage landed: at most n younger loads outstanding; no LDS read moves above
-#define MOE_LANDED(n)                                  \
-    __builtin_amdgcn_s_waitcnt(MOE_VMCNT(n));          \
-    asm volatile("" ::: "memory");                     \
-    __builtin_amdgcn_sched_barrier(0)
-    const int n = end > first ? (end - first + step - 1) / step : 0;
-    if (n > 0) {
-      int st = first, i = 0;
-      issue(0, st);
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+            stage_mma<F, TILED, HILO>(acc[s][b], a[p], F == F_MX8 ? s8[p][s] : 0,
+                                      scales + s * 8192, K, lo * KST, 2 * (st - lo),
+                                      lds + s * NB * 2048, b, lane);
+        // the slot's reads are done before a copy may land in it again
+        __builtin_amdgcn_s_waitcnt(0xC07F);    // lgkmcnt(0)
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      // at most n younger loads outstanding; no LDS read moves above
+#define MOE_LANDED(n)                                \
+      __builtin_amdgcn_s_waitcnt(MOE_VMCNT(n));      \
+      asm volatile("" ::: "memory");                 \
+      __builtin_amdgcn_sched_barrier(0)
+      int st = lo + wave;
+      const int n = hi > st ? (hi - st + waves - 1) / waves : 0;
+      if (n > 0) issue(0, st);
+      if (n > 1) issue(1, st + waves);
+      if constexpr (is_fp4<F>()) {
+        // the scales are older than the stages issued
+        if (n > 1) { MOE_LANDED(2 * VM); } else { MOE_LANDED(0); }
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+      }
       if (n > 1) {
-        issue(1, st + step);
-        for (; i + 3 < n; i += 2, st += 2 * step) {
+        int i = 0;
+        for (; i + 3 < n; i += 2, st += 2 * waves) {
           MOE_LANDED(VM);
-          compute(0);
-          issue(0, st + 2 * step);
+          compute(0, st);
+          issue(0, st + 2 * waves);
           MOE_LANDED(VM);
-          compute(1);
-          issue(1, st + 3 * step);
+          compute(1, st + waves);
+          issue(1, st + 3 * waves);
         }
         MOE_LANDED(VM);
-        compute(0);
-        if (i + 2 < n) issue(0, st + 2 * step);
+        compute(0, st);
+        if (i + 2 < n) issue(0, st + 2 * waves);
         MOE_LANDED(0);
-        compute(1);
-        if (i + 2 < n) compute(0);
-      } else {
+        compute(1, st + waves);
+        if (i + 2 < n) compute(0, st + 2 * waves);
+      } else if (n == 1) {
         MOE_LANDED(0);
-        compute(0);
+        compute(0, st);
       }
-    }
 #undef MOE_LANDED
+    }
   }
 }
 
@@ -773,15 +792,13 @@ __device__ __forceinline__ void make_plan(const FewArgs &a, PlanScratch &p, floa
 }
 
 // ---------------------------------------------------------------------------
-// Tile of gate|up: 16 NB columns of H.  `waves` of the workgroup split the
-// inputs, this one taking stages gw, gw + waves, ...
-template <int F, int L, int NB>
+// Tile of gate|up: 16 NB columns of H; the wave's partial products to `mine`.
+template <int F, bool TILED, int NB>
 __device__ __forceinline__ void up_tile(const FewArgs &a, const TSrc &xs, const void *wg,
                                         const void *wu, const uint8_t *sg, const uint8_t *su,
-                                        int n0, uint32_t row, bool there, int gw, int waves,
-                                        int lane, uint8_t *ring0, uint8_t *ring1, float *mine) {
-  constexpr int KST = stage_inputs<F>();
-  const int nst = (a.d + KST - 1) / KST;
+                                        int n0, uint32_t row, bool there, int wave, int waves,
+                                        int lane, uint8_t *ring0, uint8_t *ring1, uint8_t *scales,
+                                        float *mine) {
   const WSrc ws[2] = {w_source<F>(wg, sg, a.I, a.d, n0, 16 * NB),
                       w_source<F>(wu, su, a.I, a.d, n0, 16 * NB)};
   f32x4 acc[2][NB];
@@ -789,13 +806,14 @@ __device__ __forceinline__ void up_tile(const FewArgs &a, const TSrc &xs, const 
   for (int s = 0; s < 2; ++s)
 #pragma unroll
     for (int b = 0; b < NB; ++b) acc[s][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-  tile_dot<F, L, false, NB>(acc, xs, ws, a.d, lane, row, there, gw, waves, nst, ring0, ring1);
+  tile_dot<F, TILED, false, NB>(acc, xs, ws, a.d, lane, row, there, wave, waves, ring0, ring1,
+                                scales);
   put_partial<NB>(mine, acc, lane);
 }
 
 // few_plan: workgroup 0 routes; the others stream the shared expert's gate|up,
 // 16 columns each, 8 waves splitting the inputs.
-template <int F, int L>
+template <int F, bool TILED>
 __global__ __launch_bounds__(512, 2) void few_plan(const FewArgs a) {
   constexpr int SLOT = F == F_F32 ? 2048 : 4096;
   constexpr int PLAN = (int)sizeof(PlanScratch);
@@ -812,8 +830,8 @@ __global__ __launch_bounds__(512, 2) void few_plan(const FewArgs a) {
   const int n0 = (blockIdx.x - 1) * 16, t0 = lane & 15;
   const TSrc xs = {resource(a.x, (int64_t)a.T * a.d * es), resource(a.x, 0)};
   float *red = (float *)R0;
-  up_tile<F, L, 1>(a, xs, a.sh_gate, a.sh_up, nullptr, nullptr, n0, t0, t0 < a.T, wave, 8, lane,
-                       R0 + wave * SLOT, F == F_F32 ? R0 : R1 + wave * SLOT,
+  up_tile<F, TILED, 1>(a, xs, a.sh_gate, a.sh_up, nullptr, nullptr, n0, t0, t0 < a.T, wave, 8, lane,
+                       R0 + wave * SLOT, F == F_F32 ? R0 : R1 + wave * SLOT, nullptr,
                        red + wave * (SLOT / 4));
   __syncthreads();
   for (int e = threadIdx.x; e < 256; e += 512) {
@@ -832,29 +850,29 @@ __global__ __launch_bounds__(512, 2) void few_plan(const FewArgs a) {
   }
 }
 
-// Waves that take a tile together: the largest power of two that leaves every
-// resident wave at most one tile (few tiles need their inputs split to fill
-// the GPU; many run longer per wave, with fewer ends at which loads drain).
-__device__ __forceinline__ int waves_per_tile(int tiles, int resident) {
-  int g = 4;
-  while (g > 1 && tiles * g > resident) g >>= 1;
-  return g;
-}
+// LDS of the up and down launches: two ring slots of 8 KB a wave and the FP4
+// scales, 80 KB, so that two workgroups share a CU and cover each other's
+// starts and ends.
+#define MOE_FEW_LDS(F)                                                                        \
+  constexpr int SLOT = F == F_F32 ? 4096 : 8192;                                              \
+  __shared__ __attribute__((aligned(1024))) uint8_t R0[4 * SLOT];                             \
+  __shared__ __attribute__((aligned(1024))) uint8_t R1[F == F_F32 ? 16 : 4 * SLOT];           \
+  __shared__ __attribute__((aligned(1024))) uint8_t SC[is_fp4<F>() ? 16384 : 16];             \
+  float *red = (float *)R0;                                                                   \
+  const int lane = threadIdx.x & 63;                                                          \
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);                          \
+  uint8_t *ring0 = R0 + wave * SLOT, *ring1 = F == F_F32 ? R0 : R1 + wave * SLOT
 
-// few_up: 32 columns of H of one slot per tile (an MXFP8 scale block).
-template <int F, int L>
+// few_up: a workgroup takes 32 columns of H of one slot (an MXFP8 scale block),
+// its four waves splitting the inputs.
+template <int F, bool TILED>
 __global__ __launch_bounds__(256, 2) void few_up(const FewArgs a) {
   constexpr bool MX = F == F_MX4 || F == F_MX8;
-  constexpr int NB = 2, SLOT = F == F_F32 ? 4096 : 8192;
+  constexpr int NB = 2;
   constexpr int es = F == F_F32 ? 4 : 2;
-  __shared__ __attribute__((aligned(1024))) uint8_t R0[4 * SLOT];
-  __shared__ __attribute__((aligned(1024))) uint8_t R1[F == F_F32 ? 16 : 4 * SLOT];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  MOE_FEW_LDS(F);
   const int T = a.T, d = a.d, I = a.I;
   const int blocks = (I + 31) / 32, tiles = a.plan_slots[0] * blocks;
-  const int G = waves_per_tile(tiles, 4 * gridDim.x);
-  const int per = 4 / G, gw = wave & (G - 1);
   TSrc xs;
   if constexpr (MX) {
     xs.r = resource(a.xq, (int64_t)T * d);
@@ -863,53 +881,44 @@ __global__ __launch_bounds__(256, 2) void few_up(const FewArgs a) {
     xs.r = resource(a.x, (int64_t)T * d * es);
     xs.r2 = xs.r;
   }
-  float *red = (float *)R0;
-  for (int base = blockIdx.x * per; base < tiles; base += gridDim.x * per) {
-    const int tile = base + wave / G;
-    const bool live = tile < tiles;
-    const int slot = (live ? tile : base) / blocks;
-    const int n0 = ((live ? tile : base) - slot * blocks) * 32;
+  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const int slot = tile / blocks, n0 = (tile - slot * blocks) * 32;
     const int16_t *rows = a.plan_row + slot * kRows;
-    if (live) {
-      const int e = __builtin_amdgcn_readfirstlane(a.plan_expert[slot]);
-      const int64_t at = e * ((int64_t)I * row_bytes<F>(d));
-      const int64_t sat = e * ((int64_t)I * d / (F == F_MX8 ? 16384 : 32));
-      up_tile<F, L, NB>(a, xs, (const uint8_t *)a.w_gate + at, (const uint8_t *)a.w_up + at,
-                            a.s_gate + sat, a.s_up + sat, n0, lane & 15, rows[lane & 15] >= 0, gw, G,
-                            lane, R0 + wave * SLOT, F == F_F32 ? R0 : R1 + wave * SLOT,
-                            red + wave * (SLOT / 4));
-    }
+    const int64_t e = a.plan_expert[slot];
+    const int64_t at = e * ((int64_t)I * row_bytes<F>(d));
+    const int64_t sat = e * ((int64_t)I * d / (F == F_MX8 ? 16384 : 32));
+    up_tile<F, TILED, NB>(a, xs, (const uint8_t *)a.w_gate + at, (const uint8_t *)a.w_up + at,
+                          a.s_gate + sat, a.s_up + sat, n0, lane & 15, rows[lane & 15] >= 0, wave,
+                          4, lane, ring0, ring1, SC, red + wave * (SLOT / 4));
     __syncthreads();
-    if (live) {
-      // a half-wave takes a token's 32 columns
-      const float *part = red + (wave - gw) * (SLOT / 4);
-      for (int t = gw * 2 + (lane >> 5); t < kRows; t += G * 2) {
-        const int pair = rows[t], c = lane & 31, n = n0 + c;
-        const int el = (c >> 4) * 256 + t * 16 + (c & 15);
-        float g = 0.f, u = 0.f;
-        for (int w = 0; w < G; ++w) {
-          g += part[w * (SLOT / 4) + el];
-          u += part[w * (SLOT / 4) + NB * 256 + el];
+    // a half-wave takes a token's 32 columns
+    for (int t = threadIdx.x >> 5; t < kRows; t += 8) {
+      const int pair = rows[t], c = lane & 31, n = n0 + c;
+      const int el = (c >> 4) * 256 + t * 16 + (c & 15);
+      float g = 0.f, u = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        g += red[w * (SLOT / 4) + el];
+        u += red[w * (SLOT / 4) + NB * 256 + el];
+      }
+      const float v = swiglu_pair(g, u, a.limit);
+      if constexpr (MX) {
+        float amax = fabsf(v);
+        amax = fmaxf(amax, xor_lane<1>(amax));
+        amax = fmaxf(amax, xor_lane<2>(amax));
+        amax = fmaxf(amax, xor_lane<4>(amax));
+        amax = fmaxf(amax, xor_lane<8>(amax));
+        amax = fmaxf(amax, xor_lane<16>(amax));
+        const int X = mx_exponent(amax);
+        const int word = __builtin_amdgcn_cvt_pk_fp8_f32(mx_element(v, X), 0.f, 0, false);
+        if (pair >= 0) {
+          a.hq[(int64_t)pair * I + n] = (uint8_t)word;
+          if (c == 0) a.hq_scales[(int64_t)pair * (I / 32) + n0 / 32] = (uint8_t)(X + 127);
         }
-        const float v = swiglu_pair(g, u, a.limit);
-        if constexpr (MX) {
-          float amax = fabsf(v);
-          amax = fmaxf(amax, xor_lane<1>(amax));
-          amax = fmaxf(amax, xor_lane<2>(amax));
-          amax = fmaxf(amax, xor_lane<4>(amax));
-          amax = fmaxf(amax, xor_lane<8>(amax));
-          amax = fmaxf(amax, xor_lane<16>(amax));
-          const int X = mx_exponent(amax);
-          const int word = __builtin_amdgcn_cvt_pk_fp8_f32(mx_element(v, X), 0.f, 0, false);
-          if (pair >= 0) {
-            a.hq[(int64_t)pair * I + n] = (uint8_t)word;
-            if (c == 0) a.hq_scales[(int64_t)pair * (I / 32) + n0 / 32] = (uint8_t)(X + 127);
-          }
-        } else if (pair >= 0 && n < I) {
-          const int64_t o = (int64_t)pair * I + n;
-          if constexpr (F == F_F32) ((float *)a.h)[o] = v;
-          else store_hilo((bf16 *)a.h, (bf16 *)a.h_lo, o, v);
-        }
+      } else if (pair >= 0 && n < I) {
+        const int64_t o = (int64_t)pair * I + n;
+        if constexpr (F == F_F32) ((float *)a.h)[o] = v;
+        else store_hilo((bf16 *)a.h, (bf16 *)a.h_lo, o, v);
       }
     }
     __syncthreads();
@@ -917,93 +926,79 @@ __global__ __launch_bounds__(256, 2) void few_up(const FewArgs a) {
 }
 
 // Tile of W_down: 64 output columns of one slot; the wave's partial to `mine`.
-template <int F, int L, bool HILO>
+template <int F, bool TILED, bool HILO>
 __device__ __forceinline__ void down_tile(const FewArgs &a, const TSrc &hs, const void *w,
-                                          const uint8_t *sc, int n0, int row, int gw, int waves,
-                                          int lane, uint8_t *ring0, uint8_t *ring1, float *mine) {
-  constexpr int KST = stage_inputs<F>(), NB = 2;
-  const int nst = (a.I + KST - 1) / KST;
+                                          const uint8_t *sc, int n0, int row, int wave, int lane,
+                                          uint8_t *ring0, uint8_t *ring1, uint8_t *scales,
+                                          float *mine) {
+  constexpr int NB = 2;
   const WSrc ws[2] = {w_source<F>(w, sc, a.d, a.I, n0, 32), w_source<F>(w, sc, a.d, a.I, n0 + 32, 32)};
   f32x4 acc[2][NB];
 #pragma unroll
   for (int s = 0; s < 2; ++s)
 #pragma unroll
     for (int b = 0; b < NB; ++b) acc[s][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-  tile_dot<F, L, HILO, NB>(acc, hs, ws, a.I, lane, row < 0 ? 0 : row, row >= 0, gw, waves, nst,
-                               ring0, ring1);
+  tile_dot<F, TILED, HILO, NB>(acc, hs, ws, a.I, lane, row < 0 ? 0 : row, row >= 0, wave, 4, ring0,
+                               ring1, scales);
   put_partial<NB>(mine, acc, lane);
 }
 
 // few_down: yrows[pair] = w (H[pair] W_down^T) in fp32, rows T*k .. the shared
-// expert's.  The shared tiles (longer, in bf16) come first, four waves each.
+// expert's; 64 columns of one slot per workgroup, the shared tiles (longer, in
+// bf16) first.
 // PACK (T <= 8): the two halves of H ride in one operand, MFMA row t the high
 // half of token t and row 8 + t the low one, whose products are added at the
 // end; more tokens take a second operand.
-template <int F, int L, bool PACK>
+template <int F, bool TILED, bool PACK>
 __global__ __launch_bounds__(256, 2) void few_down(const FewArgs a) {
   constexpr bool MX = F == F_MX4 || F == F_MX8;
   constexpr bool F32 = F == F_F32;
-  constexpr int SLOT = F32 ? 4096 : 8192;
   constexpr int kLow = 8 * 16;                 // the low half's products in a 16 x 16 block
-  __shared__ __attribute__((aligned(1024))) uint8_t R0[4 * SLOT];
-  __shared__ __attribute__((aligned(1024))) uint8_t R1[F32 ? 16 : 4 * SLOT];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  MOE_FEW_LDS(F);
   const int T = a.T, d = a.d, I = a.I, pairs = T * a.k;
   const int blocks = (d + 63) / 64;
   const int shared = a.has_shared ? blocks : 0;
-  const int tiles = a.plan_slots[0] * blocks;
+  const int tiles = shared + a.plan_slots[0] * blocks;
   const int hrows = pairs + (a.has_shared ? T : 0);
   const int64_t hbytes = (int64_t)hrows * I * (F32 ? 4 : 2);
   // the low halves follow the high ones
   const TSrc hs = {resource(a.h, F32 ? hbytes : 2 * hbytes), resource(F32 ? a.h : a.h_lo, hbytes)};
   const TSrc qs = {resource(a.hq, MX ? (int64_t)pairs * I : 0),
                    resource(a.hq_scales, MX ? (int64_t)pairs * (I / 32) : 0)};
-  float *red = (float *)R0;
-  uint8_t *ring0 = R0 + wave * SLOT, *ring1 = F32 ? R0 : R1 + wave * SLOT;
-  const int resident = 4 * ((int)gridDim.x - shared);
-  const int G = waves_per_tile(tiles, resident > 4 ? resident : 4);
-  const int per = 4 / G;
-  // work units of a workgroup: the shared tiles, then `per` routed tiles each
-  const int units = shared + (tiles + per - 1) / per;
-  for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
-    const bool sh = unit < shared;
-    const int g = sh ? 4 : G, gw = wave & (g - 1);
-    const int tile = sh ? unit : (unit - shared) * per + wave / g;
-    const bool live = sh || tile < tiles;
-    const int slot = sh || !live ? 0 : tile / blocks;
-    const int n0 = (live ? tile - slot * blocks : 0) * 64;
+  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const bool sh = tile < shared;
+    const int slot = sh ? 0 : (tile - shared) / blocks;
+    const int n0 = (sh ? tile : tile - shared - slot * blocks) * 64;
     const int16_t *rows = a.plan_row + slot * kRows;
     const bool packed = PACK && (sh || !MX);
     const int t = packed ? lane & 7 : lane & 15;
     const int low = packed && (lane & 8) ? hrows : 0;
+    float *mine = red + wave * (SLOT / 4);
     if (sh) {
-      down_tile<F32 ? F_F32 : F_BF16, L, !F32 && !PACK>(
-          a, hs, a.sh_down, nullptr, n0, t < T ? pairs + t + low : -1, gw, 4, lane, ring0, ring1,
-          red + wave * (SLOT / 4));
-    } else if (live) {
-      const int e = __builtin_amdgcn_readfirstlane(a.plan_expert[slot]);
+      down_tile<F32 ? F_F32 : F_BF16, TILED && !F32, !F32 && !PACK>(
+          a, hs, a.sh_down, nullptr, n0, t < T ? pairs + t + low : -1, wave, lane, ring0, ring1, SC,
+          mine);
+    } else {
+      const int64_t e = a.plan_expert[slot];
       const int64_t at = e * ((int64_t)d * row_bytes<F>(I));
       const int64_t sat = e * ((int64_t)d * I / (F == F_MX8 ? 16384 : 32));
       const int row = rows[t];
-      down_tile<F, L, !F32 && !MX && !PACK>(a, MX ? qs : hs, (const uint8_t *)a.w_down + at,
-                                            a.s_down + sat, n0, row < 0 ? row : row + low, gw, g,
-                                            lane, ring0, ring1, red + wave * (SLOT / 4));
+      down_tile<F, TILED, !F32 && !MX && !PACK>(a, MX ? qs : hs, (const uint8_t *)a.w_down + at,
+                                                a.s_down + sat, n0, row < 0 ? row : row + low, wave,
+                                                lane, ring0, ring1, SC, mine);
     }
     __syncthreads();
-    if (live) {
-      const float *part = red + (wave - gw) * (SLOT / 4);
-      for (int tt = gw; tt < T; tt += g) {
-        const int pair = sh ? pairs + tt : rows[tt], n = n0 + lane;
-        if (pair < 0 || n >= d) continue;
-        const int el = (lane >> 4) * 256 + tt * 16 + (lane & 15);
-        float v = 0.f;
-        for (int w = 0; w < g; ++w) {
-          v += part[w * (SLOT / 4) + el];
-          if (packed) v += part[w * (SLOT / 4) + el + kLow];
-        }
-        a.yrows[(int64_t)pair * d + n] = sh ? v : a.plan_w[slot * kRows + tt] * v;
+    for (int tt = wave; tt < T; tt += 4) {
+      const int pair = sh ? pairs + tt : rows[tt], n = n0 + lane;
+      if (pair < 0 || n >= d) continue;
+      const int el = (lane >> 4) * 256 + tt * 16 + (lane & 15);
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        v += red[w * (SLOT / 4) + el];
+        if (packed) v += red[w * (SLOT / 4) + el + kLow];
       }
+      a.yrows[(int64_t)pair * d + n] = sh ? v : a.plan_w[slot * kRows + tt] * v;
     }
     __syncthreads();
   }
@@ -1042,8 +1037,6 @@ template <int F, bool TILED>
 hipError_t run_few(FewArgs a, hipStream_t s) {
   constexpr bool MX = F == F_MX4 || F == F_MX8;
   constexpr int FS = F == F_F32 ? F_F32 : F_BF16;
-  constexpr bool FP4 = F == F_FP4;             // MXFP8 layers have K % 128 == 0
-  constexpr int L = TILED ? TILES : ROWS, L_ODD = FP4 && !TILED ? ROWS_ODD : L;
   hipError_t err;
   const int pairs = a.T * a.k;
   const int quant = MX ? (a.T * a.d / 32 + 255) / 256 : 0;
@@ -1052,26 +1045,18 @@ hipError_t run_few(FewArgs a, hipStream_t s) {
     if ((err = hipGetLastError()) != hipSuccess) return err;
   }
   const int shared = a.has_shared ? (a.I + 15) / 16 : 0;
-  hipLaunchKernelGGL((few_plan<FS, TILED ? TILES : ROWS>), dim3(1 + shared), dim3(512), 0, s, a);
+  hipLaunchKernelGGL((few_plan<FS, TILED && F != F_F32>), dim3(1 + shared), dim3(512), 0, s, a);
   if ((err = hipGetLastError()) != hipSuccess) return err;
   const int64_t up = (int64_t)pairs * ((a.I + 31) / 32);
-  const dim3 up_grid(up < kGroups ? (unsigned)up : kGroups);
-  if (TILED || !FP4 || a.d % 128 == 0)
-    hipLaunchKernelGGL((few_up<F, L>), up_grid, dim3(256), 0, s, a);
-  else
-    hipLaunchKernelGGL((few_up<F, L_ODD>), up_grid, dim3(256), 0, s, a);
+  hipLaunchKernelGGL((few_up<F, TILED>), dim3(up < kGroups ? (unsigned)up : kGroups), dim3(256), 0,
+                     s, a);
   if ((err = hipGetLastError()) != hipSuccess) return err;
   const int64_t down = (int64_t)(pairs + (a.has_shared ? 1 : 0)) * ((a.d + 63) / 64);
   const dim3 down_grid(down < kGroups ? (unsigned)down : kGroups);
-  const bool odd = !TILED && FP4 && a.I % 128 != 0;
-  if (F == F_F32 || a.T > 8) {
-    if (odd) hipLaunchKernelGGL((few_down<F, L_ODD, false>), down_grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((few_down<F, L, false>), down_grid, dim3(256), 0, s, a);
-  } else {
-    constexpr bool P = F != F_F32;
-    if (odd) hipLaunchKernelGGL((few_down<F, L_ODD, P>), down_grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((few_down<F, L, P>), down_grid, dim3(256), 0, s, a);
-  }
+  if (F == F_F32 || a.T > 8)
+    hipLaunchKernelGGL((few_down<F, TILED, false>), down_grid, dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((few_down<F, TILED, F != F_F32>), down_grid, dim3(256), 0, s, a);
   if ((err = hipGetLastError()) != hipSuccess) return err;
   const dim3 grid((unsigned)((a.d + 1023) / 1024), (unsigned)a.T);
   if (F == F_F32) hipLaunchKernelGGL((few_combine<float>), grid, dim3(256), 0, s, a);

@@ -665,10 +665,13 @@ int moe_forward_few(const moe_config *cfg, const moe_weights *w, const void *x,
                              cfg->expert_dtype == MOE_DTYPE_FP8_E4M3_B128;
   const bool learned = cfg->route_mode == MOE_ROUTE_LEARNED;
   const bool shared = cfg->n_shared_experts == 1;
-  // 16-byte loads of x and of every matrix row
-  for (const void *p : {x, (const void *)y, w->w_gate, w->w_up, w->w_down,
-                        learned ? w->gate_w : nullptr, shared ? w->sh_gate : nullptr,
-                        shared ? w->sh_up : nullptr, shared ? w->sh_down : nullptr})
+  // 16-byte loads of x and of every matrix row, FP4 scales among them
+  const bool scaled = cfg->expert_dtype == MOE_DTYPE_FP4_E2M1;
+  for (const void *p :
+       {x, (const void *)y, w->w_gate, w->w_up, w->w_down, learned ? w->gate_w : nullptr,
+        shared ? w->sh_gate : nullptr, shared ? w->sh_up : nullptr, shared ? w->sh_down : nullptr,
+        scaled ? (const void *)w->s_gate : nullptr, scaled ? (const void *)w->s_up : nullptr,
+        scaled ? (const void *)w->s_down : nullptr})
     if ((uintptr_t)p % 16) return MOE_ERR_INVALID_ARG;
   if (!ws || ((uintptr_t)ws % kAlign) != 0 || ws_bytes < L.total_bytes) return MOE_ERR_WORKSPACE;
 
