@@ -144,27 +144,26 @@ __device__ __forceinline__ u32x4 w_operand(const uint8_t *lds, int b, int f, int
 
 // FP4 scales.  Eight scale bytes of a row go with a stage of it; loaded stage
 // by stage they touch as many cache lines as the weights and cost 20 % of the
-// stream, so the workgroup, which works on one tile, first copies the scales of
-// the tile's rows for up to kScaleSpan inputs (31 stages, 248 bytes a row): per
-// source 8 KB of LDS, row layout 256 bytes a row, from the row's first byte
-// rounded down to four; tiled layout as the row blocks lie, 4 KB each.
-constexpr int kScaleSpan = 31 * 256;           // inputs
+// stream, so those of the tile's rows are first copied to LDS, SW bytes a row
+// (SW = 256: 31 stages; 64: 7): row layout from the row's first byte rounded
+// down to four, tiled layout as the row blocks lie, 16 SW bytes each.
 template <int F> constexpr bool is_fp4() { return F == F_FP4 || F == F_MX4; }
 
-// This wave's (of four) share of the 32 rows' scales for inputs k0 ...
-template <bool TILED>
+// One wave's share (of W = SW / 64 waves) of a source's 32 rows, inputs k0 ...
+template <bool TILED, int SW>
 __device__ __forceinline__ void copy_scales(const WSrc &w, int K, int k0, int wave, int lane,
                                             uint8_t *lds) {
+  constexpr int W = SW / 64;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int u = wave + 4 * i;                // 1 KB unit
+    const int u = wave + W * i;                // 1 KB unit
     uint32_t off;
     if constexpr (TILED) {
-      const uint32_t in = (uint32_t)k0 / 2 + (u & 3) * 1024 + lane * 16;
-      off = in < (uint32_t)K / 2 ? (u >> 2) * (K / 2) + in : kOut;
+      const uint32_t in = (uint32_t)k0 / 2 + (u % W) * 1024 + lane * 16;
+      off = in < (uint32_t)K / 2 ? (u / W) * (K / 2) + in : kOut;
     } else {
-      const uint32_t row = (4 * u + (lane >> 4)) * (K / 32);
-      const uint32_t at = ((row + k0 / 32) & ~3u) + (lane & 15) * 16;
+      const uint32_t row = (u * (1024 / SW) + lane / (SW / 16)) * (K / 32);
+      const uint32_t at = ((row + k0 / 32) & ~3u) + lane % (SW / 16) * 16;
       off = at < row + K / 32 ? at : kOut;
     }
     __builtin_amdgcn_raw_ptr_buffer_load_lds(w.rs, (MOE_LDS void *)(lds + u * 1024), 16, off, 0, 0,
@@ -172,13 +171,13 @@ __device__ __forceinline__ void copy_scales(const WSrc &w, int K, int k0, int wa
   }
 }
 // The scale byte of row block b's row l % 16 for its 32 inputs of half `half`
-// (of 128 inputs, from the span's start k0).
-template <bool TILED>
+// (of 128 inputs, from the copied span's start k0).
+template <bool TILED, int SW>
 __device__ __forceinline__ uint32_t scale_byte(const uint8_t *lds, int K, int k0, int b, int half,
                                                int lane) {
   const int r = 16 * b + (lane & 15), q = lane >> 4;
-  return TILED ? lds[b * 4096 + (2 * half + (q >> 1)) * 32 + (lane & 15) * 2 + (q & 1)]
-               : lds[r * 256 + ((r * (K / 32) + k0 / 32) & 3) + half * 4 + q];
+  return TILED ? lds[b * 16 * SW + (2 * half + (q >> 1)) * 32 + (lane & 15) * 2 + (q & 1)]
+               : lds[r * SW + ((r * (K / 32) + k0 / 32) & 3) + half * 4 + q];
 }
 
 // ---------------------------------------------------------------------------
@@ -252,7 +251,7 @@ __device__ __forceinline__ i32x8 wide(const u32x4 &a, const u32x4 &b) {
 
 // acc += tokens x the 16 rows of row block b over one stage; scl: the source's
 // FP4 scales in LDS, `half` the stage's first half in them; s8: the FP8 scale.
-template <int F, bool TILED, bool HILO>
+template <int F, bool TILED, bool HILO, int SW>
 __device__ __forceinline__ void stage_mma(f32x4 &acc, const Tokens<F, HILO> &a, uint32_t s8,
                                           const uint8_t *scl, int K, int k0, int half,
                                           const uint8_t *lds, int b, int lane) {
@@ -267,7 +266,7 @@ __device__ __forceinline__ void stage_mma(f32x4 &acc, const Tokens<F, HILO> &a, 
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const u32x4 codes = w_operand<F, TILED>(lds, b, h, lane);
-      const float scale = __uint_as_float(scale_byte<TILED>(scl, K, k0, b, half + h, lane) << 23);
+      const float scale = __uint_as_float(scale_byte<TILED, SW>(scl, K, k0, b, half + h, lane) << 23);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const bf16x2 v0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[i], scale, 0);
@@ -285,7 +284,7 @@ __device__ __forceinline__ void stage_mma(f32x4 &acc, const Tokens<F, HILO> &a, 
     for (int h = 0; h < 2; ++h)
       acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
           wide(a.v[2 * h], a.v[2 * h + 1]), wide(w_operand<F, TILED>(lds, b, h, lane), u32x4{}),
-          acc, 0, 4, 0, (int)a.s[h], 0, (int)scale_byte<TILED>(scl, K, k0, b, half + h, lane));
+          acc, 0, 4, 0, (int)a.s[h], 0, (int)scale_byte<TILED, SW>(scl, K, k0, b, half + h, lane));
   } else {
     acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
         wide(a.v[0], a.v[1]),
@@ -306,9 +305,10 @@ __device__ __forceinline__ u32x4 w_direct(const WSrc &w, int K, int lane, int b,
 
 // The wave's tile of products: acc[s][b] = tokens x row block b of source s,
 // over stages wave, wave + waves, ..., two stages in flight.  ring0 / ring1: the
-// wave's two slots of 4 NB KB; scales: the workgroup's 16 KB (FP4; four waves,
-// NB = 2, every wave calls).
-template <int F, bool TILED, bool HILO, int NB>
+// wave's two slots of 4 NB KB; scales: 64 SW bytes (FP4, NB = 2), shared by the
+// waves of the tile (four of them for SW = 256, and all call together; one for
+// SW = 64).
+template <int F, bool TILED, bool HILO, int NB, int SW = 256>
 __device__ __forceinline__ void tile_dot(f32x4 (&acc)[2][NB], const TSrc &ts, const WSrc (&ws)[2],
                                          int K, int lane, uint32_t row, bool there, int wave,
                                          int waves, uint8_t *ring0, uint8_t *ring1,
@@ -336,17 +336,18 @@ __device__ __forceinline__ void tile_dot(f32x4 (&acc)[2][NB], const TSrc &ts, co
     constexpr int VM = 4 * NB + Tokens<F, HILO>::kLoads + (F == F_MX8 ? 2 : 0);
     static_assert(2 * VM <= 63, "vmcnt holds 6 bits");
     static_assert(!is_fp4<F>() || NB == 2, "32 rows of scales a source");
-    constexpr int SPAN = is_fp4<F>() ? kScaleSpan / KST : 1 << 30;
+    constexpr int SPAN = is_fp4<F>() ? SW / 8 - 1 : 1 << 30;   // stages
     Tokens<F, HILO> a[2];
     uint32_t s8[2][2];
     // stages lo .. hi - 1 (whose scales are in LDS)
     for (int lo = 0; lo < nst; lo += SPAN) {
       const int hi = nst - lo > SPAN ? lo + SPAN : nst;
       if constexpr (is_fp4<F>()) {
-        if (lo > 0) __syncthreads();           // every wave is done with the last scales
+        // every wave is done with the last scales
+        if (lo > 0 && SW == 256) __syncthreads();
 #pragma unroll
         for (int s = 0; s < 2; ++s)
-          copy_scales<TILED>(ws[s], K, lo * KST, wave, lane, scales + s * 8192);
+          copy_scales<TILED, SW>(ws[s], K, lo * KST, wave, lane, scales + s * 32 * SW);
       }
       auto issue = [&](int p, int st) {
         uint8_t *lds = p ? ring1 : ring0;
@@ -366,8 +367,8 @@ __device__ __forceinline__ void tile_dot(f32x4 (&acc)[2][NB], const TSrc &ts, co
         for (int s = 0; s < 2; ++s)
 #pragma unroll
           for (int b = 0; b < NB; ++b)
-            stage_mma<F, TILED, HILO>(acc[s][b], a[p], F == F_MX8 ? s8[p][s] : 0,
-                                      scales + s * 8192, K, lo * KST, 2 * (st - lo),
+            stage_mma<F, TILED, HILO, SW>(acc[s][b], a[p], F == F_MX8 ? s8[p][s] : 0,
+                                      scales + s * 32 * SW, K, lo * KST, 2 * (st - lo),
                                       lds + s * NB * 2048, b, lane);
         // the slot's reads are done before a copy may land in it again
         __builtin_amdgcn_s_waitcnt(0xC07F);    // lgkmcnt(0)
@@ -385,7 +386,7 @@ __device__ __forceinline__ void tile_dot(f32x4 (&acc)[2][NB], const TSrc &ts, co
       if constexpr (is_fp4<F>()) {
         // the scales are older than the stages issued
         if (n > 1) { MOE_LANDED(2 * VM); } else { MOE_LANDED(0); }
-        __builtin_amdgcn_s_barrier();
+        if (SW == 256) __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
       }
       if (n > 1) {
@@ -676,7 +677,7 @@ __device__ __forceinline__ void select_any(const FewArgs &a, int t, int lane, fl
 // by first appearance in (token, choice) order), for each slot and token the H
 // row (the pair's number t*k + j; -1: not chosen) and the gate value (summed
 // where a token has the expert twice), and for each token the choices that
-// hold a row.  One workgroup of 8 waves; a thread per pair.
+// hold a row.  One workgroup of 16 waves; a thread per pair.
 struct PlanScratch {
   float w[256];
   int32_t e[256];
@@ -691,7 +692,7 @@ __device__ __forceinline__ void make_plan(const FewArgs &a, PlanScratch &p, floa
   const int T = a.T, k = a.k, E = a.E, pairs = T * k;
   if (tid == 0) p.misc[0] = 0;
   if (tid < kRows) p.mask[tid] = 0;
-  for (int i = tid; i < pairs * kRows; i += 512) {
+  for (int i = tid; i < pairs * kRows; i += 1024) {
     p.cell_w[i] = 0.f;
     p.cell_row[i] = -1;
   }
@@ -699,7 +700,7 @@ __device__ __forceinline__ void make_plan(const FewArgs &a, PlanScratch &p, floa
     // affinities of all tokens by all threads (softmax: the logits), the parts
     // of a logit added in order; then a wave per token
     const int n = T * E;
-    for (int i = tid; i < n; i += 512) {
+    for (int i = tid; i < n; i += 1024) {
       float part[kLogitParts];
 #pragma unroll
       for (int q = 0; q < kLogitParts; ++q) part[q] = q < a.KS ? a.scores[(int64_t)q * n + i] : 0.f;
@@ -712,7 +713,7 @@ __device__ __forceinline__ void make_plan(const FewArgs &a, PlanScratch &p, floa
       scores[i] = z;
     }
     __syncthreads();
-    for (int t = wave; t < T; t += 8) select_any(a, t, lane, p.w, p.e, scores);
+    for (int t = wave; t < T; t += 16) select_any(a, t, lane, p.w, p.e, scores);
     __syncthreads();
   } else {
     __syncthreads();
@@ -784,7 +785,7 @@ __device__ __forceinline__ void make_plan(const FewArgs &a, PlanScratch &p, floa
     }
   }
   __syncthreads();
-  for (int i = tid; i < slots * kRows; i += 512) {
+  for (int i = tid; i < slots * kRows; i += 1024) {
     a.plan_w[i] = p.cell_w[i];
     a.plan_row[i] = p.cell_row[i];
   }
@@ -812,14 +813,14 @@ __device__ __forceinline__ void up_tile(const FewArgs &a, const TSrc &xs, const 
 }
 
 // few_plan: workgroup 0 routes; the others stream the shared expert's gate|up,
-// 16 columns each, 8 waves splitting the inputs.
+// 16 columns each, 16 waves splitting the inputs.
 template <int F, bool TILED>
-__global__ __launch_bounds__(512, 2) void few_plan(const FewArgs a) {
+__global__ __launch_bounds__(1024) void few_plan(const FewArgs a) {
   constexpr int SLOT = F == F_F32 ? 2048 : 4096;
   constexpr int PLAN = (int)sizeof(PlanScratch);
-  __shared__ __attribute__((aligned(1024))) uint8_t R0[8 * SLOT > PLAN ? 8 * SLOT : PLAN];
-  __shared__ __attribute__((aligned(1024))) uint8_t R1[kRows * 512 * 4];
-  static_assert(sizeof(R1) >= 8 * SLOT, "ring slots");
+  __shared__ __attribute__((aligned(1024))) uint8_t R0[16 * SLOT > PLAN ? 16 * SLOT : PLAN];
+  __shared__ __attribute__((aligned(1024))) uint8_t R1[16 * 4096];
+  static_assert(sizeof(R1) >= kRows * 512 * 4, "affinities of all tokens");
   if (blockIdx.x == 0) {
     make_plan(a, *(PlanScratch *)R0, (float *)R1);
     return;
@@ -830,16 +831,16 @@ __global__ __launch_bounds__(512, 2) void few_plan(const FewArgs a) {
   const int n0 = (blockIdx.x - 1) * 16, t0 = lane & 15;
   const TSrc xs = {resource(a.x, (int64_t)a.T * a.d * es), resource(a.x, 0)};
   float *red = (float *)R0;
-  up_tile<F, TILED, 1>(a, xs, a.sh_gate, a.sh_up, nullptr, nullptr, n0, t0, t0 < a.T, wave, 8, lane,
+  up_tile<F, TILED, 1>(a, xs, a.sh_gate, a.sh_up, nullptr, nullptr, n0, t0, t0 < a.T, wave, 16, lane,
                        R0 + wave * SLOT, F == F_F32 ? R0 : R1 + wave * SLOT, nullptr,
                        red + wave * (SLOT / 4));
   __syncthreads();
-  for (int e = threadIdx.x; e < 256; e += 512) {
+  for (int e = threadIdx.x; e < 256; e += 1024) {
     const int t = e >> 4, n = n0 + (e & 15);
     if (t >= a.T || n >= a.I) continue;
     float g = 0.f, u = 0.f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
+    for (int w = 0; w < 16; ++w) {
       g += red[w * (SLOT / 4) + e];
       u += red[w * (SLOT / 4) + 256 + e];
     }
@@ -926,10 +927,10 @@ __global__ __launch_bounds__(256, 2) void few_up(const FewArgs a) {
 }
 
 // Tile of W_down: 64 output columns of one slot; the wave's partial to `mine`.
-template <int F, bool TILED, bool HILO>
+template <int F, bool TILED, bool HILO, int SW>
 __device__ __forceinline__ void down_tile(const FewArgs &a, const TSrc &hs, const void *w,
-                                          const uint8_t *sc, int n0, int row, int wave, int lane,
-                                          uint8_t *ring0, uint8_t *ring1, uint8_t *scales,
+                                          const uint8_t *sc, int n0, int row, int wave, int waves,
+                                          int lane, uint8_t *ring0, uint8_t *ring1, uint8_t *scales,
                                           float *mine) {
   constexpr int NB = 2;
   const WSrc ws[2] = {w_source<F>(w, sc, a.d, a.I, n0, 32), w_source<F>(w, sc, a.d, a.I, n0 + 32, 32)};
@@ -938,68 +939,76 @@ __device__ __forceinline__ void down_tile(const FewArgs &a, const TSrc &hs, cons
   for (int s = 0; s < 2; ++s)
 #pragma unroll
     for (int b = 0; b < NB; ++b) acc[s][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-  tile_dot<F, TILED, HILO, NB>(acc, hs, ws, a.I, lane, row < 0 ? 0 : row, row >= 0, wave, 4, ring0,
-                               ring1, scales);
+  tile_dot<F, TILED, HILO, NB, SW>(acc, hs, ws, a.I, lane, row < 0 ? 0 : row, row >= 0, wave, waves,
+                                   ring0, ring1, scales);
   put_partial<NB>(mine, acc, lane);
 }
 
 // few_down: yrows[pair] = w (H[pair] W_down^T) in fp32, rows T*k .. the shared
-// expert's; 64 columns of one slot per workgroup, the shared tiles (longer, in
-// bf16) first.
+// expert's.  A tile is 64 columns of one slot, taken by G waves: four, or one
+// where the tile is a few stages long (FP4 with I <= 1792: MXFP8 at 16 tokens
+// 108 -> 89 us; four waves had one or two stages each).  The shared tiles
+// (longer, in bf16, four waves) come first.
 // PACK (T <= 8): the two halves of H ride in one operand, MFMA row t the high
 // half of token t and row 8 + t the low one, whose products are added at the
 // end; more tokens take a second operand.
-template <int F, bool TILED, bool PACK>
+template <int F, bool TILED, bool PACK, int G>
 __global__ __launch_bounds__(256, 2) void few_down(const FewArgs a) {
   constexpr bool MX = F == F_MX4 || F == F_MX8;
   constexpr bool F32 = F == F_F32;
   constexpr int kLow = 8 * 16;                 // the low half's products in a 16 x 16 block
+  constexpr int SW = G == 4 ? 256 : 64, PER = 4 / G;
   MOE_FEW_LDS(F);
   const int T = a.T, d = a.d, I = a.I, pairs = T * a.k;
   const int blocks = (d + 63) / 64;
   const int shared = a.has_shared ? blocks : 0;
-  const int tiles = shared + a.plan_slots[0] * blocks;
+  const int tiles = a.plan_slots[0] * blocks;
+  const int units = shared + (tiles + PER - 1) / PER;
   const int hrows = pairs + (a.has_shared ? T : 0);
   const int64_t hbytes = (int64_t)hrows * I * (F32 ? 4 : 2);
   // the low halves follow the high ones
   const TSrc hs = {resource(a.h, F32 ? hbytes : 2 * hbytes), resource(F32 ? a.h : a.h_lo, hbytes)};
   const TSrc qs = {resource(a.hq, MX ? (int64_t)pairs * I : 0),
                    resource(a.hq_scales, MX ? (int64_t)pairs * (I / 32) : 0)};
-  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const bool sh = tile < shared;
-    const int slot = sh ? 0 : (tile - shared) / blocks;
-    const int n0 = (sh ? tile : tile - shared - slot * blocks) * 64;
+  float *mine = red + wave * (SLOT / 4);
+  for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    const bool sh = unit < shared;
+    const int tile = sh ? unit : (unit - shared) * PER + (G == 1 ? wave : 0);
+    const bool live = sh || tile < tiles;
+    const int slot = sh || !live ? 0 : tile / blocks;
+    const int n0 = (live ? tile - slot * blocks : 0) * 64;
     const int16_t *rows = a.plan_row + slot * kRows;
     const bool packed = PACK && (sh || !MX);
     const int t = packed ? lane & 7 : lane & 15;
     const int low = packed && (lane & 8) ? hrows : 0;
-    float *mine = red + wave * (SLOT / 4);
     if (sh) {
-      down_tile<F32 ? F_F32 : F_BF16, TILED && !F32, !F32 && !PACK>(
-          a, hs, a.sh_down, nullptr, n0, t < T ? pairs + t + low : -1, wave, lane, ring0, ring1, SC,
-          mine);
-    } else {
-      const int64_t e = a.plan_expert[slot];
+      down_tile<F32 ? F_F32 : F_BF16, TILED && !F32, !F32 && !PACK, 256>(
+          a, hs, a.sh_down, nullptr, n0, t < T ? pairs + t + low : -1, wave, 4, lane, ring0, ring1,
+          nullptr, mine);
+    } else if (live) {
+      const int64_t e = __builtin_amdgcn_readfirstlane(a.plan_expert[slot]);
       const int64_t at = e * ((int64_t)d * row_bytes<F>(I));
       const int64_t sat = e * ((int64_t)d * I / (F == F_MX8 ? 16384 : 32));
       const int row = rows[t];
-      down_tile<F, TILED, !F32 && !MX && !PACK>(a, MX ? qs : hs, (const uint8_t *)a.w_down + at,
-                                                a.s_down + sat, n0, row < 0 ? row : row + low, wave,
-                                                lane, ring0, ring1, SC, mine);
+      down_tile<F, TILED, !F32 && !MX && !PACK, SW>(
+          a, MX ? qs : hs, (const uint8_t *)a.w_down + at, a.s_down + sat, n0,
+          row < 0 ? row : row + low, G == 1 ? 0 : wave, G, lane, ring0, ring1,
+          SC + (G == 1 ? wave * 64 * SW : 0), mine);
     }
     __syncthreads();
-    for (int tt = wave; tt < T; tt += 4) {
-      const int pair = sh ? pairs + tt : rows[tt], n = n0 + lane;
-      if (pair < 0 || n >= d) continue;
-      const int el = (lane >> 4) * 256 + tt * 16 + (lane & 15);
-      float v = 0.f;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        v += red[w * (SLOT / 4) + el];
-        if (packed) v += red[w * (SLOT / 4) + el + kLow];
+    const bool own = G == 1 && !sh;            // the wave's tile is its own
+    if (live)
+      for (int tt = own ? 0 : wave; tt < T; tt += own ? 1 : 4) {
+        const int pair = sh ? pairs + tt : rows[tt], n = n0 + lane;
+        if (pair < 0 || n >= d) continue;
+        const int el = (lane >> 4) * 256 + tt * 16 + (lane & 15);
+        float v = 0.f;
+        for (int w = own ? wave : 0; w < (own ? wave + 1 : 4); ++w) {
+          v += red[w * (SLOT / 4) + el];
+          if (packed) v += red[w * (SLOT / 4) + el + kLow];
+        }
+        a.yrows[(int64_t)pair * d + n] = sh ? v : a.plan_w[slot * kRows + tt] * v;
       }
-      a.yrows[(int64_t)pair * d + n] = sh ? v : a.plan_w[slot * kRows + tt] * v;
-    }
     __syncthreads();
   }
 }
@@ -1045,18 +1054,27 @@ hipError_t run_few(FewArgs a, hipStream_t s) {
     if ((err = hipGetLastError()) != hipSuccess) return err;
   }
   const int shared = a.has_shared ? (a.I + 15) / 16 : 0;
-  hipLaunchKernelGGL((few_plan<FS, TILED && F != F_F32>), dim3(1 + shared), dim3(512), 0, s, a);
+  hipLaunchKernelGGL((few_plan<FS, TILED && F != F_F32>), dim3(1 + shared), dim3(1024), 0, s, a);
   if ((err = hipGetLastError()) != hipSuccess) return err;
   const int64_t up = (int64_t)pairs * ((a.I + 31) / 32);
   hipLaunchKernelGGL((few_up<F, TILED>), dim3(up < kGroups ? (unsigned)up : kGroups), dim3(256), 0,
                      s, a);
   if ((err = hipGetLastError()) != hipSuccess) return err;
-  const int64_t down = (int64_t)(pairs + (a.has_shared ? 1 : 0)) * ((a.d + 63) / 64);
-  const dim3 down_grid(down < kGroups ? (unsigned)down : kGroups);
-  if (F == F_F32 || a.T > 8)
-    hipLaunchKernelGGL((few_down<F, TILED, false>), down_grid, dim3(256), 0, s, a);
+  // one wave a tile where the scales of all its inputs fit a wave's share of LDS
+  constexpr bool FP4 = is_fp4<F>();
+  const bool one = FP4 && a.I <= 7 * 256;
+  const int64_t blocks = (a.d + 63) / 64;
+  const int64_t down = (pairs * blocks + (one ? 3 : 0)) / (one ? 4 : 1) + (a.has_shared ? blocks : 0);
+  const dim3 dg(down < kGroups ? (unsigned)down : kGroups);
+  constexpr bool P = F != F_F32;
+  if (one && a.T <= 8)
+    hipLaunchKernelGGL((few_down<F, TILED, P, FP4 ? 1 : 4>), dg, dim3(256), 0, s, a);
+  else if (one)
+    hipLaunchKernelGGL((few_down<F, TILED, false, FP4 ? 1 : 4>), dg, dim3(256), 0, s, a);
+  else if (P && a.T <= 8)
+    hipLaunchKernelGGL((few_down<F, TILED, P, 4>), dg, dim3(256), 0, s, a);
   else
-    hipLaunchKernelGGL((few_down<F, TILED, F != F_F32>), down_grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((few_down<F, TILED, false, 4>), dg, dim3(256), 0, s, a);
   if ((err = hipGetLastError()) != hipSuccess) return err;
   const dim3 grid((unsigned)((a.d + 1023) / 1024), (unsigned)a.T);
   if (F == F_F32) hipLaunchKernelGGL((few_combine<float>), grid, dim3(256), 0, s, a);
