@@ -227,29 +227,21 @@ struct Operand {
   static __device__ __forceinline__ int swz(int k) { return ES == 2 && TC >= 128 ? (k & 3) << 2 : 0; }
 
   // Byte offset, from the stage's origin, of what lane l copies to byte 16 l of
-  // unit u; kc: its first contraction index (row operands).
-  static __device__ __forceinline__ uint32_t source(int u, int lane, int64_t ld, int *kc) {
+  // unit u.
+  static __device__ __forceinline__ uint32_t source(int u, int lane, int64_t ld) {
     if constexpr (!COL) {
       const int r = u * 16 + (lane >> 2);
-      const int c = (lane & 3) ^ ((r >> 3) & 3);
-      *kc = c * (16 / ES);
-      return (uint32_t)(r * ld * ES) + c * 16;
+      return (uint32_t)(r * ld * ES) + ((lane & 3) ^ ((r >> 3) & 3)) * 16;
     } else {
       const int byte = u * 1024 + lane * 16;
       const int k = byte / RB;
-      const int c = (byte % RB / 16) ^ swz(k);
-      *kc = 0;
-      return (uint32_t)(k * ld * ES) + c * 16;
+      return (uint32_t)(k * ld * ES) + ((byte % RB / 16) ^ swz(k)) * 16;
     }
   }
-  static __device__ __forceinline__ rsrc_t origin(const Matrix &m, int64_t tile0, int64_t k0,
-                                                  bool there) {
-    const int64_t at = (COL ? k0 * m.ld + tile0 : tile0 * m.ld + k0) * ES;
-    int64_t left = ((m.rows - 1) * m.ld + m.cols) * ES - at;
-    left = left < 0 || !there ? 0 : left < (int64_t)kOut ? left : (int64_t)kOut;
-    const uint8_t *p = (const uint8_t *)m.p + (left > 0 ? at : 0);
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, (uint32_t)left,
-                                             0x00027000);
+  // First contraction index, within the stage, of the piece lane l copies of a
+  // row operand (a wave's units have the same parity, so the same pieces).
+  static __device__ __forceinline__ int first_k(int wave, int lane) {
+    return ((lane & 3) ^ ((2 * wave + (lane >> 5)) & 3)) * (16 / ES);
   }
   // One lane's fragment of the 32 rows (columns of D) from `base`, step s.
   static __device__ __forceinline__ u32x4 fragment(const uint8_t *lds, int base, int s, int lane) {
@@ -311,13 +303,52 @@ __device__ __forceinline__ bool gemm_item(const GemmOp &g, int64_t *mt, int *nt,
   return true;
 }
 
+// Where an operand's next stage starts: address, bytes from there to the end of
+// the matrix (a copy past it reads zeros), bytes to the stage after.
+struct Cursor {
+  const uint8_t *p;
+  int64_t left, step;
+};
+template <typename T, bool COL>
+__device__ __forceinline__ Cursor cursor(const Matrix &m, int64_t tile0, int64_t k0) {
+  constexpr int ES = sizeof(T), KB = 64 / ES;
+  const int64_t at = (COL ? k0 * m.ld + tile0 : tile0 * m.ld + k0) * ES;
+  return Cursor{(const uint8_t *)m.p + at, ((m.rows - 1) * m.ld + m.cols) * ES - at,
+                COL ? KB * m.ld * ES : 64};
+}
+__device__ __forceinline__ rsrc_t cursor_rsrc(const Cursor &c) {
+  const int hi = (int)(c.left >> 32);
+  const uint32_t lo = (uint32_t)c.left;
+  const uint32_t n = hi < 0 ? 0 : (hi > 0 || lo > kOut) ? kOut : lo;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(c.p), 0, n, 0x00027000);
+}
+
+// The order a step's instructions are issued in: one LDS read (of DS) after
+// each of the first MFMAs (of N), the copies (of VM) spread over all of them.
+// The scheduler otherwise sinks the reads to their use in the next step and
+// gathers the copies at the end.
+template <int I, int N, int DS, int VM>
+__device__ __forceinline__ void interleave() {
+  if constexpr (I < N) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);           // MFMA
+    constexpr int F = N * 3 / 4 > 0 ? N * 3 / 4 : 1;             // reads end three quarters through
+    constexpr int d1 = DS * (I + 1) / F < DS ? DS * (I + 1) / F : DS;
+    constexpr int d0 = DS * I / F < DS ? DS * I / F : DS;
+    if constexpr (d1 > d0) __builtin_amdgcn_sched_group_barrier(0x100, d1 - d0, 0);
+    constexpr int v = VM * (I + 1) / N - VM * I / N;
+    if constexpr (v > 0) __builtin_amdgcn_sched_group_barrier(0x010, v, 0);
+    interleave<I + 1, N, DS, VM>();
+  }
+}
+
 template <typename T, int MI, int NI, bool AC, bool BC, bool DUAL>
-__global__ __launch_bounds__(256, MI *NI >= 8 ? 1 : 2) void gemm_kernel(const GemmOp g) {
+__device__ __forceinline__ void gemm_tile(const GemmOp &g) {
   constexpr int ES = sizeof(T), KB = 64 / ES, NS = 4;
   constexpr int TM = 64 * MI, TN = 64 * NI;
   constexpr int UA = TM / 16, UB = TN / 16;    // 1 KB copy units per stage
-  constexpr int VM = (UA + UB) / 4;            // per wave
+  constexpr int VA = UA / 4, VB = UB / 4, VM = VA + VB;          // per wave
   constexpr int SLOT = (TM + TN) * 64;
+  constexpr bool SEGS = !AC && BC;             // two contraction segments occur (dx of swiglu)
   static_assert(!DUAL || (!AC && !BC), "the two-matrix product is the forward one");
   static_assert(UA % 4 == 0 && UB % 4 == 0, "units split evenly");
   using OA = Operand<T, AC, TM>;
@@ -339,45 +370,64 @@ __global__ __launch_bounds__(256, MI *NI >= 8 ? 1 : 2) void gemm_kernel(const Ge
   const int64_t m0 = mt * TM, n0 = (int64_t)nt * TO;
 
   const int st_seg0 = (int)((g.kdim[0] + KB - 1) / KB);
-  const int st_all = st_seg0 + (g.segments > 1 ? (int)((g.kdim[1] + KB - 1) / KB) : 0);
+  const int st_all = SEGS && g.segments > 1 ? st_seg0 + (int)((g.kdim[1] + KB - 1) / KB) : st_seg0;
   const int st_first = (int)((int64_t)st_all * part / g.parts);
   const int nst = (int)((int64_t)st_all * (part + 1) / g.parts) - st_first;
 
-  // the segments share strides (dz, du and W, W_up have the same shapes)
-  uint32_t off[VM];
-  int kc[VM];
+  // sources of the next stage to copy; `rest` counts contraction elements left
+  // of its segment for the row operands' ragged ends
+  const bool second = SEGS && st_first >= st_seg0;
+  const int64_t k_first = (int64_t)(second ? st_first - st_seg0 : st_first) * KB;
+  Cursor ca = cursor<T, AC>(second ? g.a[1] : g.a[0], m0, k_first);
+  Cursor cb = cursor<T, BC>(second ? g.b[1] : g.b[0], n0, k_first);
+  Cursor cu = DUAL ? cursor<T, BC>(g.b_up, n0, k_first) : cb;
+  const Cursor ca1 = SEGS ? cursor<T, AC>(g.a[1], m0, 0) : ca;
+  const Cursor cb1 = SEGS ? cursor<T, BC>(g.b[1], n0, 0) : cb;
+  int to_switch = SEGS && g.segments > 1 && !second ? st_seg0 - st_first : -1;
+  int rest = (int)((second ? g.kdim[1] : g.kdim[0]) - k_first), rest_b = rest;
+  int to_switch_b = to_switch;
+  const int rest1 = (int)g.kdim[1];
+  int to_end = nst, to_end_b = nst;            // stages left to copy
+
+  uint32_t off_a[VA], off_b[VB];
 #pragma unroll
-  for (int q = 0; q < VM; ++q) {
-    const int u = wave + 4 * q;
-    if (q < UA / 4) {
-      off[q] = OA::source(u, lane, g.a[0].ld, &kc[q]);
-    } else {
-      int ub = u - UA;
-      if (DUAL && ub >= UB / 2) ub -= UB / 2;
-      off[q] = OB::source(ub, lane, g.b[0].ld, &kc[q]);
-    }
+  for (int q = 0; q < VA; ++q) off_a[q] = OA::source(wave + 4 * q, lane, g.a[0].ld);
+#pragma unroll
+  for (int q = 0; q < VB; ++q) {
+    int u = wave + 4 * q;
+    if (DUAL && u >= UB / 2) u -= UB / 2;
+    off_b[q] = OB::source(u, lane, g.b[0].ld);
   }
-  auto issue = [&](int slot, int st, int q) {
-    const bool there = st < nst;
-    const int abs_st = st_first + st;
-    const int seg = abs_st >= st_seg0 ? 1 : 0;
-    const int64_t k0 = (int64_t)(abs_st - (seg ? st_seg0 : 0)) * KB;
-    const int64_t kd = seg ? g.kdim[1] : g.kdim[0];
-    const int u = wave + 4 * q;
-    uint32_t o = off[q];
-    rsrc_t r;
-    if (q < UA / 4) {
-      const Matrix m = seg ? g.a[1] : g.a[0];
-      r = OA::origin(m, m0, k0, there);
-      if (!AC && k0 + kc[q] >= kd) o = kOut;
-    } else {
-      Matrix m = seg ? g.b[1] : g.b[0];
-      if (DUAL && u - UA >= UB / 2) m = g.b_up;
-      r = OB::origin(m, n0, k0, there);
-      if (!BC && k0 + kc[q] >= kd) o = kOut;
+  const int ka = OA::first_k(wave, lane);
+  auto copy_a = [&](int slot) {
+    rsrc_t r = cursor_rsrc(ca);
+    const uint32_t tail = (!AC && ka >= rest) || to_end <= 0 ? kOut : 0u;
+#pragma unroll
+    for (int q = 0; q < VA; ++q)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (MOE_LDS void *)(ring[slot] + (wave + 4 * q) * 1024),
+                                               16, off_a[q] | tail, 0, 0, 0);
+    ca.p += ca.step; ca.left -= ca.step; rest -= KB; --to_end;
+    if constexpr (SEGS) {
+      const bool sw = --to_switch == 0;
+      ca.p = sw ? ca1.p : ca.p; ca.left = sw ? ca1.left : ca.left; rest = sw ? rest1 : rest;
     }
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (MOE_LDS void *)(ring[slot] + u * 1024), 16, o, 0,
-                                             0, 0);
+  };
+  auto copy_b = [&](int slot) {
+    const uint32_t tail = (!BC && ka >= rest_b) || to_end_b <= 0 ? kOut : 0u;
+#pragma unroll
+    for (int q = 0; q < VB; ++q) {
+      const int u = wave + 4 * q;
+      // units of the second half hold W_up's rows
+      const bool up = DUAL && (UB >= 8 ? q >= VB / 2 : u >= UB / 2);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(cursor_rsrc(up ? cu : cb), (MOE_LDS void *)(ring[slot] + (UA + u) * 1024), 16,
+                                               off_b[q] | tail, 0, 0, 0);
+    }
+    cb.p += cb.step; cb.left -= cb.step; rest_b -= KB; --to_end_b;
+    if constexpr (DUAL) { cu.p += cb.step; cu.left -= cb.step; }
+    if constexpr (SEGS) {
+      const bool sw = --to_switch_b == 0;
+      cb.p = sw ? cb1.p : cb.p; cb.left = sw ? cb1.left : cb.left; rest_b = sw ? rest1 : rest_b;
+    }
   };
 
   f32x16 acc[MI][NI];
@@ -392,9 +442,9 @@ __global__ __launch_bounds__(256, MI *NI >= 8 ? 1 : 2) void gemm_kernel(const Ge
   auto read = [&](int buf, int slot, int s) {
     const uint8_t *A = ring[slot], *B = ring[slot] + UA * 1024;
 #pragma unroll
-    for (int i = 0; i < MI; ++i) fa[buf][i] = OA::fragment(A, (wm * MI + i) * 32, s, lane);
-#pragma unroll
     for (int j = 0; j < NI; ++j) fb[buf][j] = OB::fragment(B, (wn * NI + j) * 32, s, lane);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) fa[buf][i] = OA::fragment(A, (wm * MI + i) * 32, s, lane);
   };
   auto multiply = [&](int buf) {
 #pragma unroll
@@ -402,34 +452,47 @@ __global__ __launch_bounds__(256, MI *NI >= 8 ? 1 : 2) void gemm_kernel(const Ge
 #pragma unroll
       for (int j = 0; j < NI; ++j) mma<T>(acc[i][j], fa[buf][i], fb[buf][j]);
   };
+  // instructions of a step
+  constexpr int kMma = MI * NI * (ES == 2 ? 1 : 4);
+  constexpr int kReadsA = MI * (!AC ? 1 : ES == 2 ? 2 : 4);
+  constexpr int kReadsB = NI * (!BC ? 1 : ES == 2 ? 2 : 4);
 
 #pragma unroll
-  for (int p = 0; p < NS - 1; ++p)
-#pragma unroll
-    for (int q = 0; q < VM; ++q) issue(p, p, q);
+  for (int p = 0; p < NS - 1; ++p) { copy_a(p); copy_b(p); }
   __builtin_amdgcn_s_waitcnt(MOE_VMCNT(2 * VM));
   __builtin_amdgcn_s_barrier();
   read(0, 0, 0);
-  // Stage st from slot p.  Its second step's fragments are read while the
-  // first step multiplies; then, with every read of this slot done and the
-  // next stage landed (two younger stages may be in flight), one barrier, the
-  // next stage's first fragments, and the second step's MFMAs.  The slot the
-  // previous stage used (free since the previous barrier) is refilled during
-  // the first step.  Stages past the end copy nothing.
-  for (int st0 = 0; st0 < nst; st0 += NS) {
+  // Stage st from slot p.  The second step's fragments are read while the first
+  // step multiplies; then, with every read of this slot done and the next stage
+  // landed (younger: one stage and the A half of another), one barrier, and the
+  // next stage's first fragments are read while the second step multiplies.
+  // The slot the previous stage used (free since the previous barrier) is
+  // refilled meanwhile, A in the first step, B in the second.  Stages past the
+  // end copy nothing.
+  auto stage = [&](int p) {
+    __builtin_amdgcn_sched_barrier(0);
+    read(1, p, 1);
+    copy_a((p + NS - 1) % NS);
+    multiply(0);
+    interleave<0, kMma, kReadsA + kReadsB, VA>();
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(MOE_VMCNT(VM + VA) & ~(15 << 8));   // and lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    read(0, (p + 1) % NS, 0);
+    copy_b((p + NS - 1) % NS);
+    multiply(1);
+    interleave<0, kMma, kReadsA + kReadsB, VB>();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  int st = 0;
+  for (; st + NS <= nst; st += NS) {
 #pragma unroll
-    for (int p = 0; p < NS; ++p) {
-      const int st = st0 + p;
-      read(1, p, 1);
-#pragma unroll
-      for (int q = 0; q < VM; ++q) issue((p + NS - 1) % NS, st + NS - 1, q);
-      multiply(0);
-      __builtin_amdgcn_s_waitcnt(MOE_VMCNT(2 * VM) & ~(15 << 8));    // and lgkmcnt(0)
-      __builtin_amdgcn_s_barrier();
-      read(0, (p + 1) % NS, 0);
-      multiply(1);
-    }
+    for (int p = 0; p < NS; ++p) stage(p);
   }
+#pragma unroll
+  for (int p = 0; p < NS - 1; ++p)
+    if (st + p < nst) stage(p);
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
 
@@ -475,6 +538,11 @@ __global__ __launch_bounds__(256, MI *NI >= 8 ? 1 : 2) void gemm_kernel(const Ge
       }
     }
   }
+}
+
+template <typename T, int MI, int NI, bool AC, bool BC, bool DUAL>
+__global__ __launch_bounds__(256, MI *NI >= 8 ? 1 : 2) void gemm_kernel(const GemmOp g) {
+  gemm_tile<T, MI, NI, AC, BC, DUAL>(g);
 }
 
 // Sum of the parts of a split product, in order, and the epilogue.
