@@ -98,16 +98,28 @@ constexpr float kGeluA = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float kGeluB = 0.044715f;
 
 template <typename T>
-__device__ __forceinline__ float activate(float z, int act) {
+__device__ __forceinline__ void activate8(float (&v)[8], int act) {
   switch (act) {
-    case MOE_ACTIVATION_RELU: return z > 0.f ? z : (z != z ? z : 0.f);
-    case MOE_ACTIVATION_SILU: return z * sigmoid<T>(z);
-    case MOE_ACTIVATION_GELU: return 0.5f * z * erfcf(-z * 0.7071067811865476f);
+    case MOE_ACTIVATION_RELU:
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = v[j] > 0.f ? v[j] : (v[j] != v[j] ? v[j] : 0.f);
+      break;
+    case MOE_ACTIVATION_SILU:
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= sigmoid<T>(v[j]);
+      break;
+    case MOE_ACTIVATION_GELU:
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= 0.5f * erfcf(-v[j] * 0.7071067811865476f);
+      break;
     case MOE_ACTIVATION_GELU_TANH:
       // 0.5 z (1 + tanh q) = z sigmoid(2q), which keeps its relative accuracy
       // for large negative z
-      return z * sigmoid<T>(2.f * kGeluA * (z + kGeluB * z * z * z));
-    default: return z;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        v[j] *= sigmoid<T>(2.f * kGeluA * (v[j] + kGeluB * v[j] * v[j] * v[j]));
+      break;
+    default: break;
   }
 }
 
@@ -144,10 +156,11 @@ __device__ __forceinline__ float saved(float v, float L) {
   return __uint_as_float(a > L ? bits + 0x10000u : bits - 0x10000u);
 }
 
-// y (and z) of eight columns n .. of row m from the raw products v (and u).
+// y (and z) of eight columns n .. of row m from the raw products v (and u); res:
+// the residual there (loaded ahead by the caller, if there is one).
 template <typename T, bool DUAL>
-__device__ __forceinline__ void finish8(const Epilogue &e, float (&v)[8], float (&u)[8], int64_t m,
-                                        int n) {
+__device__ __forceinline__ void finish8(const Epilogue &e, float (&v)[8], float (&u)[8],
+                                        const float (&res)[8], int64_t m, int n) {
   const int left = e.N - n;
   const bool vec = e.vec != 0;
   float b[8];
@@ -185,13 +198,11 @@ __device__ __forceinline__ void finish8(const Epilogue &e, float (&v)[8], float 
       v[j] = g * sigmoid<T>(g) * w;
     }
   } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = activate<T>(v[j], e.act);
+    activate8<T>(v, e.act);
   }
   if (e.residual) {
-    load8<T>(b, (const T *)e.residual + m * e.ld_res + n, left, vec);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += b[j];
+    for (int j = 0; j < 8; ++j) v[j] += res[j];
   }
   store8<T>((T *)e.y + m * e.ld_y + n, v, left, vec);
 }
@@ -210,7 +221,12 @@ struct GemmOp {
   int64_t M;                   // rows of D
   int n_tiles, parts;
   int64_t m_tiles;
-  float *part;                 // parts > 1: [parts][DUAL ? 2 : 1][M][ldp]
+  // dW of swiglu: two products of the same shape in one launch, row tiles of
+  // the second (a_up^T b -> y_up) after the first's
+  Matrix a_up;
+  void *y_up;
+  int halves;                  // 1 or 2
+  float *part;                 // parts > 1: [parts][halves, or 2 for swiglu][M][ldp]
   int64_t ldp;
   Epilogue e;
 };
@@ -271,15 +287,17 @@ struct Operand {
   }
 };
 
+// acc (32 x 32, transposed: lane l holds D's row l % 32, columns 8 (e / 4) +
+// 4 (l / 32) + e % 4) += a b.
 template <typename T>
 __device__ __forceinline__ void mma(f32x16 &acc, const u32x4 &a, const u32x4 &b) {
   if constexpr (sizeof(T) == 2) {
-    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
-                                                  __builtin_bit_cast(bf16x8, b), acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, b),
+                                                  __builtin_bit_cast(bf16x8, a), acc, 0, 0, 0);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[i]), __uint_as_float(b[i]), acc,
+      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(b[i]), __uint_as_float(a[i]), acc,
                                                  0, 0, 0);
   }
 }
@@ -367,6 +385,12 @@ __device__ __forceinline__ void gemm_tile(const GemmOp &g) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1;
   constexpr int TO = DUAL ? TN / 2 : TN;       // output columns of a tile
+  int half = 0;
+  if constexpr (AC) {                          // dW
+    const int64_t per = g.m_tiles / g.halves;
+    half = mt >= per ? 1 : 0;
+    mt -= half * per;
+  }
   const int64_t m0 = mt * TM, n0 = (int64_t)nt * TO;
 
   const int st_seg0 = (int)((g.kdim[0] + KB - 1) / KB);
@@ -378,7 +402,7 @@ __device__ __forceinline__ void gemm_tile(const GemmOp &g) {
   // of its segment for the row operands' ragged ends
   const bool second = SEGS && st_first >= st_seg0;
   const int64_t k_first = (int64_t)(second ? st_first - st_seg0 : st_first) * KB;
-  Cursor ca = cursor<T, AC>(second ? g.a[1] : g.a[0], m0, k_first);
+  Cursor ca = cursor<T, AC>(second ? g.a[1] : half ? g.a_up : g.a[0], m0, k_first);
   Cursor cb = cursor<T, BC>(second ? g.b[1] : g.b[0], n0, k_first);
   Cursor cu = DUAL ? cursor<T, BC>(g.b_up, n0, k_first) : cb;
   const Cursor ca1 = SEGS ? cursor<T, AC>(g.a[1], m0, 0) : ca;
@@ -438,11 +462,16 @@ __device__ __forceinline__ void gemm_tile(const GemmOp &g) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
 
+  // 32-column block j of the wave; swiglu: the first half of a wave's blocks are
+  // gate columns, the rest the up columns that go with them
+  auto col_block = [&](int j) {
+    return DUAL ? (j < NI / 2 ? wn * (NI / 2) + j : NI + wn * (NI / 2) + j - NI / 2) : wn * NI + j;
+  };
   u32x4 fa[2][MI], fb[2][NI];
   auto read = [&](int buf, int slot, int s) {
     const uint8_t *A = ring[slot], *B = ring[slot] + UA * 1024;
 #pragma unroll
-    for (int j = 0; j < NI; ++j) fb[buf][j] = OB::fragment(B, (wn * NI + j) * 32, s, lane);
+    for (int j = 0; j < NI; ++j) fb[buf][j] = OB::fragment(B, col_block(j) * 32, s, lane);
 #pragma unroll
     for (int i = 0; i < MI; ++i) fa[buf][i] = OA::fragment(A, (wm * MI + i) * 32, s, lane);
   };
@@ -494,49 +523,87 @@ __device__ __forceinline__ void gemm_tile(const GemmOp &g) {
   for (int p = 0; p < NS - 1; ++p)
     if (st + p < nst) stage(p);
   __builtin_amdgcn_s_waitcnt(0);
-  __syncthreads();
+  __syncthreads();                             // every wave is done with the ring
 
-  // Epilogue: 32 rows of each wave row (64 rows of D) at a time go through LDS
-  // as fp32, so that a thread then holds eight consecutive columns of a row.
-  // Consecutive groups use the two halves of the ring in turn.
-  constexpr int PIECES = TO / 8;
+  // Epilogue.  32 rows of the wave's quarter at a time go through the wave's own
+  // part of LDS (no barrier), so that a lane then has eight consecutive columns
+  // of a row and 16 or 8 lanes a whole line; the residual of the next pieces is
+  // on its way while these are finished.
+  constexpr int NJ = DUAL ? NI / 2 : NI;       // output column blocks of the wave
+  constexpr int PC = NJ * 4;                   // pieces of 8 columns per row
+  constexpr int PPI = 32 * PC / 64;            // pieces per lane and 32 rows
+  constexpr int CH = PPI < 4 ? PPI : 4;        // of them at a time
+  constexpr int LD = NI * 32 + 4;              // floats per LDS row (padded)
+  static_assert(32 * LD * 4 <= SLOT, "a wave's rows fit a ring slot");
+  float *stage_f = (float *)(wave == 0 ? L0 : wave == 1 ? L1 : wave == 2 ? L2 : L3);
+  const bool plain = g.parts > 1;
+  auto place = [&](int c, int q, int64_t *m, int64_t *n, int *r, int *pc) {
+    const int idx = (c % (PPI / CH) * CH + q) * 64 + lane;
+    *r = idx / PC;
+    *pc = idx - *r * PC;
+    *m = m0 + (wm * MI + c / (PPI / CH)) * 32 + *r;
+    *n = n0 + (int64_t)wn * NJ * 32 + *pc * 8;
+  };
+  float res[CH][8], ahead[CH][8];
+  auto fetch = [&](int c) {
 #pragma unroll
-  for (int i = 0; i < MI; ++i) {
-    float *h0 = (float *)((i & 1) ? L2 : L0), *h1 = (float *)((i & 1) ? L3 : L1);
-    float *half = wm ? h1 : h0;
+    for (int q = 0; q < CH; ++q) {
+      int64_t m, n;
+      int r, pc;
+      place(c, q, &m, &n, &r, &pc);
+      if (m < g.M && n < g.e.N)
+        load8<T>(ahead[q], (const T *)g.e.residual + m * g.e.ld_res + n, (int)(g.e.N - n),
+                 g.e.vec != 0);
+    }
+  };
+  const bool has_res = !BC && g.e.residual && !plain;
+  if (has_res) fetch(0);
+  for (int c = 0; c < MI * (PPI / CH); ++c) {
+    if (c % (PPI / CH) == 0) {
+      const int ci = c / (PPI / CH);
 #pragma unroll
-    for (int j = 0; j < NI; ++j)
+      for (int i = 0; i < MI; ++i)
+        if (i == ci) {                         // uniform; the accumulators keep their registers
 #pragma unroll
-      for (int e = 0; e < 16; ++e)
-        half[(8 * (e >> 2) + 4 * (lane >> 5) + (e & 3)) * TN + (wn * NI + j) * 32 + (lane & 31)] =
-            acc[i][j][e];
-    __syncthreads();
-    for (int idx = threadIdx.x; idx < 64 * PIECES; idx += 256) {
-      const int r = idx / PIECES, c = (idx - r * PIECES) * 8;
-      const int64_t m = m0 + (r >> 5) * (32 * MI) + i * 32 + (r & 31);
-      const int64_t n = n0 + c;
-      if (m >= g.M || n >= g.e.N) continue;
-      const float *row = (r >> 5 ? h1 : h0) + (r & 31) * TN + c;
-      float v[8], u[8];
+          for (int j = 0; j < NI; ++j)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const f32x4 w = *(const f32x4 *)(row + 4 * h);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[4 * h + j] = w[j];
-        if constexpr (DUAL) {
-          const f32x4 w2 = *(const f32x4 *)(row + TO + 4 * h);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) u[4 * h + j] = w2[j];
+            for (int e = 0; e < 4; ++e)
+              *(f32x4 *)(stage_f + (lane & 31) * LD + j * 32 + 8 * e + 4 * (lane >> 5)) =
+                  f32x4{acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2],
+                        acc[i][j][4 * e + 3]};
         }
-      }
-      if (g.parts > 1) {
-        float *o = g.part + (((int64_t)part * (DUAL ? 2 : 1)) * g.M + m) * g.ldp + n;
+      __builtin_amdgcn_wave_barrier();
+    }
+    if (has_res) {
+#pragma unroll
+      for (int q = 0; q < CH; ++q)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) res[q][j] = ahead[q][j];
+      if (c + 1 < MI * (PPI / CH)) fetch(c + 1);
+    }
+#pragma unroll
+    for (int q = 0; q < CH; ++q) {
+      int64_t m, n;
+      int r, pc;
+      place(c, q, &m, &n, &r, &pc);
+      float v[8], u[8];
+      load8<float>(v, stage_f + r * LD + pc * 8, 8, true);
+      if constexpr (DUAL) load8<float>(u, stage_f + r * LD + NJ * 32 + pc * 8, 8, true);
+      if (m >= g.M || n >= g.e.N) continue;
+      if (plain) {
+        // rows of ldp, a multiple of 8: whole pieces
+        float *o =
+            g.part + (((int64_t)part * (DUAL ? 2 : g.halves) + half) * g.M + m) * g.ldp + n;
         store8<float>(o, v, 8, true);
         if constexpr (DUAL) store8<float>(o + g.M * g.ldp, u, 8, true);
+      } else if constexpr (BC) {               // a gradient: no epilogue
+        store8<T>((T *)(half ? g.y_up : g.e.y) + m * g.e.ld_y + n, v, (int)(g.e.N - n),
+                  g.e.vec != 0);
       } else {
-        finish8<T, DUAL>(g.e, v, u, m, (int)n);
+        finish8<T, DUAL>(g.e, v, u, res[q], m, (int)n);
       }
     }
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
@@ -550,13 +617,17 @@ template <typename T, bool DUAL>
 __global__ __launch_bounds__(256) void sum_parts_kernel(const GemmOp g) {
   const int pieces = (g.e.N + 7) / 8;
   const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (idx >= g.M * pieces) return;
-  const int64_t m = idx / pieces;
-  const int n = (int)(idx - m * pieces) * 8;
-  constexpr int D = DUAL ? 2 : 1;
-  float v[8] = {}, u[8] = {}, t[8];
+  if (idx >= g.halves * g.M * pieces) return;
+  const int64_t mm = idx / pieces;
+  const int n = (int)(idx - mm * pieces) * 8;
+  const int half = mm >= g.M ? 1 : 0;
+  const int64_t m = mm - half * g.M;
+  const int D = DUAL ? 2 : g.halves;
+  float v[8] = {}, u[8] = {}, t[8], res[8];
+  if (g.e.residual)
+    load8<T>(res, (const T *)g.e.residual + m * g.e.ld_res + n, g.e.N - n, g.e.vec != 0);
   for (int p = 0; p < g.parts; ++p) {
-    const float *o = g.part + ((int64_t)p * D * g.M + m) * g.ldp + n;
+    const float *o = g.part + (((int64_t)p * D + half) * g.M + m) * g.ldp + n;
     load8<float>(t, o, 8, true);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] += t[j];
@@ -566,7 +637,9 @@ __global__ __launch_bounds__(256) void sum_parts_kernel(const GemmOp g) {
       for (int j = 0; j < 8; ++j) u[j] += t[j];
     }
   }
-  finish8<T, DUAL>(g.e, v, u, m, n);
+  Epilogue e = g.e;
+  if (half) e.y = g.y_up;
+  finish8<T, DUAL>(e, v, u, res, m, n);
 }
 
 // ---------------------------------------------------------------------------
@@ -656,17 +729,26 @@ __global__ __launch_bounds__(256) void slope_kernel(const SlopeArgs a) {
   }
 }
 
-// db: the parts' column sums added in order.
+// db: the parts' column sums.  A workgroup takes 32 columns, eight threads each
+// a column's parts p, p + 8, ... (loads that do not wait for one another), added
+// in a fixed order.
 template <typename T>
 __global__ __launch_bounds__(256) void bias_sum_kernel(const float *sums, int N, int parts, int d,
                                                        T *db, T *db_up) {
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  if (i >= N * d) return;
-  const int which = i / N, n = i - which * N;
-  T *out = which ? db_up : db;
-  if (!out) return;
+  __shared__ float red[8][33];
+  const int c = threadIdx.x & 31, p0 = threadIdx.x >> 5, which = blockIdx.y;
+  const int n = blockIdx.x * 32 + c;
   float v = 0.f;
-  for (int p = 0; p < parts; ++p) v += sums[((int64_t)p * d + which) * N + n];
+  if (n < N)
+#pragma unroll 4
+    for (int p = p0; p < parts; p += 8) v += sums[((int64_t)p * d + which) * N + n];
+  red[p0][c] = v;
+  __syncthreads();
+  T *out = which ? db_up : db;
+  if (p0 || n >= N || !out) return;
+  v = 0.f;
+#pragma unroll
+  for (int p = 0; p < 8; ++p) v += red[p][c];
   out[n] = (T)v;
 }
 
@@ -678,9 +760,9 @@ struct Shape { int mi, ni, parts; };
 // Per-CU cost of a stage in cycles, from the MFMA cycles of the tile (each
 // 32 x 32 block and step 32 cycles on one of four SIMDs) and the share of them
 // the shapes reach on long contractions.
-Shape pick_shape(int64_t rows, int64_t cols, int64_t stages, bool f32) {
+Shape pick_shape(int64_t rows, int64_t cols, int64_t stages, bool f32, bool dual) {
   struct { int mi, ni; double eff; } shapes[] = {
-      {4, 4, 0.85}, {4, 2, 0.75}, {2, 2, 0.6}, {1, 1, 0.3}};
+      {4, 4, 0.5}, {4, 2, 0.45}, {2, 2, 0.35}, {1, dual ? 2 : 1, 0.2}};
   Shape best = {1, 1, 1};
   double best_t = 1e300;
   for (const auto &sh : shapes) {
@@ -702,11 +784,12 @@ Shape pick_shape(int64_t rows, int64_t cols, int64_t stages, bool f32) {
   return best;
 }
 
-Shape shape_of(int64_t rows, int64_t cols, const int64_t *kdim, int segments, int dtype) {
+Shape shape_of(int64_t rows, int64_t cols, const int64_t *kdim, int segments, int dtype,
+               bool dual) {
   const int64_t kb = dtype == MOE_DTYPE_F32 ? 16 : 32;
   int64_t st = 0;
   for (int i = 0; i < segments; ++i) st += (kdim[i] + kb - 1) / kb;
-  return pick_shape(rows, cols, st, dtype == MOE_DTYPE_F32);
+  return pick_shape(rows, cols, st, dtype == MOE_DTYPE_F32, dual);
 }
 
 size_t part_bytes(int64_t rows, int64_t cols, bool dual, const Shape &s) {
@@ -716,14 +799,14 @@ size_t part_bytes(int64_t rows, int64_t cols, bool dual, const Shape &s) {
 template <typename T, int MI, int NI, bool AC, bool BC, bool DUAL>
 hipError_t run_gemm_shape(GemmOp g, hipStream_t s) {
   constexpr int TM = 64 * MI, TO = DUAL ? 32 * NI : 64 * NI;
-  g.m_tiles = (g.M + TM - 1) / TM;
+  g.m_tiles = (g.M + TM - 1) / TM * g.halves;
   g.n_tiles = (g.e.N + TO - 1) / TO;
   const int64_t items = g.m_tiles * g.n_tiles * g.parts;
   hipLaunchKernelGGL((gemm_kernel<T, MI, NI, AC, BC, DUAL>), dim3((unsigned)(8 * ((items + 7) / 8))),
                      dim3(256), 0, s, g);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess || g.parts == 1) return err;
-  const int64_t pieces = g.M * ((g.e.N + 7) / 8);
+  const int64_t pieces = g.halves * g.M * ((g.e.N + 7) / 8);
   hipLaunchKernelGGL((sum_parts_kernel<T, DUAL>), dim3((unsigned)((pieces + 255) / 256)), dim3(256),
                      0, s, g);
   return hipGetLastError();
@@ -732,12 +815,13 @@ hipError_t run_gemm_shape(GemmOp g, hipStream_t s) {
 template <typename T, bool AC, bool BC, bool DUAL>
 hipError_t run_gemm(GemmOp g, const Shape &sh, void *part, hipStream_t s) {
   g.parts = sh.parts;
+  if (g.halves < 1) g.halves = 1;
   g.part = (float *)part;
   g.ldp = (g.e.N + 7) / 8 * 8;
   if (sh.mi == 4 && sh.ni == 4) return run_gemm_shape<T, 4, 4, AC, BC, DUAL>(g, s);
   if (sh.mi == 4) return run_gemm_shape<T, 4, 2, AC, BC, DUAL>(g, s);
   if (sh.mi == 2) return run_gemm_shape<T, 2, 2, AC, BC, DUAL>(g, s);
-  return run_gemm_shape<T, 1, 1, AC, BC, DUAL>(g, s);
+  return run_gemm_shape<T, 1, DUAL ? 2 : 1, AC, BC, DUAL>(g, s);
 }
 
 template <typename T>
@@ -800,7 +884,7 @@ hipError_t linear_forward(const moe_linear_config &c, const moe_linear_weights &
   e.vec = !odd_rows(N, c.ld_y, c.dtype) && (!residual || !odd_rows(N, c.ld_residual, c.dtype)) &&
           N % 8 == 0 && aligned16(y) && aligned16(z) && aligned16(z_up) && aligned16(residual) &&
           aligned16(w.bias) && aligned16(w.bias_up);
-  const Shape sh = shape_of(M, dual ? 2 * N : N, g.kdim, 1, c.dtype);
+  const Shape sh = shape_of(M, dual ? 2 * N : N, g.kdim, 1, c.dtype, dual);
   return dual ? run_gemm<T, false, false, true>(g, sh, ws + L.part, s)
               : run_gemm<T, false, false, false>(g, sh, ws + L.part, s);
 }
@@ -840,8 +924,8 @@ hipError_t linear_backward(const moe_linear_config &c, const moe_linear_weights 
     if ((err = hipGetLastError()) != hipSuccess) return err;
     if (want_db) {
       const int d = dual ? 2 : 1;
-      hipLaunchKernelGGL((bias_sum_kernel<T>), dim3((unsigned)((N * d + 255) / 256)), dim3(256), 0,
-                         s, (const float *)(ws + L.colsum), (int)N, a.parts, d, (T *)gr.dbias,
+      hipLaunchKernelGGL((bias_sum_kernel<T>), dim3((unsigned)((N + 31) / 32), (unsigned)d),
+                         dim3(256), 0, s, (const float *)(ws + L.colsum), (int)N, a.parts, d, (T *)gr.dbias,
                          (T *)gr.dbias_up);
       if ((err = hipGetLastError()) != hipSuccess) return err;
     }
@@ -864,7 +948,7 @@ hipError_t linear_backward(const moe_linear_config &c, const moe_linear_weights 
     g.M = M;
     g.e.y = gr.dx; g.e.ld_y = c.ld_x; g.e.N = (int)K; g.e.act = MOE_ACTIVATION_NONE;
     g.e.vec = !odd_rows(K, c.ld_x, c.dtype) && K % 8 == 0 && aligned16(gr.dx);
-    const Shape sh = shape_of(M, K, g.kdim, g.segments, c.dtype);
+    const Shape sh = shape_of(M, K, g.kdim, g.segments, c.dtype, false);
     if ((err = run_gemm<T, false, true, false>(g, sh, ws + L.part, s)) != hipSuccess) return err;
   }
   if (want_dw) {
@@ -873,19 +957,20 @@ hipError_t linear_backward(const moe_linear_config &c, const moe_linear_weights 
       if ((err = pad_rows<T>(x, c.ld_x, M, (int)K, ws + L.x, Kp, s)) != hipSuccess) return err;
       mx = {ws + L.x, Kp, M, Kp};
     }
-    for (int i = 0; i < (dual ? 2 : 1); ++i) {
-      void *out = i ? gr.dw_up : gr.dw;
-      if (!out) continue;
-      GemmOp g = {};
-      g.a[0] = i ? mu : mz; g.b[0] = mx;
-      g.kdim[0] = M;
-      g.segments = 1;
-      g.M = N;
-      g.e.y = out; g.e.ld_y = K; g.e.N = (int)K; g.e.act = MOE_ACTIVATION_NONE;
-      g.e.vec = K % 8 == 0 && aligned16(out);
-      const Shape sh = shape_of(N, K, g.kdim, 1, c.dtype);
-      if ((err = run_gemm<T, true, true, false>(g, sh, ws + L.part, s)) != hipSuccess) return err;
-    }
+    // both products of swiglu in one launch, or the one that is wanted
+    const bool both = gr.dw && gr.dw_up;
+    GemmOp g = {};
+    g.a[0] = gr.dw ? mz : mu; g.b[0] = mx;
+    g.a_up = mu; g.y_up = gr.dw_up;
+    g.halves = both ? 2 : 1;
+    g.kdim[0] = M;
+    g.segments = 1;
+    g.M = N;
+    g.e.y = gr.dw ? gr.dw : gr.dw_up; g.e.ld_y = K; g.e.N = (int)K;
+    g.e.act = MOE_ACTIVATION_NONE;
+    g.e.vec = K % 8 == 0 && aligned16(gr.dw) && aligned16(gr.dw_up);
+    const Shape sh = shape_of(g.halves * N, K, g.kdim, 1, c.dtype, false);
+    if ((err = run_gemm<T, true, true, false>(g, sh, ws + L.part, s)) != hipSuccess) return err;
   }
   return hipSuccess;
 }
@@ -911,7 +996,7 @@ LinearSpace linear_space(const moe_linear_config &c, bool backward, bool dx, boo
   size_t part = 0;
   auto need = [&](int64_t rows, int64_t cols, int64_t k, int segments, bool two) {
     const int64_t kd[2] = {k, k};
-    const Shape s = shape_of(rows, two ? 2 * cols : cols, kd, segments, c.dtype);
+    const Shape s = shape_of(rows, two ? 2 * cols : cols, kd, segments, c.dtype, two);
     const size_t b = part_bytes(rows, cols, two, s);
     if (b > part) part = b;
   };
@@ -921,7 +1006,10 @@ LinearSpace linear_space(const moe_linear_config &c, bool backward, bool dx, boo
     l.du = take(dual && (dx || dw) ? es * M * Np : 0);
     l.colsum = take(db ? sizeof(float) * colsum_parts(M, (int)N) * (dual ? 2 : 1) * N : 0);
     if (dx) need(M, K, N, dual ? 2 : 1, false);
-    if (dw) need(N, K, M, 1, false);
+    if (dw) {
+      need(N, K, M, 1, false);
+      if (dual) need(2 * N, K, M, 1, false);
+    }
   } else {
     need(M, N, K, 1, dual);
   }
