@@ -83,6 +83,41 @@ __device__ __forceinline__ void store8(T *p, const float (&v)[8], int n, bool ve
   }
 }
 
+// Eight elements as they are stored, zeros past n, for later.
+template <typename T>
+struct Raw8 {
+  uint32_t w[2 * sizeof(T)];
+};
+template <typename T>
+__device__ __forceinline__ void fetch8(Raw8<T> &r, const T *p, int n, bool vec) {
+  if (vec && n >= 8) {
+#pragma unroll
+    for (int h = 0; h < (int)sizeof(T) / 2; ++h) {
+      const u32x4 v = ((const u32x4 *)p)[h];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r.w[4 * h + j] = v[j];
+    }
+  } else if constexpr (sizeof(T) == 2) {
+    const uint16_t *q = (const uint16_t *)p;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      r.w[j] = (2 * j < n ? q[2 * j] : 0u) | (2 * j + 1 < n ? (uint32_t)q[2 * j + 1] << 16 : 0u);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r.w[j] = j < n ? ((const uint32_t *)p)[j] : 0u;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void widen8(float (&v)[8], const Raw8<T> &r) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if constexpr (sizeof(T) == 2)
+      v[j] = __uint_as_float(j & 1 ? r.w[j / 2] & 0xffff0000u : r.w[j / 2] << 16);
+    else
+      v[j] = __uint_as_float(r.w[j]);
+  }
+}
+
 // fp32 layers take the accurate exponential; before a rounding to bf16 the
 // hardware one (relative error below 2^-20 at the arguments that matter) does.
 template <typename T>
@@ -522,85 +557,86 @@ __device__ __forceinline__ void gemm_tile(const GemmOp &g) {
 #pragma unroll
   for (int p = 0; p < NS - 1; ++p)
     if (st + p < nst) stage(p);
-  __builtin_amdgcn_s_waitcnt(0);
-  __syncthreads();                             // every wave is done with the ring
-
   // Epilogue.  32 rows of the wave's quarter at a time go through the wave's own
   // part of LDS (no barrier), so that a lane then has eight consecutive columns
-  // of a row and 16 or 8 lanes a whole line; the residual of the next pieces is
-  // on its way while these are finished.
+  // of a row and 16 or 8 lanes a whole line.  bf16: the whole tile's residual is
+  // asked for at once, into the registers that the operands have left (in 32-row
+  // pieces a read's latency bounded it: 161 instead of 140 us at 4096x2048->7168).
   constexpr int NJ = DUAL ? NI / 2 : NI;       // output column blocks of the wave
   constexpr int PC = NJ * 4;                   // pieces of 8 columns per row
   constexpr int PPI = 32 * PC / 64;            // pieces per lane and 32 rows
-  constexpr int CH = PPI < 4 ? PPI : 4;        // of them at a time
   constexpr int LD = NI * 32 + 4;              // floats per LDS row (padded)
+  constexpr bool RES = !AC && !BC;             // gradients have no residual
+  constexpr int AHEAD = RES && ES == 2 ? MI : 1;
   static_assert(32 * LD * 4 <= SLOT, "a wave's rows fit a ring slot");
   float *stage_f = (float *)(wave == 0 ? L0 : wave == 1 ? L1 : wave == 2 ? L2 : L3);
   const bool plain = g.parts > 1;
-  auto place = [&](int c, int q, int64_t *m, int64_t *n, int *r, int *pc) {
-    const int idx = (c % (PPI / CH) * CH + q) * 64 + lane;
-    *r = idx / PC;
-    *pc = idx - *r * PC;
-    *m = m0 + (wm * MI + c / (PPI / CH)) * 32 + *r;
-    *n = n0 + (int64_t)wn * NJ * 32 + *pc * 8;
+  // piece q of the wave's rows 32 i ..: row and piece in the block, place in the output
+  struct Place {
+    int r, pc;
+    int64_t m;
+    int n;
   };
-  float res[CH][8], ahead[CH][8];
-  auto fetch = [&](int c) {
+  auto place = [&](int i, int q) {
+    const int idx = q * 64 + lane;
+    const int r = idx / PC, pc = idx - r * PC;
+    return Place{r, pc, m0 + (wm * MI + i) * 32 + r, (int)n0 + wn * NJ * 32 + pc * 8};
+  };
+  Raw8<T> res[PPI], ahead[AHEAD][PPI];
+  auto fetch = [&](int i, Raw8<T> (&to)[PPI]) {
 #pragma unroll
-    for (int q = 0; q < CH; ++q) {
-      int64_t m, n;
-      int r, pc;
-      place(c, q, &m, &n, &r, &pc);
-      if (m < g.M && n < g.e.N)
-        load8<T>(ahead[q], (const T *)g.e.residual + m * g.e.ld_res + n, (int)(g.e.N - n),
-                 g.e.vec != 0);
+    for (int q = 0; q < PPI; ++q) {
+      const Place o = place(i, q);
+      if (o.m < g.M && o.n < g.e.N)
+        fetch8<T>(to[q], (const T *)g.e.residual + o.m * g.e.ld_res + o.n, g.e.N - o.n,
+                  g.e.vec != 0);
     }
   };
-  const bool has_res = !BC && g.e.residual && !plain;
-  if (has_res) fetch(0);
-  for (int c = 0; c < MI * (PPI / CH); ++c) {
-    if (c % (PPI / CH) == 0) {
-      const int ci = c / (PPI / CH);
+  const bool has_res = RES && g.e.residual && !plain;
+  __builtin_amdgcn_s_waitcnt(0);
+  if (AHEAD > 1 && has_res) {
 #pragma unroll
-      for (int i = 0; i < MI; ++i)
-        if (i == ci) {                         // uniform; the accumulators keep their registers
+    for (int i = 0; i < AHEAD; ++i) fetch(i, ahead[i]);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_barrier();                // every wave is done with the ring
+  __builtin_amdgcn_sched_barrier(0);
+  for (int ci = 0; ci < MI; ++ci) {
+    if (AHEAD == 1 && has_res) fetch(ci, res);
 #pragma unroll
-          for (int j = 0; j < NI; ++j)
+    for (int i = 0; i < MI; ++i)
+      if (i == ci) {                           // uniform; the accumulators keep their registers
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              *(f32x4 *)(stage_f + (lane & 31) * LD + j * 32 + 8 * e + 4 * (lane >> 5)) =
-                  f32x4{acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2],
-                        acc[i][j][4 * e + 3]};
-        }
-      __builtin_amdgcn_wave_barrier();
-    }
-    if (has_res) {
+        for (int j = 0; j < NI; ++j)
 #pragma unroll
-      for (int q = 0; q < CH; ++q)
+          for (int e = 0; e < 4; ++e)
+            *(f32x4 *)(stage_f + (lane & 31) * LD + j * 32 + 8 * e + 4 * (lane >> 5)) =
+                f32x4{acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2],
+                      acc[i][j][4 * e + 3]};
+        if constexpr (AHEAD > 1)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) res[q][j] = ahead[q][j];
-      if (c + 1 < MI * (PPI / CH)) fetch(c + 1);
-    }
+          for (int q = 0; q < PPI; ++q) res[q] = ahead[i][q];
+      }
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int q = 0; q < CH; ++q) {
-      int64_t m, n;
-      int r, pc;
-      place(c, q, &m, &n, &r, &pc);
-      float v[8], u[8];
-      load8<float>(v, stage_f + r * LD + pc * 8, 8, true);
-      if constexpr (DUAL) load8<float>(u, stage_f + r * LD + NJ * 32 + pc * 8, 8, true);
-      if (m >= g.M || n >= g.e.N) continue;
+    for (int q = 0; q < PPI; ++q) {
+      const Place o = place(ci, q);
+      float v[8], u[8], rs[8];
+      load8<float>(v, stage_f + o.r * LD + o.pc * 8, 8, true);
+      if constexpr (DUAL) load8<float>(u, stage_f + o.r * LD + NJ * 32 + o.pc * 8, 8, true);
+      if (o.m >= g.M || o.n >= g.e.N) continue;
       if (plain) {
         // rows of ldp, a multiple of 8: whole pieces
-        float *o =
-            g.part + (((int64_t)part * (DUAL ? 2 : g.halves) + half) * g.M + m) * g.ldp + n;
-        store8<float>(o, v, 8, true);
-        if constexpr (DUAL) store8<float>(o + g.M * g.ldp, u, 8, true);
-      } else if constexpr (BC) {               // a gradient: no epilogue
-        store8<T>((T *)(half ? g.y_up : g.e.y) + m * g.e.ld_y + n, v, (int)(g.e.N - n),
+        float *to =
+            g.part + (((int64_t)part * (DUAL ? 2 : g.halves) + half) * g.M + o.m) * g.ldp + o.n;
+        store8<float>(to, v, 8, true);
+        if constexpr (DUAL) store8<float>(to + g.M * g.ldp, u, 8, true);
+      } else if constexpr (!RES) {             // a gradient: no epilogue
+        store8<T>((T *)(half ? g.y_up : g.e.y) + o.m * g.e.ld_y + o.n, v, g.e.N - o.n,
                   g.e.vec != 0);
       } else {
-        finish8<T, DUAL>(g.e, v, u, res[q], m, (int)n);
+        if (has_res) widen8<T>(rs, res[q]);
+        finish8<T, DUAL>(g.e, v, u, rs, o.m, o.n);
       }
     }
     __builtin_amdgcn_wave_barrier();
@@ -754,27 +790,38 @@ __global__ __launch_bounds__(256) void bias_sum_kernel(const float *sums, int N,
 
 // ---------------------------------------------------------------------------
 // Tile shape and parts of a product of `rows` x `cols` (cols of both matrices
-// for swiglu) over `stages` stages.
+// for swiglu) over `stages` stages: the one with the least estimated time.
+//
+// One workgroup a CU and round; a round costs its stages and a fixed part (first
+// copies, epilogue).  The constants are microseconds measured over products of
+// 1024..8192 a side, one shape forced at a time (bf16 4096x4096 over K = 1024,
+// 2048, 4096: 256x256 tiles 44, 69, 121 us, 256x128 52, 85, 163, 128x128 46, 85,
+// 168, 64x64 67, 134, 271).  A round that fills part of the GPU runs at a higher
+// clock (4096x2048 over K = 4096 with 128 tiles of 256x256: 105 us).
 struct Shape { int mi, ni, parts; };
 
-// Per-CU cost of a stage in cycles, from the MFMA cycles of the tile (each
-// 32 x 32 block and step 32 cycles on one of four SIMDs) and the share of them
-// the shapes reach on long contractions.
-Shape pick_shape(int64_t rows, int64_t cols, int64_t stages, bool f32, bool dual) {
-  struct { int mi, ni; double eff; } shapes[] = {
-      {4, 4, 0.5}, {4, 2, 0.45}, {2, 2, 0.35}, {1, dual ? 2 : 1, 0.2}};
+Shape pick_shape(int64_t rows, int64_t cols, int64_t stages, bool f32, bool dual, bool col) {
+  // stage of row operands alone, with a column operand, of fp32; fixed part
+  struct { int mi, ni; double row, col, f32, fixed; } shapes[] = {
+      {4, 4, 0.80, 0.82, 3.8, 14.0},
+      {4, 2, 0.51, 0.68, 1.9, 8.0},
+      {2, 2, 0.28, 0.31, 0.94, 3.5},
+      {1, dual ? 2 : 1, dual ? 0.186 : 0.127, 0.15, dual ? 0.5 : 0.254, 1.0}};
   Shape best = {1, 1, 1};
   double best_t = 1e300;
   for (const auto &sh : shapes) {
     const int64_t tiles = ((rows + 64 * sh.mi - 1) / (64 * sh.mi)) *
                           ((cols + 64 * sh.ni - 1) / (64 * sh.ni));
-    const double stage = 64.0 * sh.mi * sh.ni * (f32 ? 8 : 1) / sh.eff;
+    const double stage = f32 ? sh.f32 : col ? sh.col : sh.row;
     for (int parts = 1; parts <= 16; parts *= 2) {
       if (parts > 1 && (stages < 16 * parts || tiles * parts > 1024)) break;
-      const double rounds = (double)((tiles * parts + 255) / 256);
-      double t = rounds * ((double)((stages + parts - 1) / parts) * stage + 3000.0);
-      // partial sums: written, read and finished at about 1500 bytes a cycle
-      if (parts > 1) t += 8000.0 + (double)rows * cols * 8.0 * parts / 1500.0;
+      const int64_t items = tiles * parts, full = items / 256;
+      const double last = (double)(items - full * 256) / 256;
+      const double work = (double)((stages + parts - 1) / parts) * stage;
+      double t = full * (work + sh.fixed);
+      if (last > 0) t += work * (0.7 + 0.3 * last) + sh.fixed;
+      // partial sums: a launch, and written and read at 8 TB/s in all
+      if (parts > 1) t += 5.0 + (double)rows * cols * parts * 1e-6;
       if (t < best_t) {
         best_t = t;
         best = {sh.mi, sh.ni, parts};
@@ -785,11 +832,11 @@ Shape pick_shape(int64_t rows, int64_t cols, int64_t stages, bool f32, bool dual
 }
 
 Shape shape_of(int64_t rows, int64_t cols, const int64_t *kdim, int segments, int dtype,
-               bool dual) {
+               bool dual, bool col) {
   const int64_t kb = dtype == MOE_DTYPE_F32 ? 16 : 32;
   int64_t st = 0;
   for (int i = 0; i < segments; ++i) st += (kdim[i] + kb - 1) / kb;
-  return pick_shape(rows, cols, st, dtype == MOE_DTYPE_F32, dual);
+  return pick_shape(rows, cols, st, dtype == MOE_DTYPE_F32, dual, col);
 }
 
 size_t part_bytes(int64_t rows, int64_t cols, bool dual, const Shape &s) {
@@ -884,7 +931,7 @@ hipError_t linear_forward(const moe_linear_config &c, const moe_linear_weights &
   e.vec = !odd_rows(N, c.ld_y, c.dtype) && (!residual || !odd_rows(N, c.ld_residual, c.dtype)) &&
           N % 8 == 0 && aligned16(y) && aligned16(z) && aligned16(z_up) && aligned16(residual) &&
           aligned16(w.bias) && aligned16(w.bias_up);
-  const Shape sh = shape_of(M, dual ? 2 * N : N, g.kdim, 1, c.dtype, dual);
+  const Shape sh = shape_of(M, dual ? 2 * N : N, g.kdim, 1, c.dtype, dual, false);
   return dual ? run_gemm<T, false, false, true>(g, sh, ws + L.part, s)
               : run_gemm<T, false, false, false>(g, sh, ws + L.part, s);
 }
@@ -948,7 +995,7 @@ hipError_t linear_backward(const moe_linear_config &c, const moe_linear_weights 
     g.M = M;
     g.e.y = gr.dx; g.e.ld_y = c.ld_x; g.e.N = (int)K; g.e.act = MOE_ACTIVATION_NONE;
     g.e.vec = !odd_rows(K, c.ld_x, c.dtype) && K % 8 == 0 && aligned16(gr.dx);
-    const Shape sh = shape_of(M, K, g.kdim, g.segments, c.dtype, false);
+    const Shape sh = shape_of(M, K, g.kdim, g.segments, c.dtype, false, true);
     if ((err = run_gemm<T, false, true, false>(g, sh, ws + L.part, s)) != hipSuccess) return err;
   }
   if (want_dw) {
@@ -969,7 +1016,7 @@ hipError_t linear_backward(const moe_linear_config &c, const moe_linear_weights 
     g.e.y = gr.dw ? gr.dw : gr.dw_up; g.e.ld_y = K; g.e.N = (int)K;
     g.e.act = MOE_ACTIVATION_NONE;
     g.e.vec = K % 8 == 0 && aligned16(gr.dw) && aligned16(gr.dw_up);
-    const Shape sh = shape_of(g.halves * N, K, g.kdim, 1, c.dtype, false);
+    const Shape sh = shape_of(g.halves * N, K, g.kdim, 1, c.dtype, false, true);
     if ((err = run_gemm<T, true, true, false>(g, sh, ws + L.part, s)) != hipSuccess) return err;
   }
   return hipSuccess;
@@ -996,7 +1043,7 @@ LinearSpace linear_space(const moe_linear_config &c, bool backward, bool dx, boo
   size_t part = 0;
   auto need = [&](int64_t rows, int64_t cols, int64_t k, int segments, bool two) {
     const int64_t kd[2] = {k, k};
-    const Shape s = shape_of(rows, two ? 2 * cols : cols, kd, segments, c.dtype, two);
+    const Shape s = shape_of(rows, two ? 2 * cols : cols, kd, segments, c.dtype, two, backward);
     const size_t b = part_bytes(rows, cols, two, s);
     if (b > part) part = b;
   };
