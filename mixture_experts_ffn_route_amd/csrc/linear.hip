@@ -294,11 +294,17 @@ struct Operand {
   static __device__ __forceinline__ int first_k(int wave, int lane) {
     return ((lane & 3) ^ ((2 * wave + (lane >> 5)) & 3)) * (16 / ES);
   }
-  // One lane's fragment of the 32 rows (columns of D) from `base`, step s.
-  static __device__ __forceinline__ u32x4 fragment(const uint8_t *lds, int base, int s, int lane) {
+  // One lane's fragment of the 32 rows (columns of D) from `base`, step s, of
+  // the stage at `lds` + `at`.  Each address is the LDS object and one offset: the
+  // compiler loses track of the object over longer chains, and then lets a read
+  // wait for all copies in flight (dx and dW with 128x128 tiles took up to twice
+  // as long).
+  static __device__ __forceinline__ u32x4 fragment(const uint8_t *lds, uint32_t at, int base, int s,
+                                                   int lane) {
     if constexpr (!COL) {
       const int r = base + (lane & 31);
-      return *(const u32x4 *)(lds + r * 64 + ((2 * s + (lane >> 5)) ^ ((r >> 3) & 3)) * 16);
+      const uint32_t o = at + r * 64 + ((2 * s + (lane >> 5)) ^ ((r >> 3) & 3)) * 16;
+      return *(const u32x4 *)(lds + o);
     } else if constexpr (ES == 2) {
       const int col = base + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
       const int k0 = 16 * s + 8 * (lane >> 5) + ((lane & 15) >> 2);
@@ -306,8 +312,8 @@ struct Operand {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int k = k0 + 4 * i;
-        v[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (MOE_LDS s16x4 *)(lds + k * RB + ((col >> 3) ^ swz(k)) * 16 + (col & 7) * 2));
+        const uint32_t o = at + k * RB + ((col >> 3) ^ swz(k)) * 16 + (col & 7) * 2;
+        v[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4 *)(lds + o));
       }
       const u32x2 a = __builtin_bit_cast(u32x2, v[0]), b = __builtin_bit_cast(u32x2, v[1]);
       return u32x4{a[0], a[1], b[0], b[1]};
@@ -315,8 +321,10 @@ struct Operand {
       const int col = base + (lane & 31);
       u32x4 v;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        v[j] = *(const uint32_t *)(lds + (8 * s + 4 * (lane >> 5) + j) * RB + col * 4);
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t o = at + (8 * s + 4 * (lane >> 5) + j) * RB + col * 4;
+        v[j] = *(const uint32_t *)(lds + o);
+      }
       return v;
     }
   }
@@ -504,11 +512,10 @@ __device__ __forceinline__ void gemm_tile(const GemmOp &g) {
   };
   u32x4 fa[2][MI], fb[2][NI];
   auto read = [&](int buf, int slot, int s) {
-    const uint8_t *A = ring[slot], *B = ring[slot] + UA * 1024;
 #pragma unroll
-    for (int j = 0; j < NI; ++j) fb[buf][j] = OB::fragment(B, col_block(j) * 32, s, lane);
+    for (int j = 0; j < NI; ++j) fb[buf][j] = OB::fragment(ring[slot], UA * 1024, col_block(j) * 32, s, lane);
 #pragma unroll
-    for (int i = 0; i < MI; ++i) fa[buf][i] = OA::fragment(A, (wm * MI + i) * 32, s, lane);
+    for (int i = 0; i < MI; ++i) fa[buf][i] = OA::fragment(ring[slot], 0, (wm * MI + i) * 32, s, lane);
   };
   auto multiply = [&](int buf) {
 #pragma unroll
@@ -795,24 +802,24 @@ __global__ __launch_bounds__(256) void bias_sum_kernel(const float *sums, int N,
 // One workgroup a CU and round; a round costs its stages and a fixed part (first
 // copies, epilogue).  The constants are microseconds measured over products of
 // 1024..8192 a side, one shape forced at a time (bf16 4096x4096 over K = 1024,
-// 2048, 4096: 256x256 tiles 44, 69, 121 us, 256x128 52, 85, 163, 128x128 46, 85,
-// 168, 64x64 67, 134, 271).  A round that fills part of the GPU runs at a higher
-// clock (4096x2048 over K = 4096 with 128 tiles of 256x256: 105 us).
+// 2048, 4096: 256x256 tiles 44, 69, 121 us, 256x128 52, 85, 150, 128x128 46, 85,
+// 165, 64x64 67, 134, 271; dx and dW of that size within 10% of these).  A round
+// that fills part of the GPU runs at a higher clock (4096x2048 over K = 4096 with
+// 128 tiles of 256x256: 105 us).
 struct Shape { int mi, ni, parts; };
 
-Shape pick_shape(int64_t rows, int64_t cols, int64_t stages, bool f32, bool dual, bool col) {
-  // stage of row operands alone, with a column operand, of fp32; fixed part
-  struct { int mi, ni; double row, col, f32, fixed; } shapes[] = {
-      {4, 4, 0.80, 0.82, 3.8, 14.0},
-      {4, 2, 0.51, 0.68, 1.9, 8.0},
-      {2, 2, 0.28, 0.31, 0.94, 3.5},
-      {1, dual ? 2 : 1, dual ? 0.186 : 0.127, 0.15, dual ? 0.5 : 0.254, 1.0}};
+Shape pick_shape(int64_t rows, int64_t cols, int64_t stages, bool f32, bool dual) {
+  struct { int mi, ni; double stage, stage_f32, fixed; } shapes[] = {
+      {4, 4, 0.80, 3.8, 14.0},
+      {4, 2, 0.52, 1.9, 8.0},
+      {2, 2, 0.27, 0.94, 3.5},
+      {1, dual ? 2 : 1, dual ? 0.186 : 0.127, dual ? 0.5 : 0.254, 1.0}};
   Shape best = {1, 1, 1};
   double best_t = 1e300;
   for (const auto &sh : shapes) {
     const int64_t tiles = ((rows + 64 * sh.mi - 1) / (64 * sh.mi)) *
                           ((cols + 64 * sh.ni - 1) / (64 * sh.ni));
-    const double stage = f32 ? sh.f32 : col ? sh.col : sh.row;
+    const double stage = f32 ? sh.stage_f32 : sh.stage;
     for (int parts = 1; parts <= 16; parts *= 2) {
       if (parts > 1 && (stages < 16 * parts || tiles * parts > 1024)) break;
       const int64_t items = tiles * parts, full = items / 256;
@@ -832,11 +839,11 @@ Shape pick_shape(int64_t rows, int64_t cols, int64_t stages, bool f32, bool dual
 }
 
 Shape shape_of(int64_t rows, int64_t cols, const int64_t *kdim, int segments, int dtype,
-               bool dual, bool col) {
+               bool dual) {
   const int64_t kb = dtype == MOE_DTYPE_F32 ? 16 : 32;
   int64_t st = 0;
   for (int i = 0; i < segments; ++i) st += (kdim[i] + kb - 1) / kb;
-  return pick_shape(rows, cols, st, dtype == MOE_DTYPE_F32, dual, col);
+  return pick_shape(rows, cols, st, dtype == MOE_DTYPE_F32, dual);
 }
 
 size_t part_bytes(int64_t rows, int64_t cols, bool dual, const Shape &s) {
@@ -931,7 +938,7 @@ hipError_t linear_forward(const moe_linear_config &c, const moe_linear_weights &
   e.vec = !odd_rows(N, c.ld_y, c.dtype) && (!residual || !odd_rows(N, c.ld_residual, c.dtype)) &&
           N % 8 == 0 && aligned16(y) && aligned16(z) && aligned16(z_up) && aligned16(residual) &&
           aligned16(w.bias) && aligned16(w.bias_up);
-  const Shape sh = shape_of(M, dual ? 2 * N : N, g.kdim, 1, c.dtype, dual, false);
+  const Shape sh = shape_of(M, dual ? 2 * N : N, g.kdim, 1, c.dtype, dual);
   return dual ? run_gemm<T, false, false, true>(g, sh, ws + L.part, s)
               : run_gemm<T, false, false, false>(g, sh, ws + L.part, s);
 }
@@ -995,7 +1002,7 @@ hipError_t linear_backward(const moe_linear_config &c, const moe_linear_weights 
     g.M = M;
     g.e.y = gr.dx; g.e.ld_y = c.ld_x; g.e.N = (int)K; g.e.act = MOE_ACTIVATION_NONE;
     g.e.vec = !odd_rows(K, c.ld_x, c.dtype) && K % 8 == 0 && aligned16(gr.dx);
-    const Shape sh = shape_of(M, K, g.kdim, g.segments, c.dtype, false, true);
+    const Shape sh = shape_of(M, K, g.kdim, g.segments, c.dtype, false);
     if ((err = run_gemm<T, false, true, false>(g, sh, ws + L.part, s)) != hipSuccess) return err;
   }
   if (want_dw) {
@@ -1016,7 +1023,7 @@ hipError_t linear_backward(const moe_linear_config &c, const moe_linear_weights 
     g.e.y = gr.dw ? gr.dw : gr.dw_up; g.e.ld_y = K; g.e.N = (int)K;
     g.e.act = MOE_ACTIVATION_NONE;
     g.e.vec = K % 8 == 0 && aligned16(gr.dw) && aligned16(gr.dw_up);
-    const Shape sh = shape_of(g.halves * N, K, g.kdim, 1, c.dtype, false, true);
+    const Shape sh = shape_of(g.halves * N, K, g.kdim, 1, c.dtype, false);
     if ((err = run_gemm<T, true, true, false>(g, sh, ws + L.part, s)) != hipSuccess) return err;
   }
   return hipSuccess;
@@ -1043,7 +1050,7 @@ LinearSpace linear_space(const moe_linear_config &c, bool backward, bool dx, boo
   size_t part = 0;
   auto need = [&](int64_t rows, int64_t cols, int64_t k, int segments, bool two) {
     const int64_t kd[2] = {k, k};
-    const Shape s = shape_of(rows, two ? 2 * cols : cols, kd, segments, c.dtype, two, backward);
+    const Shape s = shape_of(rows, two ? 2 * cols : cols, kd, segments, c.dtype, two);
     const size_t b = part_bytes(rows, cols, two, s);
     if (b > part) part = b;
   };
