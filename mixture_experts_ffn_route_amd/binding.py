@@ -394,32 +394,48 @@ _LINEAR_DTYPE = {"f32": torch.float32, "bf16": torch.bfloat16}
 
 
 def _linear_config(cfg: LinearConfig, x, y, residual=None) -> MoeLinearConfigC:
-    """cfg with the row strides of x, y (or dy) and the residual."""
+    """cfg with the row strides of x, y (or dy) and the residual.  One row has
+    none to speak of, whatever its tensor says."""
     return MoeLinearConfigC(
         cfg.rows, cfg.in_dim, cfg.out_dim, DTYPE[cfg.dtype], ACTIVATION[cfg.activation], cfg.limit,
-        0 if x is None else x.stride(0), 0 if y is None else y.stride(0),
-        0 if residual is None else residual.stride(0))
+        *(0 if t is None or cfg.rows < 2 else t.stride(0) for t in (x, y, residual)))
 
 
 def _linear_check(cfg: LinearConfig, where, matrices, contiguous):
-    """Types, shapes and strides of a call's tensors (None: not given): the
-    library sees addresses only."""
-    dt = _LINEAR_DTYPE[cfg.dtype]
-    for name, t, shape in matrices + contiguous:
+    """Types, shapes, strides and devices of a call's tensors (None: not given):
+    the library sees addresses only."""
+    dt, device = _LINEAR_DTYPE[cfg.dtype], None
+    for name, t, shape in matrices:
         if t is None:
             continue
-        if t.dtype != dt or tuple(t.shape) != shape:
+        if t.dtype is not dt or t.shape != shape:
             raise ValueError(f"{where}: {name} is {tuple(t.shape)} {t.dtype}, "
                              f"expected {shape} {dt}")
-        if t.numel() and t.stride(-1) != 1:
-            raise ValueError(f"{where}: {name}'s rows are not contiguous")
-    for name, t, _ in contiguous:
-        if t is not None and not t.is_contiguous():
+        if not t.is_contiguous() and t.numel() and (
+                t.stride(1) != 1 and shape[1] > 1 or t.stride(0) < shape[1] and shape[0] > 1):
+            raise ValueError(f"{where}: {name}'s rows are not contiguous or overlap")
+        device = device or t.device
+        if t.device != device:
+            raise ValueError(f"{where}: {name} is on {t.device}, others on {device}")
+    for name, t, shape in contiguous:
+        if t is None:
+            continue
+        if t.dtype is not dt or t.shape != shape:
+            raise ValueError(f"{where}: {name} is {tuple(t.shape)} {t.dtype}, "
+                             f"expected {shape} {dt}")
+        if not t.is_contiguous():
             raise ValueError(f"{where}: {name} is not contiguous")
+        if t.device != device:
+            raise ValueError(f"{where}: {name} is on {t.device}, others on {device}")
+    if cfg.rows and (device is None or device.type != "cuda"):
+        raise ValueError(f"{where}: tensors on {device}, expected a GPU")
 
 
 def _raw(t):
     return None if t is None else t.data_ptr()
+
+
+MOE_LINEAR_MAX_LD = 1 << 20
 
 
 def moe_linear_workspace_size(cfg: LinearConfig, backward=False, ld_x=0, ld_y=0,
@@ -566,8 +582,16 @@ def few_views(cfg: MoEConfig, T: int, ws):
 
 def alloc_linear_workspace(cfg: LinearConfig, backward=False, device="cuda", **strides):
     """Workspace of moe_linear, or with `backward` one that serves both it and
-    moe_linear_backward; strides: ld_x, ld_y, ld_residual where not contiguous."""
-    sizes = [moe_linear_workspace_size(cfg, b, **strides) for b in {False, bool(backward)}]
+    moe_linear_backward.  strides: ld_x, ld_y, ld_residual; without them it is
+    large enough for tensors of any strides."""
+    ways = [strides]
+    if not strides:
+        # what a call needs goes by which of its row strides are odd
+        ways = [{"ld_x": cfg.in_dim + i, "ld_y": cfg.out_dim + j} for i in (0, 1) for j in (0, 1)
+                if max(cfg.in_dim + i, cfg.out_dim + j) <= MOE_LINEAR_MAX_LD]
+    sizes = [moe_linear_workspace_size(cfg, k, **w) for k in {False, bool(backward)} for w in ways]
+    if not sizes:
+        raise MoEError(MOE_ERR_UNSUPPORTED, "moe_linear_workspace_size")
     if 0 in sizes:
         raise MoEError(MOE_ERR_INVALID_ARG, "moe_linear_workspace_size")
     return torch.empty(max(sizes), dtype=torch.uint8, device=device)

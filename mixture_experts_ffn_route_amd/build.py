@@ -19,7 +19,7 @@ LIB_NAME = "libmoe_mi355x.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 
 SOURCES = ["moe_api.cpp", "route.hip", "permute.hip", "experts.hip", "pack.hip", "probe.hip", "experts_mx.hip", "redequant.hip", "dense.hip",
-           "few.hip", "linear.hip"]
+           "few.hip", "linear.hip", "linear_small.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 COMMON_FLAGS = [

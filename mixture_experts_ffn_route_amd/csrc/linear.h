@@ -23,6 +23,28 @@ inline int64_t linear_pad(int64_t n, int dtype) {
   return (n + m - 1) / m * m;
 }
 
+// Epilogue, shared by all its kernels: eight consecutive columns of one row.
+struct Epilogue {
+  const void *bias, *bias_up, *residual;
+  void *y, *z, *z_up;
+  int64_t ld_y, ld_res, ld_z;
+  int N;                       // output columns
+  int act;                     // moe_activation
+  float limit;
+  int vec;                     // every row piece of 8 columns is 16-byte aligned
+};
+
+// Arguments of the kernels for few rows and small products (linear_small.hip).
+struct SmallArgs {
+  const void *x, *w, *w_up;
+  const void *dy, *z, *z_up;   // backward
+  void *dx, *dw, *dw_up, *db, *db_up;
+  int64_t M, K, ld_x, ld_dy, ld_dx;
+  int64_t dx_tiles;            // set at launch
+  Epilogue e;                  // backward: N, act, limit
+};
+constexpr int kFewRows = 16;   // rows that the few-row kernel takes
+
 LinearSpace linear_space(const moe_linear_config &c, bool backward, bool dx, bool dw, bool db);
 
 hipError_t launch_linear(const moe_linear_config &c, const moe_linear_weights &w, const void *x,
@@ -31,5 +53,11 @@ hipError_t launch_linear(const moe_linear_config &c, const moe_linear_weights &w
 hipError_t launch_linear_backward(const moe_linear_config &c, const moe_linear_weights &w,
                                   const void *x, const void *dy, const void *z, const void *z_up,
                                   const moe_linear_grads &g, char *ws, hipStream_t s);
+
+// rows <= kFewRows; rows of x and w whole 16-byte pieces at 16-byte strides.
+template <typename T> hipError_t launch_few_rows(const SmallArgs &a, bool dual, hipStream_t s);
+// Any widths and strides.
+template <typename T> hipError_t launch_small_forward(const SmallArgs &a, bool dual, hipStream_t s);
+template <typename T> hipError_t launch_small_backward(SmallArgs a, bool dual, hipStream_t s);
 
 }  // namespace moe

@@ -23,224 +23,10 @@
 // size.  Rows that are not whole 16-byte pieces (odd widths or strides) are
 // first copied to padded rows in the workspace.
 
-#include "gemm.h"
-#include "linear.h"
+#include "linear_device.h"
 
 namespace moe {
 namespace {
-
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
-typedef __amdgpu_buffer_rsrc_t rsrc_t;
-constexpr uint32_t kOut = 0x80000000u;         // an offset past every resource here
-
-// ---------------------------------------------------------------------------
-// Epilogue, shared by the GEMM, the sum of split products and the few-row
-// kernel: eight consecutive columns of one row.
-struct Epilogue {
-  const void *bias, *bias_up, *residual;
-  void *y, *z, *z_up;
-  int64_t ld_y, ld_res, ld_z;
-  int N;                       // output columns
-  int act;                     // moe_activation
-  float limit;
-  int vec;                     // every row piece of 8 columns is 16-byte aligned
-};
-
-template <typename T>
-__device__ __forceinline__ void load8(float (&v)[8], const T *p, int n, bool vec) {
-  if (vec && n >= 8) {
-    if constexpr (sizeof(T) == 2) {
-      const bf16x8 w = *(const bf16x8 *)p;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = (float)w[j];
-    } else {
-      const f32x4 a = *(const f32x4 *)p, b = *(const f32x4 *)(p + 4);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) { v[j] = a[j]; v[4 + j] = b[j]; }
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = j < n ? (float)p[j] : 0.f;
-  }
-}
-template <typename T>
-__device__ __forceinline__ void store8(T *p, const float (&v)[8], int n, bool vec) {
-  if (vec && n >= 8) {
-    if constexpr (sizeof(T) == 2) {
-      bf16x8 w;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = (bf16)v[j];
-      *(bf16x8 *)p = w;
-    } else {
-      *(f32x4 *)p = f32x4{v[0], v[1], v[2], v[3]};
-      *(f32x4 *)(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < n) p[j] = (T)v[j];
-  }
-}
-
-// Eight elements as they are stored, zeros past n, for later.
-template <typename T>
-struct Raw8 {
-  uint32_t w[2 * sizeof(T)];
-};
-template <typename T>
-__device__ __forceinline__ void fetch8(Raw8<T> &r, const T *p, int n, bool vec) {
-  if (vec && n >= 8) {
-#pragma unroll
-    for (int h = 0; h < (int)sizeof(T) / 2; ++h) {
-      const u32x4 v = ((const u32x4 *)p)[h];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) r.w[4 * h + j] = v[j];
-    }
-  } else if constexpr (sizeof(T) == 2) {
-    const uint16_t *q = (const uint16_t *)p;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      r.w[j] = (2 * j < n ? q[2 * j] : 0u) | (2 * j + 1 < n ? (uint32_t)q[2 * j + 1] << 16 : 0u);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) r.w[j] = j < n ? ((const uint32_t *)p)[j] : 0u;
-  }
-}
-template <typename T>
-__device__ __forceinline__ void widen8(float (&v)[8], const Raw8<T> &r) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if constexpr (sizeof(T) == 2)
-      v[j] = __uint_as_float(j & 1 ? r.w[j / 2] & 0xffff0000u : r.w[j / 2] << 16);
-    else
-      v[j] = __uint_as_float(r.w[j]);
-  }
-}
-
-// fp32 layers take the accurate exponential; before a rounding to bf16 the
-// hardware one (relative error below 2^-20 at the arguments that matter) does.
-template <typename T>
-__device__ __forceinline__ float exp_of(float v) {
-  return sizeof(T) == 4 ? expf(v) : __expf(v);
-}
-template <typename T>
-__device__ __forceinline__ float sigmoid(float v) {
-  return 1.f / (1.f + exp_of<T>(-v));
-}
-
-constexpr float kGeluA = 0.7978845608028654f;  // sqrt(2 / pi)
-constexpr float kGeluB = 0.044715f;
-
-template <typename T>
-__device__ __forceinline__ void activate8(float (&v)[8], int act) {
-  switch (act) {
-    case MOE_ACTIVATION_RELU:
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = v[j] > 0.f ? v[j] : (v[j] != v[j] ? v[j] : 0.f);
-      break;
-    case MOE_ACTIVATION_SILU:
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= sigmoid<T>(v[j]);
-      break;
-    case MOE_ACTIVATION_GELU:
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= 0.5f * erfcf(-v[j] * 0.7071067811865476f);
-      break;
-    case MOE_ACTIVATION_GELU_TANH:
-      // 0.5 z (1 + tanh q) = z sigmoid(2q), which keeps its relative accuracy
-      // for large negative z
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        v[j] *= sigmoid<T>(2.f * kGeluA * (v[j] + kGeluB * v[j] * v[j] * v[j]));
-      break;
-    default: break;
-  }
-}
-
-// act'(z).
-template <typename T>
-__device__ __forceinline__ float slope(float z, int act) {
-  switch (act) {
-    case MOE_ACTIVATION_RELU: return z > 0.f ? 1.f : (z != z ? z : 0.f);
-    case MOE_ACTIVATION_SILU: {
-      const float s = sigmoid<T>(z);
-      return s * (1.f + z * (1.f - s));
-    }
-    case MOE_ACTIVATION_GELU:
-      return 0.5f * erfcf(-z * 0.7071067811865476f) + z * 0.3989422804014327f * exp_of<T>(-0.5f * z * z);
-    case MOE_ACTIVATION_GELU_TANH: {
-      const float s = sigmoid<T>(2.f * kGeluA * (z + kGeluB * z * z * z));
-      return s + z * s * (1.f - s) * 2.f * kGeluA * (1.f + 3.f * kGeluB * z * z);
-    }
-    default: return 1.f;
-  }
-}
-
-// The value of v in storage type T, kept on v's side of the clamp: the saved
-// pre-activation decides in the backward pass whether the clamp was active,
-// so rounding must not carry it across (v > L has to stay above L, v <= L at
-// or below it).  One step of the type towards the right side otherwise.
-template <typename T>
-__device__ __forceinline__ float saved(float v, float L) {
-  const float r = (float)(T)v;
-  if (sizeof(T) == 4 || !(L > 0.f)) return r;
-  const float a = fabsf(v), b = fabsf(r);
-  if ((a > L) == (b > L) || v != v) return r;
-  const uint32_t bits = __float_as_uint(r);
-  return __uint_as_float(a > L ? bits + 0x10000u : bits - 0x10000u);
-}
-
-// y (and z) of eight columns n .. of row m from the raw products v (and u); res:
-// the residual there (loaded ahead by the caller, if there is one).
-template <typename T, bool DUAL>
-__device__ __forceinline__ void finish8(const Epilogue &e, float (&v)[8], float (&u)[8],
-                                        const float (&res)[8], int64_t m, int n) {
-  const int left = e.N - n;
-  const bool vec = e.vec != 0;
-  float b[8];
-  if (e.bias) {
-    load8<T>(b, (const T *)e.bias + n, left, vec);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += b[j];
-  }
-  if constexpr (DUAL) {
-    if (e.bias_up) {
-      load8<T>(b, (const T *)e.bias_up + n, left, vec);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) u[j] += b[j];
-    }
-  }
-  if (e.z) {
-    float k[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) k[j] = saved<T>(v[j], DUAL ? e.limit : 0.f);
-    store8<T>((T *)e.z + m * e.ld_z + n, k, left, vec);
-    if constexpr (DUAL) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) k[j] = saved<T>(u[j], e.limit);
-      store8<T>((T *)e.z_up + m * e.ld_z + n, k, left, vec);
-    }
-  }
-  if constexpr (DUAL) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float g = v[j], w = u[j];
-      if (e.limit > 0.f) {                     // NaN passes
-        g = g > e.limit ? e.limit : g;
-        w = w > e.limit ? e.limit : (w < -e.limit ? -e.limit : w);
-      }
-      v[j] = g * sigmoid<T>(g) * w;
-    }
-  } else {
-    activate8<T>(v, e.act);
-  }
-  if (e.residual) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += res[j];
-  }
-  store8<T>((T *)e.y + m * e.ld_y + n, v, left, vec);
-}
 
 // ---------------------------------------------------------------------------
 // The GEMM.
@@ -729,27 +515,15 @@ __global__ __launch_bounds__(256) void slope_kernel(const SlopeArgs a) {
     if (left <= 0 && n >= a.ldz) break;
     load8<T>(g, (const T *)a.dy + m * a.ld_dy + n, left, vec);
     if (a.z) load8<T>(z, (const T *)a.z + m * a.N + n, left, vec);
+    else for (float &v : z) v = 0.f;
     if constexpr (DUAL) load8<T>(u, (const T *)a.z_up + m * a.N + n, left, vec);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      if constexpr (DUAL) {
-        float gg = z[j], w = u[j];
-        bool on = j < left, on_up = on;        // clamped: no gradient, whatever dy holds
-        if (a.limit > 0.f) {
-          if (gg > a.limit) { gg = a.limit; on = false; }
-          if (w > a.limit) { w = a.limit; on_up = false; }
-          if (w < -a.limit) { w = -a.limit; on_up = false; }
-        }
-        const float sg = sigmoid<T>(gg);
-        dz[j] = on ? g[j] * w * sg * (1.f + gg * (1.f - sg)) : 0.f;
-        du[j] = on_up ? g[j] * gg * sg : 0.f;
-        s[0][j] += dz[j];
-        s[D - 1][j] += du[j];
-      } else {
-        const float sl = a.z ? slope<T>(z[j], a.act) : 1.f;
-        dz[j] = sl != 0.f && j < left ? g[j] * sl : 0.f;
-        s[0][j] += dz[j];
-      }
+      // `none` has slope 1 for any z
+      dz[j] = du[j] = 0.f;
+      if (j < left) grad_of<T, DUAL>(g[j], z[j], u[j], a.act, a.limit, &dz[j], &du[j]);
+      s[0][j] += dz[j];
+      if constexpr (DUAL) s[1][j] += du[j];
     }
     if (a.dz && n < a.ldz) {
       store8<T>((T *)a.dz + m * a.ldz + n, dz, (int)(a.ldz - n < 8 ? a.ldz - n : 8), true);
@@ -803,36 +577,39 @@ __global__ __launch_bounds__(256) void bias_sum_kernel(const float *sums, int N,
 // copies, epilogue).  The constants are microseconds measured over products of
 // 1024..8192 a side, one shape forced at a time (bf16 4096x4096 over K = 1024,
 // 2048, 4096: 256x256 tiles 44, 69, 121 us, 256x128 52, 85, 150, 128x128 46, 85,
-// 165, 64x64 67, 134, 271; dx and dW of that size within 10% of these).  A round
-// that fills part of the GPU runs at a higher clock (4096x2048 over K = 4096 with
-// 128 tiles of 256x256: 105 us).
-struct Shape { int mi, ni, parts; };
+// 165, 64x64 67, 134, 271; dx and dW of that size within 10% of these).  A bf16
+// round that fills part of the GPU runs at a higher clock (4096x2048 over K =
+// 4096 with 128 tiles of 256x256: 105 us).  `alone`: a stage of a workgroup that
+// has its CU to itself, where that is longer (one chain of MFMAs and reads).
+struct Shape {
+  int mi, ni, parts;
+  double us;                   // the estimate
+};
 
 Shape pick_shape(int64_t rows, int64_t cols, int64_t stages, bool f32, bool dual) {
-  struct { int mi, ni; double stage, stage_f32, fixed; } shapes[] = {
-      {4, 4, 0.80, 3.8, 14.0},
-      {4, 2, 0.52, 1.9, 8.0},
-      {2, 2, 0.27, 0.94, 3.5},
-      {1, dual ? 2 : 1, dual ? 0.186 : 0.127, dual ? 0.5 : 0.254, 1.0}};
-  Shape best = {1, 1, 1};
-  double best_t = 1e300;
+  struct { int mi, ni; double stage, alone, stage_f32, alone_f32, fixed; } shapes[] = {
+      {4, 4, 0.80, 0.56, 3.8, 3.8, 14.0},
+      {4, 2, 0.52, 0.36, 1.9, 1.9, 8.0},
+      {2, 2, 0.27, 0.22, 0.94, 0.94, 3.5},
+      {1, dual ? 2 : 1, dual ? 0.186 : 0.127, 0.2, dual ? 0.5 : 0.254, dual ? 0.6 : 0.33, 1.0}};
+  Shape best = {1, 1, 1, 1e300};
   for (const auto &sh : shapes) {
     const int64_t tiles = ((rows + 64 * sh.mi - 1) / (64 * sh.mi)) *
                           ((cols + 64 * sh.ni - 1) / (64 * sh.ni));
-    const double stage = f32 ? sh.stage_f32 : sh.stage;
+    const double stage = f32 ? sh.stage_f32 : sh.stage, alone = f32 ? sh.alone_f32 : sh.alone;
     for (int parts = 1; parts <= 16; parts *= 2) {
       if (parts > 1 && (stages < 16 * parts || tiles * parts > 1024)) break;
       const int64_t items = tiles * parts, full = items / 256;
       const double last = (double)(items - full * 256) / 256;
-      const double work = (double)((stages + parts - 1) / parts) * stage;
-      double t = full * (work + sh.fixed);
-      if (last > 0) t += work * (0.7 + 0.3 * last) + sh.fixed;
+      const double deep = (double)((stages + parts - 1) / parts);
+      double t = full * (deep * stage + sh.fixed);
+      if (last > 0) {
+        const double s = f32 ? stage : stage * (0.7 + 0.3 * last);
+        t += deep * (full == 0 && alone > s ? alone : s) + sh.fixed;
+      }
       // partial sums: a launch, and written and read at 8 TB/s in all
       if (parts > 1) t += 5.0 + (double)rows * cols * parts * 1e-6;
-      if (t < best_t) {
-        best_t = t;
-        best = {sh.mi, sh.ni, parts};
-      }
+      if (t < best.us) best = {sh.mi, sh.ni, parts, t};
     }
   }
   return best;
@@ -878,6 +655,62 @@ hipError_t run_gemm(GemmOp g, const Shape &sh, void *part, hipStream_t s) {
   return run_gemm_shape<T, 1, DUAL ? 2 : 1, AC, BC, DUAL>(g, s);
 }
 
+bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
+
+bool odd_rows(int64_t width, int64_t ld, int dtype) {
+  return width % linear_pad(1, dtype) || ld % linear_pad(1, dtype);
+}
+
+// The kernels of a call.  Up to kFewRows rows take the stream of W where no copy
+// has to be made first (1x7168->2x2048 swiglu bf16 17.5 -> 14.5 us, 16x4096->4096
+// fp32 29 -> 18 us).  Otherwise 32 x 32 tiles where their estimate is below that
+// of the GEMM with the launches around it (4 us each, with the wait for the one
+// before).  Microseconds per round of 256 tiles and eight chunks of the
+// contraction, measured with either way forced on 60 shapes: 203x777->1023 fp32
+// 30 by the GEMM and 12 by small tiles, 64x4096->512 18 and 28, 1024^3 26 and 36;
+// the backward of 301x256->320 29 and 16, of 1024^3 61 and 148.
+enum Path { PATH_GEMM, PATH_FEW, PATH_SMALL };
+
+double small_us(int64_t tiles, int64_t contraction, double chunks_us) {
+  const int64_t chunks = (contraction + 63) / 64;
+  return (double)tiles / 256 * (2.0 + (double)((chunks + 7) / 8) * chunks_us);
+}
+
+Path forward_path(const moe_linear_config &c) {
+  const int64_t M = c.rows, K = c.in_dim, N = c.out_dim;
+  const bool dual = c.activation == MOE_ACTIVATION_SWIGLU;
+  const bool copy_w = odd_rows(K, K, c.dtype), copy_x = odd_rows(K, c.ld_x, c.dtype);
+  if (M <= kFewRows && !copy_w && !copy_x) return PATH_FEW;
+  const Shape sh = shape_of(M, dual ? 2 * N : N, &K, 1, c.dtype, dual);
+  const double gemm = sh.us + 4.0 * (1 + copy_x + copy_w * (dual ? 2 : 1));
+  const int64_t tiles = (M + 31) / 32 * ((N + 31) / 32);
+  const double small = small_us((tiles + 255) / 256 * 256, K, dual ? 5.2 : 3.0) + 4.0;
+  return small < gemm ? PATH_SMALL : PATH_GEMM;
+}
+
+// By the time of all gradients, whichever are asked for: each comes out the same
+// alone and with others.
+bool backward_small(const moe_linear_config &c) {
+  const int64_t M = c.rows, K = c.in_dim, N = c.out_dim;
+  if (M == 0) return false;
+  const bool dual = c.activation == MOE_ACTIVATION_SWIGLU;
+  const double chunks_us = dual ? 9.0 : 7.0;
+  const int64_t kt = (K + 31) / 32, both = dual ? 2 : 1, kd[2] = {N, N};
+  const Shape dx = shape_of(M, K, kd, (int)both, c.dtype, false);
+  const Shape dw = shape_of(both * N, K, &M, 1, c.dtype, false);
+  // slope, column sums, products and copies
+  const double gemm = 16.0 + dx.us + dw.us + (odd_rows(K, K, c.dtype) ? 4.0 * both : 0.0) +
+                      (odd_rows(K, c.ld_x, c.dtype) ? 4.0 : 0.0);
+  // the workgroups of dx and dW fill the GPU together
+  double small = small_us((M + 31) / 32 * kt, both * N, chunks_us) +
+                 small_us((N + 31) / 32 * kt * both, M, chunks_us);
+  for (const int64_t chain : {both * N, M}) {
+    const double one = small_us(256, chain, chunks_us);
+    small = small > one ? small : one;
+  }
+  return small + 4.0 < gemm;
+}
+
 template <typename T>
 hipError_t pad_rows(const void *src, int64_t ld, int64_t rows, int cols, void *dst, int64_t ldo,
                     hipStream_t s) {
@@ -888,8 +721,6 @@ hipError_t pad_rows(const void *src, int64_t ld, int64_t rows, int cols, void *d
   return hipGetLastError();
 }
 
-bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
-
 // Row chunks of the column sums: enough workgroups to fill the GPU, each with
 // rows to add.
 int colsum_parts(int64_t M, int N) {
@@ -899,10 +730,6 @@ int colsum_parts(int64_t M, int N) {
   return (int)(parts > most ? most : parts);
 }
 
-bool odd_rows(int64_t width, int64_t ld, int dtype) {
-  return width % linear_pad(1, dtype) || ld % linear_pad(1, dtype);
-}
-
 template <typename T>
 hipError_t linear_forward(const moe_linear_config &c, const moe_linear_weights &w, const void *x,
                           const void *residual, void *y, void *z, void *z_up, char *ws,
@@ -910,6 +737,22 @@ hipError_t linear_forward(const moe_linear_config &c, const moe_linear_weights &
   const LinearSpace L = linear_space(c, false, false, false, false);
   const int64_t M = c.rows, K = c.in_dim, N = c.out_dim;
   const bool dual = c.activation == MOE_ACTIVATION_SWIGLU;
+  Epilogue e = {};
+  e.bias = w.bias; e.bias_up = w.bias_up; e.residual = residual;
+  e.y = y; e.z = z; e.z_up = z_up;
+  e.ld_y = c.ld_y; e.ld_res = c.ld_residual; e.ld_z = N;
+  e.N = (int)N; e.act = c.activation; e.limit = c.limit;
+  e.vec = !odd_rows(N, c.ld_y, c.dtype) && (!residual || !odd_rows(N, c.ld_residual, c.dtype)) &&
+          N % 8 == 0 && aligned16(y) && aligned16(z) && aligned16(z_up) && aligned16(residual) &&
+          aligned16(w.bias) && aligned16(w.bias_up);
+  const Path path = forward_path(c);
+  if (path != PATH_GEMM) {
+    SmallArgs a = {};
+    a.x = x; a.w = w.w; a.w_up = w.w_up;
+    a.M = M; a.K = K; a.ld_x = c.ld_x;
+    a.e = e;
+    return path == PATH_FEW ? launch_few_rows<T>(a, dual, s) : launch_small_forward<T>(a, dual, s);
+  }
   hipError_t err;
   Matrix mx = {x, c.ld_x, M, K}, mw = {w.w, K, N, K}, mu = {w.w_up, K, N, K};
   const int64_t Kp = linear_pad(K, c.dtype);
@@ -930,14 +773,7 @@ hipError_t linear_forward(const moe_linear_config &c, const moe_linear_weights &
   g.kdim[0] = K;
   g.segments = 1;
   g.M = M;
-  Epilogue &e = g.e;
-  e.bias = w.bias; e.bias_up = w.bias_up; e.residual = residual;
-  e.y = y; e.z = z; e.z_up = z_up;
-  e.ld_y = c.ld_y; e.ld_res = c.ld_residual; e.ld_z = N;
-  e.N = (int)N; e.act = c.activation; e.limit = c.limit;
-  e.vec = !odd_rows(N, c.ld_y, c.dtype) && (!residual || !odd_rows(N, c.ld_residual, c.dtype)) &&
-          N % 8 == 0 && aligned16(y) && aligned16(z) && aligned16(z_up) && aligned16(residual) &&
-          aligned16(w.bias) && aligned16(w.bias_up);
+  g.e = e;
   const Shape sh = shape_of(M, dual ? 2 * N : N, g.kdim, 1, c.dtype, dual);
   return dual ? run_gemm<T, false, false, true>(g, sh, ws + L.part, s)
               : run_gemm<T, false, false, false>(g, sh, ws + L.part, s);
@@ -953,6 +789,15 @@ hipError_t linear_backward(const moe_linear_config &c, const moe_linear_weights 
   const int64_t M = c.rows, K = c.in_dim, N = c.out_dim;
   const int64_t Kp = linear_pad(K, c.dtype), Np = linear_pad(N, c.dtype);
   hipError_t err;
+  if (backward_small(c)) {
+    SmallArgs a = {};
+    a.x = x; a.w = w.w; a.w_up = w.w_up;
+    a.dy = dy; a.z = c.activation == MOE_ACTIVATION_NONE ? nullptr : z; a.z_up = z_up;
+    a.dx = gr.dx; a.dw = gr.dw; a.dw_up = gr.dw_up; a.db = gr.dbias; a.db_up = gr.dbias_up;
+    a.M = M; a.K = K; a.ld_x = c.ld_x; a.ld_dy = c.ld_y; a.ld_dx = c.ld_x;
+    a.e.N = (int)N; a.e.act = c.activation; a.e.limit = c.limit;
+    return launch_small_backward<T>(a, dual, s);
+  }
   // dz: dy itself where nothing changes it and its rows are whole pieces
   const bool same = c.activation == MOE_ACTIVATION_NONE && !odd_rows(N, c.ld_y, c.dtype);
   Matrix mz = {dy, c.ld_y, M, N}, mu = {};
@@ -1023,7 +868,7 @@ hipError_t linear_backward(const moe_linear_config &c, const moe_linear_weights 
     g.e.y = gr.dw ? gr.dw : gr.dw_up; g.e.ld_y = K; g.e.N = (int)K;
     g.e.act = MOE_ACTIVATION_NONE;
     g.e.vec = K % 8 == 0 && aligned16(gr.dw) && aligned16(gr.dw_up);
-    const Shape sh = shape_of(g.halves * N, K, g.kdim, 1, c.dtype, false);
+    const Shape sh = shape_of(dual ? 2 * N : N, K, g.kdim, 1, c.dtype, false);
     if ((err = run_gemm<T, true, true, false>(g, sh, ws + L.part, s)) != hipSuccess) return err;
   }
   return hipSuccess;
@@ -1043,6 +888,7 @@ LinearSpace linear_space(const moe_linear_config &c, bool backward, bool dx, boo
     off = (off + bytes + 255) / 256 * 256;
     return o;
   };
+  // what the GEMM takes, also where another kernel runs: one size per shape
   const bool use_x = !backward || dw, use_w = !backward || dx;
   l.x = take(use_x && odd_rows(K, c.ld_x, c.dtype) ? es * M * Kp : 0);
   l.w = take(use_w && odd_rows(K, K, c.dtype) ? es * N * Kp : 0);
@@ -1060,10 +906,7 @@ LinearSpace linear_space(const moe_linear_config &c, bool backward, bool dx, boo
     l.du = take(dual && (dx || dw) ? es * M * Np : 0);
     l.colsum = take(db ? sizeof(float) * colsum_parts(M, (int)N) * (dual ? 2 : 1) * N : 0);
     if (dx) need(M, K, N, dual ? 2 : 1, false);
-    if (dw) {
-      need(N, K, M, 1, false);
-      if (dual) need(2 * N, K, M, 1, false);
-    }
+    if (dw) need(dual ? 2 * N : N, K, M, 1, false);
   } else {
     need(M, N, K, 1, dual);
   }

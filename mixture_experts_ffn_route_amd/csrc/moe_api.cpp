@@ -800,8 +800,13 @@ int moe_forward_ex(const moe_config *cfg, const moe_weights *w, const void *x,
 size_t moe_linear_workspace_size(const moe_linear_config *cfg, int32_t backward) {
   moe_linear_config c;
   if (check_linear(cfg, &c) != MOE_OK) return 0;
-  const size_t n = moe::linear_space(c, backward != 0, true, true, true).total;
-  return n < kAlign ? kAlign : n;
+  // whichever gradients a call asks for
+  size_t n = kAlign;
+  for (int want = backward ? 1 : 7; want < 8; ++want) {
+    const size_t b = moe::linear_space(c, backward != 0, want & 1, want & 2, want & 4).total;
+    if (b > n) n = b;
+  }
+  return n;
 }
 
 int moe_linear(const moe_linear_config *cfg, const moe_linear_weights *w, const void *x,
