@@ -521,9 +521,10 @@ typedef struct {               /* contiguous, dtype; w and w_up 16-byte aligned 
 } moe_linear_weights;
 
 typedef struct {               /* contiguous except dx; NULL: not wanted         */
-  void *dx;                    /* [M, K], stride ld_x                            */
+  void *dx;                    /* [M, K], stride ld_dx                           */
   void *dw, *dw_up;            /* [N, K]                                         */
   void *dbias, *dbias_up;      /* [N]                                            */
+  int64_t ld_dx;               /* 0: K                                           */
 } moe_linear_grads;
 
 /* Workspace of moe_linear (backward = 0) or moe_linear_backward (backward = 1,

@@ -88,7 +88,8 @@ class MoeLinearWeightsC(ctypes.Structure):
 
 
 class MoeLinearGradsC(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_void_p) for n in ("dx", "dw", "dw_up", "dbias", "dbias_up")]
+    _fields_ = [*((n, ctypes.c_void_p) for n in ("dx", "dw", "dw_up", "dbias", "dbias_up")),
+                ("ld_dx", ctypes.c_int64)]
 
 
 def _load():
@@ -466,7 +467,7 @@ def moe_linear(cfg: LinearConfig, x, w, y, *, bias=None, residual=None, w_up=Non
 def moe_linear_backward(cfg: LinearConfig, dy, x, w, *, w_up=None, z=None, z_up=None, dx=None,
                         dw=None, dw_up=None, dbias=None, dbias_up=None, ws=None, stream=None):
     """Gradients of moe_linear for dy, into the tensors given (the residual's
-    is dy itself).  dx has x's row stride where both are given."""
+    is dy itself)."""
     M, K, N = cfg.rows, cfg.in_dim, cfg.out_dim
     _linear_check(cfg, "moe_linear_backward",
                   [("dy", dy, (M, N)), ("x", x, (M, K)), ("dx", dx, (M, K))],
@@ -474,9 +475,10 @@ def moe_linear_backward(cfg: LinearConfig, dy, x, w, *, w_up=None, z=None, z_up=
                    ("z_up", z_up, (M, N)), ("dw", dw, (N, K)), ("dw_up", dw_up, (N, K)),
                    ("dbias", dbias, (N,)), ("dbias_up", dbias_up, (N,))])
     weights = MoeLinearWeightsC(_raw(w), _raw(w_up), None, None)
-    grads = MoeLinearGradsC(_raw(dx), _raw(dw), _raw(dw_up), _raw(dbias), _raw(dbias_up))
+    grads = MoeLinearGradsC(_raw(dx), _raw(dw), _raw(dw_up), _raw(dbias), _raw(dbias_up),
+                            0 if dx is None or M < 2 else dx.stride(0))
     _check(_lib.moe_linear_backward(
-        ctypes.byref(_linear_config(cfg, x if x is not None else dx, dy)), ctypes.byref(weights),
+        ctypes.byref(_linear_config(cfg, x, dy)), ctypes.byref(weights),
         _raw(x), _raw(dy), _raw(z), _raw(z_up), ctypes.byref(grads), _raw(ws),
         0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)),
         "moe_linear_backward")

@@ -794,7 +794,7 @@ hipError_t linear_backward(const moe_linear_config &c, const moe_linear_weights 
     a.x = x; a.w = w.w; a.w_up = w.w_up;
     a.dy = dy; a.z = c.activation == MOE_ACTIVATION_NONE ? nullptr : z; a.z_up = z_up;
     a.dx = gr.dx; a.dw = gr.dw; a.dw_up = gr.dw_up; a.db = gr.dbias; a.db_up = gr.dbias_up;
-    a.M = M; a.K = K; a.ld_x = c.ld_x; a.ld_dy = c.ld_y; a.ld_dx = c.ld_x;
+    a.M = M; a.K = K; a.ld_x = c.ld_x; a.ld_dy = c.ld_y; a.ld_dx = gr.ld_dx;
     a.e.N = (int)N; a.e.act = c.activation; a.e.limit = c.limit;
     return launch_small_backward<T>(a, dual, s);
   }
@@ -845,8 +845,8 @@ hipError_t linear_backward(const moe_linear_config &c, const moe_linear_weights 
     g.kdim[0] = N; g.kdim[1] = N;
     g.segments = dual ? 2 : 1;
     g.M = M;
-    g.e.y = gr.dx; g.e.ld_y = c.ld_x; g.e.N = (int)K; g.e.act = MOE_ACTIVATION_NONE;
-    g.e.vec = !odd_rows(K, c.ld_x, c.dtype) && K % 8 == 0 && aligned16(gr.dx);
+    g.e.y = gr.dx; g.e.ld_y = gr.ld_dx; g.e.N = (int)K; g.e.act = MOE_ACTIVATION_NONE;
+    g.e.vec = !odd_rows(K, gr.ld_dx, c.dtype) && K % 8 == 0 && aligned16(gr.dx);
     const Shape sh = shape_of(M, K, g.kdim, g.segments, c.dtype, false);
     if ((err = run_gemm<T, false, true, false>(g, sh, ws + L.part, s)) != hipSuccess) return err;
   }

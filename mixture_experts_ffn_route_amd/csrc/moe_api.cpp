@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <initializer_list>
 #include <cstring>
 #include <mutex>
 #include <numeric>
@@ -198,6 +199,18 @@ int check_linear(const moe_linear_config *c, moe_linear_config *out) {
 }
 
 bool misaligned(const void *p, size_t n) { return (uintptr_t)p % n != 0; }
+
+// Whether an output is an input, or another output (by address; null: not there).
+bool overlap(std::initializer_list<const void *> out, std::initializer_list<const void *> in) {
+  for (auto o = out.begin(); o != out.end(); ++o) {
+    if (!*o) continue;
+    for (const void *i : in)
+      if (*o == i) return true;
+    for (auto p = out.begin(); p != o; ++p)
+      if (*o == *p) return true;
+  }
+  return false;
+}
 
 int hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
@@ -821,7 +834,8 @@ int moe_linear(const moe_linear_config *cfg, const moe_linear_weights *w, const 
     return MOE_ERR_INVALID_ARG;
   if ((z && dual && !z_up) || (z_up && (!z || !dual))) return MOE_ERR_INVALID_ARG;
   if (c.rows == 0) return MOE_OK;
-  if (!x || !y || x == y || y == z || y == z_up || (residual == y && c.ld_residual != c.ld_y))
+  if (!x || !y || (residual == y && c.ld_residual != c.ld_y)) return MOE_ERR_INVALID_ARG;
+  if (overlap({y, z, z_up}, {x, w->w, w->w_up, w->bias, w->bias_up}) || overlap({z, z_up}, {residual}))
     return MOE_ERR_INVALID_ARG;
   if (misaligned(x, 16) || misaligned(w->w, 16) || misaligned(w->w_up, 16))
     return MOE_ERR_INVALID_ARG;
@@ -853,8 +867,14 @@ int moe_linear_backward(const moe_linear_config *cfg, const moe_linear_weights *
     if (want_dw && !x) return MOE_ERR_INVALID_ARG;
     if (misaligned(x, 16) || misaligned(w->w, 16) || misaligned(w->w_up, 16))
       return MOE_ERR_INVALID_ARG;
-    if (grads->dx && (grads->dx == dy || grads->dx == x)) return MOE_ERR_INVALID_ARG;
   }
+  if (overlap({grads->dx, grads->dw, grads->dw_up, grads->dbias, grads->dbias_up},
+              {x, dy, z, z_up, w->w, w->w_up}))
+    return MOE_ERR_INVALID_ARG;
+  moe_linear_grads gr = *grads;
+  if (gr.ld_dx == 0) gr.ld_dx = c.in_dim;
+  if (gr.dx && gr.ld_dx < c.in_dim) return MOE_ERR_INVALID_ARG;
+  if (gr.dx && gr.ld_dx > MOE_LINEAR_MAX_LD) return MOE_ERR_UNSUPPORTED;
   for (const void *p : {z, z_up, (const void *)grads->dx, (const void *)grads->dw,
                         (const void *)grads->dw_up, (const void *)grads->dbias,
                         (const void *)grads->dbias_up})
@@ -862,7 +882,7 @@ int moe_linear_backward(const moe_linear_config *cfg, const moe_linear_weights *
   const size_t need =
       moe::linear_space(c, true, grads->dx != nullptr, want_dw, want_db).total;
   if (need > 0 && (!ws || misaligned(ws, kAlign) || ws_bytes < need)) return MOE_ERR_WORKSPACE;
-  return hip_status(moe::launch_linear_backward(c, *w, x, dy, z, z_up, *grads, (char *)ws,
+  return hip_status(moe::launch_linear_backward(c, *w, x, dy, z, z_up, gr, (char *)ws,
                                                 (hipStream_t)stream));
 }
 
