@@ -195,7 +195,7 @@ def _prepare_linear(c, seed):
     if own:
         from mixture_experts_ffn_route_amd import binding, config
         cfg = config.LinearConfig(rows=M, in_dim=K, out_dim=N, dtype=c["dtype"],
-                                  activation=c["act"], limit=c["limit"])
+                                  activation=c["act"], limit=c["limit"] if two else 0.0)
         s["B"], s["cfg"] = binding, cfg
         s["ws"] = binding.alloc_linear_workspace(cfg, backward=train)
 
