@@ -505,9 +505,9 @@ typedef struct {
   int32_t dtype;               /* moe_dtype F32 or BF16, of every tensor         */
   int32_t activation;          /* moe_activation                                 */
   float limit;                 /* swiglu clamp L > 0; 0: none                    */
-  int64_t ld_x;                /* row strides in elements, 0 = contiguous: x and
-                                  dx (>= K), y and dy (>= N), residual (>= N);
-                                  up to MOE_LINEAR_MAX_LD                        */
+  int64_t ld_x;                /* row strides in elements, 0 = contiguous: x
+                                  (>= K), y and dy (>= N), residual (>= N); up
+                                  to MOE_LINEAR_MAX_LD                           */
   int64_t ld_y;
   int64_t ld_residual;
 } moe_linear_config;
@@ -535,15 +535,16 @@ size_t moe_linear_workspace_size(const moe_linear_config *cfg, int32_t backward)
 /* The forward product.
  *   x         [M, K] stride ld_x, 16-byte aligned
  *   residual  [M, N] stride ld_residual, or NULL; may be y itself (same stride)
- *   y         [M, N] stride ld_y out; not x
+ *   y         [M, N] stride ld_y out
  *   z, z_up   [M, N] contiguous out, or NULL: the pre-activations z (and zu),
  *             which the gradient needs unless the activation is NONE.  Rounded
  *             to dtype, but never across the clamp's border
  *   ws        device workspace of at least moe_linear_workspace_size(cfg, 0)
  *             bytes, 256-byte aligned; nothing in it needs to start at any value
  * Products accumulate in fp32, the epilogue is fp32, y is rounded once.  All
- * sizes and strides are taken; rows that are not whole 16-byte pieces are
- * first copied to padded ones in the workspace.  Results do not depend on what
+ * sizes and strides are taken; for large products, rows that are not whole
+ * 16-byte pieces are first copied to padded ones in the workspace.  No output
+ * may overlap an input (but y the residual) or another output.  Results do not depend on what
  * else runs (no atomics).  Only kernels are enqueued on `stream`, so the call
  * can be captured in a HIP graph.  rows == 0 is a no-op. */
 int moe_linear(const moe_linear_config *cfg, const moe_linear_weights *w, const void *x,
@@ -558,9 +559,12 @@ int moe_linear(const moe_linear_config *cfg, const moe_linear_weights *w, const 
  *   x         needed for dw / dw_up; w->w, w->w_up for dx; else may be NULL
  *             (biases are not read)
  *   grads     at least one member; outputs are overwritten, not added to
- * dz is rounded to dtype before the products (they run on the matrix cores);
- * sums are fp32, outputs are rounded once.  rows == 0 writes zeros to the
- * weight and bias gradients. */
+ * Large products round dz to dtype first, as their matrix cores take it: with
+ * the rounding of z that makes bf16 gradients 3e-3 of their norm off, where
+ * fp32 throughout is 1.7e-3 off (the output's own rounding); small ones keep dz
+ * in fp32.  Sums are fp32, outputs are rounded once.  No output may overlap an
+ * input or another output.  rows == 0 writes zeros to the weight and bias
+ * gradients. */
 int moe_linear_backward(const moe_linear_config *cfg, const moe_linear_weights *w, const void *x,
                         const void *dy, const void *z, const void *z_up,
                         const moe_linear_grads *grads, void *ws, size_t ws_bytes, void *stream);
