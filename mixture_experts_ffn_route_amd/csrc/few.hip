@@ -568,15 +568,15 @@ __device__ __forceinline__ float wave_max_dpp(float v) {
 
 template <int EPL>
 __device__ __forceinline__ void select_few(const FewArgs &a, int t, int lane, float *out_w,
-                                           int32_t *out_e, const float *scores) {
+                                           int32_t *out_e, const float *scores,
+                                           const float *gate_bias) {
   const int E = a.E;
   float s[EPL], key[EPL], bias[EPL];
-  const rsrc_t br = resource(a.bias, a.bias ? (int64_t)E * 4 : 0);
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
     const int e = lane * EPL + j;
     s[j] = e < E ? scores[t * E + e] : 0.f;
-    bias[j] = __uint_as_float(load4(br, e < E ? (uint32_t)e * 4 : kOut));
+    bias[j] = a.bias && e < E ? gate_bias[e] : 0.f;
   }
   if (a.score == MOE_SCORE_SOFTMAX) {
     float m = -INFINITY;
@@ -660,16 +660,16 @@ __device__ __forceinline__ void select_few(const FewArgs &a, int t, int lane, fl
 }
 
 __device__ __forceinline__ void select_any(const FewArgs &a, int t, int lane, float *w, int32_t *e,
-                                           const float *scores) {
+                                           const float *scores, const float *bias) {
   switch ((a.E + 63) / 64) {
-    case 1: return select_few<1>(a, t, lane, w, e, scores);
-    case 2: return select_few<2>(a, t, lane, w, e, scores);
-    case 3: return select_few<3>(a, t, lane, w, e, scores);
-    case 4: return select_few<4>(a, t, lane, w, e, scores);
-    case 5: return select_few<5>(a, t, lane, w, e, scores);
-    case 6: return select_few<6>(a, t, lane, w, e, scores);
-    case 7: return select_few<7>(a, t, lane, w, e, scores);
-    default: return select_few<8>(a, t, lane, w, e, scores);
+    case 1: return select_few<1>(a, t, lane, w, e, scores, bias);
+    case 2: return select_few<2>(a, t, lane, w, e, scores, bias);
+    case 3: return select_few<3>(a, t, lane, w, e, scores, bias);
+    case 4: return select_few<4>(a, t, lane, w, e, scores, bias);
+    case 5: return select_few<5>(a, t, lane, w, e, scores, bias);
+    case 6: return select_few<6>(a, t, lane, w, e, scores, bias);
+    case 7: return select_few<7>(a, t, lane, w, e, scores, bias);
+    default: return select_few<8>(a, t, lane, w, e, scores, bias);
   }
 }
 
@@ -700,6 +700,9 @@ __device__ __forceinline__ void make_plan(const FewArgs &a, PlanScratch &p, floa
     // affinities of all tokens by all threads (softmax: the logits), the parts
     // of a logit added in order; then a wave per token
     const int n = T * E;
+    float *bias = (float *)p.lead;             // until the leaders
+    if (a.bias)
+      for (int i = tid; i < E; i += 1024) bias[i] = a.bias[i];
     for (int i = tid; i < n; i += 1024) {
       float part[kLogitParts];
 #pragma unroll
@@ -713,7 +716,7 @@ __device__ __forceinline__ void make_plan(const FewArgs &a, PlanScratch &p, floa
       scores[i] = z;
     }
     __syncthreads();
-    for (int t = wave; t < T; t += 16) select_any(a, t, lane, p.w, p.e, scores);
+    for (int t = wave; t < T; t += 16) select_any(a, t, lane, p.w, p.e, scores, bias);
     __syncthreads();
   } else {
     __syncthreads();
@@ -873,7 +876,15 @@ __global__ __launch_bounds__(256, 2) void few_up(const FewArgs a) {
   constexpr int es = F == F_F32 ? 4 : 2;
   MOE_FEW_LDS(F);
   const int T = a.T, d = a.d, I = a.I;
-  const int blocks = (I + 31) / 32, tiles = a.plan_slots[0] * blocks;
+  const int blocks = (I + 31) / 32, pairs = T * a.k;
+  // a tile's slot, asked for with the number of slots (past it: not used)
+  auto slot_of = [&](int tile) {
+    const int s = tile / blocks;
+    return s < pairs ? s : pairs - 1;
+  };
+  int expert = a.plan_expert[slot_of(blockIdx.x)];
+  int16_t row = a.plan_row[slot_of(blockIdx.x) * kRows + (lane & 15)];
+  const int tiles = a.plan_slots[0] * blocks;
   TSrc xs;
   if constexpr (MX) {
     xs.r = resource(a.xq, (int64_t)T * d);
@@ -885,12 +896,14 @@ __global__ __launch_bounds__(256, 2) void few_up(const FewArgs a) {
   for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     const int slot = tile / blocks, n0 = (tile - slot * blocks) * 32;
     const int16_t *rows = a.plan_row + slot * kRows;
-    const int64_t e = a.plan_expert[slot];
+    const int64_t e = expert;
     const int64_t at = e * ((int64_t)I * row_bytes<F>(d));
     const int64_t sat = e * ((int64_t)I * d / (F == F_MX8 ? 16384 : 32));
     up_tile<F, TILED, NB>(a, xs, (const uint8_t *)a.w_gate + at, (const uint8_t *)a.w_up + at,
-                          a.s_gate + sat, a.s_up + sat, n0, lane & 15, rows[lane & 15] >= 0, wave,
-                          4, lane, ring0, ring1, SC, red + wave * (SLOT / 4));
+                          a.s_gate + sat, a.s_up + sat, n0, lane & 15, row >= 0, wave, 4, lane,
+                          ring0, ring1, SC, red + wave * (SLOT / 4));
+    expert = a.plan_expert[slot_of(tile + gridDim.x)];
+    row = a.plan_row[slot_of(tile + gridDim.x) * kRows + (lane & 15)];
     __syncthreads();
     // a half-wave takes a token's 32 columns
     for (int t = threadIdx.x >> 5; t < kRows; t += 8) {
@@ -962,6 +975,12 @@ __global__ __launch_bounds__(256, 2) void few_down(const FewArgs a) {
   const int T = a.T, d = a.d, I = a.I, pairs = T * a.k;
   const int blocks = (d + 63) / 64;
   const int shared = a.has_shared ? blocks : 0;
+  // as in few_up
+  auto slot_of = [&](int unit) {
+    const int s = ((unit - shared) * PER + (G == 1 ? wave : 0)) / blocks;
+    return s < 0 ? 0 : s < pairs ? s : pairs - 1;
+  };
+  int expert = a.plan_expert[slot_of(blockIdx.x)];
   const int tiles = a.plan_slots[0] * blocks;
   const int units = shared + (tiles + PER - 1) / PER;
   const int hrows = pairs + (a.has_shared ? T : 0);
@@ -986,7 +1005,7 @@ __global__ __launch_bounds__(256, 2) void few_down(const FewArgs a) {
           a, hs, a.sh_down, nullptr, n0, t < T ? pairs + t + low : -1, wave, 4, lane, ring0, ring1,
           nullptr, mine);
     } else if (live) {
-      const int64_t e = __builtin_amdgcn_readfirstlane(a.plan_expert[slot]);
+      const int64_t e = __builtin_amdgcn_readfirstlane(expert);
       const int64_t at = e * ((int64_t)d * row_bytes<F>(I));
       const int64_t sat = e * ((int64_t)d * I / (F == F_MX8 ? 16384 : 32));
       const int row = rows[t];
@@ -995,6 +1014,7 @@ __global__ __launch_bounds__(256, 2) void few_down(const FewArgs a) {
           row < 0 ? row : row + low, G == 1 ? 0 : wave, G, lane, ring0, ring1,
           SC + (G == 1 ? wave * 64 * SW : 0), mine);
     }
+    expert = a.plan_expert[slot_of(unit + gridDim.x)];
     __syncthreads();
     const bool own = G == 1 && !sh;            // the wave's tile is its own
     if (live)
@@ -1020,7 +1040,7 @@ __global__ __launch_bounds__(256) void few_combine(const FewArgs a) {
   const int t = blockIdx.y, n = (blockIdx.x * 256 + threadIdx.x) * 4;
   if (n >= a.d) return;
   const int left = a.d - n;
-  uint32_t mask = (uint32_t)a.plan_mask[t];
+  const uint32_t mask = (uint32_t)a.plan_mask[t];
   const bool whole = left >= 4 && a.d % 4 == 0;
   auto row = [&](int r) {
     const float *p = a.yrows + (int64_t)r * a.d + n;
@@ -1029,13 +1049,19 @@ __global__ __launch_bounds__(256) void few_combine(const FewArgs a) {
     for (int i = 0; i < 4 && i < left; ++i) v[i] = p[i];
     return v;
   };
-  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-  while (mask) {
-    const int j = __builtin_ctz(mask);
-    mask &= mask - 1;
-    sum += row(t * a.k + j);
+  // eight rows asked for at a time, beside the mask that says which were written,
+  // and added in the order of the choices
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+  f32x4 sum = zero, last = zero;
+  if (a.has_shared) last = row(a.T * a.k + t);
+  for (int j0 = 0; j0 < a.k; j0 += 8) {
+    f32x4 v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j0 + j < a.k ? row(t * a.k + j0 + j) : zero;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum += mask >> (j0 + j) & 1u ? v[j] : zero;
   }
-  if (a.has_shared) sum += row(a.T * a.k + t);
+  sum += last;
   T *y = (T *)a.y + (int64_t)t * a.d + n;
   for (int i = 0; i < 4 && i < left; ++i) y[i] = (T)sum[i];
 }

@@ -83,15 +83,17 @@ __device__ __forceinline__ void widen8(float (&v)[8], const Raw8<T> &r) {
   }
 }
 
-// fp32 layers take the accurate exponential; before a rounding to bf16 the
-// hardware one (relative error below 2^-20 at the arguments that matter) does.
+// fp32 layers take the accurate exponential and division; before a rounding to
+// bf16 the hardware ones (relative error below 2^-20 at the arguments that
+// matter) do.
 template <typename T>
 __device__ __forceinline__ float exp_of(float v) {
   return sizeof(T) == 4 ? expf(v) : __expf(v);
 }
 template <typename T>
 __device__ __forceinline__ float sigmoid(float v) {
-  return 1.f / (1.f + exp_of<T>(-v));
+  const float q = 1.f + exp_of<T>(-v);
+  return sizeof(T) == 4 ? 1.f / q : __builtin_amdgcn_rcpf(q);
 }
 
 constexpr float kGeluA = 0.7978845608028654f;  // sqrt(2 / pi)
