@@ -146,8 +146,15 @@ __device__ __forceinline__ u32x4 w_operand(const uint8_t *lds, int b, int f, int
 // by stage they touch as many cache lines as the weights and cost 20 % of the
 // stream, so those of the tile's rows are first copied to LDS, SW bytes a row
 // (SW = 256: 31 stages; 64: 7): row layout from the row's first byte rounded
-// down to four, tiled layout as the row blocks lie, 16 SW bytes each.
+// down to four, its 16-byte pieces permuted so that a half-wave's 16 rows lie in
+// distinct banks (unpermuted, a quarter of the LDS cycles were conflicts);
+// tiled layout as the row blocks lie, 16 SW bytes each.
 template <int F> constexpr bool is_fp4() { return F == F_FP4 || F == F_MX4; }
+
+template <int SW>
+__device__ __forceinline__ int scale_swizzle(int r) {
+  return SW == 256 ? r & 15 : r >> 2 & 3;
+}
 
 // One wave's share (of W = SW / 64 waves) of a source's 32 rows, inputs k0 ...
 template <bool TILED, int SW>
@@ -162,8 +169,10 @@ __device__ __forceinline__ void copy_scales(const WSrc &w, int K, int k0, int wa
       const uint32_t in = (uint32_t)k0 / 2 + (u % W) * 1024 + lane * 16;
       off = in < (uint32_t)K / 2 ? (u / W) * (K / 2) + in : kOut;
     } else {
-      const uint32_t row = (u * (1024 / SW) + lane / (SW / 16)) * (K / 32);
-      const uint32_t at = ((row + k0 / 32) & ~3u) + lane % (SW / 16) * 16;
+      const int r = u * (1024 / SW) + lane / (SW / 16);
+      const uint32_t row = r * (K / 32);
+      const uint32_t at =
+          ((row + k0 / 32) & ~3u) + (lane % (SW / 16) ^ scale_swizzle<SW>(r)) * 16;
       off = at < row + K / 32 ? at : kOut;
     }
     __builtin_amdgcn_raw_ptr_buffer_load_lds(w.rs, (MOE_LDS void *)(lds + u * 1024), 16, off, 0, 0,
@@ -176,8 +185,9 @@ template <bool TILED, int SW>
 __device__ __forceinline__ uint32_t scale_byte(const uint8_t *lds, int K, int k0, int b, int half,
                                                int lane) {
   const int r = 16 * b + (lane & 15), q = lane >> 4;
-  return TILED ? lds[b * 16 * SW + (2 * half + (q >> 1)) * 32 + (lane & 15) * 2 + (q & 1)]
-               : lds[r * SW + ((r * (K / 32) + k0 / 32) & 3) + half * 4 + q];
+  if (TILED) return lds[b * 16 * SW + (2 * half + (q >> 1)) * 32 + (lane & 15) * 2 + (q & 1)];
+  const int o = ((r * (K / 32) + k0 / 32) & 3) + half * 4 + q;
+  return lds[r * SW + (o ^ scale_swizzle<SW>(r) << 4)];
 }
 
 // ---------------------------------------------------------------------------
