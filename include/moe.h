@@ -394,11 +394,12 @@ int moe_forward_noalloc(const moe_config *cfg, const moe_weights *w, const void 
                         const int32_t *token_ids, int64_t T, void *y, void *stream);
 
 /* moe_forward for a few tokens (T of 1 .. MOE_FEW_MAX_TOKENS): the decode step
- * of a handful of sequences.  The same layer -- every routing, expert type,
- * activation encoding and weight layout moe_forward takes -- without the
- * permutation and with the inputs of a weight stream in mind.  Results agree with moe_forward's to rounding (H keeps 16
- * bits and the weighted expert outputs are summed in fp32, so this form rounds
- * less); the routing follows the same rules.
+ * of a handful of sequences.  The same layer, with every routing, expert type,
+ * activation encoding and weight layout that moe_forward takes, run as a stream
+ * of the chosen experts' weights without a permutation.  Results agree with
+ * moe_forward's to rounding (this form rounds less: H is kept to 16 bits and the
+ * weighted expert outputs are summed in fp32); the routing follows the same
+ * rules.
  *   x, token_ids, y, w, stream  as moe_forward; x, y, the matrices and the FP4
  *       scales 16-byte aligned
  *   ws  device workspace of at least moe_few_workspace_size(cfg, T) bytes,

@@ -560,8 +560,7 @@ def workspace_views(cfg: MoEConfig, T: int, ws):
 
 
 def alloc_few_workspace(cfg, T: int, device="cuda"):
-    """Workspace of moe_forward_few for T tokens (one that fits more fits fewer
-    tokens only of the same configuration)."""
+    """Workspace of moe_forward_few for up to T tokens of this configuration."""
     lay = moe_few_workspace_layout(cfg, T)
     return torch.empty(max(lay["total_bytes"], 1), dtype=torch.uint8, device=device)
 

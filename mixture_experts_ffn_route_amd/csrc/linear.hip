@@ -18,6 +18,14 @@
 // read from LDS while the MFMAs of this one run.  Column operands are read
 // back transposed by ds_read_b64_tr_b16 (fp32: one dword per lane).
 //
+// What bounds it: 256x256 tiles take 64 KB of LDS reads and 32 KB of copies per
+// 1024 MFMA cycles, so LDS is busy three quarters of the time that the matrix
+// cores need at best; 128 x 128 outputs a wave (256 accumulator registers) is
+// the least LDS traffic per product that the registers allow.  bf16 4096x8192
+// ->4096 1200, dx 4096x4096x8192 1280, dW 8192x4096x4096 1340 TFLOP/s; the
+// library's product reaches 1310 at 8192^3, the power limit's clock (2.05 of
+// 2.4 GHz) included.  fp32 143 TFLOP/s (library 150).
+//
 // Copies are buffer loads into LDS: a piece past the end of a matrix or of the
 // contraction arrives as zeros without traffic, which covers every ragged
 // size.  Rows that are not whole 16-byte pieces (odd widths or strides) are
@@ -354,7 +362,7 @@ __device__ __forceinline__ void gemm_tile(const GemmOp &g) {
   // part of LDS (no barrier), so that a lane then has eight consecutive columns
   // of a row and 16 or 8 lanes a whole line.  bf16: the whole tile's residual is
   // asked for at once, into the registers that the operands have left (in 32-row
-  // pieces a read's latency bounded it: 161 instead of 140 us at 4096x2048->7168).
+  // pieces a read's latency bounded it: 161 instead of 146 us at 4096x2048->7168).
   constexpr int NJ = DUAL ? NI / 2 : NI;       // output column blocks of the wave
   constexpr int PC = NJ * 4;                   // pieces of 8 columns per row
   constexpr int PPI = 32 * PC / 64;            // pieces per lane and 32 rows

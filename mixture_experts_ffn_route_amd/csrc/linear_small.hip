@@ -8,7 +8,9 @@
 // into the wave's own part of LDS and read back in MFMA operand order (the
 // operand order straight from memory, 16 rows x 64 bytes a load, reaches 5 of
 // the 7 TB/s); x comes from L2 to registers.  MFMA rows are rows of W, columns
-// rows of x, so a lane ends with four consecutive columns of y.
+// rows of x, so a lane ends with four consecutive columns of y.  1x7168->2x2048
+// swiglu bf16 (59 MB) 11.5 us, 5.1 TB/s with launch and start; 1x5120->27648 (283
+// MB) 45 us, 6.3 TB/s.
 //
 // small_forward_kernel and small_backward_kernel, small products: time goes by
 // launches and the longest chain in a workgroup, not by bytes or MFMAs.  A
@@ -19,6 +21,7 @@
 // padded copy.  The backward kernel forms dz = dy act'(z) as it reads dy and z
 // and computes dx, dW and db in one launch: tiles recompute dz instead of waiting
 // for it.  fp32 MFMAs for both types; the products of bf16 values are exact.
+// 203x777->1023 fp32 gelu 12 us; 301x256->320 fp32 silu forward 6, backward 12 us.
 
 #include "linear_device.h"
 
