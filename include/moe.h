@@ -541,7 +541,8 @@ size_t moe_linear_workspace_size(const moe_linear_config *cfg, int32_t backward)
  *             which the gradient needs unless the activation is NONE.  Rounded
  *             to dtype, but never across the clamp's border
  *   ws        device workspace of at least moe_linear_workspace_size(cfg, 0)
- *             bytes, 256-byte aligned; nothing in it needs to start at any value
+ *             bytes, 256-byte aligned; nothing in it needs to start at any
+ *             value.  Calls that share one must be ordered on one stream
  * Products accumulate in fp32, the epilogue is fp32, y is rounded once.  All
  * sizes and strides are taken; for large products, rows that are not whole
  * 16-byte pieces are first copied to padded ones in the workspace.  No output

@@ -430,6 +430,8 @@ def _linear_check(cfg: LinearConfig, where, matrices, contiguous):
             raise ValueError(f"{where}: {name} is on {t.device}, others on {device}")
     if cfg.rows and (device is None or device.type != "cuda"):
         raise ValueError(f"{where}: tensors on {device}, expected a GPU")
+    if cfg.rows and device.index != torch.cuda.current_device():
+        raise ValueError(f"{where}: tensors on {device}, not the current device")
 
 
 def _raw(t):
