@@ -394,7 +394,10 @@ __device__ __forceinline__ void gemm_tile(const GemmOp &g) {
     }
   };
   const bool has_res = RES && g.e.residual && !plain;
+  Biases<T, DUAL> bias;                        // a lane's columns are the same in every piece
+  static_assert(64 % PC == 0, "they are");
   __builtin_amdgcn_s_waitcnt(0);
+  if (RES && !plain) bias.fetch(g.e, place(0, 0).n);
   if (AHEAD > 1 && has_res) {
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) fetch(i, ahead[i]);
@@ -437,7 +440,7 @@ __device__ __forceinline__ void gemm_tile(const GemmOp &g) {
                   g.e.vec != 0);
       } else {
         if (has_res) widen8<T>(rs, res[q]);
-        finish8<T, DUAL>(g.e, v, u, rs, o.m, o.n);
+        finish8<T, DUAL>(g.e, v, u, bias, rs, o.m, o.n);
       }
     }
     __builtin_amdgcn_wave_barrier();
@@ -461,6 +464,8 @@ __global__ __launch_bounds__(256) void sum_parts_kernel(const GemmOp g) {
   const int64_t m = mm - half * g.M;
   const int D = DUAL ? 2 : g.halves;
   float v[8] = {}, u[8] = {}, t[8], res[8];
+  Biases<T, DUAL> bias;
+  bias.fetch(g.e, n);
   if (g.e.residual)
     load8<T>(res, (const T *)g.e.residual + m * g.e.ld_res + n, g.e.N - n, g.e.vec != 0);
   for (int p = 0; p < g.parts; ++p) {
@@ -476,7 +481,7 @@ __global__ __launch_bounds__(256) void sum_parts_kernel(const GemmOp g) {
   }
   Epilogue e = g.e;
   if (half) e.y = g.y_up;
-  finish8<T, DUAL>(e, v, u, res, m, n);
+  finish8<T, DUAL>(e, v, u, bias, res, m, n);
 }
 
 // ---------------------------------------------------------------------------

@@ -74,6 +74,8 @@ __device__ __forceinline__ void few_rows(const SmallArgs &a) {
   const int ft = threadIdx.x / PC, fn = n0 + (int)(threadIdx.x % PC) * 8;
   const bool finishes = threadIdx.x < 16 * PC && ft < M && fn < N;
   Raw8<T> res = {};
+  Biases<T, DUAL> bias;
+  if (finishes) bias.fetch(a.e, fn);
   if (finishes && a.e.residual)
     fetch8<T>(res, (const T *)a.e.residual + ft * a.e.ld_res + fn, N - fn, a.e.vec != 0);
 
@@ -136,7 +138,7 @@ __device__ __forceinline__ void few_rows(const SmallArgs &a) {
     }
   }
   widen8<T>(rs, res);
-  finish8<T, DUAL>(a.e, v, u, rs, ft, fn);
+  finish8<T, DUAL>(a.e, v, u, bias, rs, ft, fn);
 }
 template <typename T, bool DUAL>
 __global__ __launch_bounds__(512, 4) void few_rows_kernel(const SmallArgs a) {
@@ -253,6 +255,8 @@ __global__ __launch_bounds__(512, 2) void small_forward_kernel(const SmallArgs a
   const int fn = n0 + fc * 8;
   const bool finishes = threadIdx.x < 128 && fm < a.M && fn < a.e.N;
   Raw8<T> res = {};
+  Biases<T, DUAL> bias;
+  if (finishes) bias.fetch(a.e, fn);
   if (finishes && a.e.residual)
     fetch8<T>(res, (const T *)a.e.residual + fm * a.e.ld_res + fn, a.e.N - fn, a.e.vec != 0);
   f32x16 acc = {}, acc_up = {};
@@ -282,7 +286,7 @@ __global__ __launch_bounds__(512, 2) void small_forward_kernel(const SmallArgs a
   take_sums(v, lds[0][0], ft, fc);
   if constexpr (DUAL) take_sums(u, lds[0][1], ft, fc);
   widen8<T>(rs, res);
-  finish8<T, DUAL>(a.e, v, u, rs, fm, fn);
+  finish8<T, DUAL>(a.e, v, u, bias, rs, fm, fn);
 }
 
 // dz (or du) of a chunk, from dy, z (and z_up) read in the same order.
