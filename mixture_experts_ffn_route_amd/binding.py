@@ -165,9 +165,15 @@ def _ptr(t):
     raise TypeError(type(t))
 
 
+# The current stream's handle without a Stream object around it (3 us a call).
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if isinstance(stream, int):              # a raw hipStream_t (0 = default stream)
         return ctypes.c_void_p(stream)
+    if stream is None and _current_raw_stream is not None:
+        return ctypes.c_void_p(_current_raw_stream(torch.cuda.current_device()))
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
