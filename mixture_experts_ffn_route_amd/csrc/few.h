@@ -33,7 +33,7 @@ struct FewArgs {
   int32_t *plan_mask;                          // [T] choices that hold a row
   float *yrows;                                // [T*k + T, d] weighted expert outputs
   void *y;
-  int score_items;                             // set by launch_few
+  int score_items, small_gate;                 // set by launch_few
 };
 
 int few_logit_parts(int d, bool f32);

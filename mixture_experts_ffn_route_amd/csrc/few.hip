@@ -5,8 +5,8 @@
 // At these sizes the layer is a stream of the chosen experts' weights: every
 // weight is used by one or two tokens, so the time is (bytes of the distinct
 // chosen experts) / (HBM rate) plus launches and the waits between dependent
-// steps.  Five launches, no permutation:
-//   few_scores   gate logits and affinities; MXFP8 codes of x
+// steps.  Four or five launches, no permutation:
+//   few_scores   gate logits (a small gate's: few_plan); MXFP8 codes of x
 //   few_plan     one workgroup selects the experts of every token and lists the
 //                distinct ones ("slots"); meanwhile the others stream the shared
 //                expert's gate|up, which needs x alone
@@ -472,6 +472,54 @@ __device__ __forceinline__ float mx_element(float v, int X) {
 // workgroup takes 16 experts and one of KS parts of the inputs, its four waves
 // splitting those, each with one burst of loads: latency, not bandwidth, is
 // what the gate matrix (a few MB) costs.
+// Logits of 16 experts from n0 for every token over stages first .. end - 1, of
+// which wave kw of four takes every fourth: red[token * 16 + expert].
+template <int F>
+__device__ __forceinline__ void score_block(const FewArgs &a, int n0, int first, int end, int kw,
+                                            int lane, float *red) {
+  constexpr int DEPTH = 4;
+  constexpr int es = F == F_F32 ? 4 : 2;
+  const int d = a.d, T = a.T, r = lane & 15, q = lane >> 4;
+  const TSrc ts = {resource(a.x, (int64_t)T * d * es), resource(a.x, 0)};
+  const int have = a.E - n0 < 16 ? a.E - n0 : 16;
+  const WSrc w = {resource((const uint8_t *)a.gate_w + (int64_t)n0 * d * es, (int64_t)have * d * es),
+                  resource(a.gate_w, 0)};
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  Tokens<F, false> tk[DEPTH];
+  u32x4 wv[DEPTH][2];
+  auto load = [&](int p, int st) {
+    load_tokens<F, false>(tk[p], ts, d, lane, r, st, st < end && r < T ? 0u : kOut);
+    if constexpr (F == F_F32) {
+      wv[p][0] = w_direct(w, d, lane, 0, st);
+    } else {
+      const uint32_t off = ((uint32_t)r * d + st * 64 + q * 8) * 2;
+      wv[p][0] = load16(w.r, st < end ? off : kOut);
+      wv[p][1] = load16(w.r, st < end ? off + 64 : kOut);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // whole bursts of DEPTH stages a wave; tokens past the end read as zeros
+  for (int st = first + kw; st < end; st += 4 * DEPTH) {
+#pragma unroll
+    for (int p = 0; p < DEPTH; ++p) load(p, st + 4 * p);
+#pragma unroll
+    for (int p = 0; p < DEPTH; ++p) {
+      if constexpr (F == F_F32) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          acc = __builtin_amdgcn_mfma_f32_16x16x4f32(
+              __uint_as_float(tk[p].v[0][i]),
+              st + 4 * p < end ? __uint_as_float(wv[p][0][i]) : 0.f, acc, 0, 0, 0);
+      } else {
+        acc = mma16(tk[p].v[0], wv[p][0], acc);
+        acc = mma16(tk[p].v[1], wv[p][1], acc);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) red[(q * 4 + i) * 16 + r] = acc[i];
+}
+
 template <int F>
 __global__ __launch_bounds__(256) void few_scores(const FewArgs a) {
   __shared__ float red[4 * 256];
@@ -480,49 +528,10 @@ __global__ __launch_bounds__(256) void few_scores(const FewArgs a) {
   const int d = a.d, T = a.T;
   int item = blockIdx.x;
   if (item < a.score_items) {
-    constexpr int KST = stage_inputs<F>(), DEPTH = 4;
-    constexpr int es = F == F_F32 ? 4 : 2;
+    constexpr int KST = stage_inputs<F>();
     const int part = item % a.KS, n0 = item / a.KS * 16, nst = (d + KST - 1) / KST;
-    const int end = (int)((int64_t)nst * (part + 1) / a.KS);
-    const int r = lane & 15, q = lane >> 4;
-    const TSrc ts = {resource(a.x, (int64_t)T * d * es), resource(a.x, 0)};
-    const int have = a.E - n0 < 16 ? a.E - n0 : 16;
-    const WSrc w = {resource((const uint8_t *)a.gate_w + (int64_t)n0 * d * es, (int64_t)have * d * es),
-                    resource(a.gate_w, 0)};
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    Tokens<F, false> tk[DEPTH];
-    u32x4 wv[DEPTH][2];
-    auto load = [&](int p, int st) {
-      load_tokens<F, false>(tk[p], ts, d, lane, r, st, st < end && r < T ? 0u : kOut);
-      if constexpr (F == F_F32) {
-        wv[p][0] = w_direct(w, d, lane, 0, st);
-      } else {
-        const uint32_t off = ((uint32_t)r * d + st * 64 + q * 8) * 2;
-        wv[p][0] = load16(w.r, st < end ? off : kOut);
-        wv[p][1] = load16(w.r, st < end ? off + 64 : kOut);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    };
-    // whole bursts of DEPTH stages a wave; tokens past the end read as zeros
-    for (int st = (int)((int64_t)nst * part / a.KS) + wave; st < end; st += 4 * DEPTH) {
-#pragma unroll
-      for (int p = 0; p < DEPTH; ++p) load(p, st + 4 * p);
-#pragma unroll
-      for (int p = 0; p < DEPTH; ++p) {
-        if constexpr (F == F_F32) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            acc = __builtin_amdgcn_mfma_f32_16x16x4f32(
-                __uint_as_float(tk[p].v[0][i]),
-                st + 4 * p < end ? __uint_as_float(wv[p][0][i]) : 0.f, acc, 0, 0, 0);
-        } else {
-          acc = mma16(tk[p].v[0], wv[p][0], acc);
-          acc = mma16(tk[p].v[1], wv[p][1], acc);
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) red[wave * 256 + (q * 4 + i) * 16 + r] = acc[i];
+    score_block<F>(a, n0, (int)((int64_t)nst * part / a.KS),
+                   (int)((int64_t)nst * (part + 1) / a.KS), wave, lane, red + wave * 256);
     __syncthreads();
     const int t = threadIdx.x >> 4, e = n0 + (threadIdx.x & 15);
     if (t < T && e < a.E)
@@ -705,6 +714,7 @@ struct PlanScratch {
   float cell_w[256 * kRows];
   int16_t cell_row[256 * kRows];
 };
+template <int F>
 __device__ __forceinline__ void make_plan(const FewArgs &a, PlanScratch &p, float *scores) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int T = a.T, k = a.k, E = a.E, pairs = T * k;
@@ -721,13 +731,28 @@ __device__ __forceinline__ void make_plan(const FewArgs &a, PlanScratch &p, floa
     float *bias = (float *)p.lead;             // until the leaders
     if (a.bias)
       for (int i = tid; i < E; i += 1024) bias[i] = a.bias[i];
+    float *red = scores + kRows * 512;
+    if (a.small_gate) {                        // four waves a block of 16 experts
+      if (wave / 4 * 16 < E)
+        score_block<F>(a, wave / 4 * 16, 0, (a.d + stage_inputs<F>() - 1) / stage_inputs<F>(),
+                       wave & 3, lane, red + wave * 256);
+      __syncthreads();
+    }
     for (int i = tid; i < n; i += 1024) {
-      float part[kLogitParts];
+      float z;
+      if (a.small_gate) {
+        const int t = i / E, e = i - t * E;
+        const float *r = red + e / 16 * 1024 + t * 16 + e % 16;
+        z = ((r[0] + r[256]) + r[512]) + r[768];
+      } else {
+        float part[kLogitParts];
 #pragma unroll
-      for (int q = 0; q < kLogitParts; ++q) part[q] = q < a.KS ? a.scores[(int64_t)q * n + i] : 0.f;
-      float z = part[0];
+        for (int q = 0; q < kLogitParts; ++q)
+          part[q] = q < a.KS ? a.scores[(int64_t)q * n + i] : 0.f;
+        z = part[0];
 #pragma unroll
-      for (int q = 1; q < kLogitParts; ++q) z += part[q];
+        for (int q = 1; q < kLogitParts; ++q) z += part[q];
+      }
       if (a.score == MOE_SCORE_SIGMOID) z = 1.f / (1.f + expf(-z));
       else if (a.score == MOE_SCORE_SQRTSOFTPLUS)
         z = sqrtf(fmaxf(z, 0.f) + log1pf(expf(-fabsf(z))));
@@ -841,9 +866,9 @@ __global__ __launch_bounds__(1024) void few_plan(const FewArgs a) {
   constexpr int PLAN = (int)sizeof(PlanScratch);
   __shared__ __attribute__((aligned(1024))) uint8_t R0[16 * SLOT > PLAN ? 16 * SLOT : PLAN];
   __shared__ __attribute__((aligned(1024))) uint8_t R1[16 * 4096];
-  static_assert(sizeof(R1) >= kRows * 512 * 4, "affinities of all tokens");
+  static_assert(sizeof(R1) >= kRows * 512 * 4 + 16 * 256 * 4, "affinities, logits of a small gate");
   if (blockIdx.x == 0) {
-    make_plan(a, *(PlanScratch *)R0, (float *)R1);
+    make_plan<F>(a, *(PlanScratch *)R0, (float *)R1);
     return;
   }
   const int lane = threadIdx.x & 63;
@@ -1137,7 +1162,13 @@ int few_logit_parts(int d, bool f32) {
 
 hipError_t launch_few(FewArgs a, const moe_config &cfg, hipStream_t s) {
   const bool tiled = cfg.weight_layout == MOE_LAYOUT_TILED;
-  a.score_items = cfg.route_mode == MOE_ROUTE_LEARNED ? (a.E + 15) / 16 * a.KS : 0;
+  const bool learned = cfg.route_mode == MOE_ROUTE_LEARNED;
+  // A gate of at most 64 experts and 2 KB a row: the routing workgroup computes
+  // its logits itself, two bursts of loads in place of a launch (20.6 -> 18.9 us for
+  // a 3-token layer of 16 experts).  MXFP8 layers need the launch for x's codes.
+  a.small_gate = learned && a.E <= 64 && !a.xq &&
+                 (int64_t)a.d * (cfg.act_dtype == MOE_DTYPE_F32 ? 4 : 2) <= 2048;
+  a.score_items = learned && !a.small_gate ? (a.E + 15) / 16 * a.KS : 0;
   if (cfg.act_dtype == MOE_DTYPE_F32) return run_few<F_F32, false>(a, s);
   if (cfg.expert_dtype == MOE_DTYPE_FP8_E4M3_B128) return run_few<F_MX8, true>(a, s);
   if (cfg.expert_dtype == MOE_DTYPE_BF16)

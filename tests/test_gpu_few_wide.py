@@ -1,5 +1,6 @@
 """moe_forward_few on FP4 layers so wide that a row's scales go through LDS in
-several pieces, and at the width where its down launch changes form."""
+several pieces, at the width where its down launch changes form, and around the
+size from which a gate has a launch of its own."""
 
 from dataclasses import replace
 
@@ -41,3 +42,22 @@ def test_wide_fp4(base, dim, inter, T, gpu, monkeypatch):
     yt, _ = F.few(tcfg, tlayer, T)
     torch.cuda.synchronize()
     assert torch.equal(y, yt)
+
+
+@pytest.mark.parametrize("base,dim,experts", [
+    ("tiny_fp32", 512, 64), ("tiny_fp32", 512, 65), ("tiny_fp32", 513, 64), ("tiny_fp32", 511, 33),
+    ("v3_small", 1024, 64), ("v3_small", 1088, 64), ("v3_small", 1024, 72), ("v3_small", 64, 17)])
+@pytest.mark.parametrize("T", [1, 16])
+def test_gate_sizes(base, dim, experts, T, gpu, monkeypatch):
+    """Around the largest gate whose logits need no launch of their own."""
+    w = W[base]
+    wl = replace(w, name=f"{base}_{dim}_{experts}", T=16, cfg=replace(
+        w.cfg, dim=dim, n_routed_experts=experts, n_expert_groups=1, n_limited_groups=1,
+        n_activated_experts=3))
+    monkeypatch.setitem(F.LAYERS, wl.name, wl)
+    wl, cfg, run, plain = F.make(wl.name, T, gpu)
+    print(f"[few] {wl.name} T={T}", flush=True)
+    ws = torch.full((B.moe_few_workspace_size(cfg, T),), 0xFF, dtype=torch.uint8, device=gpu)
+    y, _ = F.few(cfg, run, T, ws)
+    torch.cuda.synchronize()
+    F.check(wl, cfg, plain, T, y, ws, f"{wl.name} T={T}")
