@@ -523,13 +523,22 @@ __global__ __launch_bounds__(256) void slope_kernel(const SlopeArgs a) {
   const int left = a.N - n;
   const bool vec = a.vec != 0;
   float s[D][8] = {};
+  // a row's loads are under way while the one before is finished
+  Raw8<T> ng = {}, nz = {}, nu = {};
+  auto fetch = [&](int64_t m) {
+    if (left <= 0 || m >= hi) return;
+    fetch8<T>(ng, (const T *)a.dy + m * a.ld_dy + n, left, vec);
+    if (a.z) fetch8<T>(nz, (const T *)a.z + m * a.N + n, left, vec);
+    if constexpr (DUAL) fetch8<T>(nu, (const T *)a.z_up + m * a.N + n, left, vec);
+  };
+  fetch(lo + r0);
   for (int64_t m = lo + r0; m < hi; m += 32) {
     float g[8], z[8], u[8], dz[8], du[8];
     if (left <= 0 && n >= a.ldz) break;
-    load8<T>(g, (const T *)a.dy + m * a.ld_dy + n, left, vec);
-    if (a.z) load8<T>(z, (const T *)a.z + m * a.N + n, left, vec);
-    else for (float &v : z) v = 0.f;
-    if constexpr (DUAL) load8<T>(u, (const T *)a.z_up + m * a.N + n, left, vec);
+    widen8<T>(g, ng);
+    widen8<T>(z, nz);
+    if constexpr (DUAL) widen8<T>(u, nu);
+    fetch(m + 32);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       // `none` has slope 1 for any z
