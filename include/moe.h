@@ -399,7 +399,9 @@ int moe_forward_noalloc(const moe_config *cfg, const moe_weights *w, const void 
  * of the chosen experts' weights without a permutation.  Results agree with
  * moe_forward's to rounding (this form rounds less: H is kept to 16 bits and the
  * weighted expert outputs are summed in fp32); the routing follows the same
- * rules.
+ * rules.  A NaN passes the clamp, and in MXFP8 rows a NaN or an infinity is the
+ * NaN code, so that a token's bad input or weight shows in its output
+ * (moe_forward has the clamp's or the code's bound in its place).
  *   x, token_ids, y, w, stream  as moe_forward; x, y, the matrices and the FP4
  *       scales 16-byte aligned
  *   ws  device workspace of at least moe_few_workspace_size(cfg, T) bytes,

@@ -455,7 +455,24 @@ __device__ __forceinline__ void store_hilo(bf16 *hi, bf16 *lo, int64_t at, float
   lo[at] = (__float_as_uint(hf) & 0x7F800000u) == 0x7F800000u ? (bf16)0.f : (bf16)(v - hf);
 }
 
-// Shared exponent of an MXFP8 block with maximum magnitude amax (OCP MX).
+// SwiGLU of a gate / up pair as swiglu_pair computes it, clamped by comparisons
+// that a NaN passes (a minimum or maximum would put the bound in its place).
+__device__ __forceinline__ float swiglu_few(float g, float u, float L) {
+  if (L > 0.f) {
+    g = g > L ? L : g;
+    u = u > L ? L : (u < -L ? -L : u);
+  }
+  return swiglu_pair(g, u, 0.f);
+}
+
+// MXFP8 (OCP MX): what a value adds to its block's maximum magnitude, the
+// block's shared exponent, and the element to encode.  E4M3 has no infinity, and
+// a maximum over NaN or infinities gives no exponent: those values take the NaN
+// code each and leave the block's exponent to the others.
+__device__ __forceinline__ float mx_magnitude(float v) {
+  const float m = fabsf(v);
+  return m < INFINITY ? m : 0.f;
+}
 __device__ __forceinline__ int mx_exponent(float amax) {
   if (!(amax > 0.f)) return 0;
   int ex;
@@ -464,7 +481,7 @@ __device__ __forceinline__ int mx_exponent(float amax) {
   return X < -127 ? -127 : (X > 127 ? 127 : X);
 }
 __device__ __forceinline__ float mx_element(float v, int X) {
-  return fminf(fmaxf(ldexpf(v, -X), -448.f), 448.f);
+  return fabsf(v) < INFINITY ? fminf(fmaxf(ldexpf(v, -X), -448.f), 448.f) : NAN;
 }
 
 // ---------------------------------------------------------------------------
@@ -552,7 +569,7 @@ __global__ __launch_bounds__(256) void few_scores(const FewArgs a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         v[8 * c + j] = (float)w[j];
-        amax = fmaxf(amax, fabsf(v[8 * c + j]));
+        amax = fmaxf(amax, mx_magnitude(v[8 * c + j]));
       }
     }
     const int X = mx_exponent(amax);
@@ -890,7 +907,7 @@ __global__ __launch_bounds__(1024) void few_plan(const FewArgs a) {
       g += red[w * (SLOT / 4) + e];
       u += red[w * (SLOT / 4) + 256 + e];
     }
-    const float v = swiglu_pair(g, u, a.limit);
+    const float v = swiglu_few(g, u, a.limit);
     const int64_t at = (int64_t)(a.T * a.k + t) * a.I + n;
     if constexpr (F == F_F32) ((float *)a.h)[at] = v;
     else store_hilo((bf16 *)a.h, (bf16 *)a.h_lo, at, v);
@@ -958,9 +975,9 @@ __global__ __launch_bounds__(256, 2) void few_up(const FewArgs a) {
         g += red[w * (SLOT / 4) + el];
         u += red[w * (SLOT / 4) + NB * 256 + el];
       }
-      const float v = swiglu_pair(g, u, a.limit);
+      const float v = swiglu_few(g, u, a.limit);
       if constexpr (MX) {
-        float amax = fabsf(v);
+        float amax = mx_magnitude(v);
         amax = fmaxf(amax, xor_lane<1>(amax));
         amax = fmaxf(amax, xor_lane<2>(amax));
         amax = fmaxf(amax, xor_lane<4>(amax));

@@ -1,0 +1,105 @@
+"""moe_forward_few on inputs that a plain batch does not hold: each test is of one
+edge, named by it."""
+
+from dataclasses import replace
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from mixture_experts_ffn_route_amd import binding as B
+from mixture_experts_ffn_route_amd import config as C
+from tests import parity_helpers as H
+from tests import test_gpu_few as F
+
+pytestmark = pytest.mark.gpu
+
+W = C.SMALL_WORKLOADS
+T = 6
+
+
+def put(monkeypatch, base, name, **change):
+    """A layer of its own name, from a named one with another configuration."""
+    wl = replace(W[base], name=name, T=16, cfg=replace(W[base].cfg, **change))
+    monkeypatch.setitem(F.LAYERS, name, wl)
+    return name
+
+
+def hashed(monkeypatch, base, **change):
+    """The layer under hash routing (weights that no input reaches) and a clamp."""
+    return put(monkeypatch, base, f"{base}_hashed", route_mode="hash", vocab_size=500,
+               n_expert_groups=1, n_limited_groups=1, n_activated_experts=2, swiglu_limit=10.0,
+               has_bias=False, **change)
+
+
+def h_values(cfg, ws, T):
+    """H of the routed pairs as the call left it: fp32, the high bf16 halves or MXFP8 codes."""
+    lay = B.moe_few_workspace_layout(cfg, T)
+    n, I = T * cfg.n_activated_experts, cfg.moe_inter_dim
+    if cfg.act_quant == "mxfp8":
+        return ws[lay["hq"]:lay["hq"] + n * I].view(n, I)
+    dt, size = (torch.float32, 4) if cfg.act_dtype == "f32" else (torch.bfloat16, 2)
+    return ws[lay["h"]:lay["h"] + size * n * I].view(dt).view(n, I)
+
+
+@pytest.mark.parametrize("base", ["tiny_fp32", "hash_small", "fp4_small", "fp4_mx_small", "fp8_mx_small"])
+@pytest.mark.parametrize("shared", [0, 1])
+def test_nan_token_comes_out_nan(base, shared, gpu, monkeypatch):
+    wl, cfg, run, _ = F.make(hashed(monkeypatch, base, n_shared_experts=shared), T, gpu)
+    y0, _ = F.few(cfg, run, T)
+    x = run["x"].clone()
+    x[3] = float("nan")
+    y1, _ = F.few(cfg, run, T, x=x)
+    x[3] = run["x"][3]
+    x[3, 5] = float("nan")                     # one input, in one MXFP8 block
+    y2, ws = F.few(cfg, run, T, x=x)
+    torch.cuda.synchronize()
+    keep = [t for t in range(T) if t != 3]
+    for y in (y1, y2):
+        assert torch.isnan(y[3].float()).all()
+        assert torch.equal(y[keep], y0[keep])
+    if cfg.act_quant == "mxfp8":
+        assert bool(((h_values(cfg, ws, T)[6:8] & 0x7F) == 0x7F).all())    # token 3's rows, E4M3 NaN
+
+
+@pytest.mark.parametrize("base", ["tiny_fp32", "hash_small"])
+@pytest.mark.parametrize("name", ["w_gate", "w_up", "sh_gate", "sh_up"])
+def test_nan_weight_reaches_its_tokens(base, name, gpu, monkeypatch):
+    wl, cfg, run, _ = F.make(hashed(monkeypatch, base), T, gpu)
+    y0, ws = F.few(cfg, run, T)
+    torch.cuda.synchronize()
+    idx = B.few_views(cfg, T, ws)["route_indices"]
+    w = run[name].clone()
+    if name.startswith("sh"):
+        w[7, 3] = float("nan")
+        hit = torch.ones(T, dtype=torch.bool, device=gpu)
+    else:
+        e = int(idx[0, 0])
+        w[e, 7, 3] = float("nan")
+        hit = (idx == e).any(dim=1)
+        assert bool((~hit).any())
+    y1, _ = F.few(cfg, dict(run, **{name: w}), T)
+    torch.cuda.synchronize()
+    assert torch.isnan(y1[hit].float()).all()
+    assert torch.equal(y1[~hit], y0[~hit])
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_mxfp8_block_keeps_its_other_codes(value, gpu, monkeypatch):
+    """A value that E4M3 has no number for becomes its NaN; the block's scale and
+    other codes are those of the block without it."""
+    wl, cfg, run, _ = F.make(hashed(monkeypatch, "fp4_mx_small"), T, gpu)
+    x = run["x"].clone()
+    x[3, 5] = value
+    _, ws = F.few(cfg, run, T, x=x)
+    torch.cuda.synchronize()
+    lay, d = B.moe_few_workspace_layout(cfg, T), cfg.dim
+    codes = H.cpu_np(ws[lay["xq"]:lay["xq"] + T * d]).reshape(T, d)
+    scales = H.cpu_np(ws[lay["xq_scales"]:lay["xq_scales"] + T * d // 32]).reshape(T, -1)
+    x[3, 5] = 0
+    want, want_scales = oracle.mxfp8_quantize(H.f64(x))
+    assert np.array_equal(scales, want_scales)
+    assert codes[3, 5] & 0x7F == 0x7F
+    codes[3, 5] = want[3, 5]
+    assert np.array_equal(codes & 0x7F, want & 0x7F)
