@@ -455,14 +455,18 @@ __device__ __forceinline__ void store_hilo(bf16 *hi, bf16 *lo, int64_t at, float
   lo[at] = (__float_as_uint(hf) & 0x7F800000u) == 0x7F800000u ? (bf16)0.f : (bf16)(v - hf);
 }
 
-// SwiGLU of a gate / up pair as swiglu_pair computes it, clamped by comparisons
-// that a NaN passes (a minimum or maximum would put the bound in its place).
+// SwiGLU of a gate / up pair, clamped by comparisons that a NaN passes (a
+// minimum or maximum would put the bound in its place).  H of an fp32 layer is
+// stored as it comes, so its exponential and division are the accurate ones; the
+// others round H to 16 bits or fewer and take the hardware's (swiglu_pair).
+template <int F>
 __device__ __forceinline__ float swiglu_few(float g, float u, float L) {
   if (L > 0.f) {
     g = g > L ? L : g;
     u = u > L ? L : (u < -L ? -L : u);
   }
-  return swiglu_pair(g, u, 0.f);
+  if constexpr (F == F_F32) return g / (1.f + expf(-g)) * u;
+  else return swiglu_pair(g, u, 0.f);
 }
 
 // MXFP8 (OCP MX): what a value adds to its block's maximum magnitude, the
@@ -907,7 +911,7 @@ __global__ __launch_bounds__(1024) void few_plan(const FewArgs a) {
       g += red[w * (SLOT / 4) + e];
       u += red[w * (SLOT / 4) + 256 + e];
     }
-    const float v = swiglu_few(g, u, a.limit);
+    const float v = swiglu_few<F>(g, u, a.limit);
     const int64_t at = (int64_t)(a.T * a.k + t) * a.I + n;
     if constexpr (F == F_F32) ((float *)a.h)[at] = v;
     else store_hilo((bf16 *)a.h, (bf16 *)a.h_lo, at, v);
@@ -975,7 +979,7 @@ __global__ __launch_bounds__(256, 2) void few_up(const FewArgs a) {
         g += red[w * (SLOT / 4) + el];
         u += red[w * (SLOT / 4) + NB * 256 + el];
       }
-      const float v = swiglu_few(g, u, a.limit);
+      const float v = swiglu_few<F>(g, u, a.limit);
       if constexpr (MX) {
         float amax = mx_magnitude(v);
         amax = fmaxf(amax, xor_lane<1>(amax));

@@ -103,3 +103,29 @@ def test_mxfp8_block_keeps_its_other_codes(value, gpu, monkeypatch):
     assert codes[3, 5] & 0x7F == 0x7F
     codes[3, 5] = want[3, 5]
     assert np.array_equal(codes & 0x7F, want & 0x7F)
+
+
+def test_fp32_swiglu_to_fp32(gpu):
+    """H of an fp32 layer against float64 for gates whose exponential is large:
+    the exponential within 3 ulp (3 2^-23), the sum and the division a rounding
+    each (2^-24), the product by u = 1 exact: 2^-21 in all."""
+    I, d = 1050, 4
+    cfg = C.MoEConfig(dim=d, n_routed_experts=1, n_activated_experts=1, moe_inter_dim=I,
+                      n_shared_experts=1, score_func="softmax", act_dtype="f32", expert_dtype="f32")
+    g = torch.linspace(-85.0, 20.0, I, device=gpu)
+    z = lambda *s: torch.zeros(s, device=gpu)
+    L = dict(x=z(1, d), gate_w=z(1, d), gate_bias=None, w_gate=z(1, I, d), w_up=z(1, I, d),
+             w_down=z(1, d, I), sh_gate=z(I, d), sh_up=z(I, d), sh_down=z(d, I), token_ids=None)
+    L["x"][0, 0] = 1
+    for n in ("w_gate", "sh_gate"):
+        L[n][..., 0] = g
+    for n in ("w_up", "sh_up"):
+        L[n][..., 0] = 1
+    _, ws = F.few(cfg, L, 1)
+    torch.cuda.synchronize()
+    lay = B.moe_few_workspace_layout(cfg, 1)
+    h = ws[lay["h"]:lay["h"] + 8 * I].view(torch.float32).view(2, I).double()     # routed, shared
+    want = g.double() / (1 + torch.exp(-g.double()))
+    err = ((h - want).abs() / want.abs().clamp(min=1e-300)).amax(dim=1)
+    print(f"[few] fp32 SwiGLU: worst {err.tolist()} of {2.0 ** -21}", flush=True)
+    assert bool(((h - want).abs() <= 2.0 ** -21 * want.abs()).all())
