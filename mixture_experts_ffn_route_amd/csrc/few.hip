@@ -188,14 +188,18 @@ __device__ __forceinline__ void copy_scales(const WSrc &w, int K, int k0, int wa
   }
 }
 // The scale byte of row block b's row l % 16 for its 32 inputs of half `half`
-// (of 128 inputs, from the copied span's start k0).
+// (of 128 inputs, from the copied span's start k0); 0 past the row's end.  There
+// codes and tokens are zeros, but the copied piece goes on with the next row's
+// scales, of which a NaN (0xFF) would not vanish in the product (tiled layout: a
+// piece ends with its row block's scales).
 template <bool TILED, int SW>
 __device__ __forceinline__ uint32_t scale_byte(const uint8_t *lds, int K, int k0, int b, int half,
                                                int lane) {
   const int r = 16 * b + (lane & 15), q = lane >> 4;
   if (TILED) return lds[b * 16 * SW + (2 * half + (q >> 1)) * 32 + (lane & 15) * 2 + (q & 1)];
   const int o = ((r * (K / 32) + k0 / 32) & 3) + half * 4 + q;
-  return lds[r * SW + (o ^ scale_swizzle<SW>(r) << 4)];
+  const uint32_t v = lds[r * SW + (o ^ scale_swizzle<SW>(r) << 4)];
+  return k0 + 128 * half + 32 * q < K ? v : 0u;
 }
 
 // ---------------------------------------------------------------------------

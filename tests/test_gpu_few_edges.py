@@ -129,3 +129,46 @@ def test_fp32_swiglu_to_fp32(gpu):
     err = ((h - want).abs() / want.abs().clamp(min=1e-300)).amax(dim=1)
     print(f"[few] fp32 SwiGLU: worst {err.tolist()} of {2.0 ** -21}", flush=True)
     assert bool(((h - want).abs() <= 2.0 ** -21 * want.abs()).all())
+
+
+@pytest.mark.parametrize("base,width", [("fp4_small", 64), ("fp4_small", 448), ("fp4_mx_small", 128),
+                                        ("fp4_mx_small", 384)])
+def test_fp4_scale_stays_in_its_row(base, width, gpu, monkeypatch):
+    """A NaN scale (0xFF) as the first of a row: the row before, whose last
+    stage ends inside that row's scales, does not see it, in either layout."""
+    name = put(monkeypatch, base, f"{base}_{width}", dim=width, moe_inter_dim=width, n_routed_experts=8,
+               n_expert_groups=1, n_limited_groups=1, n_activated_experts=2)
+    wl, cfg, run, _ = F.make(name, T, gpu)
+    y0, ws0 = F.few(cfg, run, T)
+    torch.cuda.synchronize()
+    idx = B.few_views(cfg, T, ws0)["route_indices"]
+    e, n = int(idx[0, 0]), 17
+    hit = (idx == e).any(dim=1)
+    rest = [c for c in range(width) if c != n]
+    bad = dict(run)
+    for s in ("s_gate", "s_up", "s_down"):
+        bad[s] = run[s].clone()
+        bad[s][e, n, 0] = 0xFF
+    tiled_cfg, tiled_bad = B.pack_layer(cfg, bad)
+    _, tiled_good = B.pack_layer(cfg, run)
+    for good, wrong, c in ((run, bad, cfg), (tiled_good, tiled_bad, tiled_cfg)):
+        # the down product alone: outputs of the other columns as they were
+        y1, _ = F.few(c, dict(good, s_down=wrong["s_down"]), T)
+        torch.cuda.synchronize()
+        assert torch.equal(y1[:, rest], y0[:, rest])
+        assert not torch.isfinite(y1[hit][:, n].float()).any()
+        assert torch.equal(y1[~hit], y0[~hit])
+        # gate and up: H of the other columns as it was (an MXFP8 block has a scale of its own)
+        for s in ("s_gate", "s_up"):
+            _, ws1 = F.few(c, dict(good, **{s: wrong[s]}), T)
+            torch.cuda.synchronize()
+            first = [i for i in range(idx.numel()) if int(idx.view(-1)[i]) == e]
+            h0, h1 = (h_values(cfg, w, T)[first] for w in (ws0, ws1))
+            if cfg.act_quant == "mxfp8":
+                assert bool(((h1[:, n] & 0x7F) == 0x7F).all())
+                keep = [c for c in rest if c // 32 != n // 32]
+                assert not bool(((h1[:, rest] & 0x7F) == 0x7F).any())
+            else:
+                assert not torch.isfinite(h1[:, n].float()).any()
+                keep = rest
+            assert torch.equal(h1[:, keep], h0[:, keep])
