@@ -411,7 +411,8 @@ int moe_forward_noalloc(const moe_config *cfg, const moe_weights *w, const void 
  * Only kernels are enqueued: no allocation, memset or synchronisation, so the
  * call can be captured in a HIP graph.  Calls that share a workspace must be
  * ordered on one stream.  T == 0 is a no-op; T above MOE_FEW_MAX_TOKENS, or a
- * dim or moe_inter_dim above MOE_FEW_MAX_DIM, is MOE_ERR_UNSUPPORTED. */
+ * dim or moe_inter_dim above MOE_FEW_MAX_DIM, is MOE_ERR_UNSUPPORTED.  Groups
+ * may have any size, also those that moe_forward refuses. */
 #define MOE_FEW_MAX_TOKENS 16
 #define MOE_FEW_MAX_DIM (1 << 20)
 typedef struct {

@@ -598,7 +598,8 @@ __global__ __launch_bounds__(256) void few_scores(const FewArgs a) {
 
 // ---------------------------------------------------------------------------
 // Selection of one token by one wave, as route.hip's select_token: the same
-// affinities, bias, group limit, top-k and ties.  Lane l holds experts
+// affinities, bias, group limit, top-k and ties, with groups of any size (a
+// group of one expert scores by it alone).  Lane l holds experts
 // l*EPL .. l*EPL+EPL-1.
 template <int CTRL, int ROWS>
 __device__ __forceinline__ float dpp_max_step(float v) {
@@ -618,9 +619,47 @@ __device__ __forceinline__ float wave_max_dpp(float v) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
-template <int EPL>
+// A wave's LDS accesses stay in order across this.
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// Group limit where a group is no power of two of whole lanes, in LDS: `row` holds the
+// token's E keys and becomes 1 for each of the G groups that stays, 0 for the
+// others; `score` takes the groups' scores.  A lane takes groups lane, lane + 64,
+// ...; the loops stay loops, or the selection's registers would spill.
+__device__ __forceinline__ void limit_groups(const FewArgs &a, int lane, float *row, float *score) {
+  const int G = a.G, size = a.E / G;
+  wave_order();
+#pragma unroll 1
+  for (int g = lane; g < G; g += 64) {
+    float a1 = -INFINITY, a2 = -INFINITY;
+#pragma unroll 1
+    for (int e = g * size; e < (g + 1) * size; ++e) {
+      const float v = row[e];
+      if (v > a1) { a2 = a1; a1 = v; } else if (v > a2) { a2 = v; }
+    }
+    score[g] = a.bias && size > 1 ? a1 + a2 : a1;
+  }
+  wave_order();
+#pragma unroll 1
+  for (int g = lane; g < G; g += 64) {
+    const float own = score[g];
+    int rank = 0;
+#pragma unroll 1
+    for (int gg = 0; gg < G; ++gg) {
+      const float v = score[gg];
+      rank += (v > own) || (v == own && gg < g);
+    }
+    row[g] = rank < a.kept ? 1.f : 0.f;
+  }
+  wave_order();
+}
+
+template <int EPL, bool ODD>
 __device__ __forceinline__ void select_few(const FewArgs &a, int t, int lane, float *out_w,
-                                           int32_t *out_e, const float *scores,
+                                           int32_t *out_e, float *scores,
                                            const float *gate_bias) {
   const int E = a.E;
   float s[EPL], key[EPL], bias[EPL];
@@ -651,8 +690,19 @@ __device__ __forceinline__ void select_few(const FewArgs &a, int t, int lane, fl
     // NaN scores come last
     if (lane * EPL + j >= E || key[j] != key[j]) key[j] = -INFINITY;
   }
-  if (a.G > 1) {
-    const int lpg = (E / a.G) / EPL;           // a power of two (checked on the host)
+  if constexpr (ODD) {
+    float *row = scores + t * E;               // read by this wave alone, and no more
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+      if (lane * EPL + j < E) row[lane * EPL + j] = key[j];
+    limit_groups(a, lane, row, scores + (kRows + t) * 512);
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      const int e = lane * EPL + j;
+      if (e < E && row[e / (E / a.G)] == 0.f) key[j] = -INFINITY;
+    }
+  } else if (a.G > 1) {
+    const int size = E / a.G, lpg = size / EPL;  // experts and lanes of a group
     float a1 = -INFINITY, a2 = -INFINITY;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
@@ -669,7 +719,7 @@ __device__ __forceinline__ void select_few(const FewArgs &a, int t, int lane, fl
     MOE_GROUP_MERGE(1) MOE_GROUP_MERGE(2) MOE_GROUP_MERGE(4)
     MOE_GROUP_MERGE(8) MOE_GROUP_MERGE(16) MOE_GROUP_MERGE(32)
 #undef MOE_GROUP_MERGE
-    const float gs = a.bias ? (a1 + a2) : a1;
+    const float gs = a.bias && size > 1 ? a1 + a2 : a1;
     const int g = lane / lpg;
     int rank = 0;
     for (int gg = 0; gg < a.G; ++gg) {
@@ -711,17 +761,18 @@ __device__ __forceinline__ void select_few(const FewArgs &a, int t, int lane, fl
   }
 }
 
+template <bool ODD>
 __device__ __forceinline__ void select_any(const FewArgs &a, int t, int lane, float *w, int32_t *e,
-                                           const float *scores, const float *bias) {
+                                           float *scores, const float *bias) {
   switch ((a.E + 63) / 64) {
-    case 1: return select_few<1>(a, t, lane, w, e, scores, bias);
-    case 2: return select_few<2>(a, t, lane, w, e, scores, bias);
-    case 3: return select_few<3>(a, t, lane, w, e, scores, bias);
-    case 4: return select_few<4>(a, t, lane, w, e, scores, bias);
-    case 5: return select_few<5>(a, t, lane, w, e, scores, bias);
-    case 6: return select_few<6>(a, t, lane, w, e, scores, bias);
-    case 7: return select_few<7>(a, t, lane, w, e, scores, bias);
-    default: return select_few<8>(a, t, lane, w, e, scores, bias);
+    case 1: return select_few<1, ODD>(a, t, lane, w, e, scores, bias);
+    case 2: return select_few<2, ODD>(a, t, lane, w, e, scores, bias);
+    case 3: return select_few<3, ODD>(a, t, lane, w, e, scores, bias);
+    case 4: return select_few<4, ODD>(a, t, lane, w, e, scores, bias);
+    case 5: return select_few<5, ODD>(a, t, lane, w, e, scores, bias);
+    case 6: return select_few<6, ODD>(a, t, lane, w, e, scores, bias);
+    case 7: return select_few<7, ODD>(a, t, lane, w, e, scores, bias);
+    default: return select_few<8, ODD>(a, t, lane, w, e, scores, bias);
   }
 }
 
@@ -739,7 +790,7 @@ struct PlanScratch {
   float cell_w[256 * kRows];
   int16_t cell_row[256 * kRows];
 };
-template <int F>
+template <int F, bool ODD>
 __device__ __forceinline__ void make_plan(const FewArgs &a, PlanScratch &p, float *scores) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int T = a.T, k = a.k, E = a.E, pairs = T * k;
@@ -784,7 +835,7 @@ __device__ __forceinline__ void make_plan(const FewArgs &a, PlanScratch &p, floa
       scores[i] = z;
     }
     __syncthreads();
-    for (int t = wave; t < T; t += 16) select_any(a, t, lane, p.w, p.e, scores, bias);
+    for (int t = wave; t < T; t += 16) select_any<ODD>(a, t, lane, p.w, p.e, scores, bias);
     __syncthreads();
   } else {
     __syncthreads();
@@ -884,16 +935,19 @@ __device__ __forceinline__ void up_tile(const FewArgs &a, const TSrc &xs, const 
 }
 
 // few_plan: workgroup 0 routes; the others stream the shared expert's gate|up,
-// 16 columns each, 16 waves splitting the inputs.
-template <int F, bool TILED>
+// 16 columns each, 16 waves splitting the inputs.  ODD: groups through LDS, a
+// kernel of its own, since that code beside the lanes' one slowed every layer (18.8
+// -> 20.2 us for a 3-token layer of 16 experts without groups).
+template <int F, bool TILED, bool ODD>
 __global__ __launch_bounds__(1024) void few_plan(const FewArgs a) {
   constexpr int SLOT = F == F_F32 ? 2048 : 4096;
   constexpr int PLAN = (int)sizeof(PlanScratch);
   __shared__ __attribute__((aligned(1024))) uint8_t R0[16 * SLOT > PLAN ? 16 * SLOT : PLAN];
   __shared__ __attribute__((aligned(1024))) uint8_t R1[16 * 4096];
   static_assert(sizeof(R1) >= kRows * 512 * 4 + 16 * 256 * 4, "affinities, logits of a small gate");
+  static_assert(sizeof(R1) >= 2 * kRows * 512 * 4, "affinities, scores of odd groups");
   if (blockIdx.x == 0) {
-    make_plan<F>(a, *(PlanScratch *)R0, (float *)R1);
+    make_plan<F, ODD>(a, *(PlanScratch *)R0, (float *)R1);
     return;
   }
   const int lane = threadIdx.x & 63;
@@ -1148,7 +1202,17 @@ hipError_t run_few(FewArgs a, hipStream_t s) {
     if ((err = hipGetLastError()) != hipSuccess) return err;
   }
   const int shared = a.has_shared ? (a.I + 15) / 16 : 0;
-  hipLaunchKernelGGL((few_plan<FS, TILED && F != F_F32>), dim3(1 + shared), dim3(1024), 0, s, a);
+  // lanes hold ceil(E / 64) experts: their selection takes groups of whole lanes,
+  // a power of two of them
+  const int size = a.E / a.G, epl = (a.E + 63) / 64, lanes = size / epl;
+  const bool odd = a.route_mode == MOE_ROUTE_LEARNED && a.G > 1 &&
+                   (size % epl != 0 || (lanes & (lanes - 1)) != 0);
+  if (odd)
+    hipLaunchKernelGGL((few_plan<FS, TILED && F != F_F32, true>), dim3(1 + shared), dim3(1024), 0, s,
+                       a);
+  else
+    hipLaunchKernelGGL((few_plan<FS, TILED && F != F_F32, false>), dim3(1 + shared), dim3(1024), 0,
+                       s, a);
   if ((err = hipGetLastError()) != hipSuccess) return err;
   const int64_t up = (int64_t)pairs * ((a.I + 31) / 32);
   hipLaunchKernelGGL((few_up<F, TILED>), dim3(up < kGroups ? (unsigned)up : kGroups), dim3(256), 0,

@@ -25,7 +25,8 @@ size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
 bool is_pow2(int v) { return v > 0 && (v & (v - 1)) == 0; }
 
-int validate(const moe_config *c) {
+// any_groups: the few-token layer, whose selection takes groups of any size.
+int validate(const moe_config *c, bool any_groups = false) {
   if (!c) return MOE_ERR_INVALID_ARG;
   const int E = c->n_routed_experts, k = c->n_activated_experts, G = c->n_expert_groups;
   if (c->dim < 1 || E < 1 || k < 1 || c->moe_inter_dim < 1) return MOE_ERR_INVALID_ARG;
@@ -78,7 +79,7 @@ int validate(const moe_config *c) {
     if (c->vocab_size < 1 || c->vocab_size > INT32_MAX) return MOE_ERR_INVALID_ARG;
   } else {
     if (E > 512) return MOE_ERR_UNSUPPORTED;
-    if (G > 1) {
+    if (G > 1 && !any_groups) {
       const int epl = (E + 63) / 64;
       const int gs = E / G;
       if (G > 64 || gs % epl != 0 || !is_pow2(gs / epl)) return MOE_ERR_UNSUPPORTED;
@@ -135,7 +136,7 @@ int make_layout(const moe_config *c, int64_t T, moe_ws_layout *out) {
 }
 
 int make_few_layout(const moe_config *c, int64_t T, moe_few_layout *out) {
-  const int st = validate(c);
+  const int st = validate(c, true);
   if (st != MOE_OK) return st;
   if (T < 0) return MOE_ERR_INVALID_ARG;
   // the kernels address rows of x and H with 32-bit byte offsets

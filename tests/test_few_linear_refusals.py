@@ -1,0 +1,21 @@
+"""What moe_forward_few, moe_linear and moe_linear_backward take and refuse,
+without a GPU: nothing here comes to a launch."""
+
+from dataclasses import replace
+
+import pytest
+import torch
+
+from mixture_experts_ffn_route_amd import binding as B
+from mixture_experts_ffn_route_amd import config as C
+
+
+@pytest.mark.parametrize("E,G,kept", [(48, 4, 2), (48, 8, 4), (96, 8, 4), (130, 65, 4), (504, 7, 3), (24, 24, 9)])
+def test_few_takes_groups_of_any_size(E, G, kept):
+    cfg = replace(C.V3_PREFILL.cfg, n_routed_experts=E, n_expert_groups=G, n_limited_groups=kept,
+                  n_activated_experts=4)
+    assert B.alloc_few_workspace(cfg, 16, "cpu").numel() == B.moe_few_workspace_size(cfg, 16) > 0
+    with pytest.raises(B.MoEError):
+        B.alloc_few_workspace(replace(cfg, n_limited_groups=G + 1), 16, "cpu")
+    with pytest.raises(B.MoEError):
+        B.alloc_few_workspace(replace(cfg, n_expert_groups=E - 1), 16, "cpu")

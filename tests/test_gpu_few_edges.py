@@ -172,3 +172,38 @@ def test_fp4_scale_stays_in_its_row(base, width, gpu, monkeypatch):
                 assert not torch.isfinite(h1[:, n].float()).any()
                 keep = rest
             assert torch.equal(h1[:, keep], h0[:, keep])
+
+
+GROUPS = [(48, 4, 2, 6), (48, 8, 5, 6), (96, 8, 3, 8), (130, 10, 4, 5), (130, 65, 7, 6), (504, 7, 3, 8),
+          (21, 3, 2, 5)]
+
+
+@pytest.mark.parametrize("E,G,kept,k", GROUPS)
+@pytest.mark.parametrize("score,bias", [("sigmoid", True), ("softmax", False), ("sqrtsoftplus", True)])
+@pytest.mark.parametrize("T", [1, 13])
+def test_groups_of_any_size(E, G, kept, k, score, bias, T, gpu, monkeypatch):
+    name = put(monkeypatch, "v3_small", f"groups_{E}_{G}", dim=192, moe_inter_dim=64, n_routed_experts=E,
+               n_expert_groups=G, n_limited_groups=kept, n_activated_experts=k, score_func=score,
+               has_bias=bias)
+    wl, cfg, run, plain = F.make(name, T, gpu)
+    ws = torch.full((B.moe_few_workspace_size(cfg, T),), 0xFF, dtype=torch.uint8, device=gpu)
+    y, _ = F.few(cfg, run, T, ws)
+    torch.cuda.synchronize()
+    F.check(wl, cfg, plain, T, y, ws, f"{name} {score} bias={bias} T={T}")
+
+
+@pytest.mark.parametrize("E", [16, 96])
+def test_groups_of_one_expert(E, gpu, monkeypatch):
+    """A group of one expert scores by it alone, with a bias too: the best
+    groups hold the best experts, as without groups."""
+    change = dict(dim=192, moe_inter_dim=64, n_routed_experts=E, n_activated_experts=4)
+    name = put(monkeypatch, "v3_small", f"ones_{E}", n_expert_groups=E, n_limited_groups=9, **change)
+    none = put(monkeypatch, "v3_small", f"none_{E}", n_expert_groups=1, n_limited_groups=1, **change)
+    _, cfg, run, _ = F.make(name, 11, gpu)
+    _, cfg1, run1, _ = F.make(none, 11, gpu)
+    assert run["gate_bias"] is not None
+    y, ws = F.few(cfg, run, 11)
+    y1, ws1 = F.few(cfg1, run1, 11)
+    torch.cuda.synchronize()
+    assert torch.equal(B.few_views(cfg, 11, ws)["route_indices"], B.few_views(cfg1, 11, ws1)["route_indices"])
+    assert torch.equal(y, y1)
