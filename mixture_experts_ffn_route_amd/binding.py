@@ -408,9 +408,10 @@ def _linear_config(cfg: LinearConfig, x, y, residual=None) -> MoeLinearConfigC:
         *(0 if t is None or cfg.rows < 2 else t.stride(0) for t in (x, y, residual)))
 
 
-def _linear_check(cfg: LinearConfig, where, matrices, contiguous):
+def _linear_check(cfg: LinearConfig, where, launches, matrices, contiguous):
     """Types, shapes, strides and devices of a call's tensors (None: not given):
-    the library sees addresses only."""
+    the library sees addresses only.  launches: whether the call writes anything
+    (an empty batch's gradients are written, with zeros)."""
     dt, device = _LINEAR_DTYPE[cfg.dtype], None
     for name, t, shape in matrices:
         if t is None:
@@ -432,11 +433,12 @@ def _linear_check(cfg: LinearConfig, where, matrices, contiguous):
                              f"expected {shape} {dt}")
         if not t.is_contiguous():
             raise ValueError(f"{where}: {name} is not contiguous")
+        device = device or t.device
         if t.device != device:
             raise ValueError(f"{where}: {name} is on {t.device}, others on {device}")
-    if cfg.rows and (device is None or device.type != "cuda"):
+    if launches and (device is None or device.type != "cuda"):
         raise ValueError(f"{where}: tensors on {device}, expected a GPU")
-    if cfg.rows and device.index != torch.cuda.current_device():
+    if launches and device.index != torch.cuda.current_device():
         raise ValueError(f"{where}: tensors on {device}, not the current device")
 
 
@@ -461,8 +463,8 @@ def moe_linear(cfg: LinearConfig, x, w, y, *, bias=None, residual=None, w_up=Non
     pre-activations that moe_linear_backward takes.  x, y and residual may be
     rows of wider buffers.  ws: alloc_linear_workspace."""
     M, K, N = cfg.rows, cfg.in_dim, cfg.out_dim
-    _linear_check(cfg, "moe_linear", [("x", x, (M, K)), ("y", y, (M, N)),
-                                      ("residual", residual, (M, N))],
+    _linear_check(cfg, "moe_linear", cfg.rows > 0,
+                  [("x", x, (M, K)), ("y", y, (M, N)), ("residual", residual, (M, N))],
                   [("w", w, (N, K)), ("w_up", w_up, (N, K)), ("bias", bias, (N,)),
                    ("bias_up", bias_up, (N,)), ("z", z, (M, N)), ("z_up", z_up, (M, N))])
     weights = MoeLinearWeightsC(_raw(w), _raw(w_up), _raw(bias), _raw(bias_up))
@@ -477,7 +479,7 @@ def moe_linear_backward(cfg: LinearConfig, dy, x, w, *, w_up=None, z=None, z_up=
     """Gradients of moe_linear for dy, into the tensors given (the residual's
     is dy itself)."""
     M, K, N = cfg.rows, cfg.in_dim, cfg.out_dim
-    _linear_check(cfg, "moe_linear_backward",
+    _linear_check(cfg, "moe_linear_backward", True,
                   [("dy", dy, (M, N)), ("x", x, (M, K)), ("dx", dx, (M, K))],
                   [("w", w, (N, K)), ("w_up", w_up, (N, K)), ("z", z, (M, N)),
                    ("z_up", z_up, (M, N)), ("dw", dw, (N, K)), ("dw_up", dw_up, (N, K)),

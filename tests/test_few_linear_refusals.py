@@ -19,3 +19,26 @@ def test_few_takes_groups_of_any_size(E, G, kept):
         B.alloc_few_workspace(replace(cfg, n_limited_groups=G + 1), 16, "cpu")
     with pytest.raises(B.MoEError):
         B.alloc_few_workspace(replace(cfg, n_expert_groups=E - 1), 16, "cpu")
+
+
+LINEAR = C.LinearConfig(4, 16, 8)
+
+
+def bf(*shape, device="cpu"):
+    return torch.zeros(shape, dtype=torch.bfloat16, device=device)
+
+
+@pytest.mark.parametrize("grads", [dict(dw=bf(8, 16)), dict(dbias=bf(8)), dict(dw=bf(8, 16), dbias=bf(8))])
+def test_empty_batch_has_its_gradients_checked(grads):
+    """No rows: zeros are written all the same, so not to host memory."""
+    c = replace(LINEAR, rows=0)
+    with pytest.raises(ValueError, match="expected a GPU"):
+        B.moe_linear_backward(c, bf(0, 8), bf(0, 16), bf(8, 16), stream=0, **grads)
+    with pytest.raises(ValueError, match="expected a GPU"):
+        B.moe_linear_backward(c, None, None, None, stream=0, **grads)
+    with pytest.raises(ValueError, match="is on"):
+        B.moe_linear_backward(c, bf(0, 8, device="meta"), None, None, stream=0, **grads)
+
+
+def test_empty_forward_is_a_no_op():
+    B.moe_linear(replace(LINEAR, rows=0), bf(0, 16), bf(8, 16), bf(0, 8), stream=0)
