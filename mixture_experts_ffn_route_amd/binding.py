@@ -408,7 +408,18 @@ def _linear_config(cfg: LinearConfig, x, y, residual=None) -> MoeLinearConfigC:
         *(0 if t is None or cfg.rows < 2 else t.stride(0) for t in (x, y, residual)))
 
 
-def _linear_check(cfg: LinearConfig, where, launches, matrices, contiguous):
+def _ws_check(where, ws, device):
+    """A workspace is memory of the call's device in one piece (None: the library
+    refuses it where it needs one)."""
+    if ws is None:
+        return
+    if not ws.is_contiguous():
+        raise ValueError(f"{where}: ws is not contiguous")
+    if ws.device != device:
+        raise ValueError(f"{where}: ws is on {ws.device}, others on {device}")
+
+
+def _linear_check(cfg: LinearConfig, where, launches, matrices, contiguous, ws):
     """Types, shapes, strides and devices of a call's tensors (None: not given):
     the library sees addresses only.  launches: whether the call writes anything
     (an empty batch's gradients are written, with zeros)."""
@@ -436,9 +447,12 @@ def _linear_check(cfg: LinearConfig, where, launches, matrices, contiguous):
         device = device or t.device
         if t.device != device:
             raise ValueError(f"{where}: {name} is on {t.device}, others on {device}")
-    if launches and (device is None or device.type != "cuda"):
+    if not launches:
+        return
+    _ws_check(where, ws, device)
+    if device is None or device.type != "cuda":
         raise ValueError(f"{where}: tensors on {device}, expected a GPU")
-    if launches and device.index != torch.cuda.current_device():
+    if device.index != torch.cuda.current_device():
         raise ValueError(f"{where}: tensors on {device}, not the current device")
 
 
@@ -466,7 +480,7 @@ def moe_linear(cfg: LinearConfig, x, w, y, *, bias=None, residual=None, w_up=Non
     _linear_check(cfg, "moe_linear", cfg.rows > 0,
                   [("x", x, (M, K)), ("y", y, (M, N)), ("residual", residual, (M, N))],
                   [("w", w, (N, K)), ("w_up", w_up, (N, K)), ("bias", bias, (N,)),
-                   ("bias_up", bias_up, (N,)), ("z", z, (M, N)), ("z_up", z_up, (M, N))])
+                   ("bias_up", bias_up, (N,)), ("z", z, (M, N)), ("z_up", z_up, (M, N))], ws)
     weights = MoeLinearWeightsC(_raw(w), _raw(w_up), _raw(bias), _raw(bias_up))
     _check(_lib.moe_linear(ctypes.byref(_linear_config(cfg, x, y, residual)),
                            ctypes.byref(weights), _raw(x), _raw(residual), _raw(y), _raw(z),
@@ -483,7 +497,7 @@ def moe_linear_backward(cfg: LinearConfig, dy, x, w, *, w_up=None, z=None, z_up=
                   [("dy", dy, (M, N)), ("x", x, (M, K)), ("dx", dx, (M, K))],
                   [("w", w, (N, K)), ("w_up", w_up, (N, K)), ("z", z, (M, N)),
                    ("z_up", z_up, (M, N)), ("dw", dw, (N, K)), ("dw_up", dw_up, (N, K)),
-                   ("dbias", dbias, (N,)), ("dbias_up", dbias_up, (N,))])
+                   ("dbias", dbias, (N,)), ("dbias_up", dbias_up, (N,))], ws)
     weights = MoeLinearWeightsC(_raw(w), _raw(w_up), None, None)
     grads = MoeLinearGradsC(_raw(dx), _raw(dw), _raw(dw_up), _raw(dbias), _raw(dbias_up),
                             0 if dx is None or M < 2 else dx.stride(0))

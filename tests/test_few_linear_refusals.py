@@ -42,3 +42,19 @@ def test_empty_batch_has_its_gradients_checked(grads):
 
 def test_empty_forward_is_a_no_op():
     B.moe_linear(replace(LINEAR, rows=0), bf(0, 16), bf(8, 16), bf(0, 8), stream=0)
+
+
+WRONG_WORKSPACES = [
+    (torch.empty(4096, dtype=torch.uint8), "ws is on cpu"),
+    (torch.empty((64, 64), dtype=torch.uint8, device="meta")[:, :32], "ws is not contiguous"),
+]
+
+
+@pytest.mark.parametrize("ws,message", WRONG_WORKSPACES)
+def test_linear_checks_its_workspace(ws, message):
+    """Tensors that are elsewhere than the workspace; the workspace in pieces."""
+    x, w, y = (bf(*s, device="meta") for s in ((4, 16), (8, 16), (4, 8)))
+    with pytest.raises(ValueError, match=message):
+        B.moe_linear(LINEAR, x, w, y, ws=ws, stream=0)
+    with pytest.raises(ValueError, match=message):
+        B.moe_linear_backward(LINEAR, y, x, w, dx=x, ws=ws, stream=0)
