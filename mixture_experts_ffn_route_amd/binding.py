@@ -189,9 +189,7 @@ def config_c(cfg: MoEConfig) -> MoeConfigC:
 
 
 def weights_c(layer: dict) -> MoeWeightsC:
-    return MoeWeightsC(*[_ptr(layer.get(n)) for n in (
-        "gate_w", "gate_bias", "w_gate", "w_up", "w_down", "s_gate", "s_up", "s_down",
-        "sh_gate", "sh_up", "sh_down", "tid2eid")])
+    return MoeWeightsC(*[_ptr(layer.get(n)) for n, _ in MoeWeightsC._fields_])
 
 
 def moe_status_string(status: int) -> str:
@@ -386,12 +384,62 @@ def moe_few_workspace_size(cfg, T: int) -> int:
     return _lib.moe_few_workspace_size(_config_ref(cfg), T)
 
 
+def _ws_check(where, ws, device):
+    """A workspace is memory of the call's device in one piece (None: the library
+    refuses it where it needs one)."""
+    if ws is None:
+        return
+    if not ws.is_contiguous():
+        raise ValueError(f"{where}: ws is not contiguous")
+    if ws.device != device:
+        raise ValueError(f"{where}: ws is on {ws.device}, others on {device}")
+
+
+def _few_check(c: MoeConfigC, layer, x, token_ids, T, y, ws):
+    """Types, sizes, contiguity and devices of a call's tensors (None: the library
+    refuses it where it needs one); of weights_c's addresses nothing is known."""
+    where, device = "moe_forward_few", None
+    dt = torch.float32 if c.act_dtype == DTYPE["f32"] else torch.bfloat16
+    ids = {ROUTE["hash"]: 1, ROUTE["ngram"]: 2}.get(c.route_mode)
+    for name, t, dtype, width in (("x", x, dt, c.dim), ("y", y, dt, c.dim),
+                                  ("token_ids", token_ids if ids else None, torch.int32, ids)):
+        if t is None:
+            continue
+        if t.dtype is not dtype:
+            raise ValueError(f"{where}: {name} is {t.dtype}, expected {dtype}")
+        if t.numel() < T * width or (dtype is dt and t.shape[-1] != width):
+            raise ValueError(f"{where}: {name} holds {tuple(t.shape)}, expected {T} x {width}")
+        if not t.is_contiguous():
+            raise ValueError(f"{where}: {name} is not contiguous")
+        device = device or t.device
+        if t.device != device:
+            raise ValueError(f"{where}: {name} is on {t.device}, others on {device}")
+    if not isinstance(layer, MoeWeightsC):
+        for name, _ in MoeWeightsC._fields_:
+            t = layer.get(name)
+            if t is None:
+                continue
+            if not t.is_contiguous():
+                raise ValueError(f"{where}: {name} is not contiguous")
+            device = device or t.device
+            if t.device != device:
+                raise ValueError(f"{where}: {name} is on {t.device}, others on {device}")
+    _ws_check(where, ws, device)
+    if device is not None and device.type != "cuda":
+        raise ValueError(f"{where}: tensors on {device}, expected a GPU")
+    if device is not None and device.index != torch.cuda.current_device():
+        raise ValueError(f"{where}: tensors on {device}, not the current device")
+
+
 def moe_forward_few(cfg, layer, x, token_ids, T: int, y, ws, stream=None):
     """moe_forward for T <= MOE_FEW_MAX_TOKENS tokens.  A decode loop may build
     the C structs once and pass them: cfg a MoEConfig or config_c of it, layer
     the weights' dict or weights_c of it.  ws: alloc_few_workspace."""
+    c = cfg if isinstance(cfg, MoeConfigC) else config_c(cfg)
+    if 0 < T <= MOE_FEW_MAX_TOKENS:
+        _few_check(c, layer, x, token_ids, T, y, ws)
     w = layer if isinstance(layer, MoeWeightsC) else weights_c(layer)
-    _check(_lib.moe_forward_few(_config_ref(cfg), ctypes.byref(w), _ptr(x), _ptr(token_ids), T,
+    _check(_lib.moe_forward_few(ctypes.byref(c), ctypes.byref(w), _ptr(x), _ptr(token_ids), T,
                                 _ptr(y), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
                                 _stream(stream)),
            "moe_forward_few")
@@ -406,17 +454,6 @@ def _linear_config(cfg: LinearConfig, x, y, residual=None) -> MoeLinearConfigC:
     return MoeLinearConfigC(
         cfg.rows, cfg.in_dim, cfg.out_dim, DTYPE[cfg.dtype], ACTIVATION[cfg.activation], cfg.limit,
         *(0 if t is None or cfg.rows < 2 else t.stride(0) for t in (x, y, residual)))
-
-
-def _ws_check(where, ws, device):
-    """A workspace is memory of the call's device in one piece (None: the library
-    refuses it where it needs one)."""
-    if ws is None:
-        return
-    if not ws.is_contiguous():
-        raise ValueError(f"{where}: ws is not contiguous")
-    if ws.device != device:
-        raise ValueError(f"{where}: ws is on {ws.device}, others on {device}")
 
 
 def _linear_check(cfg: LinearConfig, where, launches, matrices, contiguous, ws):

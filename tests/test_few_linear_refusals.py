@@ -58,3 +58,43 @@ def test_linear_checks_its_workspace(ws, message):
         B.moe_linear(LINEAR, x, w, y, ws=ws, stream=0)
     with pytest.raises(ValueError, match=message):
         B.moe_linear_backward(LINEAR, y, x, w, dx=x, ws=ws, stream=0)
+
+
+FEW = replace(C.SMALL_WORKLOADS["hash_small"].cfg, dim=64, moe_inter_dim=64, n_routed_experts=4,
+              n_activated_experts=2, vocab_size=10)
+
+
+def few_layer(device):
+    layer = {n: bf(4, 64, 64, device=device) for n in ("w_gate", "w_up", "w_down")}
+    layer.update({n: bf(64, 64, device=device) for n in ("sh_gate", "sh_up", "sh_down")})
+    layer["tid2eid"] = torch.zeros((10, 2), dtype=torch.int32, device=device)
+    return layer
+
+
+IDS = torch.zeros(3, dtype=torch.int32, device="meta")
+
+
+@pytest.mark.parametrize("change,message", [
+    (dict(x=bf(3, 63, device="meta")), "x holds"), (dict(x=bf(2, 64, device="meta")), "x holds"),
+    (dict(x=bf(3, 64, device="meta").float()), "x is"), (dict(x=bf(64, 3, device="meta").t()), "x is not contiguous"),
+    (dict(y=bf(2, 64, device="meta")), "y holds"), (dict(y=bf(3, 128, device="meta")[:, :64]), "y is not contiguous"),
+    (dict(y=bf(3, 64)), "y is on cpu"), (dict(token_ids=torch.zeros(3, dtype=torch.int32)), "token_ids is on cpu"),
+    (dict(token_ids=IDS.long()), "token_ids is"), (dict(token_ids=IDS[:2]), "token_ids holds"),
+    (dict(ws=torch.empty(1 << 20, dtype=torch.uint8)), "ws is on cpu"),
+    (dict(layer=few_layer("cpu")), "w_gate is on cpu"),
+    (dict(layer=dict(few_layer("meta"), w_up=bf(4, 64, 128, device="meta")[..., :64])), "w_up is not contiguous"),
+    (dict(), "expected a GPU"),
+])
+def test_few_checks_its_tensors(change, message):
+    t = dict(x=bf(3, 64, device="meta"), y=bf(3, 64, device="meta"), token_ids=IDS,
+             layer=few_layer("meta"), ws=torch.empty(1 << 20, dtype=torch.uint8, device="meta"))
+    t.update(change)
+    for cfg in (FEW, B.config_c(FEW)):
+        with pytest.raises(ValueError, match=message):
+            B.moe_forward_few(cfg, t["layer"], t["x"], t["token_ids"], 3, t["y"], t["ws"], stream=0)
+
+
+def test_few_of_no_tokens_is_a_no_op():
+    B.moe_forward_few(FEW, few_layer("cpu"), None, None, 0, None, None, stream=0)
+    with pytest.raises(B.MoEError):
+        B.moe_forward_few(FEW, few_layer("cpu"), None, None, -1, None, None, stream=0)
