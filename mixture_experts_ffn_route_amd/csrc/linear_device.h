@@ -138,7 +138,8 @@ __device__ __forceinline__ float slope(float z, int act) {
       return 0.5f * erfcf(-z * 0.7071067811865476f) + z * 0.3989422804014327f * exp_of<T>(-0.5f * z * z);
     case MOE_ACTIVATION_GELU_TANH: {
       const float s = sigmoid<T>(2.f * kGeluA * (z + kGeluB * z * z * z));
-      return s + z * s * (1.f - s) * 2.f * kGeluA * (1.f + 3.f * kGeluB * z * z);
+      const float t = s * (1.f - s);           // 0 far out, where z^2 may overflow
+      return t > 0.f ? s + z * t * 2.f * kGeluA * (1.f + 3.f * kGeluB * z * z) : s;
     }
     default: return 1.f;
   }
