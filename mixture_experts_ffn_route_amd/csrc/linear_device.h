@@ -148,12 +148,13 @@ __device__ __forceinline__ float slope(float z, int act) {
 // The value of v in storage type T, kept on v's side of the clamp: the saved
 // pre-activation decides in the backward pass whether the clamp was active,
 // so rounding must not carry it across (v > L has to stay above L, v <= L at
-// or below it).  One step of the type towards the right side otherwise.
-template <typename T>
+// or below it).  One step of the type towards the right side otherwise.  The
+// gate has that border at L, the up value (BOTH) at -L as well.
+template <typename T, bool BOTH>
 __device__ __forceinline__ float saved(float v, float L) {
   const float r = (float)(T)v;
   if (sizeof(T) == 4 || !(L > 0.f)) return r;
-  const float a = fabsf(v), b = fabsf(r);
+  const float a = BOTH ? fabsf(v) : v, b = BOTH ? fabsf(r) : r;
   if ((a > L) == (b > L) || v != v) return r;
   const uint32_t bits = __float_as_uint(r);
   return __uint_as_float(a > L ? bits + 0x10000u : bits - 0x10000u);
@@ -196,11 +197,11 @@ __device__ __forceinline__ void finish8(const Epilogue &e, float (&v)[8], float 
   if (e.z) {
     float k[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) k[j] = saved<T>(v[j], DUAL ? e.limit : 0.f);
+    for (int j = 0; j < 8; ++j) k[j] = saved<T, false>(v[j], DUAL ? e.limit : 0.f);
     store8<T>((T *)e.z + m * e.ld_z + n, k, left, vec);
     if constexpr (DUAL) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) k[j] = saved<T>(u[j], e.limit);
+      for (int j = 0; j < 8; ++j) k[j] = saved<T, true>(u[j], e.limit);
       store8<T>((T *)e.z_up + m * e.ld_z + n, k, left, vec);
     }
   }

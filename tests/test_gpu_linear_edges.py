@@ -28,3 +28,26 @@ def test_slopes_of_large_values(activation, M, N, dtype, gpu):
     torch.cuda.synchronize()
     assert torch.equal(dx, (z > 0).to(dt))
     assert torch.equal(db, (z[0] > 0).to(dt) * M)
+
+
+@pytest.mark.parametrize("limit", [1.0, 0.7, 3.3])
+def test_saved_gate_is_the_nearest_value_below_zero(limit, gpu):
+    """The gate is clamped from above alone: around -L its saved value is the
+    nearest one, as everywhere but at +L (sums of two terms, exact)."""
+    steps = torch.arange(-40, 41, device="cuda").float() * 2.0 ** -10
+    want = -limit + steps * limit
+    hi = want.to(torch.bfloat16)
+    lo = (want - hi.float()).to(torch.bfloat16)
+    exact = hi.float() + lo.float()
+    M = want.numel()
+    x = torch.zeros((M, 8), dtype=torch.bfloat16, device="cuda")
+    x[:, 0], x[:, 1] = hi, lo
+    w = torch.zeros((8, 8), dtype=torch.bfloat16, device="cuda")
+    w[:, 0] = w[:, 1] = 1
+    c = C.LinearConfig(M, 8, 8, "bf16", "swiglu", limit)
+    y, z, zu = L.outputs(c, {})
+    B.moe_linear(c, x, w, y, w_up=w, z=z, z_up=zu, ws=B.alloc_linear_workspace(c))
+    torch.cuda.synchronize()
+    assert torch.equal(z[:, 0], exact.to(torch.bfloat16))
+    bound = float(torch.tensor(limit, dtype=torch.float32))
+    assert torch.equal(zu[:, 0].float() < -bound, exact < -bound)      # the up value has that border
