@@ -517,7 +517,7 @@ typedef struct {
 } moe_linear_config;
 #define MOE_LINEAR_MAX_LD (1 << 20)
 
-typedef struct {               /* contiguous, dtype; w and w_up 16-byte aligned  */
+typedef struct {               /* contiguous, dtype                              */
   const void *w;               /* [N, K]                                         */
   const void *w_up;            /* [N, K] swiglu only, else NULL                  */
   const void *bias;            /* [N], or NULL                                   */
@@ -537,7 +537,7 @@ typedef struct {               /* contiguous except dx; NULL: not wanted        
 size_t moe_linear_workspace_size(const moe_linear_config *cfg, int32_t backward);
 
 /* The forward product.
- *   x         [M, K] stride ld_x, 16-byte aligned
+ *   x         [M, K] stride ld_x
  *   residual  [M, N] stride ld_residual, or NULL; may be y itself (same stride)
  *   y         [M, N] stride ld_y out
  *   z, z_up   [M, N] contiguous out, or NULL: the pre-activations z (and zu),
@@ -548,9 +548,11 @@ size_t moe_linear_workspace_size(const moe_linear_config *cfg, int32_t backward)
  *             value.  Calls that share one must be ordered on one stream
  * Products accumulate in fp32, the epilogue is fp32, y is rounded once.  All
  * sizes and strides are taken; for large products, rows that are not whole
- * 16-byte pieces are first copied to padded ones in the workspace.  No output
- * may overlap an input (but y the residual) or another output.  Results do not depend on what
- * else runs (no atomics).  Only kernels are enqueued on `stream`, so the call
+ * 16-byte pieces are first copied to padded ones in the workspace.  Alignment: x
+ * and w, w_up 16 bytes where their rows are whole 16-byte pieces at 16-byte
+ * strides, an element's size where not; the others an element's size.  No output
+ * may overlap an input (but y the residual) or another output.  Results do not
+ * depend on what else runs (no atomics).  Only kernels are enqueued on `stream`, so the call
  * can be captured in a HIP graph.  rows == 0 is a no-op. */
 int moe_linear(const moe_linear_config *cfg, const moe_linear_weights *w, const void *x,
                const void *residual, void *y, void *z, void *z_up,
@@ -559,7 +561,7 @@ int moe_linear(const moe_linear_config *cfg, const moe_linear_weights *w, const 
 /* The gradient of moe_linear for the output gradient dy:
  *   dz = dy act'(z)          (swiglu: for both products; a clamped value has none)
  *   dx = dz W,  dW = dz^T x,  dbias = sum over rows of dz;  dresidual is dy
- *   dy        [M, N] stride ld_y, 16-byte aligned
+ *   dy        [M, N] stride ld_y, aligned as x and w are
  *   z, z_up   as moe_linear wrote them (activation NONE: ignored)
  *   x         needed for dw / dw_up; w->w, w->w_up for dx; else may be NULL
  *             (biases are not read)

@@ -23,6 +23,13 @@ inline int64_t linear_pad(int64_t n, int dtype) {
   return (n + m - 1) / m * m;
 }
 
+// Rows that are not whole 16-byte pieces at 16-byte strides: their elements are
+// read one by one (and copied to padded rows for the tiles), so that their
+// matrix needs the alignment of an element alone.
+inline bool linear_odd_rows(int64_t width, int64_t ld, int dtype) {
+  return width % linear_pad(1, dtype) || ld % linear_pad(1, dtype);
+}
+
 // Epilogue, shared by all its kernels: eight consecutive columns of one row.
 struct Epilogue {
   const void *bias, *bias_up, *residual;

@@ -679,10 +679,6 @@ hipError_t run_gemm(GemmOp g, const Shape &sh, void *part, hipStream_t s) {
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 
-bool odd_rows(int64_t width, int64_t ld, int dtype) {
-  return width % linear_pad(1, dtype) || ld % linear_pad(1, dtype);
-}
-
 // The kernels of a call.  Up to kFewRows rows take the stream of W where no copy
 // has to be made first (1x7168->2x2048 swiglu bf16 17.5 -> 14.5 us, 16x4096->4096
 // fp32 29 -> 18 us).  Otherwise 32 x 32 tiles where their estimate is below that
@@ -701,7 +697,7 @@ double small_us(int64_t tiles, int64_t contraction, double chunks_us) {
 Path forward_path(const moe_linear_config &c) {
   const int64_t M = c.rows, K = c.in_dim, N = c.out_dim;
   const bool dual = c.activation == MOE_ACTIVATION_SWIGLU;
-  const bool copy_w = odd_rows(K, K, c.dtype), copy_x = odd_rows(K, c.ld_x, c.dtype);
+  const bool copy_w = linear_odd_rows(K, K, c.dtype), copy_x = linear_odd_rows(K, c.ld_x, c.dtype);
   if (M <= kFewRows && !copy_w && !copy_x) return PATH_FEW;
   const Shape sh = shape_of(M, dual ? 2 * N : N, &K, 1, c.dtype, dual);
   const double gemm = sh.us + 4.0 * (1 + copy_x + copy_w * (dual ? 2 : 1));
@@ -721,8 +717,8 @@ bool backward_small(const moe_linear_config &c) {
   const Shape dx = shape_of(M, K, kd, (int)both, c.dtype, false);
   const Shape dw = shape_of(both * N, K, &M, 1, c.dtype, false);
   // slope, column sums, products and copies
-  const double gemm = 16.0 + dx.us + dw.us + (odd_rows(K, K, c.dtype) ? 4.0 * both : 0.0) +
-                      (odd_rows(K, c.ld_x, c.dtype) ? 4.0 : 0.0);
+  const double gemm = 16.0 + dx.us + dw.us + (linear_odd_rows(K, K, c.dtype) ? 4.0 * both : 0.0) +
+                      (linear_odd_rows(K, c.ld_x, c.dtype) ? 4.0 : 0.0);
   // the workgroups of dx and dW fill the GPU together
   double small = small_us((M + 31) / 32 * kt, both * N, chunks_us) +
                  small_us((N + 31) / 32 * kt * both, M, chunks_us);
@@ -764,7 +760,7 @@ hipError_t linear_forward(const moe_linear_config &c, const moe_linear_weights &
   e.y = y; e.z = z; e.z_up = z_up;
   e.ld_y = c.ld_y; e.ld_res = c.ld_residual; e.ld_z = N;
   e.N = (int)N; e.act = c.activation; e.limit = c.limit;
-  e.vec = !odd_rows(N, c.ld_y, c.dtype) && (!residual || !odd_rows(N, c.ld_residual, c.dtype)) &&
+  e.vec = !linear_odd_rows(N, c.ld_y, c.dtype) && (!residual || !linear_odd_rows(N, c.ld_residual, c.dtype)) &&
           N % 8 == 0 && aligned16(y) && aligned16(z) && aligned16(z_up) && aligned16(residual) &&
           aligned16(w.bias) && aligned16(w.bias_up);
   const Path path = forward_path(c);
@@ -778,11 +774,11 @@ hipError_t linear_forward(const moe_linear_config &c, const moe_linear_weights &
   hipError_t err;
   Matrix mx = {x, c.ld_x, M, K}, mw = {w.w, K, N, K}, mu = {w.w_up, K, N, K};
   const int64_t Kp = linear_pad(K, c.dtype);
-  if (odd_rows(K, c.ld_x, c.dtype)) {
+  if (linear_odd_rows(K, c.ld_x, c.dtype)) {
     if ((err = pad_rows<T>(x, c.ld_x, M, (int)K, ws + L.x, Kp, s)) != hipSuccess) return err;
     mx = {ws + L.x, Kp, M, Kp};
   }
-  if (odd_rows(K, K, c.dtype)) {
+  if (linear_odd_rows(K, K, c.dtype)) {
     if ((err = pad_rows<T>(w.w, K, N, (int)K, ws + L.w, Kp, s)) != hipSuccess) return err;
     mw = {ws + L.w, Kp, N, Kp};
     if (dual) {
@@ -821,7 +817,7 @@ hipError_t linear_backward(const moe_linear_config &c, const moe_linear_weights 
     return launch_small_backward<T>(a, dual, s);
   }
   // dz: dy itself where nothing changes it and its rows are whole pieces
-  const bool same = c.activation == MOE_ACTIVATION_NONE && !odd_rows(N, c.ld_y, c.dtype);
+  const bool same = c.activation == MOE_ACTIVATION_NONE && !linear_odd_rows(N, c.ld_y, c.dtype);
   Matrix mz = {dy, c.ld_y, M, N}, mu = {};
   if (!same) {
     mz = {ws + L.dz, Np, M, Np};
@@ -836,7 +832,7 @@ hipError_t linear_backward(const moe_linear_config &c, const moe_linear_weights 
     a.M = M; a.ld_dy = c.ld_y; a.ldz = Np; a.N = (int)N; a.act = c.activation;
     a.limit = c.limit;
     a.parts = colsum_parts(M, (int)N);
-    a.vec = !odd_rows(N, c.ld_y, c.dtype) && N % 8 == 0 && aligned16(z) && aligned16(z_up);
+    a.vec = !linear_odd_rows(N, c.ld_y, c.dtype) && N % 8 == 0 && aligned16(z) && aligned16(z_up);
     const dim3 grid((unsigned)((Np + 63) / 64), (unsigned)a.parts);
     if (M > 0) {                               // no rows: the sums below are empty
       if (dual) hipLaunchKernelGGL((slope_kernel<T, true>), grid, dim3(256), 0, s, a);
@@ -853,7 +849,7 @@ hipError_t linear_backward(const moe_linear_config &c, const moe_linear_weights 
   }
   if (gr.dx && M > 0) {
     Matrix mw = {w.w, K, N, K}, mwu = {w.w_up, K, N, K};
-    if (odd_rows(K, K, c.dtype)) {
+    if (linear_odd_rows(K, K, c.dtype)) {
       if ((err = pad_rows<T>(w.w, K, N, (int)K, ws + L.w, Kp, s)) != hipSuccess) return err;
       mw = {ws + L.w, Kp, N, Kp};
       if (dual) {
@@ -868,13 +864,13 @@ hipError_t linear_backward(const moe_linear_config &c, const moe_linear_weights 
     g.segments = dual ? 2 : 1;
     g.M = M;
     g.e.y = gr.dx; g.e.ld_y = gr.ld_dx; g.e.N = (int)K; g.e.act = MOE_ACTIVATION_NONE;
-    g.e.vec = !odd_rows(K, gr.ld_dx, c.dtype) && K % 8 == 0 && aligned16(gr.dx);
+    g.e.vec = !linear_odd_rows(K, gr.ld_dx, c.dtype) && K % 8 == 0 && aligned16(gr.dx);
     const Shape sh = shape_of(M, K, g.kdim, g.segments, c.dtype, false);
     if ((err = run_gemm<T, false, true, false>(g, sh, ws + L.part, s)) != hipSuccess) return err;
   }
   if (want_dw) {
     Matrix mx = {x, c.ld_x, M, K};
-    if (odd_rows(K, c.ld_x, c.dtype)) {
+    if (linear_odd_rows(K, c.ld_x, c.dtype)) {
       if ((err = pad_rows<T>(x, c.ld_x, M, (int)K, ws + L.x, Kp, s)) != hipSuccess) return err;
       mx = {ws + L.x, Kp, M, Kp};
     }
@@ -912,9 +908,9 @@ LinearSpace linear_space(const moe_linear_config &c, bool backward, bool dx, boo
   };
   // what the GEMM takes, also where another kernel runs: one size per shape
   const bool use_x = !backward || dw, use_w = !backward || dx;
-  l.x = take(use_x && odd_rows(K, c.ld_x, c.dtype) ? es * M * Kp : 0);
-  l.w = take(use_w && odd_rows(K, K, c.dtype) ? es * N * Kp : 0);
-  l.w_up = take(use_w && dual && odd_rows(K, K, c.dtype) ? es * N * Kp : 0);
+  l.x = take(use_x && linear_odd_rows(K, c.ld_x, c.dtype) ? es * M * Kp : 0);
+  l.w = take(use_w && linear_odd_rows(K, K, c.dtype) ? es * N * Kp : 0);
+  l.w_up = take(use_w && dual && linear_odd_rows(K, K, c.dtype) ? es * N * Kp : 0);
   size_t part = 0;
   auto need = [&](int64_t rows, int64_t cols, int64_t k, int segments, bool two) {
     const int64_t kd[2] = {k, k};
@@ -923,7 +919,7 @@ LinearSpace linear_space(const moe_linear_config &c, bool backward, bool dx, boo
     if (b > part) part = b;
   };
   if (backward) {
-    const bool same = c.activation == MOE_ACTIVATION_NONE && !odd_rows(N, c.ld_y, c.dtype);
+    const bool same = c.activation == MOE_ACTIVATION_NONE && !linear_odd_rows(N, c.ld_y, c.dtype);
     l.dz = take(!same && (dx || dw) ? es * M * Np : 0);
     l.du = take(dual && (dx || dw) ? es * M * Np : 0);
     l.colsum = take(db ? sizeof(float) * colsum_parts(M, (int)N) * (dual ? 2 : 1) * N : 0);

@@ -201,6 +201,12 @@ int check_linear(const moe_linear_config *c, moe_linear_config *out) {
 
 bool misaligned(const void *p, size_t n) { return (uintptr_t)p % n != 0; }
 
+// The alignment of a linear layer's matrix with rows of `width` at stride ld.
+size_t linear_align(int64_t width, int64_t ld, int dtype) {
+  if (!moe::linear_odd_rows(width, ld, dtype)) return 16;
+  return dtype == MOE_DTYPE_F32 ? 4 : 2;
+}
+
 // Whether an output is an input, or another output (by address; null: not there).
 bool overlap(std::initializer_list<const void *> out, std::initializer_list<const void *> in) {
   for (auto o = out.begin(); o != out.end(); ++o) {
@@ -838,7 +844,9 @@ int moe_linear(const moe_linear_config *cfg, const moe_linear_weights *w, const 
   if (!x || !y || (residual == y && c.ld_residual != c.ld_y)) return MOE_ERR_INVALID_ARG;
   if (overlap({y, z, z_up}, {x, w->w, w->w_up, w->bias, w->bias_up}) || overlap({z, z_up}, {residual}))
     return MOE_ERR_INVALID_ARG;
-  if (misaligned(x, 16) || misaligned(w->w, 16) || misaligned(w->w_up, 16))
+  const size_t wa = linear_align(c.in_dim, c.in_dim, c.dtype);
+  if (misaligned(x, linear_align(c.in_dim, c.ld_x, c.dtype)) || misaligned(w->w, wa) ||
+      misaligned(w->w_up, wa))
     return MOE_ERR_INVALID_ARG;
   for (const void *p : {(const void *)y, residual, (const void *)z, (const void *)z_up, w->bias,
                         w->bias_up})
@@ -862,11 +870,13 @@ int moe_linear_backward(const moe_linear_config *cfg, const moe_linear_weights *
   if (!grads->dx && !want_dw && !want_db) return MOE_ERR_INVALID_ARG;
   if (!dual && (grads->dw_up || grads->dbias_up)) return MOE_ERR_INVALID_ARG;
   if (c.rows > 0) {
-    if (!dy || misaligned(dy, 16)) return MOE_ERR_INVALID_ARG;
+    if (!dy || misaligned(dy, linear_align(c.out_dim, c.ld_y, c.dtype))) return MOE_ERR_INVALID_ARG;
     if (c.activation != MOE_ACTIVATION_NONE && (!z || (dual && !z_up))) return MOE_ERR_INVALID_ARG;
     if (grads->dx && (!w->w || (dual && !w->w_up))) return MOE_ERR_INVALID_ARG;
     if (want_dw && !x) return MOE_ERR_INVALID_ARG;
-    if (misaligned(x, 16) || misaligned(w->w, 16) || misaligned(w->w_up, 16))
+    const size_t wa = linear_align(c.in_dim, c.in_dim, c.dtype);
+    if (misaligned(x, linear_align(c.in_dim, c.ld_x, c.dtype)) || misaligned(w->w, wa) ||
+        misaligned(w->w_up, wa))
       return MOE_ERR_INVALID_ARG;
   }
   if (overlap({grads->dx, grads->dw, grads->dw_up, grads->dbias, grads->dbias_up},

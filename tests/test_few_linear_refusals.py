@@ -98,3 +98,32 @@ def test_few_of_no_tokens_is_a_no_op():
     B.moe_forward_few(FEW, few_layer("cpu"), None, None, 0, None, None, stream=0)
     with pytest.raises(B.MoEError):
         B.moe_forward_few(FEW, few_layer("cpu"), None, None, -1, None, None, stream=0)
+
+
+def status(M, K, N, dtype, x=0x1000, w=0x2000, ld_x=0, dy=0x3000, ld_y=0):
+    """Of a forward and a backward call without a workspace: where the addresses
+    pass, the workspace is what is missing."""
+    c = B.MoeLinearConfigC(M, K, N, C.DTYPE[dtype], C.ACTIVATION["silu"], 0.0, ld_x, ld_y, 0)
+    weights = B.MoeLinearWeightsC(w, None, None, None)
+    grads = B.MoeLinearGradsC(0x5000, 0x6000)
+    return (B._lib.moe_linear(c, weights, x, None, 0x4000, None, None, None, 0, None),
+            B._lib.moe_linear_backward(c, weights, x, dy, 0x7000, None, grads, None, 0, None))
+
+
+@pytest.mark.parametrize("dtype,size,whole", [("bf16", 2, 8), ("f32", 4, 4)])
+def test_addresses_of_odd_rows(dtype, size, whole):
+    """An element's alignment where rows are not whole 16-byte pieces, 16 bytes
+    where they are; never less than an element's."""
+    bad, ok = B.MOE_ERR_INVALID_ARG, B.MOE_ERR_WORKSPACE
+    K, N = 8 * whole + 1, 4 * whole + 1
+    for change in (dict(x=0x1000 + size), dict(w=0x2000 + size)):
+        assert status(8, K, N, dtype, **change) == (ok, ok)
+    assert status(8, K, N, dtype, dy=0x3000 + size) == (ok, ok)
+    assert status(8, 8 * whole, N, dtype, x=0x1000 + size, ld_x=9 * whole + 1) == (ok, ok)
+    assert status(8, 8 * whole, N, dtype, x=0x1000 + size) == (bad, bad)
+    assert status(8, 8 * whole, N, dtype, w=0x2000 + size, ld_x=9 * whole + 1) == (bad, bad)
+    assert status(8, K, 4 * whole, dtype, dy=0x3000 + size) == (ok, bad)
+    assert status(8, K, 4 * whole, dtype, dy=0x3000 + size, ld_y=5 * whole + 1) == (ok, ok)
+    for change in (dict(x=0x1001), dict(w=0x2001)):
+        assert status(8, K, N, dtype, **change) == (bad, bad)
+    assert status(8, K, N, dtype, dy=0x3001) == (ok, bad)

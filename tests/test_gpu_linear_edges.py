@@ -51,3 +51,19 @@ def test_saved_gate_is_the_nearest_value_below_zero(limit, gpu):
     assert torch.equal(z[:, 0], exact.to(torch.bfloat16))
     bound = float(torch.tensor(limit, dtype=torch.float32))
     assert torch.equal(zu[:, 0].float() < -bound, exact < -bound)      # the up value has that border
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,K,N", [(1, 63, 5), (9, 777, 1023), (203, 63, 97), (2300, 515, 1031)])
+@pytest.mark.parametrize("activation", ["none", "swiglu"])
+def test_addresses_inside_odd_rows(M, K, N, activation, dtype, gpu):
+    """x, dy and the weights from the second row or matrix of a larger one of
+    odd widths, where no address is a multiple of 16 bytes."""
+    c, t = L.make(M, K, N, dtype, activation, 31)
+    for n in ("x", "dy", "w", "w_up"):
+        if n in t:
+            whole = torch.zeros((t[n].shape[0] + 1, t[n].shape[1]), dtype=t[n].dtype, device=gpu)
+            whole[1:] = t[n]
+            t[n] = whole[1:]
+            assert t[n].data_ptr() % 16
+    L.check_all(c, t, f"{dtype} {activation} {M}x{K}x{N} inside")
