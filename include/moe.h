@@ -576,6 +576,27 @@ int moe_linear_backward(const moe_linear_config *cfg, const moe_linear_weights *
                         const void *dy, const void *z, const void *z_up,
                         const moe_linear_grads *grads, void *ws, size_t ws_bytes, void *stream);
 
+/* Which kernels a product of these calls takes (host-only, for tests and
+ * profiles): a choice by sizes, types and row strides alone.  Of the backward
+ * products, DX and DW; DW is both weight gradients of swiglu in one launch. */
+typedef enum {
+  MOE_LINEAR_FORWARD = 0,
+  MOE_LINEAR_DX = 1,
+  MOE_LINEAR_DW = 2
+} moe_linear_product;
+typedef enum {
+  MOE_LINEAR_PATH_TILED = 0,   /* 64..256-square tiles, with copies of odd rows  */
+  MOE_LINEAR_PATH_FEW = 1,     /* up to 16 rows: a stream of the weights         */
+  MOE_LINEAR_PATH_SMALL = 2    /* 32 x 32 tiles, elements read one by one        */
+} moe_linear_path_kind;
+typedef struct {
+  int32_t path;                /* moe_linear_path_kind                           */
+  int32_t tile_rows;           /* tiled, else 0: a workgroup's rows and columns  */
+  int32_t tile_cols;           /* (swiglu forward: columns of both products)     */
+  int32_t parts;               /* workgroups that share a tile's contraction     */
+} moe_linear_path_info;
+int moe_linear_path(const moe_linear_config *cfg, int32_t product, moe_linear_path_info *info);
+
 /* Roofline probes: the achievable HBM read rate and bf16 / FP8 MFMA rates of
  * the GPU, measured with the instruction forms the layer kernels use (16-byte
  * nontemporal vector loads; v_mfma_f32_16x16x32_bf16, v_mfma_f32_32x32x16_bf16,

@@ -35,7 +35,7 @@ EXPORTED_SYMBOLS = (
     "moe_pack_weights", "moe_build_tid2eid_multistart", "moe_update_bias", "moe_probe_read",
     "moe_probe_mfma", "moe_redequant_fp8", "moe_forward_ex", "moe_forward_noalloc",
     "moe_few_workspace_layout", "moe_few_workspace_size", "moe_forward_few",
-    "moe_linear_workspace_size", "moe_linear", "moe_linear_backward",
+    "moe_linear_workspace_size", "moe_linear", "moe_linear_backward", "moe_linear_path",
 )
 MOE_STAGES = ("route", "permute", "gemm1", "gemm2", "combine")
 
@@ -92,6 +92,10 @@ class MoeLinearGradsC(ctypes.Structure):
                 ("ld_dx", ctypes.c_int64)]
 
 
+class MoeLinearPathC(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("path", "tile_rows", "tile_cols", "parts")]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise RuntimeError(f"{LIB_PATH} is not built; run __graft_entry__.build() first")
@@ -129,7 +133,9 @@ def _load():
     lib.moe_linear.argtypes = [lcp, lwp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
     lib.moe_linear_backward.argtypes = [lcp, lwp, vp, vp, vp, vp, ctypes.POINTER(MoeLinearGradsC),
                                         vp, ctypes.c_size_t, vp]
-    for f in ("moe_few_workspace_layout", "moe_forward_few", "moe_linear", "moe_linear_backward"):
+    lib.moe_linear_path.argtypes = [lcp, i32, ctypes.POINTER(MoeLinearPathC)]
+    for f in ("moe_few_workspace_layout", "moe_forward_few", "moe_linear", "moe_linear_backward",
+              "moe_linear_path"):
         getattr(lib, f).restype = ctypes.c_int
     for f in ("moe_validate_config", "moe_build_tid2eid", "moe_workspace_layout", "moe_route",
               "moe_permute", "moe_forward", "moe_forward_profiled", "moe_forward_ex",
@@ -506,6 +512,21 @@ def moe_linear_workspace_size(cfg: LinearConfig, backward=False, ld_x=0, ld_y=0,
     c = MoeLinearConfigC(cfg.rows, cfg.in_dim, cfg.out_dim, DTYPE[cfg.dtype],
                          ACTIVATION[cfg.activation], cfg.limit, ld_x, ld_y, ld_residual)
     return _lib.moe_linear_workspace_size(ctypes.byref(c), int(bool(backward)))
+
+
+LINEAR_PRODUCT = {"forward": 0, "dx": 1, "dw": 2}
+LINEAR_PATH = ("tiled", "few", "small")
+
+
+def moe_linear_path(cfg: LinearConfig, product="forward", ld_x=0, ld_y=0) -> tuple:
+    """(path, tile rows, tile columns, parts) of a product of calls whose tensors
+    have these row strides (0: contiguous)."""
+    c = MoeLinearConfigC(cfg.rows, cfg.in_dim, cfg.out_dim, DTYPE[cfg.dtype],
+                         ACTIVATION[cfg.activation], cfg.limit, ld_x, ld_y, 0)
+    info = MoeLinearPathC()
+    _check(_lib.moe_linear_path(ctypes.byref(c), LINEAR_PRODUCT[product], ctypes.byref(info)),
+           "moe_linear_path")
+    return LINEAR_PATH[info.path], info.tile_rows, info.tile_cols, info.parts
 
 
 def moe_linear(cfg: LinearConfig, x, w, y, *, bias=None, residual=None, w_up=None, bias_up=None,

@@ -54,6 +54,9 @@ constexpr int kFewRows = 16;   // rows that the few-row kernel takes
 
 LinearSpace linear_space(const moe_linear_config &c, bool backward, bool dx, bool dw, bool db);
 
+// Which kernels a product takes (moe_linear_product, of a checked configuration).
+moe_linear_path_info linear_path(const moe_linear_config &c, int32_t product);
+
 hipError_t launch_linear(const moe_linear_config &c, const moe_linear_weights &w, const void *x,
                          const void *residual, void *y, void *z, void *z_up, char *ws,
                          hipStream_t s);

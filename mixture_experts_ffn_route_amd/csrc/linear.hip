@@ -679,6 +679,15 @@ hipError_t run_gemm(GemmOp g, const Shape &sh, void *part, hipStream_t s) {
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 
+// Tile shape and parts of a product of a call, wherever they are asked for.
+Shape product_shape(const moe_linear_config &c, int32_t product) {
+  const int64_t M = c.rows, K = c.in_dim, N = c.out_dim, kd[2] = {N, N};
+  const bool dual = c.activation == MOE_ACTIVATION_SWIGLU;
+  if (product == MOE_LINEAR_FORWARD) return shape_of(M, dual ? 2 * N : N, &K, 1, c.dtype, dual);
+  if (product == MOE_LINEAR_DX) return shape_of(M, K, kd, dual ? 2 : 1, c.dtype, false);
+  return shape_of(dual ? 2 * N : N, K, &M, 1, c.dtype, false);
+}
+
 // The kernels of a call.  Up to kFewRows rows take the stream of W where no copy
 // has to be made first (1x7168->2x2048 swiglu bf16 17.5 -> 14.5 us, 16x4096->4096
 // fp32 29 -> 18 us).  Otherwise 32 x 32 tiles where their estimate is below that
@@ -687,23 +696,21 @@ bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 // contraction, measured with either way forced on 60 shapes: 203x777->1023 fp32
 // 30 by the GEMM and 12 by small tiles, 64x4096->512 18 and 28, 1024^3 26 and 36;
 // the backward of 301x256->320 29 and 16, of 1024^3 61 and 148.
-enum Path { PATH_GEMM, PATH_FEW, PATH_SMALL };
-
 double small_us(int64_t tiles, int64_t contraction, double chunks_us) {
   const int64_t chunks = (contraction + 63) / 64;
   return (double)tiles / 256 * (2.0 + (double)((chunks + 7) / 8) * chunks_us);
 }
 
-Path forward_path(const moe_linear_config &c) {
+moe_linear_path_kind forward_path(const moe_linear_config &c) {
   const int64_t M = c.rows, K = c.in_dim, N = c.out_dim;
   const bool dual = c.activation == MOE_ACTIVATION_SWIGLU;
   const bool copy_w = linear_odd_rows(K, K, c.dtype), copy_x = linear_odd_rows(K, c.ld_x, c.dtype);
-  if (M <= kFewRows && !copy_w && !copy_x) return PATH_FEW;
-  const Shape sh = shape_of(M, dual ? 2 * N : N, &K, 1, c.dtype, dual);
+  if (M <= kFewRows && !copy_w && !copy_x) return MOE_LINEAR_PATH_FEW;
+  const Shape sh = product_shape(c, MOE_LINEAR_FORWARD);
   const double gemm = sh.us + 4.0 * (1 + copy_x + copy_w * (dual ? 2 : 1));
   const int64_t tiles = (M + 31) / 32 * ((N + 31) / 32);
   const double small = small_us((tiles + 255) / 256 * 256, K, dual ? 5.2 : 3.0) + 4.0;
-  return small < gemm ? PATH_SMALL : PATH_GEMM;
+  return small < gemm ? MOE_LINEAR_PATH_SMALL : MOE_LINEAR_PATH_TILED;
 }
 
 // By the time of all gradients, whichever are asked for: each comes out the same
@@ -713,9 +720,8 @@ bool backward_small(const moe_linear_config &c) {
   if (M == 0) return false;
   const bool dual = c.activation == MOE_ACTIVATION_SWIGLU;
   const double chunks_us = dual ? 9.0 : 7.0;
-  const int64_t kt = (K + 31) / 32, both = dual ? 2 : 1, kd[2] = {N, N};
-  const Shape dx = shape_of(M, K, kd, (int)both, c.dtype, false);
-  const Shape dw = shape_of(both * N, K, &M, 1, c.dtype, false);
+  const int64_t kt = (K + 31) / 32, both = dual ? 2 : 1;
+  const Shape dx = product_shape(c, MOE_LINEAR_DX), dw = product_shape(c, MOE_LINEAR_DW);
   // slope, column sums, products and copies
   const double gemm = 16.0 + dx.us + dw.us + (linear_odd_rows(K, K, c.dtype) ? 4.0 * both : 0.0) +
                       (linear_odd_rows(K, c.ld_x, c.dtype) ? 4.0 : 0.0);
@@ -763,13 +769,14 @@ hipError_t linear_forward(const moe_linear_config &c, const moe_linear_weights &
   e.vec = !linear_odd_rows(N, c.ld_y, c.dtype) && (!residual || !linear_odd_rows(N, c.ld_residual, c.dtype)) &&
           N % 8 == 0 && aligned16(y) && aligned16(z) && aligned16(z_up) && aligned16(residual) &&
           aligned16(w.bias) && aligned16(w.bias_up);
-  const Path path = forward_path(c);
-  if (path != PATH_GEMM) {
+  const moe_linear_path_kind path = forward_path(c);
+  if (path != MOE_LINEAR_PATH_TILED) {
     SmallArgs a = {};
     a.x = x; a.w = w.w; a.w_up = w.w_up;
     a.M = M; a.K = K; a.ld_x = c.ld_x;
     a.e = e;
-    return path == PATH_FEW ? launch_few_rows<T>(a, dual, s) : launch_small_forward<T>(a, dual, s);
+    return path == MOE_LINEAR_PATH_FEW ? launch_few_rows<T>(a, dual, s)
+                                       : launch_small_forward<T>(a, dual, s);
   }
   hipError_t err;
   Matrix mx = {x, c.ld_x, M, K}, mw = {w.w, K, N, K}, mu = {w.w_up, K, N, K};
@@ -792,7 +799,7 @@ hipError_t linear_forward(const moe_linear_config &c, const moe_linear_weights &
   g.segments = 1;
   g.M = M;
   g.e = e;
-  const Shape sh = shape_of(M, dual ? 2 * N : N, g.kdim, 1, c.dtype, dual);
+  const Shape sh = product_shape(c, MOE_LINEAR_FORWARD);
   return dual ? run_gemm<T, false, false, true>(g, sh, ws + L.part, s)
               : run_gemm<T, false, false, false>(g, sh, ws + L.part, s);
 }
@@ -865,7 +872,7 @@ hipError_t linear_backward(const moe_linear_config &c, const moe_linear_weights 
     g.M = M;
     g.e.y = gr.dx; g.e.ld_y = gr.ld_dx; g.e.N = (int)K; g.e.act = MOE_ACTIVATION_NONE;
     g.e.vec = !linear_odd_rows(K, gr.ld_dx, c.dtype) && K % 8 == 0 && aligned16(gr.dx);
-    const Shape sh = shape_of(M, K, g.kdim, g.segments, c.dtype, false);
+    const Shape sh = product_shape(c, MOE_LINEAR_DX);
     if ((err = run_gemm<T, false, true, false>(g, sh, ws + L.part, s)) != hipSuccess) return err;
   }
   if (want_dw) {
@@ -886,7 +893,7 @@ hipError_t linear_backward(const moe_linear_config &c, const moe_linear_weights 
     g.e.y = gr.dw ? gr.dw : gr.dw_up; g.e.ld_y = K; g.e.N = (int)K;
     g.e.act = MOE_ACTIVATION_NONE;
     g.e.vec = K % 8 == 0 && aligned16(gr.dw) && aligned16(gr.dw_up);
-    const Shape sh = shape_of(dual ? 2 * N : N, K, g.kdim, 1, c.dtype, false);
+    const Shape sh = product_shape(c, MOE_LINEAR_DW);
     if ((err = run_gemm<T, true, true, false>(g, sh, ws + L.part, s)) != hipSuccess) return err;
   }
   return hipSuccess;
@@ -912,10 +919,8 @@ LinearSpace linear_space(const moe_linear_config &c, bool backward, bool dx, boo
   l.w = take(use_w && linear_odd_rows(K, K, c.dtype) ? es * N * Kp : 0);
   l.w_up = take(use_w && dual && linear_odd_rows(K, K, c.dtype) ? es * N * Kp : 0);
   size_t part = 0;
-  auto need = [&](int64_t rows, int64_t cols, int64_t k, int segments, bool two) {
-    const int64_t kd[2] = {k, k};
-    const Shape s = shape_of(rows, two ? 2 * cols : cols, kd, segments, c.dtype, two);
-    const size_t b = part_bytes(rows, cols, two, s);
+  auto need = [&](int64_t rows, int64_t cols, bool two, int32_t product) {
+    const size_t b = part_bytes(rows, cols, two, product_shape(c, product));
     if (b > part) part = b;
   };
   if (backward) {
@@ -923,14 +928,26 @@ LinearSpace linear_space(const moe_linear_config &c, bool backward, bool dx, boo
     l.dz = take(!same && (dx || dw) ? es * M * Np : 0);
     l.du = take(dual && (dx || dw) ? es * M * Np : 0);
     l.colsum = take(db ? sizeof(float) * colsum_parts(M, (int)N) * (dual ? 2 : 1) * N : 0);
-    if (dx) need(M, K, N, dual ? 2 : 1, false);
-    if (dw) need(dual ? 2 * N : N, K, M, 1, false);
+    if (dx) need(M, K, false, MOE_LINEAR_DX);
+    if (dw) need(dual ? 2 * N : N, K, false, MOE_LINEAR_DW);
   } else {
-    need(M, N, K, 1, dual);
+    need(M, N, dual, MOE_LINEAR_FORWARD);
   }
   l.part = take(part);
   l.total = off;
   return l;
+}
+
+moe_linear_path_info linear_path(const moe_linear_config &c, int32_t product) {
+  moe_linear_path_info info = {};
+  if (product == MOE_LINEAR_FORWARD) info.path = forward_path(c);
+  else if (backward_small(c)) info.path = MOE_LINEAR_PATH_SMALL;
+  if (info.path != MOE_LINEAR_PATH_TILED) return info;
+  const Shape s = product_shape(c, product);
+  info.tile_rows = 64 * s.mi;
+  info.tile_cols = 64 * s.ni;
+  info.parts = s.parts;
+  return info;
 }
 
 hipError_t launch_linear(const moe_linear_config &c, const moe_linear_weights &w, const void *x,

@@ -897,6 +897,15 @@ int moe_linear_backward(const moe_linear_config *cfg, const moe_linear_weights *
                                                 (hipStream_t)stream));
 }
 
+int moe_linear_path(const moe_linear_config *cfg, int32_t product, moe_linear_path_info *info) {
+  moe_linear_config c;
+  const int st = check_linear(cfg, &c);
+  if (st != MOE_OK) return st;
+  if (!info || product < MOE_LINEAR_FORWARD || product > MOE_LINEAR_DW) return MOE_ERR_INVALID_ARG;
+  *info = moe::linear_path(c, product);
+  return MOE_OK;
+}
+
 int moe_probe_read(const void *buf, int64_t bytes, void *out, void *stream) {
   if (!buf || !out || bytes < 16 || bytes % 16 || ((uintptr_t)buf % 16)) return MOE_ERR_INVALID_ARG;
   return hip_status(moe::launch_probe_read(buf, bytes, (uint32_t *)out, (hipStream_t)stream));

@@ -127,3 +127,20 @@ def test_addresses_of_odd_rows(dtype, size, whole):
     for change in (dict(x=0x1001), dict(w=0x2001)):
         assert status(8, K, N, dtype, **change) == (bad, bad)
     assert status(8, K, N, dtype, dy=0x3001) == (ok, bad)
+
+
+def test_linear_path():
+    c = C.LinearConfig(4096, 4096, 4096)
+    assert B.moe_linear_path(c) == ("tiled", 256, 256, 1)
+    assert B.moe_linear_path(replace(c, rows=16)) == ("few", 0, 0, 0)
+    assert B.moe_linear_path(replace(c, rows=16), ld_x=4097)[0] != "few"
+    small = C.LinearConfig(301, 256, 320, "f32", "silu")
+    assert [B.moe_linear_path(small, p) for p in ("forward", "dx", "dw")] == [("small", 0, 0, 0)] * 3
+    assert B.moe_linear_path(replace(c, rows=64, in_dim=8192, out_dim=72))[3] > 1
+    for bad in (replace(c, in_dim=0), replace(c, rows=-1)):
+        with pytest.raises(B.MoEError):
+            B.moe_linear_path(bad)
+    ok = B.MoeLinearConfigC(8, 8, 8, 1, 0, 0.0, 0, 0, 0)
+    info = B.MoeLinearPathC()
+    assert B._lib.moe_linear_path(ok, 3, info) == B._lib.moe_linear_path(ok, -1, info) == B.MOE_ERR_INVALID_ARG
+    assert B._lib.moe_linear_path(ok, 0, None) == B._lib.moe_linear_path(None, 0, info) == B.MOE_ERR_INVALID_ARG
