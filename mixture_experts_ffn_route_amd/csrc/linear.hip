@@ -609,25 +609,30 @@ struct Shape {
 };
 
 Shape pick_shape(int64_t rows, int64_t cols, int64_t stages, bool f32, bool dual) {
-  struct { int mi, ni; double stage, alone, stage_f32, alone_f32, fixed; } shapes[] = {
-      {4, 4, 0.80, 0.56, 3.8, 3.8, 14.0},
-      {4, 2, 0.52, 0.36, 1.9, 1.9, 8.0},
-      {2, 2, 0.27, 0.22, 0.94, 0.94, 3.5},
-      {1, dual ? 2 : 1, dual ? 0.186 : 0.127, 0.2, dual ? 0.5 : 0.254, dual ? 0.6 : 0.33, 1.0}};
+  struct Cost { int mi, ni; double stage, alone, fixed; };
+  const Cost in_bf16[] = {{4, 4, 0.80, 0.56, 14.0},
+                          {4, 2, 0.52, 0.36, 8.0},
+                          {2, 2, 0.27, 0.22, 3.5},
+                          {1, dual ? 2 : 1, dual ? 0.186 : 0.127, 0.2, 1.0}};
+  // fp32 MFMAs bound every shape alike (256x256 3.8 a stage and 14 fixed, 256x128
+  // 1.9 and 8): the larger tiles are at best as fast, and there are none
+  const Cost in_f32[] = {{2, 2, 0.94, 0.94, 3.5},
+                         {1, dual ? 2 : 1, dual ? 0.5 : 0.254, dual ? 0.6 : 0.33, 1.0}};
+  const Cost *shapes = f32 ? in_f32 : in_bf16;
   Shape best = {1, 1, 1, 1e300};
-  for (const auto &sh : shapes) {
+  for (int i = 0; i < (f32 ? 2 : 4); ++i) {
+    const Cost &sh = shapes[i];
     const int64_t tiles = ((rows + 64 * sh.mi - 1) / (64 * sh.mi)) *
                           ((cols + 64 * sh.ni - 1) / (64 * sh.ni));
-    const double stage = f32 ? sh.stage_f32 : sh.stage, alone = f32 ? sh.alone_f32 : sh.alone;
     for (int parts = 1; parts <= 16; parts *= 2) {
       if (parts > 1 && (stages < 16 * parts || tiles * parts > 1024)) break;
       const int64_t items = tiles * parts, full = items / 256;
       const double last = (double)(items - full * 256) / 256;
       const double deep = (double)((stages + parts - 1) / parts);
-      double t = full * (deep * stage + sh.fixed);
+      double t = full * (deep * sh.stage + sh.fixed);
       if (last > 0) {
-        const double s = f32 ? stage : stage * (0.7 + 0.3 * last);
-        t += deep * (full == 0 && alone > s ? alone : s) + sh.fixed;
+        const double s = f32 ? sh.stage : sh.stage * (0.7 + 0.3 * last);
+        t += deep * (full == 0 && sh.alone > s ? sh.alone : s) + sh.fixed;
       }
       // partial sums: a launch, and written and read at 8 TB/s in all
       if (parts > 1) t += 5.0 + (double)rows * cols * parts * 1e-6;
@@ -671,8 +676,10 @@ hipError_t run_gemm(GemmOp g, const Shape &sh, void *part, hipStream_t s) {
   if (g.halves < 1) g.halves = 1;
   g.part = (float *)part;
   g.ldp = (g.e.N + 7) / 8 * 8;
-  if (sh.mi == 4 && sh.ni == 4) return run_gemm_shape<T, 4, 4, AC, BC, DUAL>(g, s);
-  if (sh.mi == 4) return run_gemm_shape<T, 4, 2, AC, BC, DUAL>(g, s);
+  if constexpr (sizeof(T) == 2) {
+    if (sh.mi == 4 && sh.ni == 4) return run_gemm_shape<T, 4, 4, AC, BC, DUAL>(g, s);
+    if (sh.mi == 4) return run_gemm_shape<T, 4, 2, AC, BC, DUAL>(g, s);
+  }
   if (sh.mi == 2) return run_gemm_shape<T, 2, 2, AC, BC, DUAL>(g, s);
   return run_gemm_shape<T, 1, DUAL ? 2 : 1, AC, BC, DUAL>(g, s);
 }
