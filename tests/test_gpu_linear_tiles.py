@@ -9,6 +9,8 @@ import pytest
 from mixture_experts_ffn_route_amd import binding as B
 from tests import test_gpu_linear as L
 
+pytestmark = pytest.mark.gpu
+
 # dtype, activation, limit, rows, in, out: tiles of the forward, dx and dW ("/": split contraction)
 CASES = [
     # gate|up widths of the named hash-routed and FP4 workloads in training
