@@ -1218,7 +1218,12 @@ hipError_t run_few(FewArgs a, hipStream_t s) {
   hipLaunchKernelGGL((few_up<F, TILED>), dim3(up < kGroups ? (unsigned)up : kGroups), dim3(256), 0,
                      s, a);
   if ((err = hipGetLastError()) != hipSuccess) return err;
-  // one wave a tile where the scales of all its inputs fit a wave's share of LDS
+  // one wave a tile where the scales of all its inputs fit a wave's share of LDS.
+  // Four waves | one in us a layer, at 1, 2, 5 and 16 tokens of 64 experts: bf16
+  // activations 5120x1536 46.5 | 46.9, 65.1 | 62.8, 102.8 | 96.6, 174 | 166; 1024x256
+  // 23.7 | 24.5, 24.7 | 25.6, 27.2 | 27.8, 38.0 | 36.3; MXFP8 5120x1536 44.8 | 42.9, 62.3 |
+  // 59.2, 96.9 | 90.4, 156 | 146: up to 1 us behind where there are few tiles, up to 11
+  // ahead where there are many
   constexpr bool FP4 = is_fp4<F>();
   const bool one = FP4 && a.I <= 7 * 256;
   const int64_t blocks = (a.d + 63) / 64;
@@ -1252,11 +1257,15 @@ int few_logit_parts(int d, bool f32) {
 hipError_t launch_few(FewArgs a, const moe_config &cfg, hipStream_t s) {
   const bool tiled = cfg.weight_layout == MOE_LAYOUT_TILED;
   const bool learned = cfg.route_mode == MOE_ROUTE_LEARNED;
-  // A gate of at most 64 experts and 2 KB a row: the routing workgroup computes
-  // its logits itself, two bursts of loads in place of a launch (20.6 -> 18.9 us for
-  // a 3-token layer of 16 experts).  MXFP8 layers need the launch for x's codes.
-  a.small_gate = learned && a.E <= 64 && !a.xq &&
-                 (int64_t)a.d * (cfg.act_dtype == MOE_DTYPE_F32 ? 4 : 2) <= 2048;
+  // A gate of at most 32 KB in rows of at most 2 KB (two bursts of loads a wave) and
+  // 64 experts (what LDS holds): the routing workgroup computes its logits itself in
+  // place of a launch.  Launch | itself in us a layer, one and 16 tokens: 8 KB (fp32,
+  // 16 experts of 128) 19.9 | 18.5 and 23.5 | 22.1; 32 KB (32 of 256) 22.1 | 20.8 and
+  // 25.6 | 25.0, (64 of 128) 20.3 | 19.7 and 24.0 | 24.4; 64 KB (64 of 256) 22.1 | 21.8
+  // and 25.8 | 27.0, (32 of 512) 25.0 | 25.3 and 29.1 | 30.3; bf16 within 0.5 of that.
+  // MXFP8 layers need the launch for x's codes.
+  const int64_t gate_row = (int64_t)a.d * (cfg.act_dtype == MOE_DTYPE_F32 ? 4 : 2);
+  a.small_gate = learned && a.E <= 64 && !a.xq && gate_row <= 2048 && a.E * gate_row <= 32768;
   a.score_items = learned && !a.small_gate ? (a.E + 15) / 16 * a.KS : 0;
   if (cfg.act_dtype == MOE_DTYPE_F32) return run_few<F_F32, false>(a, s);
   if (cfg.expert_dtype == MOE_DTYPE_FP8_E4M3_B128) return run_few<F_MX8, true>(a, s);

@@ -207,3 +207,18 @@ def test_groups_of_one_expert(E, gpu, monkeypatch):
     torch.cuda.synchronize()
     assert torch.equal(B.few_views(cfg, 11, ws)["route_indices"], B.few_views(cfg1, 11, ws1)["route_indices"])
     assert torch.equal(y, y1)
+
+
+@pytest.mark.parametrize("base,dim,E", [("tiny_fp32", 128, 64), ("tiny_fp32", 129, 64), ("tiny_fp32", 256, 32),
+                                        ("tiny_fp32", 2730, 3), ("v3_small", 256, 64), ("v3_small", 256, 65),
+                                        ("v3_small", 5120, 3)])
+@pytest.mark.parametrize("T", [1, 16])
+def test_gates_around_32_kb(base, dim, E, T, gpu, monkeypatch):
+    """Around the sizes up to which the routing workgroup computes the logits."""
+    name = put(monkeypatch, base, f"{base}_gate_{dim}_{E}", dim=dim, n_routed_experts=E, n_expert_groups=1,
+               n_limited_groups=1, n_activated_experts=3)
+    wl, cfg, run, plain = F.make(name, T, gpu)
+    ws = torch.full((B.moe_few_workspace_size(cfg, T),), 0xFF, dtype=torch.uint8, device=gpu)
+    y, _ = F.few(cfg, run, T, ws)
+    torch.cuda.synchronize()
+    F.check(wl, cfg, plain, T, y, ws, f"{name} T={T}")
