@@ -532,8 +532,8 @@ typedef struct {               /* contiguous except dx; NULL: not wanted        
 } moe_linear_grads;
 
 /* Workspace of moe_linear (backward = 0) or moe_linear_backward (backward = 1,
- * for every gradient).  Host-only; 0 for an invalid configuration, 256 at
- * least for a valid one. */
+ * for every gradient).  Host-only; 0 for a configuration that the call refuses,
+ * 256 at least for one that it takes. */
 size_t moe_linear_workspace_size(const moe_linear_config *cfg, int32_t backward);
 
 /* The forward product.
@@ -553,7 +553,9 @@ size_t moe_linear_workspace_size(const moe_linear_config *cfg, int32_t backward)
  * strides, an element's size where not; the others an element's size.  No output
  * may overlap an input (but y the residual) or another output.  Results do not
  * depend on what else runs (no atomics).  Only kernels are enqueued on `stream`, so the call
- * can be captured in a HIP graph.  rows == 0 is a no-op. */
+ * can be captured in a HIP graph.  rows == 0 is a no-op.  Sizes whose launch
+ * would have 2^32 threads or more (2^30 rows of 64 columns, or padded copies of
+ * 2^32 16-byte pieces) are MOE_ERR_UNSUPPORTED. */
 int moe_linear(const moe_linear_config *cfg, const moe_linear_weights *w, const void *x,
                const void *residual, void *y, void *z, void *z_up,
                void *ws, size_t ws_bytes, void *stream);

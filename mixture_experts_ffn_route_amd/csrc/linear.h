@@ -57,6 +57,10 @@ LinearSpace linear_space(const moe_linear_config &c, bool backward, bool dx, boo
 // Which kernels a product takes (moe_linear_product, of a checked configuration).
 moe_linear_path_info linear_path(const moe_linear_config &c, int32_t product);
 
+// Whether each launch of a call has fewer than 2^32 threads, as HIP asks (backward:
+// for every gradient).
+bool linear_launchable(const moe_linear_config &c, bool backward);
+
 hipError_t launch_linear(const moe_linear_config &c, const moe_linear_weights &w, const void *x,
                          const void *residual, void *y, void *z, void *z_up, char *ws,
                          hipStream_t s);

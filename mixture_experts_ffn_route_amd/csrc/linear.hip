@@ -957,6 +957,39 @@ moe_linear_path_info linear_path(const moe_linear_config &c, int32_t product) {
   return info;
 }
 
+bool linear_launchable(const moe_linear_config &c, bool backward) {
+  const int64_t M = c.rows, K = c.in_dim, N = c.out_dim, wide = K > N ? K : N;
+  // at most one thread an element, in tiles of 32 x 32 (512 threads): most calls
+  if ((M + 32) * (wide + 32) < (int64_t)1 << 31 && (N + 32) * (K + 32) < (int64_t)1 << 30) return true;
+  const int64_t both = c.activation == MOE_ACTIVATION_SWIGLU ? 2 : 1;
+  auto tiles = [](int64_t rows, int64_t cols, int64_t r, int64_t q) {
+    return (rows + r - 1) / r * ((cols + q - 1) / q);
+  };
+  int64_t most = 0;
+  auto launch = [&](int64_t threads) { most = threads > most ? threads : most; };
+  // the two matrices of swiglu's forward share a tile, those of its dW do not
+  auto gemm = [&](int64_t rows, int64_t cols, int32_t product) {
+    const Shape s = product_shape(c, product);
+    const int64_t wide = 64 * s.ni / (product == MOE_LINEAR_FORWARD ? both : 1);
+    const int64_t n = tiles(rows, cols, 64 * s.mi, wide) * (product == MOE_LINEAR_DW ? both : 1);
+    launch(256 * ((n * s.parts + 7) / 8 * 8));
+  };
+  const int64_t pieces = (K + linear_pad(1, c.dtype) - 1) / linear_pad(1, c.dtype);
+  if (backward && backward_small(c)) {
+    launch(512 * (tiles(M, K, 32, 32) + both * tiles(N, K, 32, 32)));
+  } else if (backward) {
+    gemm(M, K, MOE_LINEAR_DX);
+    gemm(N, K, MOE_LINEAR_DW);
+  } else if (const auto path = forward_path(c); path == MOE_LINEAR_PATH_SMALL) {
+    launch(512 * tiles(M, N, 32, 32));
+  } else if (path == MOE_LINEAR_PATH_TILED) {
+    gemm(M, N, MOE_LINEAR_FORWARD);
+  }
+  if (linear_odd_rows(K, c.ld_x, c.dtype)) launch(M * pieces + 256);
+  if (linear_odd_rows(K, K, c.dtype)) launch(N * pieces + 256);
+  return most < (int64_t)1 << 32;
+}
+
 hipError_t launch_linear(const moe_linear_config &c, const moe_linear_weights &w, const void *x,
                          const void *residual, void *y, void *z, void *z_up, char *ws,
                          hipStream_t s) {

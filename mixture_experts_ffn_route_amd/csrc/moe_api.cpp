@@ -819,7 +819,7 @@ int moe_forward_ex(const moe_config *cfg, const moe_weights *w, const void *x,
 
 size_t moe_linear_workspace_size(const moe_linear_config *cfg, int32_t backward) {
   moe_linear_config c;
-  if (check_linear(cfg, &c) != MOE_OK) return 0;
+  if (check_linear(cfg, &c) != MOE_OK || !moe::linear_launchable(c, backward != 0)) return 0;
   // whichever gradients a call asks for
   size_t n = kAlign;
   for (int want = backward ? 1 : 7; want < 8; ++want) {
@@ -841,6 +841,7 @@ int moe_linear(const moe_linear_config *cfg, const moe_linear_weights *w, const 
     return MOE_ERR_INVALID_ARG;
   if ((z && dual && !z_up) || (z_up && (!z || !dual))) return MOE_ERR_INVALID_ARG;
   if (c.rows == 0) return MOE_OK;
+  if (!moe::linear_launchable(c, false)) return MOE_ERR_UNSUPPORTED;
   if (!x || !y || (residual == y && c.ld_residual != c.ld_y)) return MOE_ERR_INVALID_ARG;
   if (overlap({y, z, z_up}, {x, w->w, w->w_up, w->bias, w->bias_up}) || overlap({z, z_up}, {residual}))
     return MOE_ERR_INVALID_ARG;
@@ -869,6 +870,7 @@ int moe_linear_backward(const moe_linear_config *cfg, const moe_linear_weights *
   const bool want_dw = grads->dw || grads->dw_up, want_db = grads->dbias || grads->dbias_up;
   if (!grads->dx && !want_dw && !want_db) return MOE_ERR_INVALID_ARG;
   if (!dual && (grads->dw_up || grads->dbias_up)) return MOE_ERR_INVALID_ARG;
+  if (!moe::linear_launchable(c, true)) return MOE_ERR_UNSUPPORTED;
   if (c.rows > 0) {
     if (!dy || misaligned(dy, linear_align(c.out_dim, c.ld_y, c.dtype))) return MOE_ERR_INVALID_ARG;
     if (c.activation != MOE_ACTIVATION_NONE && (!z || (dual && !z_up))) return MOE_ERR_INVALID_ARG;

@@ -144,3 +144,17 @@ def test_linear_path():
     info = B.MoeLinearPathC()
     assert B._lib.moe_linear_path(ok, 3, info) == B._lib.moe_linear_path(ok, -1, info) == B.MOE_ERR_INVALID_ARG
     assert B._lib.moe_linear_path(ok, 0, None) == B._lib.moe_linear_path(None, 0, info) == B.MOE_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("M,K,N,fits", [
+    (1 << 20, 8192, 8192, (True, True)), (1 << 29, 64, 8, (True, True)), ((1 << 31) - 1, 8, 8, (False, False)),
+    ((1 << 30) - 1024, 8, 8, (True, True)), (1 << 30, 8, 8, (False, False)), (1 << 30, 33, 8, (False, False)),
+    (64, (1 << 20) - 1, (1 << 20) - 1, (False, False))])
+def test_sizes_past_a_launch(M, K, N, fits):
+    """Refused before anything is launched where a launch would have 2^32 threads."""
+    c = C.LinearConfig(M, K, N)
+    assert tuple(B.moe_linear_workspace_size(c, back) > 0 for back in (False, True)) == fits
+    want = tuple(B.MOE_ERR_UNSUPPORTED if not f else None for f in fits)
+    got = status(M, K, N, "bf16")
+    assert all(w in (None, g) for g, w in zip(got, want)) and not any(
+        w is None and g == B.MOE_ERR_UNSUPPORTED for g, w in zip(got, want))
