@@ -32,11 +32,13 @@
 //
 // Measured (microseconds of the launches, row-layout weights): V4.1-Flash-shaped
 // FP4 experts on bf16 activations, one token (151 MB of weights): scores 4, plan
-// 11, up 17, down 14, combine 4; five tokens (532 MB): 5, 12, 61 (5.3 TB/s), 37,
-// 5; 16 tokens on MXFP8 activations (1.43 GB): 5, 20, 139 (6.6 TB/s), 88, 5.
-// V3-shaped bf16 experts, one token (796 MB): 4, 13, 70 (6.7 TB/s), 42, 4.
+// 11, up 17, down 14, combine 4; five tokens (532 MB): 5, 13, 61 (5.3 TB/s), 37,
+// 5; 16 tokens on MXFP8 activations (1.43 GB): 5, 20, 141 (6.5 TB/s), 88, 5.
+// V3-shaped bf16 experts, one token (796 MB): 4, 13, 71 (6.6 TB/s), 42, 4.
 // What is left over the weights' time is each launch's start (a first load
-// takes 2 - 3 us) and the routing's chain of dependent steps.
+// takes 2 - 3 us), the shared expert's gate|up on one workgroup per 16 columns (at
+// one token that stream, 34 KB a microsecond and CU, is the plan launch's time, at
+// 16 the routing is), and at one token the CUs that up, down and combine leave idle.
 
 #include <climits>
 

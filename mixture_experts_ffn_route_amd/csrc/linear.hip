@@ -21,10 +21,12 @@
 // What bounds it: 256x256 tiles take 64 KB of LDS reads and 32 KB of copies per
 // 1024 MFMA cycles, so LDS is busy three quarters of the time that the matrix
 // cores need at best; 128 x 128 outputs a wave (256 accumulator registers) is
-// the least LDS traffic per product that the registers allow.  bf16 4096x8192
-// ->4096 1200, dx 4096x4096x8192 1280, dW 8192x4096x4096 1340 TFLOP/s; the
-// library's product reaches 1310 at 8192^3, the power limit's clock (2.05 of
-// 2.4 GHz) included.  fp32 143 TFLOP/s (library 150).
+// the least LDS traffic per product that the registers allow.  A round of tiles
+// also has a start and an epilogue in which nothing multiplies, 14 us at 256x256,
+// so short rounds are slower.  bf16 TFLOP/s: 8192^3 1220, its dx 1295 and dW 1360
+// (the library's product 1310 to 1570, by the power limit's clock); 4096x8192
+// ->4096 1220; 4096^3 1125 (library 1330 - 1450), 4096x2048->7168 920 (1270 - 1300),
+// 4096x2048->2048 755 (945).  fp32 4096^3 142, 4096x2048->7168 139 (149 and 147).
 //
 // Copies are buffer loads into LDS: a piece past the end of a matrix or of the
 // contraction arrives as zeros without traffic, which covers every ragged
@@ -362,7 +364,7 @@ __device__ __forceinline__ void gemm_tile(const GemmOp &g) {
   // part of LDS (no barrier), so that a lane then has eight consecutive columns
   // of a row and 16 or 8 lanes a whole line.  bf16: the whole tile's residual is
   // asked for at once, into the registers that the operands have left (in 32-row
-  // pieces a read's latency bounded it: 161 instead of 146 us at 4096x2048->7168).
+  // pieces a read's latency bounded it: 10 % longer at 4096x2048->7168).
   constexpr int NJ = DUAL ? NI / 2 : NI;       // output column blocks of the wave
   constexpr int PC = NJ * 4;                   // pieces of 8 columns per row
   constexpr int PPI = 32 * PC / 64;            // pieces per lane and 32 rows
@@ -696,8 +698,8 @@ Shape product_shape(const moe_linear_config &c, int32_t product) {
 }
 
 // The kernels of a call.  Up to kFewRows rows take the stream of W where no copy
-// has to be made first (1x7168->2x2048 swiglu bf16 17.5 -> 14.5 us, 16x4096->4096
-// fp32 29 -> 18 us).  Otherwise 32 x 32 tiles where their estimate is below that
+// has to be made first (1x7168->2x2048 swiglu bf16 11.4 us, 17.5 by tiles;
+// 16x4096->4096 fp32 18, 29 by tiles).  Otherwise 32 x 32 tiles where their estimate is below that
 // of the GEMM with the launches around it (4 us each, with the wait for the one
 // before).  Microseconds per round of 256 tiles and eight chunks of the
 // contraction, measured with either way forced on 60 shapes: 203x777->1023 fp32

@@ -173,8 +173,8 @@ struct Biases {
 
 // y (and z) of eight columns n .. of row m from the raw products v (and u).
 // Biases and res, the residual there if there is one, are loaded ahead by the
-// caller: a load here would wait its full latency for every piece (146 instead of
-// 139 us at 4096x2048->7168).
+// caller: a load here would wait its full latency for every piece (5 % longer at
+// 4096x2048->7168).
 template <typename T, bool DUAL>
 __device__ __forceinline__ void finish8(const Epilogue &e, float (&v)[8], float (&u)[8],
                                         const Biases<T, DUAL> &bias, const float (&res)[8],

@@ -9,8 +9,8 @@
 // operand order straight from memory, 16 rows x 64 bytes a load, reaches 5 of
 // the 7 TB/s); x comes from L2 to registers.  MFMA rows are rows of W, columns
 // rows of x, so a lane ends with four consecutive columns of y.  1x7168->2x2048
-// swiglu bf16 (59 MB) 11.5 us, 5.1 TB/s with launch and start; 1x5120->27648 (283
-// MB) 45 us, 6.3 TB/s.
+// swiglu bf16 (59 MB) 11.4 us, 5.2 TB/s with launch and start; 1x5120->27648 (283
+// MB) 44 us, 6.4 TB/s.
 //
 // small_forward_kernel and small_backward_kernel, small products: time goes by
 // launches and the longest chain in a workgroup, not by bytes or MFMAs.  A
