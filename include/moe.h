@@ -599,6 +599,122 @@ typedef struct {
 } moe_linear_path_info;
 int moe_linear_path(const moe_linear_config *cfg, int32_t product, moe_linear_path_info *info);
 
+/* What trains the MoE layer: token rows to their experts and back with the gate
+ * values, the experts' products on sorted rows, each with its gradient, and 8-bit
+ * checkpoints of activations.  A training step of the routed experts is
+ *   moe_route, moe_permute, moe_dispatch, moe_experts, moe_combine
+ *   moe_combine_backward, moe_experts_backward, moe_dispatch_backward
+ * with moe_dispatch again before moe_experts_backward where the sorted rows of x
+ * were not kept (they are k times x).  "DeepSeek-V3.2-Exp - Routing weights",
+ * excerpt "moe-forward", is the forward part.
+ *
+ * Token rows to their experts and back.  Of cfg: dim, n_activated_experts (k, 1 ..
+ * 16) and act_dtype (F32 or BF16, of every row); any dim.
+ *   inverse   [T, k] int32: the sorted row of each pair, as moe_permute writes it;
+ *             one outside [0, R) has none (a dropped pair) and takes no part.  No
+ *             row stands twice in it
+ *   x, y, dx, dy, add  [T, dim];   rows, drows  [R, dim];   all contiguous
+ *   weights, dweights  [T, k] float
+ * Sums are fp32, over the slots in order; results are rounded once and do not
+ * depend on what else runs.  Alignment: an element's size.  No output may overlap
+ * an input or another output.  T == 0 is a no-op.  Sizes whose launch would have 2^32
+ * threads (a thread takes 16 bytes of a token's row) are MOE_ERR_UNSUPPORTED.  Only
+ * kernels are enqueued, so the calls can be captured in a HIP graph.
+ *
+ * rows[inverse[t, j]] = x[t]; sorted rows that stand in no pair are left alone. */
+int moe_dispatch(const moe_config *cfg, const void *x, const int32_t *inverse, int64_t T, int64_t R,
+                 void *rows, void *stream);
+/* dx[t] = sum over j of drows[inverse[t, j]]. */
+int moe_dispatch_backward(const moe_config *cfg, const void *drows, const int32_t *inverse, int64_t T,
+                          int64_t R, void *dx, void *stream);
+/* y[t] = sum over j of weights[t, j] rows[inverse[t, j]], + add[t] (the shared
+ * expert's output or a residual; NULL: none).  The gradient of add is that of y. */
+int moe_combine(const moe_config *cfg, const void *rows, const int32_t *inverse, const float *weights,
+                const void *add, int64_t T, int64_t R, void *y, void *stream);
+/* drows[inverse[t, j]] = weights[t, j] dy[t] (other rows are left alone) and
+ * dweights[t, j] = rows[inverse[t, j]] . dy[t] (0 where a pair has no row).  Either
+ * may be NULL: not wanted; rows is read for dweights alone, weights for drows. */
+int moe_combine_backward(const moe_config *cfg, const void *dy, const void *rows,
+                         const int32_t *inverse, const float *weights, int64_t T, int64_t R,
+                         void *drows, float *dweights, void *stream);
+
+/* 8-bit checkpoints: a matrix kept in 1 + 1/32 bytes a value between the forward
+ * and the backward pass (pre-activations of moe_linear, for one).  Per 32
+ * consecutive columns of a row (fewer at its end) one E8M0 scale byte X + 127 and
+ * E4M3 codes of v / 2^X, nearest value, ties to even; X is the least integer >= -127
+ * with max|v| <= 448 2^X, 0 for a block of zeros: nothing saturates, a value is off
+ * by 2^-4 of itself at most (below 2^-6 2^X: by 2^-10 2^X).
+ * limit > 0: no value is carried across +-limit (the next code on the value's side
+ * is taken), because the gradient of a clamp goes by the saved value; 0: no clamp.
+ * NaN and infinities are kept as NaN and do not count for X.
+ *   src, dst  [rows, cols] dtype (F32 or BF16), row stride ld elements (0: cols)
+ *   codes     [rows, cols] bytes;   scales  [rows, ceil(cols / 32)] bytes
+ * Any sizes and strides; alignment an element's size.  Outputs may not overlap
+ * inputs.  rows == 0 is a no-op. */
+int moe_checkpoint_save(const void *src, int32_t dtype, int64_t rows, int32_t cols, int64_t ld_src,
+                        float limit, uint8_t *codes, uint8_t *scales, void *stream);
+int moe_checkpoint_load(const uint8_t *codes, const uint8_t *scales, int32_t dtype, int64_t rows,
+                        int32_t cols, int64_t ld_dst, void *dst, void *stream);
+
+/* The routed experts on sorted rows.  For the rows r of expert e, offsets[e] ..
+ * offsets[e + 1]:
+ *   z = x W_gate^T, u = x W_up^T, y = (SiLU(min(z, L)) clamp(u, -L, L)) W_down^T
+ * without the gate value, which moe_combine applies.  Of cfg: dim,
+ * n_routed_experts (E, or one rank's share; to 1024), moe_inter_dim (I),
+ * swiglu_limit (L, 0: no clamp), act_dtype = expert_dtype (F32 or BF16),
+ * weight_layout ROWS, act_quant NONE; dim and I whole 16-byte pieces (multiples of 8
+ * in bf16, of 4 in fp32); other types, layouts and widths are MOE_ERR_UNSUPPORTED.
+ *   w         w_gate, w_up [E, I, dim], w_down [E, dim, I]
+ *   x, y      [rows, dim]; rows of no expert (rows >= offsets[E]: room that a batch
+ *             leaves) are neither read nor written, here and in the gradient
+ *   offsets   [E + 1] int32 on the device, as moe_permute writes it.  Values outside
+ *             [0, rows] or descending ones are clamped: no access is out of range
+ *   saved     where z and u go for the gradient: kind FULL in the layer's type
+ *             (never rounded across the clamp's border), kind MXFP8 as
+ *             moe_checkpoint_save with limit L keeps them (I % 32 == 0).  NULL or
+ *             kind NONE: not saved
+ *   ws        moe_experts_workspace_size(cfg, rows, 0) bytes, 256-byte aligned;
+ *             nothing in it needs to start at any value.  Calls that share one must
+ *             be ordered on one stream
+ * Products accumulate in fp32; h = SiLU(..) clamp(..) is rounded to the type once
+ * (as the next product takes it), y once.  Matrices 16-byte aligned.  No output may
+ * overlap an input or another output.  Results do not depend on what else runs (no
+ * atomics).  Only kernels are enqueued: the calls can be captured in a HIP graph,
+ * whose replays may have other offsets.  rows == 0 is a no-op. */
+typedef enum {
+  MOE_SAVE_NONE = 0,
+  MOE_SAVE_FULL = 1,
+  MOE_SAVE_MXFP8 = 2
+} moe_save_kind;
+typedef struct {
+  int32_t kind;                /* moe_save_kind                                  */
+  void *gate, *up;             /* z, u: [rows, I] act_dtype, or bytes (codes)    */
+  uint8_t *gate_scales;        /* MXFP8: [rows, I / 32]                          */
+  uint8_t *up_scales;
+} moe_experts_saved;
+typedef struct {               /* NULL: not wanted; contiguous                   */
+  void *dx;                    /* [rows, dim]                                    */
+  void *dw_gate, *dw_up;       /* [E, I, dim]                                    */
+  void *dw_down;               /* [E, dim, I]                                    */
+} moe_experts_grads;
+size_t moe_experts_workspace_size(const moe_config *cfg, int64_t rows, int32_t backward);
+int moe_experts(const moe_config *cfg, const moe_weights *w, const void *x, const int32_t *offsets,
+                int64_t rows, void *y, const moe_experts_saved *saved, void *ws, size_t ws_bytes,
+                void *stream);
+/* Its gradient for dy [rows, dim]:
+ *   dh = dy W_down, dz = dh clamp(u) SiLU'(z) where z <= L, du = dh SiLU(z) where
+ *   |u| <= L, both 0 elsewhere; h from z and u again
+ *   dx = dz W_gate + du W_up, dw_gate = dz^T x, dw_up = du^T x, dw_down = dy^T h
+ * with z and u as `saved` holds them.  Outputs are overwritten; an expert without
+ * rows gets zeros.  w_down is always read, w_gate and w_up for dx, x for dw_gate and
+ * dw_up; w's others may be NULL.  dz, du and h are rounded to the type once, as the
+ * products take them.  ws: moe_experts_workspace_size(cfg, rows, 1) bytes.
+ * rows == 0 writes zeros to the weight gradients. */
+int moe_experts_backward(const moe_config *cfg, const moe_weights *w, const void *x,
+                         const int32_t *offsets, int64_t rows, const void *dy,
+                         const moe_experts_saved *saved, const moe_experts_grads *grads, void *ws,
+                         size_t ws_bytes, void *stream);
+
 /* Roofline probes: the achievable HBM read rate and bf16 / FP8 MFMA rates of
  * the GPU, measured with the instruction forms the layer kernels use (16-byte
  * nontemporal vector loads; v_mfma_f32_16x16x32_bf16, v_mfma_f32_32x32x16_bf16,

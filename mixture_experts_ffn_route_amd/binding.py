@@ -36,6 +36,9 @@ EXPORTED_SYMBOLS = (
     "moe_probe_mfma", "moe_redequant_fp8", "moe_forward_ex", "moe_forward_noalloc",
     "moe_few_workspace_layout", "moe_few_workspace_size", "moe_forward_few",
     "moe_linear_workspace_size", "moe_linear", "moe_linear_backward", "moe_linear_path",
+    "moe_dispatch", "moe_dispatch_backward", "moe_combine", "moe_combine_backward",
+    "moe_checkpoint_save", "moe_checkpoint_load", "moe_experts_workspace_size", "moe_experts",
+    "moe_experts_backward",
 )
 MOE_STAGES = ("route", "permute", "gemm1", "gemm2", "combine")
 
@@ -96,6 +99,15 @@ class MoeLinearPathC(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("path", "tile_rows", "tile_cols", "parts")]
 
 
+class MoeExpertsSavedC(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32)] + [(n, ctypes.c_void_p) for n in (
+        "gate", "up", "gate_scales", "up_scales")]
+
+
+class MoeExpertsGradsC(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("dx", "dw_gate", "dw_up", "dw_down")]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise RuntimeError(f"{LIB_PATH} is not built; run __graft_entry__.build() first")
@@ -134,6 +146,22 @@ def _load():
     lib.moe_linear_backward.argtypes = [lcp, lwp, vp, vp, vp, vp, ctypes.POINTER(MoeLinearGradsC),
                                         vp, ctypes.c_size_t, vp]
     lib.moe_linear_path.argtypes = [lcp, i32, ctypes.POINTER(MoeLinearPathC)]
+    size = ctypes.c_size_t
+    lib.moe_dispatch.argtypes = [cfgp, vp, vp, i64, i64, vp, vp]
+    lib.moe_dispatch_backward.argtypes = lib.moe_dispatch.argtypes
+    lib.moe_combine.argtypes = [cfgp, vp, vp, vp, vp, i64, i64, vp, vp]
+    lib.moe_combine_backward.argtypes = [cfgp, vp, vp, vp, vp, i64, i64, vp, vp, vp]
+    lib.moe_checkpoint_save.argtypes = [vp, i32, i64, i32, i64, ctypes.c_float, vp, vp, vp]
+    lib.moe_checkpoint_load.argtypes = [vp, vp, i32, i64, i32, i64, vp, vp]
+    sp = ctypes.POINTER(MoeExpertsSavedC)
+    lib.moe_experts_workspace_size.restype = size
+    lib.moe_experts_workspace_size.argtypes = [cfgp, i64, i32]
+    lib.moe_experts.argtypes = [cfgp, wp, vp, vp, i64, vp, sp, vp, size, vp]
+    lib.moe_experts_backward.argtypes = [cfgp, wp, vp, vp, i64, vp, sp,
+                                         ctypes.POINTER(MoeExpertsGradsC), vp, size, vp]
+    for f in ("moe_dispatch", "moe_dispatch_backward", "moe_combine", "moe_combine_backward",
+              "moe_checkpoint_save", "moe_checkpoint_load", "moe_experts", "moe_experts_backward"):
+        getattr(lib, f).restype = ctypes.c_int
     for f in ("moe_few_workspace_layout", "moe_forward_few", "moe_linear", "moe_linear_backward",
               "moe_linear_path"):
         getattr(lib, f).restype = ctypes.c_int
@@ -566,6 +594,198 @@ def moe_linear_backward(cfg: LinearConfig, dy, x, w, *, w_up=None, z=None, z_up=
         "moe_linear_backward")
 
 
+def _tensors_check(where, tensors, ws=None, launches=True):
+    """Types, shapes, contiguity and devices of a call's tensors, (name, tensor,
+    shape, dtype) each (None: not given, which the library refuses where it needs
+    one): it sees addresses only.  ws and the current device, where it launches."""
+    device = None
+    for name, t, shape, dtype in tensors:
+        if t is None:
+            continue
+        if t.dtype is not dtype or t.shape != shape:
+            raise ValueError(f"{where}: {name} is {tuple(t.shape)} {t.dtype}, "
+                             f"expected {shape} {dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{where}: {name} is not contiguous")
+        device = device or t.device
+        if t.device != device:
+            raise ValueError(f"{where}: {name} is on {t.device}, others on {device}")
+    if launches:
+        _device_check(where, device, ws)
+
+
+def _device_check(where, device, ws=None):
+    _ws_check(where, ws, device)
+    if device is None or device.type != "cuda":
+        raise ValueError(f"{where}: tensors on {device}, expected a GPU")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"{where}: tensors on {device}, not the current device")
+
+
+def _as_config_c(cfg):
+    return cfg if isinstance(cfg, MoeConfigC) else config_c(cfg)
+
+
+def _act_dtype(c: MoeConfigC):
+    return torch.float32 if c.act_dtype == DTYPE["f32"] else torch.bfloat16
+
+
+def _sorted_rows(rows):
+    return 0 if rows is None else rows.shape[0]
+
+
+def moe_dispatch(cfg, x, inverse, T: int, rows, stream=None):
+    """rows[inverse[t, j]] = x[t] for the T tokens; inverse [T, k] as moe_permute
+    writes it.  cfg, here and below: a MoEConfig or config_c of one."""
+    c, R = _as_config_c(cfg), _sorted_rows(rows)
+    dt, d = _act_dtype(c), c.dim
+    _tensors_check("moe_dispatch", (("x", x, (T, d), dt), ("rows", rows, (R, d), dt), (
+        "inverse", inverse, (T, c.n_activated_experts), torch.int32)), launches=T > 0 and R > 0)
+    _check(_lib.moe_dispatch(ctypes.byref(c), _raw(x), _raw(inverse), T, R, _raw(rows),
+                             _stream(stream)), "moe_dispatch")
+
+
+def moe_dispatch_backward(cfg, drows, inverse, T: int, dx, stream=None):
+    """dx[t] = sum over j of drows[inverse[t, j]]."""
+    c, R = _as_config_c(cfg), _sorted_rows(drows)
+    dt, d = _act_dtype(c), c.dim
+    _tensors_check("moe_dispatch_backward", (
+        ("drows", drows, (R, d), dt), ("dx", dx, (T, d), dt),
+        ("inverse", inverse, (T, c.n_activated_experts), torch.int32)), launches=T > 0)
+    _check(_lib.moe_dispatch_backward(ctypes.byref(c), _raw(drows), _raw(inverse), T, R, _raw(dx),
+                                      _stream(stream)), "moe_dispatch_backward")
+
+
+def moe_combine(cfg, rows, inverse, weights, T: int, y, add=None, stream=None):
+    """y[t] = sum over j of weights[t, j] rows[inverse[t, j]], + add[t]."""
+    c, R = _as_config_c(cfg), _sorted_rows(rows)
+    dt, d, pairs = _act_dtype(c), c.dim, (T, c.n_activated_experts)
+    _tensors_check("moe_combine", (
+        ("rows", rows, (R, d), dt), ("y", y, (T, d), dt), ("add", add, (T, d), dt),
+        ("inverse", inverse, pairs, torch.int32), ("weights", weights, pairs, torch.float32)),
+        launches=T > 0)
+    _check(_lib.moe_combine(ctypes.byref(c), _raw(rows), _raw(inverse), _raw(weights), _raw(add), T,
+                            R, _raw(y), _stream(stream)), "moe_combine")
+
+
+def moe_combine_backward(cfg, dy, rows, inverse, weights, T: int, drows=None, dweights=None,
+                         stream=None):
+    """Gradients of moe_combine for dy, into the tensors given (add's is dy)."""
+    c = _as_config_c(cfg)
+    R = _sorted_rows(drows if rows is None else rows)
+    dt, d, pairs = _act_dtype(c), c.dim, (T, c.n_activated_experts)
+    _tensors_check("moe_combine_backward", (
+        ("dy", dy, (T, d), dt), ("rows", rows, (R, d), dt), ("drows", drows, (R, d), dt),
+        ("inverse", inverse, pairs, torch.int32), ("weights", weights, pairs, torch.float32),
+        ("dweights", dweights, pairs, torch.float32)), launches=T > 0)
+    _check(_lib.moe_combine_backward(ctypes.byref(c), _raw(dy), _raw(rows), _raw(inverse),
+                                     _raw(weights), T, R, _raw(drows), _raw(dweights),
+                                     _stream(stream)), "moe_combine_backward")
+
+
+_CHECKPOINT_DTYPE = {torch.float32: DTYPE["f32"], torch.bfloat16: DTYPE["bf16"]}
+
+
+def _checkpoint_check(where, name, m, codes, scales):
+    """(rows, cols, row stride) of the matrix and checks of its codes."""
+    if m.dtype not in _CHECKPOINT_DTYPE or m.dim() != 2:
+        raise ValueError(f"{where}: {name} is {tuple(m.shape)} {m.dtype}, "
+                         f"expected a matrix in float32 or bfloat16")
+    rows, cols = m.shape
+    if m.numel() and (m.stride(1) != 1 and cols > 1 or m.stride(0) < cols and rows > 1):
+        raise ValueError(f"{where}: {name}'s rows are not contiguous or overlap")
+    _tensors_check(where, (("codes", codes, (rows, cols), torch.uint8),
+                           ("scales", scales, (rows, -(-cols // 32)), torch.uint8)),
+                   launches=False)
+    for other, t in (("codes", codes), ("scales", scales)):
+        if t.device != m.device:
+            raise ValueError(f"{where}: {other} is on {t.device}, others on {m.device}")
+    if rows:
+        _device_check(where, m.device)
+    return rows, cols, 0 if rows < 2 else m.stride(0)
+
+
+def moe_checkpoint_save(src, codes, scales, limit: float = 0.0, stream=None):
+    """The rows of src (which may stand in a wider buffer) in 8 bits: codes [rows,
+    cols] and scales [rows, ceil(cols / 32)], uint8."""
+    rows, cols, ld = _checkpoint_check("moe_checkpoint_save", "src", src, codes, scales)
+    _check(_lib.moe_checkpoint_save(_raw(src), _CHECKPOINT_DTYPE[src.dtype], rows, cols, ld, limit,
+                                    _raw(codes), _raw(scales), _stream(stream)),
+           "moe_checkpoint_save")
+
+
+def moe_checkpoint_load(codes, scales, dst, stream=None):
+    """The values that moe_checkpoint_save kept, into dst."""
+    rows, cols, ld = _checkpoint_check("moe_checkpoint_load", "dst", dst, codes, scales)
+    _check(_lib.moe_checkpoint_load(_raw(codes), _raw(scales), _CHECKPOINT_DTYPE[dst.dtype], rows,
+                                    cols, ld, _raw(dst), _stream(stream)), "moe_checkpoint_load")
+
+
+SAVE = {"none": 0, "full": 1, "mxfp8": 2}
+
+
+def _experts_check(where, c: MoeConfigC, layer, offsets, rows, saved, row_tensors, weight_grads, ws,
+                   launches=True):
+    dt, E, d, I = _act_dtype(c), c.n_routed_experts, c.dim, c.moe_inter_dim
+    tensors = [(n, t, (rows, d), dt) for n, t in row_tensors]
+    tensors.append(("offsets", offsets, (E + 1,), torch.int32))
+    shapes = {"w_gate": (E, I, d), "w_up": (E, I, d), "w_down": (E, d, I)}
+    if not isinstance(layer, MoeWeightsC):     # of weights_c's addresses nothing is known
+        tensors += [(n, layer.get(n), s, dt) for n, s in shapes.items()]
+    tensors += [(n, t, shapes[n[1:]], dt) for n, t in weight_grads]
+    if saved is not None and saved["kind"] != "none":
+        mx = saved["kind"] == "mxfp8"
+        tensors += [(n, saved[n], (rows, I), torch.uint8 if mx else dt) for n in ("gate", "up")]
+        if mx:
+            tensors += [(n, saved[n], (rows, I // 32), torch.uint8)
+                        for n in ("gate_scales", "up_scales")]
+    _tensors_check(where, tensors, ws, launches)
+
+
+def _saved_c(saved):
+    if saved is None:
+        return None
+    return ctypes.byref(MoeExpertsSavedC(SAVE[saved["kind"]], *(
+        _raw(saved.get(n)) for n in ("gate", "up", "gate_scales", "up_scales"))))
+
+
+def moe_experts_workspace_size(cfg, rows: int, backward=False) -> int:
+    return _lib.moe_experts_workspace_size(_config_ref(cfg), rows, int(bool(backward)))
+
+
+def moe_experts(cfg, layer, x, offsets, y, ws, saved=None, stream=None):
+    """y = the routed experts' output of the sorted rows x, without gate values.
+    offsets [E + 1] int32; saved: alloc_experts_saved, for moe_experts_backward;
+    ws: alloc_experts_workspace.  A training loop may build the C structs once and
+    pass them: cfg config_c of a MoEConfig, layer weights_c of the dict."""
+    c, rows = _as_config_c(cfg), x.shape[0]
+    _experts_check("moe_experts", c, layer, offsets, rows, saved, (("x", x), ("y", y)), (), ws,
+                   rows > 0)
+    w = layer if isinstance(layer, MoeWeightsC) else weights_c(layer)
+    _check(_lib.moe_experts(ctypes.byref(c), ctypes.byref(w), _raw(x), _raw(offsets), rows, _raw(y),
+                            _saved_c(saved), _raw(ws),
+                            0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)),
+           "moe_experts")
+
+
+def moe_experts_backward(cfg, layer, x, offsets, dy, saved, grads, ws, stream=None):
+    """Gradients of moe_experts for dy, into the tensors of grads (dx, dw_gate,
+    dw_up, dw_down; those not there are not wanted)."""
+    c, rows = _as_config_c(cfg), dy.shape[0]
+    names = [n for n, _ in MoeExpertsGradsC._fields_]
+    if not set(grads) <= set(names):
+        raise ValueError(f"moe_experts_backward: grads has {sorted(set(grads) - set(names))}")
+    _experts_check("moe_experts_backward", c, layer, offsets, rows, saved,
+                   (("x", x), ("dy", dy), ("dx", grads.get("dx"))),
+                   [(n, grads.get(n)) for n in names[1:]], ws)
+    w = layer if isinstance(layer, MoeWeightsC) else weights_c(layer)
+    g = MoeExpertsGradsC(*(_raw(grads.get(n)) for n in names))
+    _check(_lib.moe_experts_backward(ctypes.byref(c), ctypes.byref(w), _raw(x), _raw(offsets), rows,
+                                     _raw(dy), _saved_c(saved), ctypes.byref(g), _raw(ws),
+                                     0 if ws is None else ws.numel() * ws.element_size(),
+                                     _stream(stream)), "moe_experts_backward")
+
+
 class HipEvents:
     """Raw HIP timing events from the HIP runtime torch already loaded."""
 
@@ -678,3 +898,28 @@ def alloc_linear_workspace(cfg: LinearConfig, backward=False, device="cuda", **s
     if 0 in sizes:
         raise MoEError(MOE_ERR_INVALID_ARG, "moe_linear_workspace_size")
     return torch.empty(max(sizes), dtype=torch.uint8, device=device)
+
+
+def alloc_experts_workspace(cfg, rows: int, backward=False, device="cuda"):
+    """Workspace of moe_experts for up to `rows` sorted rows, or with `backward` one
+    that serves both it and moe_experts_backward."""
+    size = moe_experts_workspace_size(cfg, rows, backward)
+    if size == 0:
+        raise MoEError(MOE_ERR_UNSUPPORTED, "moe_experts_workspace_size")
+    return torch.empty(size, dtype=torch.uint8, device=device)
+
+
+def alloc_experts_saved(cfg, rows: int, kind="mxfp8", device="cuda") -> dict:
+    """Where moe_experts saves the pre-activations of `rows` sorted rows: kind "full"
+    in the layer's type, "mxfp8" in 8 bits with a scale per 32."""
+    c = _as_config_c(cfg)
+    I, dt = c.moe_inter_dim, torch.uint8 if kind == "mxfp8" else _act_dtype(c)
+    saved = {"kind": kind}
+    if kind != "none":
+        saved.update({n: torch.empty((rows, I), dtype=dt, device=device) for n in ("gate", "up")})
+    if kind == "mxfp8":
+        saved.update({n: torch.empty((rows, I // 32), dtype=torch.uint8, device=device)
+                      for n in ("gate_scales", "up_scales")})
+    elif kind not in SAVE:
+        raise ValueError(f"alloc_experts_saved: kind {kind!r}, expected one of {sorted(SAVE)}")
+    return saved

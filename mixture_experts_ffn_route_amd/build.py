@@ -19,7 +19,8 @@ LIB_NAME = "libmoe_mi355x.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 
 SOURCES = ["moe_api.cpp", "route.hip", "permute.hip", "experts.hip", "pack.hip", "probe.hip", "experts_mx.hip", "redequant.hip", "dense.hip",
-           "few.hip", "linear.hip", "linear_small.hip"]
+           "few.hip", "linear.hip", "linear_small.hip", "train_api.cpp", "rows.hip", "checkpoint.hip",
+           "grouped.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 COMMON_FLAGS = [

@@ -3,455 +3,25 @@
 //   z = x W^T + b,  y = act(z) + r                 (swiglu: two products)
 //   dz = dy act'(z), dx = dz W, dW = dz^T x, db = sum over rows of dz
 //
-// One GEMM kernel serves the three products.  D[M, N] = A B with A and B given
-// either "by rows" (the contraction index is the contiguous one) or "by
-// columns" (it is the row index), so no operand is transposed in memory:
+// One GEMM tile (tile.h) serves the three products, so no operand is transposed in
+// memory:
 //   forward  A = x  by rows,        B = W  by rows
 //   dx       A = dz by rows,        B = W  by columns (contraction over out)
 //   dW       A = dz by columns,     B = x  by columns (contraction over rows)
-//
-// A workgroup of four waves computes a (64 MI) x (64 NI) tile, each wave a
-// quarter of it as MI x NI blocks of v_mfma_f32_32x32x16_bf16 (fp32 layers:
-// four v_mfma_f32_32x32x2_f32 on the same bytes).  The contraction runs in
-// stages of 64 bytes per row (32 bf16 or 16 fp32) through a four-slot LDS ring
-// filled by asynchronous 16-byte copies; the fragments of the next step are
-// read from LDS while the MFMAs of this one run.  Column operands are read
-// back transposed by ds_read_b64_tr_b16 (fp32: one dword per lane).
-//
-// What bounds it: 256x256 tiles take 64 KB of LDS reads and 32 KB of copies per
-// 1024 MFMA cycles, so LDS is busy three quarters of the time that the matrix
-// cores need at best; 128 x 128 outputs a wave (256 accumulator registers) is
-// the least LDS traffic per product that the registers allow.  A round of tiles
-// also has a start and an epilogue in which nothing multiplies, 14 us at 256x256,
-// so short rounds are slower.  bf16 TFLOP/s: 8192^3 1220, its dx 1295 and dW 1360
-// (the library's product 1310 to 1570, by the power limit's clock); 4096x8192
-// ->4096 1220; 4096^3 1125 (library 1330 - 1450), 4096x2048->7168 920 (1270 - 1300),
-// 4096x2048->2048 755 (945).  fp32 4096^3 142, 4096x2048->7168 139 (149 and 147).
-//
-// Copies are buffer loads into LDS: a piece past the end of a matrix or of the
-// contraction arrives as zeros without traffic, which covers every ragged
-// size.  Rows that are not whole 16-byte pieces (odd widths or strides) are
+// Rows that are not whole 16-byte pieces (odd widths or strides) are
 // first copied to padded rows in the workspace.
 
-#include "linear_device.h"
+#include "tile.h"
 
 namespace moe {
 namespace {
 
-// ---------------------------------------------------------------------------
-// The GEMM.
-struct Matrix {
-  const void *p;
-  int64_t ld, rows;            // as stored: rows of ld elements, cols used
-  int64_t cols;
-};
-struct GemmOp {
-  Matrix a[2], b[2], b_up;     // contraction segments added up; b_up: swiglu
-  int64_t kdim[2];             // contraction length of each segment
-  int segments;
-  int64_t M;                   // rows of D
-  int n_tiles, parts;
-  int64_t m_tiles;
-  // dW of swiglu: two products of the same shape in one launch, row tiles of
-  // the second (a_up^T b -> y_up) after the first's
-  Matrix a_up;
-  void *y_up;
-  int halves;                  // 1 or 2
-  float *part;                 // parts > 1: [parts][halves, or 2 for swiglu][M][ldp]
-  int64_t ldp;
-  Epilogue e;
-};
-
-template <typename T, bool COL, int TC>
-struct Operand {
-  static constexpr int ES = sizeof(T);
-  static constexpr int KB = 64 / ES;           // contraction elements per stage
-  static constexpr int RB = TC * ES;           // column operand: bytes of an LDS row
-  // 16-byte pieces of an LDS row are permuted so that a half-wave's reads take
-  // distinct banks: by rows, row r's piece c sits at c ^ (r / 8 % 4) (eight
-  // rows of 64 bytes cover address bits 6-8, the four pieces bits 4-5); by
-  // columns, the four rows of a transposed read sit 64 bytes apart modulo 256.
-  static __device__ __forceinline__ int swz(int k) { return ES == 2 && TC >= 128 ? (k & 3) << 2 : 0; }
-
-  // Byte offset, from the stage's origin, of what lane l copies to byte 16 l of
-  // unit u.
-  static __device__ __forceinline__ uint32_t source(int u, int lane, int64_t ld) {
-    if constexpr (!COL) {
-      const int r = u * 16 + (lane >> 2);
-      return (uint32_t)(r * ld * ES) + ((lane & 3) ^ ((r >> 3) & 3)) * 16;
-    } else {
-      const int byte = u * 1024 + lane * 16;
-      const int k = byte / RB;
-      return (uint32_t)(k * ld * ES) + ((byte % RB / 16) ^ swz(k)) * 16;
-    }
-  }
-  // First contraction index, within the stage, of the piece lane l copies of a
-  // row operand (a wave's units have the same parity, so the same pieces).
-  static __device__ __forceinline__ int first_k(int wave, int lane) {
-    return ((lane & 3) ^ ((2 * wave + (lane >> 5)) & 3)) * (16 / ES);
-  }
-  // One lane's fragment of the 32 rows (columns of D) from `base`, step s, of
-  // the stage at `lds` + `at`.  Each address is the LDS object and one offset: the
-  // compiler loses track of the object over longer chains, and then lets a read
-  // wait for all copies in flight (dx and dW with 128x128 tiles took up to twice
-  // as long).
-  static __device__ __forceinline__ u32x4 fragment(const uint8_t *lds, uint32_t at, int base, int s,
-                                                   int lane) {
-    if constexpr (!COL) {
-      const int r = base + (lane & 31);
-      const uint32_t o = at + r * 64 + ((2 * s + (lane >> 5)) ^ ((r >> 3) & 3)) * 16;
-      return *(const u32x4 *)(lds + o);
-    } else if constexpr (ES == 2) {
-      const int col = base + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-      const int k0 = 16 * s + 8 * (lane >> 5) + ((lane & 15) >> 2);
-      s16x4 v[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int k = k0 + 4 * i;
-        const uint32_t o = at + k * RB + ((col >> 3) ^ swz(k)) * 16 + (col & 7) * 2;
-        v[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4 *)(lds + o));
-      }
-      const u32x2 a = __builtin_bit_cast(u32x2, v[0]), b = __builtin_bit_cast(u32x2, v[1]);
-      return u32x4{a[0], a[1], b[0], b[1]};
-    } else {
-      const int col = base + (lane & 31);
-      u32x4 v;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t o = at + (8 * s + 4 * (lane >> 5) + j) * RB + col * 4;
-        v[j] = *(const uint32_t *)(lds + o);
-      }
-      return v;
-    }
-  }
-};
-
-// acc (32 x 32, transposed: lane l holds D's row l % 32, columns 8 (e / 4) +
-// 4 (l / 32) + e % 4) += a b.
-template <typename T>
-__device__ __forceinline__ void mma(f32x16 &acc, const u32x4 &a, const u32x4 &b) {
-  if constexpr (sizeof(T) == 2) {
-    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, b),
-                                                  __builtin_bit_cast(bf16x8, a), acc, 0, 0, 0);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(b[i]), __uint_as_float(a[i]), acc,
-                                                 0, 0, 0);
-  }
-}
-
-// Work item of this workgroup: workgroups are dealt round-robin to the 8 XCDs,
-// each XCD takes a contiguous run of items; within a part, tiles run down
-// groups of 8 row tiles before the next column tile, so the tiles an XCD works
-// on at a time form a block that shares operand rows in its L2.
-__device__ __forceinline__ bool gemm_item(const GemmOp &g, int64_t *mt, int *nt, int *part) {
-  const int64_t tiles = g.m_tiles * g.n_tiles, items = tiles * g.parts;
-  const int64_t per = (items + 7) / 8;
-  const int64_t item = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  if ((blockIdx.x >> 3) >= per || item >= items) return false;
-  *part = (int)(item / tiles);
-  const int64_t t = item - *part * tiles;
-  const int64_t group = t / (8 * g.n_tiles), first = group * 8;
-  const int64_t high = g.m_tiles - first < 8 ? g.m_tiles - first : 8;
-  const int64_t r = t - first * g.n_tiles;
-  *nt = (int)(r / high);
-  *mt = first + (r - *nt * high);
-  return true;
-}
-
-// Where an operand's next stage starts: address, bytes from there to the end of
-// the matrix (a copy past it reads zeros), bytes to the stage after.
-struct Cursor {
-  const uint8_t *p;
-  int64_t left, step;
-};
-template <typename T, bool COL>
-__device__ __forceinline__ Cursor cursor(const Matrix &m, int64_t tile0, int64_t k0) {
-  constexpr int ES = sizeof(T), KB = 64 / ES;
-  const int64_t at = (COL ? k0 * m.ld + tile0 : tile0 * m.ld + k0) * ES;
-  return Cursor{(const uint8_t *)m.p + at, ((m.rows - 1) * m.ld + m.cols) * ES - at,
-                COL ? KB * m.ld * ES : 64};
-}
-__device__ __forceinline__ rsrc_t cursor_rsrc(const Cursor &c) {
-  const int hi = (int)(c.left >> 32);
-  const uint32_t lo = (uint32_t)c.left;
-  const uint32_t n = hi < 0 ? 0 : (hi > 0 || lo > kOut) ? kOut : lo;
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(c.p), 0, n, 0x00027000);
-}
-
-// The order a step's instructions are issued in: one LDS read (of DS) after
-// each of the first MFMAs (of N), the copies (of VM) spread over all of them.
-// The scheduler otherwise sinks the reads to their use in the next step and
-// gathers the copies at the end.
-template <int I, int N, int DS, int VM>
-__device__ __forceinline__ void interleave() {
-  if constexpr (I < N) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);           // MFMA
-    constexpr int F = N * 3 / 4 > 0 ? N * 3 / 4 : 1;             // reads end three quarters through
-    constexpr int d1 = DS * (I + 1) / F < DS ? DS * (I + 1) / F : DS;
-    constexpr int d0 = DS * I / F < DS ? DS * I / F : DS;
-    if constexpr (d1 > d0) __builtin_amdgcn_sched_group_barrier(0x100, d1 - d0, 0);
-    constexpr int v = VM * (I + 1) / N - VM * I / N;
-    if constexpr (v > 0) __builtin_amdgcn_sched_group_barrier(0x010, v, 0);
-    interleave<I + 1, N, DS, VM>();
-  }
-}
-
-template <typename T, int MI, int NI, bool AC, bool BC, bool DUAL>
-__device__ __forceinline__ void gemm_tile(const GemmOp &g) {
-  constexpr int ES = sizeof(T), KB = 64 / ES, NS = 4;
-  constexpr int TM = 64 * MI, TN = 64 * NI;
-  constexpr int UA = TM / 16, UB = TN / 16;    // 1 KB copy units per stage
-  constexpr int VA = UA / 4, VB = UB / 4, VM = VA + VB;          // per wave
-  constexpr int SLOT = (TM + TN) * 64;
-  constexpr bool SEGS = !AC && BC;             // two contraction segments occur (dx of swiglu)
-  static_assert(!DUAL || (!AC && !BC), "the two-matrix product is the forward one");
-  static_assert(UA % 4 == 0 && UB % 4 == 0, "units split evenly");
-  using OA = Operand<T, AC, TM>;
-  using OB = Operand<T, BC, TN>;
-  // one LDS object per slot, so that a read of one does not wait for copies
-  // into another
-  __shared__ __attribute__((aligned(1024))) uint8_t L0[SLOT];
-  __shared__ __attribute__((aligned(1024))) uint8_t L1[SLOT];
-  __shared__ __attribute__((aligned(1024))) uint8_t L2[SLOT];
-  __shared__ __attribute__((aligned(1024))) uint8_t L3[SLOT];
-  uint8_t *const ring[4] = {L0, L1, L2, L3};
-  int64_t mt;
-  int nt, part;
-  if (!gemm_item(g, &mt, &nt, &part)) return;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave >> 1, wn = wave & 1;
-  constexpr int TO = DUAL ? TN / 2 : TN;       // output columns of a tile
-  int half = 0;
-  if constexpr (AC) {                          // dW
-    const int64_t per = g.m_tiles / g.halves;
-    half = mt >= per ? 1 : 0;
-    mt -= half * per;
-  }
-  const int64_t m0 = mt * TM, n0 = (int64_t)nt * TO;
-
-  const int st_seg0 = (int)((g.kdim[0] + KB - 1) / KB);
-  const int st_all = SEGS && g.segments > 1 ? st_seg0 + (int)((g.kdim[1] + KB - 1) / KB) : st_seg0;
-  const int st_first = (int)((int64_t)st_all * part / g.parts);
-  const int nst = (int)((int64_t)st_all * (part + 1) / g.parts) - st_first;
-
-  // sources of the next stage to copy; `rest` counts contraction elements left
-  // of its segment for the row operands' ragged ends
-  const bool second = SEGS && st_first >= st_seg0;
-  const int64_t k_first = (int64_t)(second ? st_first - st_seg0 : st_first) * KB;
-  Cursor ca = cursor<T, AC>(second ? g.a[1] : half ? g.a_up : g.a[0], m0, k_first);
-  Cursor cb = cursor<T, BC>(second ? g.b[1] : g.b[0], n0, k_first);
-  Cursor cu = DUAL ? cursor<T, BC>(g.b_up, n0, k_first) : cb;
-  const Cursor ca1 = SEGS ? cursor<T, AC>(g.a[1], m0, 0) : ca;
-  const Cursor cb1 = SEGS ? cursor<T, BC>(g.b[1], n0, 0) : cb;
-  int to_switch = SEGS && g.segments > 1 && !second ? st_seg0 - st_first : -1;
-  int rest = (int)((second ? g.kdim[1] : g.kdim[0]) - k_first), rest_b = rest;
-  int to_switch_b = to_switch;
-  const int rest1 = (int)g.kdim[1];
-  int to_end = nst, to_end_b = nst;            // stages left to copy
-
-  uint32_t off_a[VA], off_b[VB];
-#pragma unroll
-  for (int q = 0; q < VA; ++q) off_a[q] = OA::source(wave + 4 * q, lane, g.a[0].ld);
-#pragma unroll
-  for (int q = 0; q < VB; ++q) {
-    int u = wave + 4 * q;
-    if (DUAL && u >= UB / 2) u -= UB / 2;
-    off_b[q] = OB::source(u, lane, g.b[0].ld);
-  }
-  const int ka = OA::first_k(wave, lane);
-  auto copy_a = [&](int slot) {
-    rsrc_t r = cursor_rsrc(ca);
-    const uint32_t tail = (!AC && ka >= rest) || to_end <= 0 ? kOut : 0u;
-#pragma unroll
-    for (int q = 0; q < VA; ++q)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (MOE_LDS void *)(ring[slot] + (wave + 4 * q) * 1024),
-                                               16, off_a[q] | tail, 0, 0, 0);
-    ca.p += ca.step; ca.left -= ca.step; rest -= KB; --to_end;
-    if constexpr (SEGS) {
-      const bool sw = --to_switch == 0;
-      ca.p = sw ? ca1.p : ca.p; ca.left = sw ? ca1.left : ca.left; rest = sw ? rest1 : rest;
-    }
-  };
-  auto copy_b = [&](int slot) {
-    const uint32_t tail = (!BC && ka >= rest_b) || to_end_b <= 0 ? kOut : 0u;
-#pragma unroll
-    for (int q = 0; q < VB; ++q) {
-      const int u = wave + 4 * q;
-      // units of the second half hold W_up's rows
-      const bool up = DUAL && (UB >= 8 ? q >= VB / 2 : u >= UB / 2);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(cursor_rsrc(up ? cu : cb), (MOE_LDS void *)(ring[slot] + (UA + u) * 1024), 16,
-                                               off_b[q] | tail, 0, 0, 0);
-    }
-    cb.p += cb.step; cb.left -= cb.step; rest_b -= KB; --to_end_b;
-    if constexpr (DUAL) { cu.p += cb.step; cu.left -= cb.step; }
-    if constexpr (SEGS) {
-      const bool sw = --to_switch_b == 0;
-      cb.p = sw ? cb1.p : cb.p; cb.left = sw ? cb1.left : cb.left; rest_b = sw ? rest1 : rest_b;
-    }
-  };
-
-  f32x16 acc[MI][NI];
-#pragma unroll
-  for (int i = 0; i < MI; ++i)
-#pragma unroll
-    for (int j = 0; j < NI; ++j)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
-
-  // 32-column block j of the wave; swiglu: the first half of a wave's blocks are
-  // gate columns, the rest the up columns that go with them
-  auto col_block = [&](int j) {
-    return DUAL ? (j < NI / 2 ? wn * (NI / 2) + j : NI + wn * (NI / 2) + j - NI / 2) : wn * NI + j;
-  };
-  u32x4 fa[2][MI], fb[2][NI];
-  auto read = [&](int buf, int slot, int s) {
-#pragma unroll
-    for (int j = 0; j < NI; ++j) fb[buf][j] = OB::fragment(ring[slot], UA * 1024, col_block(j) * 32, s, lane);
-#pragma unroll
-    for (int i = 0; i < MI; ++i) fa[buf][i] = OA::fragment(ring[slot], 0, (wm * MI + i) * 32, s, lane);
-  };
-  auto multiply = [&](int buf) {
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
-#pragma unroll
-      for (int j = 0; j < NI; ++j) mma<T>(acc[i][j], fa[buf][i], fb[buf][j]);
-  };
-  // instructions of a step
-  constexpr int kMma = MI * NI * (ES == 2 ? 1 : 4);
-  constexpr int kReadsA = MI * (!AC ? 1 : ES == 2 ? 2 : 4);
-  constexpr int kReadsB = NI * (!BC ? 1 : ES == 2 ? 2 : 4);
-
-#pragma unroll
-  for (int p = 0; p < NS - 1; ++p) { copy_a(p); copy_b(p); }
-  __builtin_amdgcn_s_waitcnt(MOE_VMCNT(2 * VM));
-  __builtin_amdgcn_s_barrier();
-  read(0, 0, 0);
-  // Stage st from slot p.  The second step's fragments are read while the first
-  // step multiplies; then, with every read of this slot done and the next stage
-  // landed (younger: one stage and the A half of another), one barrier, and the
-  // next stage's first fragments are read while the second step multiplies.
-  // The slot the previous stage used (free since the previous barrier) is
-  // refilled meanwhile, A in the first step, B in the second.  Stages past the
-  // end copy nothing.
-  auto stage = [&](int p) {
-    __builtin_amdgcn_sched_barrier(0);
-    read(1, p, 1);
-    copy_a((p + NS - 1) % NS);
-    multiply(0);
-    interleave<0, kMma, kReadsA + kReadsB, VA>();
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(MOE_VMCNT(VM + VA) & ~(15 << 8));   // and lgkmcnt(0)
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    read(0, (p + 1) % NS, 0);
-    copy_b((p + NS - 1) % NS);
-    multiply(1);
-    interleave<0, kMma, kReadsA + kReadsB, VB>();
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  int st = 0;
-  for (; st + NS <= nst; st += NS) {
-#pragma unroll
-    for (int p = 0; p < NS; ++p) stage(p);
-  }
-#pragma unroll
-  for (int p = 0; p < NS - 1; ++p)
-    if (st + p < nst) stage(p);
-  // Epilogue.  32 rows of the wave's quarter at a time go through the wave's own
-  // part of LDS (no barrier), so that a lane then has eight consecutive columns
-  // of a row and 16 or 8 lanes a whole line.  bf16: the whole tile's residual is
-  // asked for at once, into the registers that the operands have left (in 32-row
-  // pieces a read's latency bounded it: 10 % longer at 4096x2048->7168).
-  constexpr int NJ = DUAL ? NI / 2 : NI;       // output column blocks of the wave
-  constexpr int PC = NJ * 4;                   // pieces of 8 columns per row
-  constexpr int PPI = 32 * PC / 64;            // pieces per lane and 32 rows
-  constexpr int LD = NI * 32 + 4;              // floats per LDS row (padded)
-  constexpr bool RES = !AC && !BC;             // gradients have no residual
-  constexpr int AHEAD = RES && ES == 2 ? MI : 1;
-  static_assert(32 * LD * 4 <= SLOT, "a wave's rows fit a ring slot");
-  float *stage_f = (float *)(wave == 0 ? L0 : wave == 1 ? L1 : wave == 2 ? L2 : L3);
-  const bool plain = g.parts > 1;
-  // piece q of the wave's rows 32 i ..: row and piece in the block, place in the output
-  struct Place {
-    int r, pc;
-    int64_t m;
-    int n;
-  };
-  auto place = [&](int i, int q) {
-    const int idx = q * 64 + lane;
-    const int r = idx / PC, pc = idx - r * PC;
-    return Place{r, pc, m0 + (wm * MI + i) * 32 + r, (int)n0 + wn * NJ * 32 + pc * 8};
-  };
-  Raw8<T> res[PPI], ahead[AHEAD][PPI];
-  auto fetch = [&](int i, Raw8<T> (&to)[PPI]) {
-#pragma unroll
-    for (int q = 0; q < PPI; ++q) {
-      const Place o = place(i, q);
-      if (o.m < g.M && o.n < g.e.N)
-        fetch8<T>(to[q], (const T *)g.e.residual + o.m * g.e.ld_res + o.n, g.e.N - o.n,
-                  g.e.vec != 0);
-    }
-  };
-  const bool has_res = RES && g.e.residual && !plain;
-  Biases<T, DUAL> bias;                        // a lane's columns are the same in every piece
-  static_assert(64 % PC == 0, "they are");
-  __builtin_amdgcn_s_waitcnt(0);
-  if (RES && !plain) bias.fetch(g.e, place(0, 0).n);
-  if (AHEAD > 1 && has_res) {
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i) fetch(i, ahead[i]);
-  }
-  __builtin_amdgcn_sched_barrier(0);
-  __builtin_amdgcn_s_barrier();                // every wave is done with the ring
-  __builtin_amdgcn_sched_barrier(0);
-  for (int ci = 0; ci < MI; ++ci) {
-    if (AHEAD == 1 && has_res) fetch(ci, res);
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
-      if (i == ci) {                           // uniform; the accumulators keep their registers
-#pragma unroll
-        for (int j = 0; j < NI; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            *(f32x4 *)(stage_f + (lane & 31) * LD + j * 32 + 8 * e + 4 * (lane >> 5)) =
-                f32x4{acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2],
-                      acc[i][j][4 * e + 3]};
-        if constexpr (AHEAD > 1)
-#pragma unroll
-          for (int q = 0; q < PPI; ++q) res[q] = ahead[i][q];
-      }
-    __builtin_amdgcn_wave_barrier();
-#pragma unroll
-    for (int q = 0; q < PPI; ++q) {
-      const Place o = place(ci, q);
-      float v[8], u[8], rs[8];
-      load8<float>(v, stage_f + o.r * LD + o.pc * 8, 8, true);
-      if constexpr (DUAL) load8<float>(u, stage_f + o.r * LD + NJ * 32 + o.pc * 8, 8, true);
-      if (o.m >= g.M || o.n >= g.e.N) continue;
-      if (plain) {
-        // rows of ldp, a multiple of 8: whole pieces
-        float *to =
-            g.part + (((int64_t)part * (DUAL ? 2 : g.halves) + half) * g.M + o.m) * g.ldp + o.n;
-        store8<float>(to, v, 8, true);
-        if constexpr (DUAL) store8<float>(to + g.M * g.ldp, u, 8, true);
-      } else if constexpr (!RES) {             // a gradient: no epilogue
-        store8<T>((T *)(half ? g.y_up : g.e.y) + o.m * g.e.ld_y + o.n, v, g.e.N - o.n,
-                  g.e.vec != 0);
-      } else {
-        if (has_res) widen8<T>(rs, res[q]);
-        finish8<T, DUAL>(g.e, v, u, bias, rs, o.m, o.n);
-      }
-    }
-    __builtin_amdgcn_wave_barrier();
-  }
-}
-
 template <typename T, int MI, int NI, bool AC, bool BC, bool DUAL>
 __global__ __launch_bounds__(256, MI *NI >= 8 ? 1 : 2) void gemm_kernel(const GemmOp g) {
-  gemm_tile<T, MI, NI, AC, BC, DUAL>(g);
+  int64_t mt;
+  int nt, part;
+  if (gemm_item(g, &mt, &nt, &part))
+    gemm_tile<T, MI, NI, AC, BC, DUAL>(g, mt, nt, part, LinearOut{});
 }
 
 // Sum of the parts of a split product, in order, and the epilogue.
