@@ -42,9 +42,7 @@ __global__ __launch_bounds__(256) void save_kernel(const CheckpointArgs a, uint3
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = j < p.left ? (float)src[j] : 0.f;
   }
-  float m = 0.f;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) m = fmaxf(m, keep_magnitude(v[j]));
+  float m = keep_top(v);
   m = fmaxf(m, xor_lane<1>(m));
   m = fmaxf(m, xor_lane<2>(m));
   const int X = keep_exponent(m);

@@ -13,12 +13,19 @@
 //   dWd     A = dy by columns, B = h by columns     contraction over the expert's rows
 //   dWg, dWu  A = dz, du by columns, B = x by columns, one launch
 //
-// Where an expert's rows begin is known on the device alone: every workgroup of a
-// product over rows counts the row tiles of the experts before its own (a scan over
-// the offsets by one wave), so nothing waits for a list; the launch has room for
-// the most row tiles that `rows` rows of E experts can make, and surplus workgroups
-// leave.  Offsets are clamped to [0, rows] and to ascending ones, so whatever they
-// hold no access is out of range.
+// Where an expert's rows begin is known on the device alone: every workgroup scans
+// the offsets once (one wave's prefix sum over the experts' 64-row blocks) and takes
+// an equal share of the blocks, so nothing waits for a list.  Offsets are clamped to
+// [0, rows] and to ascending ones, so whatever they hold no access is out of range.
+//
+// Workgroups are as many as the GPU holds at once and walk their tiles one after
+// another: starting a workgroup for every tile left 2.6 us between one's end and the
+// next one's first instruction, and 2 us of scan, in 15 us a tile of the weight
+// gradients.
+
+#include <stdlib.h>
+
+#include <type_traits>
 
 #include "keep.h"
 #include "tile.h"
@@ -32,9 +39,7 @@ struct GroupedOp {
   const int32_t *offsets;
   int64_t rows;
   int E;
-  int row_tiles;               // products over rows: their most
   int64_t b_expert;            // bytes from one expert's B (weights) to the next's
-  int64_t out_expert;          // dW: bytes from one expert's gradient to the next's
 };
 
 // Rows of an expert.
@@ -49,57 +54,70 @@ __device__ __forceinline__ Span span_of(const GroupedOp &q, int e) {
   return Span{lo, hi - lo};
 }
 
+// One tile: rows m0 .. of the expert's, its height in blocks of 64 rows, the column
+// tile.
 struct GroupedItem {
   int e, lo, n;                // expert, its first row and rows
-  int mt, nt;
+  int m0, blocks;
+  int nt;
 };
 
-// Work item of this workgroup in a product over rows, tiles of TM rows.  Items go
-// expert by expert, an expert's column tiles one after another with its row tiles
-// inside, and each XCD takes a contiguous run of them: the rows of an expert and the
-// weights of a column tile are then read through one L2.
-template <int TM>
-__device__ __forceinline__ bool grouped_item(const GroupedOp &q, GroupedItem *out) {
-  const int lane = threadIdx.x & 63;
-  const int chunk = (q.E + 63) / 64;           // consecutive experts a lane
-  int mine = 0;
-  for (int i = 0; i < chunk; ++i) {
-    const int e = lane * chunk + i;
-    if (e < q.E) mine += (span_of(q, e).n + TM - 1) / TM;
-  }
-  int upto = mine;
+// Tiles of up to HIGH blocks of 64 rows that cover n rows, of as equal heights as
+// blocks allow, so that none is nearly empty.
+template <int HIGH>
+__device__ __forceinline__ int tiles_of(int n) { return ((n + 63) / 64 + HIGH - 1) / HIGH; }
+__device__ __forceinline__ void height_of(int blocks, int tiles, int i, GroupedItem *out) {
+  const int first = blocks * i / tiles;
+  out->m0 = first * 64;
+  out->blocks = blocks * (i + 1) / tiles - first;
+}
+
+// What the experts before each lane's own amount to (a lane has E / 64 of them, one
+// after another), and the expert that a position falls to.
+template <class N, class F>
+struct Line {
+  const F size;                // of an expert
+  const int E, chunk;
+  N mine, upto;                // of this lane's experts, and with those before them
+  __device__ __forceinline__ Line(int experts, F f) : size(f), E(experts), chunk((experts + 63) / 64) {
+    const int lane = threadIdx.x & 63;
+    mine = 0;
+    for (int i = 0; i < chunk; ++i)
+      if (lane * chunk + i < E) mine += size(lane * chunk + i);
+    upto = mine;
 #pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int o = __shfl_up(upto, off);
-    if (lane >= off) upto += o;
-  }
-  const int nt = q.g.n_tiles;
-  const int items = __builtin_amdgcn_readlane(upto, 63) * nt;
-  const int per = (items + 7) / 8;
-  const int slot = (int)(blockIdx.x >> 3), item = (int)(blockIdx.x & 7) * per + slot;
-  if (slot >= per || item >= items) return false;
-  const int src = __ffsll((unsigned long long)__ballot(upto * nt > item)) - 1;
-  // the lane that holds the item's expert walks its own
-  int start = (upto - mine) * nt, e = 0, lo = 0, n = 0, first = 0;
-  if (lane == src) {
-    for (int i = 0; i < chunk; ++i) {
-      const int c = lane * chunk + i;
-      if (c >= q.E) break;
-      const Span s = span_of(q, c);
-      const int tiles = (s.n + TM - 1) / TM * nt;
-      if (item >= start && item < start + tiles) { e = c; lo = s.lo; n = s.n; first = start; }
-      start += tiles;
+    for (int off = 1; off < 64; off <<= 1) {
+      const N o = __shfl_up(upto, off);
+      if (lane >= off) upto += o;
     }
   }
-  out->e = __builtin_amdgcn_readlane(e, src);
-  out->lo = __builtin_amdgcn_readlane(lo, src);
-  out->n = __builtin_amdgcn_readlane(n, src);
-  const int local = item - __builtin_amdgcn_readlane(first, src);
-  const int high = (out->n + TM - 1) / TM;
-  out->nt = local / high;
-  out->mt = local - out->nt * high;
-  return true;
-}
+  static __device__ __forceinline__ N of_lane(N v, int lane) {
+    if constexpr (sizeof(N) == 4) {
+      return __builtin_amdgcn_readlane(v, lane);
+    } else {
+      const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
+      return (N)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 | lo);
+    }
+  }
+  __device__ __forceinline__ N total() const { return of_lane(upto, 63); }
+  // The expert at `pos` < total(), and where it starts.
+  __device__ __forceinline__ int at(N pos, N *start) const {
+    const int lane = threadIdx.x & 63;
+    const int src = __ffsll((unsigned long long)__ballot(upto > pos)) - 1;
+    N from = upto - mine;
+    int e = lane * chunk;
+    if (chunk > 1 && lane == src)
+      for (; e < E - 1; ++e) {
+        const N n = size(e);
+        if (pos < from + n) break;
+        from += n;
+      }
+    *start = of_lane(from, src);
+    return __builtin_amdgcn_readlane(e, src);
+  }
+};
+template <class N, class F>
+__device__ __forceinline__ Line<N, F> line_of(int experts, F f) { return Line<N, F>(experts, f); }
 
 template <typename T>
 __device__ __forceinline__ void move(Matrix &m, const GroupedItem &it) {
@@ -108,149 +126,375 @@ __device__ __forceinline__ void move(Matrix &m, const GroupedItem &it) {
 }
 
 // ---------------------------------------------------------------------------
-// Endings: rows m of the expert's, eight columns n .. .
+// Endings.  Stores (and loads) are buffer ones without a branch, past the tile's rows
+// or the matrix's columns at an offset that drops them (reads zeros), so that a load's
+// wait does not have to be one for all stores before it.
 
-// Rows of sums, rounded: y and dx.
-template <typename T>
-struct RowsOut {
-  static constexpr bool plain = false;
-  struct Ahead {};
-  T *y;                        // row 0 of the expert
-  int N;
-  __device__ __forceinline__ void fetch(Ahead &, int64_t, int) const {}
-  __device__ __forceinline__ void put(const Ahead &, int64_t m, int n, float (&v)[8], float (&)[8],
-                                      int) const {
-    store8<T>(y + m * N + n, v, N - n, true);
-  }
-};
+// Rows that a tile reads or writes, from its first.
+__device__ __forceinline__ rsrc_t rows_rsrc(const void *p, int64_t first, int rows, int64_t row_bytes) {
+  const uint8_t *at = (const uint8_t *)p + first * row_bytes;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(at), 0, (uint32_t)(rows * row_bytes),
+                                           0x00027000);
+}
 
-// An expert's weight gradient (both of gate and up in one launch).
-template <typename T>
-struct WeightOut {
-  static constexpr bool plain = false;
-  struct Ahead {};
-  T *dw, *dw_up;
-  int N;
-  __device__ __forceinline__ void fetch(Ahead &, int64_t, int) const {}
-  __device__ __forceinline__ void put(const Ahead &, int64_t m, int n, float (&v)[8], float (&)[8],
-                                      int half) const {
-    store8<T>((half ? dw_up : dw) + m * N + n, v, N - n, true);
-  }
-};
-
-// Eight values of z or u in 8 bits: the four neighbouring lanes hold a block (a
-// tile's columns start at multiples of 32, and so does its last block's end).
-__device__ __forceinline__ void keep_piece(const float (&v)[8], float limit, uint8_t *codes,
-                                           uint8_t *scales, int64_t row, int n, int N) {
-  float m = 0.f;
+// Columns 16 (l / 32) .. of row l % 32 of a 32 x 32 block of sums: what mma() leaves a
+// lane, four columns in eight, against its partner's at distance 32.
+__device__ __forceinline__ void columns16(float (&v)[16], const f32x16 &a) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) m = fmaxf(m, keep_magnitude(v[j]));
+  for (int e = 0; e < 8; ++e) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a[e]), __float_as_uint(a[e + 8]),
+                                                    false, false);
+    v[e < 4 ? e : e + 4] = __uint_as_float(r[0]);
+    v[e < 4 ? e + 4 : e + 8] = __uint_as_float(r[1]);
+  }
+}
+
+// 16 columns of type T at byte `off`, of which `left` are in the matrix (whole pieces
+// of 16 bytes).
+template <typename T>
+__device__ __forceinline__ void store16(rsrc_t r, uint32_t off, const float (&v)[16], int left) {
+  constexpr int P = 16 / sizeof(T);
+#pragma unroll
+  for (int p = 0; p < 16 / P; ++p) {
+    u32x4 w;
+    if constexpr (sizeof(T) == 2) {
+      bf16x8 b;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) b[j] = (bf16)v[8 * p + j];
+      w = __builtin_bit_cast(u32x4, b);
+    } else {
+      w = u32x4{__float_as_uint(v[4 * p]), __float_as_uint(v[4 * p + 1]), __float_as_uint(v[4 * p + 2]),
+                __float_as_uint(v[4 * p + 3])};
+    }
+    __builtin_amdgcn_raw_buffer_store_b128(w, r, p * P < left ? off + 16 * p : kOut, 0, 0);
+  }
+}
+// Eight columns, likewise.
+template <typename T>
+__device__ __forceinline__ void store_piece(rsrc_t r, uint32_t off, const float (&v)[8], int left) {
+  if constexpr (sizeof(T) == 2) {
+    bf16x8 b;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) b[j] = (bf16)v[j];
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, b), r, left > 0 ? off : kOut, 0, 0);
+  } else {
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+      __builtin_amdgcn_raw_buffer_store_b128(
+          u32x4{__float_as_uint(v[4 * p]), __float_as_uint(v[4 * p + 1]), __float_as_uint(v[4 * p + 2]),
+                __float_as_uint(v[4 * p + 3])},
+          r, left > 4 * p ? off + 16 * p : kOut, 0, 0);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void fetch_piece(Raw8<T> &a, rsrc_t r, uint32_t off, int left) {
+#pragma unroll
+  for (int p = 0; p < (int)sizeof(T) / 2; ++p) {
+    const u32x4 w = __builtin_amdgcn_raw_buffer_load_b128(
+        r, left > p * (16 / (int)sizeof(T)) ? off + 16 * p : kOut, 0, 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) a.w[4 * p + j] = w[j];
+  }
+}
+
+// Rows of sums, rounded: y and dx; the weight gradients.  Straight from the
+// accumulators, 16 columns of a row a lane: a quarter fewer instructions than through
+// LDS, though a store's 64 lanes then lie on 32 rows.
+template <typename T>
+struct SumsOut {
+  static constexpr bool direct = true;
+  struct Tile {
+    rsrc_t y;
+  };
+  T *y, *y_up;                 // y_up: of the second matrix
+  int N;
+  __device__ __forceinline__ Tile begin(int64_t first, int rows, int half) const {
+    return Tile{rows_rsrc(half ? y_up : y, first, rows, (int64_t)N * sizeof(T))};
+  }
+  __device__ __forceinline__ void put(const Tile &t, int m, int n, const float (&v)[16]) const {
+    store16<T>(t.y, ((uint32_t)m * N + n) * sizeof(T), v, N - n);
+  }
+};
+
+// Eight values of z or u in 8 bits: the four neighbouring lanes hold a block.
+__device__ __forceinline__ void keep_piece(const float (&v)[8], float limit, rsrc_t codes, rsrc_t scales,
+                                           uint32_t at, uint32_t block, bool on, bool first) {
+  float m = keep_top_of_sums(v);
   m = fmaxf(m, xor_lane<1>(m));
   m = fmaxf(m, xor_lane<2>(m));
   const int X = keep_exponent(m);
   uint32_t c[2];
   keep8(v, X, limit, c);
-  *(u32x2 *)(codes + row * N + n) = u32x2{c[0], c[1]};
-  if (n % 32 == 0) scales[row * (N / 32) + n / 32] = (uint8_t)(X + 127);
+  __builtin_amdgcn_raw_buffer_store_b64(u32x2{c[0], c[1]}, codes, on ? at : kOut, 0, 0);
+  __builtin_amdgcn_raw_buffer_store_b8((uint8_t)(X + 127), scales, on && first ? block : kOut, 0, 0);
+}
+
+// Saved z and u of a tile's rows.
+template <typename T>
+struct SavedTile {
+  rsrc_t z, u, zs, us;
+  __device__ __forceinline__ SavedTile(const moe_experts_saved &s, int64_t first, int rows, int N) {
+    const int64_t bytes = s.kind == MOE_SAVE_NONE ? 0 : s.kind == MOE_SAVE_MXFP8 ? N : N * (int64_t)sizeof(T);
+    const int64_t scales = s.kind == MOE_SAVE_MXFP8 ? N / 32 : 0;
+    z = rows_rsrc(s.gate, first, rows, bytes);
+    u = rows_rsrc(s.up, first, rows, bytes);
+    zs = rows_rsrc(s.gate_scales, first, rows, scales);
+    us = rows_rsrc(s.up_scales, first, rows, scales);
+  }
+};
+
+// Clamped gate and up values and SiLU's factor; NaN passes.  `top` is infinite
+// without a clamp.
+struct Clamped {
+  float g, w, s;
+  bool off, off_up;
+};
+template <typename T>
+__device__ __forceinline__ Clamped clamped(float z, float u, float top) {
+  Clamped c;
+  c.off = z > top;
+  c.off_up = fabsf(u) > top;
+  c.g = c.off ? top : z;
+  c.w = c.off_up ? copysignf(top, u) : u;
+  c.s = sigmoid<T>(c.g);
+  return c;
 }
 
 // h, and z and u as they are saved.
-template <typename T>
+template <typename T, int KIND>
 struct UpOut {
-  static constexpr bool plain = false;
+  static constexpr bool direct = false;
   struct Ahead {};
-  T *h;                        // row 0 of all
+  struct Tile {
+    rsrc_t h;
+    SavedTile<T> s;
+  };
+  T *h;
   moe_experts_saved s;
-  int64_t lo;
   int N;
   float limit;
-  __device__ __forceinline__ void fetch(Ahead &, int64_t, int) const {}
-  __device__ __forceinline__ void put(const Ahead &, int64_t m, int n, float (&v)[8], float (&u)[8],
-                                      int) const {
-    const int64_t row = lo + m;
-    if (s.kind == MOE_SAVE_MXFP8) {
-      keep_piece(v, limit, (uint8_t *)s.gate, s.gate_scales, row, n, N);
-      keep_piece(u, limit, (uint8_t *)s.up, s.up_scales, row, n, N);
-    } else if (s.kind == MOE_SAVE_FULL) {
+  __device__ __forceinline__ Tile begin(int64_t first, int rows, int) const {
+    return Tile{rows_rsrc(h, first, rows, (int64_t)N * sizeof(T)), SavedTile<T>(s, first, rows, N)};
+  }
+  __device__ __forceinline__ void fetch(const Tile &, Ahead &, int, int) const {}
+  __device__ __forceinline__ void put(const Tile &t, const Ahead &, int m, int n, float (&v)[8],
+                                      float (&u)[8]) const {
+    const uint32_t at = (uint32_t)m * N + n;
+    if constexpr (KIND == MOE_SAVE_MXFP8) {
+      const uint32_t block = (uint32_t)m * (N / 32) + n / 32;
+      keep_piece(v, limit, t.s.z, t.s.zs, at, block, n < N, n % 32 == 0);
+      keep_piece(u, limit, t.s.u, t.s.us, at, block, n < N, n % 32 == 0);
+    } else if constexpr (KIND == MOE_SAVE_FULL) {
       float k[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) k[j] = saved<T, false>(v[j], limit);
-      store8<T>((T *)s.gate + row * N + n, k, N - n, true);
+      store_piece<T>(t.s.z, at * sizeof(T), k, N - n);
 #pragma unroll
       for (int j = 0; j < 8; ++j) k[j] = saved<T, true>(u[j], limit);
-      store8<T>((T *)s.up + row * N + n, k, N - n, true);
+      store_piece<T>(t.s.u, at * sizeof(T), k, N - n);
     }
+    const float top = limit > 0.f ? limit : __builtin_inff();
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      float g = v[j], w = u[j];
-      if (limit > 0.f) {                       // NaN passes
-        g = g > limit ? limit : g;
-        w = w > limit ? limit : (w < -limit ? -limit : w);
-      }
-      v[j] = g * sigmoid<T>(g) * w;
+      const Clamped c = clamped<T>(v[j], u[j], top);
+      v[j] = c.g * c.s * c.w;
     }
-    store8<T>(h + row * N + n, v, N - n, true);
+    store_piece<T>(t.h, at * sizeof(T), v, N - n);
   }
 };
 
 // dz, du and h from dh and the saved z and u.
-template <typename T>
+template <typename T, int KIND>
 struct SlopeOut {
-  static constexpr bool plain = false;
+  static constexpr bool direct = false, MX = KIND == MOE_SAVE_MXFP8;
   struct Ahead {
-    Raw8<T> z, u;              // MXFP8: codes in the first two words, the scale after
+    Raw8<T> z, u;              // MXFP8: the codes in the first two words
+    uint32_t zs, us;           // and the scales
+  };
+  struct Tile {
+    rsrc_t dz, du, h;
+    SavedTile<T> s;
   };
   T *dz, *du, *h;
   moe_experts_saved s;
-  int64_t lo;
   int N;
   float limit;
-  __device__ __forceinline__ void fetch(Ahead &a, int64_t m, int n) const {
-    const int64_t row = lo + m;
-    if (s.kind == MOE_SAVE_MXFP8) {
-      const u32x2 z = *(const u32x2 *)((const uint8_t *)s.gate + row * N + n);
-      const u32x2 u = *(const u32x2 *)((const uint8_t *)s.up + row * N + n);
-      const int64_t at = row * (N / 32) + n / 32;
-      a.z.w[0] = z[0]; a.z.w[1] = z[1]; a.z.w[2] = s.gate_scales[at];
-      a.u.w[0] = u[0]; a.u.w[1] = u[1]; a.u.w[2] = s.up_scales[at];
+  __device__ __forceinline__ Tile begin(int64_t first, int rows, int) const {
+    const int64_t b = (int64_t)N * sizeof(T);
+    return Tile{rows_rsrc(dz, first, rows, b), rows_rsrc(du, first, rows, b), rows_rsrc(h, first, rows, b),
+                SavedTile<T>(s, first, rows, N)};
+  }
+  __device__ __forceinline__ void fetch(const Tile &t, Ahead &a, int m, int n) const {
+    const uint32_t at = (uint32_t)m * N + n;
+    if constexpr (MX) {
+      const uint32_t block = n < N ? (uint32_t)m * (N / 32) + n / 32 : kOut;
+      const u32x2 z = __builtin_amdgcn_raw_buffer_load_b64(t.s.z, n < N ? at : kOut, 0, 0);
+      const u32x2 u = __builtin_amdgcn_raw_buffer_load_b64(t.s.u, n < N ? at : kOut, 0, 0);
+      a.z.w[0] = z[0]; a.z.w[1] = z[1];
+      a.u.w[0] = u[0]; a.u.w[1] = u[1];
+      a.zs = __builtin_amdgcn_raw_buffer_load_b8(t.s.zs, block, 0, 0);
+      a.us = __builtin_amdgcn_raw_buffer_load_b8(t.s.us, block, 0, 0);
     } else {
-      fetch8<T>(a.z, (const T *)s.gate + row * N + n, N - n, true);
-      fetch8<T>(a.u, (const T *)s.up + row * N + n, N - n, true);
+      fetch_piece<T>(a.z, t.s.z, at * sizeof(T), N - n);
+      fetch_piece<T>(a.u, t.s.u, at * sizeof(T), N - n);
     }
   }
-  __device__ __forceinline__ void put(const Ahead &a, int64_t m, int n, float (&v)[8], float (&)[8],
-                                      int) const {
-    float z[8], u[8], gz[8], gu[8];
-    if (s.kind == MOE_SAVE_MXFP8) {
-      kept8(z, a.z.w[0], a.z.w[1], a.z.w[2]);
-      kept8(u, a.u.w[0], a.u.w[1], a.u.w[2]);
+  __device__ __forceinline__ void put(const Tile &t, const Ahead &a, int m, int n, float (&v)[8],
+                                      float (&)[8]) const {
+    float z[8], u[8];
+    if constexpr (MX) {
+      kept8(z, a.z.w[0], a.z.w[1], a.zs);
+      kept8(u, a.u.w[0], a.u.w[1], a.us);
     } else {
       widen8<T>(z, a.z);
       widen8<T>(u, a.u);
     }
+    const float top = limit > 0.f ? limit : __builtin_inff();
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      grad_of<T, true>(v[j], z[j], u[j], MOE_ACTIVATION_SWIGLU, limit, &gz[j], &gu[j]);
-      float g = z[j], w = u[j];
-      if (limit > 0.f) {
-        g = g > limit ? limit : g;
-        w = w > limit ? limit : (w < -limit ? -limit : w);
-      }
-      v[j] = g * sigmoid<T>(g) * w;
+      const Clamped c = clamped<T>(z[j], u[j], top);
+      const float q = v[j] * c.s;              // dh SiLU's factor
+      z[j] = c.off ? 0.f : q * c.w * (1.f + c.g * (1.f - c.s));
+      u[j] = c.off_up ? 0.f : q * c.g;
+      v[j] = c.g * c.s * c.w;
     }
-    const int64_t at = (lo + m) * N + n;
-    store8<T>(dz + at, gz, N - n, true);
-    store8<T>(du + at, gu, N - n, true);
-    store8<T>(h + at, v, N - n, true);
+    const uint32_t off = ((uint32_t)m * N + n) * sizeof(T);
+    store_piece<T>(t.dz, off, z, N - n);
+    store_piece<T>(t.du, off, u, N - n);
+    store_piece<T>(t.h, off, v, N - n);
   }
 };
 
 // ---------------------------------------------------------------------------
-// Products over rows.
-template <typename T, int MI, int NI, bool BC, bool DUAL, class OUT, class ARGS>
-__device__ __forceinline__ void rows_tile(const GroupedOp &q, OUT out, ARGS place) {
+// A launch's tiles: up to 64 HIGH rows, by the body of their height, 64 NI columns,
+// a ring of NS slots.
+template <int H, int N, int S>
+struct Shape {
+  static constexpr int HIGH = H, NI = N, NS = S;
+  static constexpr int PER_CU = 160 * 1024 / (S * kSlot<H, N>);  // workgroups by LDS
+};
+constexpr int kCus = 256;
+
+template <typename T, int MI, class SH, bool AC, bool BC, bool DUAL, class OUT>
+__device__ __forceinline__ void tile(const GemmOp &g, const GroupedItem &it, int64_t first, int half,
+                                     const OUT &out, uint8_t *L0, uint8_t *L1, uint8_t *L2, uint8_t *L3) {
+  constexpr int NI = SH::NI, NJ = DUAL ? NI / 2 : NI;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int n0 = it.nt * (64 * NJ);
+  f32x16 acc[MI][NI];
+  gemm_sums<T, MI, NI, AC, BC, DUAL, SH::NS>(g, it.m0, n0, 0, 0, L0, L1, L2, L3, acc);
+  // every wave is done with the ring, and the copies past the end have landed
+  __builtin_amdgcn_s_waitcnt(0);
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  const int left = (int)(g.M - it.m0), rows = left < 64 * MI ? left : 64 * MI;
+  const auto t = out.begin(first + it.m0, rows, half);
+  if constexpr (OUT::direct) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NI; ++j) {
+        float v[16];
+        f32x16 a = acc[i][j];
+        asm volatile("" : "+v"(a));            // a block's exchange after the one before's stores
+        columns16(v, a);
+        out.put(t, (wm * MI + i) * 32 + (lane & 31), n0 + (wn * NI + j) * 32 + 16 * (lane >> 5), v);
+      }
+  } else {
+    // 32 rows of the wave's quarter at a time through the wave's own part of LDS, then
+    // a piece of eight columns a lane.  The pieces' loop stays one: unrolled, the code
+    // of these endings would not stay in the instruction cache.  What the next piece
+    // reads is asked for before this one's stores.
+    constexpr int PC = NJ * 4;                 // pieces of a row
+    constexpr int PPI = 32 * PC / 64;          // pieces of a lane in 32 rows
+    constexpr int LD = NI * 32 + 4;            // floats of an LDS row (padded)
+    static_assert(32 * LD * 4 * (SH::NS > 3 ? 1 : 2) <= kSlot<SH::HIGH, NI>, "they fit");
+    float *stage = (float *)(wave == 0 ? L0 : wave == 1 ? L1 : wave == 2 ? L2
+                             : SH::NS > 3 ? L3 : L0 + 32 * LD * 4);
+    const int r0 = lane / PC, c0 = (lane % PC) * 8;      // PC divides 64
+    const int m0 = wm * MI * 32 + r0, n = n0 + wn * NJ * 32 + c0;
+    constexpr int STEP = 64 / PC;              // rows from a lane's piece to its next
+    typename OUT::Ahead next, now;
+    out.fetch(t, next, m0, n);
+#pragma unroll 1
+    for (int ci = 0; ci < MI; ++ci) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+        if (i == ci) {                         // uniform; the accumulators keep their registers
+#pragma unroll
+          for (int j = 0; j < NI; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              *(f32x4 *)(stage + (lane & 31) * LD + j * 32 + 8 * e + 4 * (lane >> 5)) =
+                  f32x4{acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2],
+                        acc[i][j][4 * e + 3]};
+        }
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+      for (int q = 0; q < PPI; ++q) {
+        const int m = m0 + ci * 32 + q * STEP;
+        now = next;
+        // the piece after: rows follow one another across the 32 of a pass
+        out.fetch(t, next, m + STEP, n);
+        float v[8], u[8];
+        const float *from = stage + (r0 + q * STEP) * LD + c0;
+        load8<float>(v, from, 8, true);
+        if constexpr (DUAL) load8<float>(u, from + NJ * 32, 8, true);
+        out.put(t, now, m, n, v, u);
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+    // the stage is part of the ring
+    __builtin_amdgcn_s_waitcnt(MOE_VMCNT(63) & ~(15 << 8));
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+template <typename T, class SH, bool AC, bool BC, bool DUAL, class OUT>
+__device__ __forceinline__ void tile_of_height(const GemmOp &g, const GroupedItem &it, int64_t first,
+                                               int half, const OUT &out, uint8_t *L0, uint8_t *L1,
+                                               uint8_t *L2, uint8_t *L3) {
+#define MOE_BODY(MI)                                                                             \
+  if constexpr (MI <= SH::HIGH) {                                                                \
+    if (it.blocks == MI)                                                                         \
+      tile<T, MI, SH, AC, BC, DUAL>(g, it, first, half, out, L0, L1, L2, L3);                    \
+  }
+  MOE_BODY(4)
+  MOE_BODY(3)
+  MOE_BODY(2)
+  MOE_BODY(1)
+#undef MOE_BODY
+}
+
+#define MOE_RING(SH)                                                                    \
+  constexpr int SLOT = kSlot<SH::HIGH, SH::NI>;                                         \
+  __shared__ __attribute__((aligned(1024))) uint8_t L0[SLOT];                           \
+  __shared__ __attribute__((aligned(1024))) uint8_t L1[SLOT];                           \
+  __shared__ __attribute__((aligned(1024))) uint8_t L2[SLOT];                           \
+  __shared__ __attribute__((aligned(1024))) uint8_t L3[SH::NS > 3 ? SLOT : 16];
+
+// Products over rows: a workgroup a tile.  Items go expert by expert, a column tile's
+// row tiles together, and each XCD takes a contiguous run of them: the rows of an
+// expert and the weights of a column tile are then read through one L2.
+template <typename T, class SH, bool BC, bool DUAL, class OUT>
+__device__ __forceinline__ void rows_product(const GroupedOp &q, const OUT &out) {
+  MOE_RING(SH)
+  const auto line = line_of<int>(q.E, [&](int e) { return tiles_of<SH::HIGH>(span_of(q, e).n); });
+  const int nt = q.g.n_tiles, items = line.total() * nt, per = (items + 7) / 8;
+  const int slot = (int)(blockIdx.x >> 3), item = (int)(blockIdx.x & 7) * per + slot;
+  if (slot >= per || item >= items) return;
   GroupedItem it;
-  if (!grouped_item<64 * MI>(q, &it)) return;
+  int start;
+  it.e = line.at(item / nt, &start);
+  const Span s = span_of(q, it.e);
+  it.lo = __builtin_amdgcn_readfirstlane(s.lo);
+  it.n = __builtin_amdgcn_readfirstlane(s.n);
+  const int high = tiles_of<SH::HIGH>(it.n), local = item - start * nt;
+  it.nt = local / high;
+  height_of((it.n + 63) / 64, high, local - it.nt * high, &it);
   GemmOp g = q.g;
   move<T>(g.a[0], it);
   move<T>(g.a[1], it);
@@ -258,69 +502,74 @@ __device__ __forceinline__ void rows_tile(const GroupedOp &q, OUT out, ARGS plac
   g.b[1].p = (const uint8_t *)g.b[1].p + it.e * q.b_expert;
   g.b_up.p = (const uint8_t *)g.b_up.p + it.e * q.b_expert;
   g.M = it.n;
-  place(out, it);
-  gemm_tile<T, MI, NI, false, BC, DUAL>(g, it.mt, it.nt, 0, out);
+  tile_of_height<T, SH, false, BC, DUAL>(g, it, it.lo, 0, out, L0, L1, L2, L3);
 }
 
-template <typename T, int MI, int NI>
-__global__ __launch_bounds__(256, MI *NI >= 8 ? 1 : 2) void up_kernel(const GroupedOp q,
-                                                                      const UpOut<T> o) {
-  rows_tile<T, MI, NI, false, true>(q, o, [](UpOut<T> &u, const GroupedItem &it) { u.lo = it.lo; });
+template <typename T, class SH, int KIND>
+__global__ __launch_bounds__(256, SH::PER_CU) void up_kernel(const GroupedOp q, const UpOut<T, KIND> o) {
+  rows_product<T, SH, false, true>(q, o);
 }
-template <typename T, int MI, int NI>
-__global__ __launch_bounds__(256, MI *NI >= 8 ? 1 : 2) void down_kernel(const GroupedOp q,
-                                                                        const RowsOut<T> o) {
-  rows_tile<T, MI, NI, false, false>(
-      q, o, [](RowsOut<T> &u, const GroupedItem &it) { u.y += (int64_t)it.lo * u.N; });
+template <typename T, class SH>
+__global__ __launch_bounds__(256, SH::PER_CU) void down_kernel(const GroupedOp q, const SumsOut<T> o) {
+  rows_product<T, SH, false, false>(q, o);
 }
-template <typename T, int MI, int NI>
-__global__ __launch_bounds__(256, MI *NI >= 8 ? 1 : 2) void dh_kernel(const GroupedOp q,
-                                                                      const SlopeOut<T> o) {
-  rows_tile<T, MI, NI, true, false>(q, o, [](SlopeOut<T> &u, const GroupedItem &it) { u.lo = it.lo; });
+template <typename T, class SH, int KIND>
+__global__ __launch_bounds__(256, SH::PER_CU) void dh_kernel(const GroupedOp q, const SlopeOut<T, KIND> o) {
+  rows_product<T, SH, true, false>(q, o);
 }
-template <typename T, int MI, int NI>
-__global__ __launch_bounds__(256, MI *NI >= 8 ? 1 : 2) void dx_kernel(const GroupedOp q,
-                                                                      const RowsOut<T> o) {
-  rows_tile<T, MI, NI, true, false>(
-      q, o, [](RowsOut<T> &u, const GroupedItem &it) { u.y += (int64_t)it.lo * u.N; });
+template <typename T, class SH>
+__global__ __launch_bounds__(256, SH::PER_CU) void dx_kernel(const GroupedOp q, const SumsOut<T> o) {
+  rows_product<T, SH, true, false>(q, o);
 }
 
-// Weight gradients: every expert has the same tiles, those of an expert without
-// rows are zeros.
-template <typename T, int MI, int NI>
-__global__ __launch_bounds__(256, MI *NI >= 8 ? 1 : 2) void dw_kernel(const GroupedOp q,
-                                                                      const WeightOut<T> o) {
-  const int tiles = (int)q.g.m_tiles * q.g.n_tiles, items = tiles * q.E;
-  const int per = (items + 7) / 8;
-  const int slot = (int)(blockIdx.x >> 3), item = (int)(blockIdx.x & 7) * per + slot;
-  if (slot >= per || item >= items) return;
-  GroupedItem it;
-  it.e = item / tiles;
-  const int local = item - it.e * tiles;
-  const int mt = local / q.g.n_tiles, nt = local - mt * q.g.n_tiles;
-  const Span s = span_of(q, it.e);
-  it.lo = __builtin_amdgcn_readfirstlane(s.lo);
-  it.n = __builtin_amdgcn_readfirstlane(s.n);
-  GemmOp g = q.g;
-  move<T>(g.a[0], it);
-  move<T>(g.a_up, it);
-  move<T>(g.b[0], it);
-  g.kdim[0] = it.n;
-  WeightOut<T> out = o;
-  out.dw = (T *)((uint8_t *)o.dw + it.e * q.out_expert);
-  out.dw_up = (T *)((uint8_t *)o.dw_up + it.e * q.out_expert);
-  gemm_tile<T, MI, NI, true, true, false>(g, mt, nt, 0, out);
+// Weight gradients: every expert has the same tiles, those of an expert without rows
+// are zeros.  An XCD takes the tiles of a range of experts, ranges of equal cost
+// (stages, and kTileStages for what a tile costs besides), and its workgroups go
+// through them side by side: the rows that they read lie in its L2.
+constexpr int kTileStages = 8;
+template <typename T, class SH>
+__global__ __launch_bounds__(256, SH::PER_CU) void dw_kernel(const GroupedOp q, const SumsOut<T> o) {
+  MOE_RING(SH)
+  constexpr int KB = 64 / sizeof(T);
+  const int tiles = (int)q.g.m_tiles * q.g.n_tiles, per_half = (int)q.g.m_tiles / q.g.halves;
+  auto cost = [&](int e) { return (span_of(q, e).n + KB - 1) / KB + kTileStages; };
+  const auto line = line_of<int64_t>(q.E, [&](int e) { return (int64_t)cost(e) * tiles; });
+  auto first_of = [&](int xcd) {
+    const int64_t pos = line.total() / 8 * xcd;
+    int64_t start;
+    const int e = line.at(pos, &start);
+    return e * tiles + (int)((pos - start) / __builtin_amdgcn_readfirstlane(cost(e)));
+  };
+  const int xcd = (int)(blockIdx.x & 7);
+  const int last = xcd == 7 ? tiles * q.E : first_of(xcd + 1);
+  for (int item = first_of(xcd) + (int)(blockIdx.x >> 3); item < last; item += (int)(gridDim.x >> 3)) {
+    GroupedItem it;
+    it.e = item / tiles;
+    const int local = item - it.e * tiles;
+    int mt = local / q.g.n_tiles;
+    it.nt = local - mt * q.g.n_tiles;
+    const int half = mt >= per_half ? 1 : 0;
+    mt -= half * per_half;
+    height_of((int)((q.g.M + 63) / 64), per_half, mt, &it);
+    const Span s = span_of(q, it.e);
+    it.lo = __builtin_amdgcn_readfirstlane(s.lo);
+    it.n = __builtin_amdgcn_readfirstlane(s.n);
+    GemmOp g = q.g;
+    if (half) g.a[0] = g.a_up;
+    move<T>(g.a[0], it);
+    move<T>(g.b[0], it);
+    g.kdim[0] = it.n;
+    tile_of_height<T, SH, true, true, false>(g, it, it.e * g.M, half, o, L0, L1, L2, L3);
+  }
 }
 
 // ---------------------------------------------------------------------------
 struct Tile {
-  int mi, ni;
+  int high, ni;
 };
 
-// The most row tiles of `rows` rows of E experts.
-int64_t most_row_tiles(int64_t rows, int E, int tm) {
-  return rows / tm + (rows < E ? rows : E);
-}
+// The most 64-row blocks of `rows` rows of E experts.
+int64_t most_blocks(int64_t rows, int E) { return rows / 64 + (rows < E ? rows : E); }
 
 GroupedOp grouped_op(const ExpertsArgs &a, int N) {
   GroupedOp q = {};
@@ -331,17 +580,24 @@ GroupedOp grouped_op(const ExpertsArgs &a, int N) {
   q.g.parts = 1;
   q.g.halves = 1;
   q.g.e.N = N;
-  q.g.e.vec = 1;
   return q;
 }
 
-unsigned grid_of(int64_t items) { return (unsigned)(8 * ((items + 7) / 8)); }
+// Workgroups that walk their items: what the GPU holds, or fewer where there is less
+// to do.
+template <class SH>
+dim3 held_grid(int64_t items) {
+  const int64_t most = kCus * SH::PER_CU, n = (items + 7) / 8 * 8;
+  return dim3((unsigned)(n < most ? n : most));
+}
 
-// Workgroups of a product over rows; sets its column tiles.
-unsigned rows_grid(GroupedOp &q, const Tile &t, bool dual) {
-  const int to = dual ? 32 * t.ni : 64 * t.ni;
+// Sets a product's column tiles; workgroups for the most row tiles that there can be.
+template <class SH>
+dim3 rows_grid(GroupedOp &q, bool dual) {
+  const int to = dual ? 32 * SH::NI : 64 * SH::NI;
   q.g.n_tiles = (q.g.e.N + to - 1) / to;
-  return grid_of(most_row_tiles(q.rows, q.E, 64 * t.mi) * q.g.n_tiles);
+  const int64_t tiles = q.rows / (64 * SH::HIGH) + (q.rows < q.E ? q.rows : q.E);
+  return dim3((unsigned)((tiles * q.g.n_tiles + 7) / 8 * 8));
 }
 
 }  // namespace
@@ -363,44 +619,122 @@ ExpertsSpace experts_space(int64_t rows, int I, int dtype, bool backward) {
 }
 
 bool experts_launchable(const ExpertsArgs &a, bool backward) {
-  // the smallest tiles make the largest launch
+  // fewer than 2^32 threads a launch; the smallest tiles are the most
   const int64_t wide = a.d > a.I ? a.d : a.I, cols = (wide + 31) / 32;
-  const int64_t by_rows = most_row_tiles(a.rows, a.E, 64) * cols;
+  const int64_t by_rows = most_blocks(a.rows, a.E) * cols;
   const int64_t by_expert =
       backward ? 2 * (int64_t)a.E * ((a.d + 63) / 64) * ((a.I + 63) / 64) : 0;
-  return (by_rows > by_expert ? by_rows : by_expert) * 256 + 2048 < (int64_t)1 << 32;
+  return by_rows * 256 + 2048 < (int64_t)1 << 32 && by_expert < INT32_MAX;
 }
 
 namespace {
 
-template <typename T, int MI, int NI>
-hipError_t run_forward(const ExpertsArgs &a, char *ws, hipStream_t s) {
-  const ExpertsSpace L = experts_space(a.rows, a.I, a.dtype, false);
-  constexpr int NU = NI > 1 ? NI : 2;          // two matrices share a tile
+enum Product { kUp, kDown, kDh, kDx, kDw };
+
+// Calls f with the shape.
+template <typename T, class F>
+hipError_t with_shape(const Tile &t, F f) {
+  if (t.high == 1 && t.ni == 1) return f(Shape<1, 1, 4>{});
+  if (t.high == 1) return f(Shape<1, 2, 4>{});
+  if constexpr (sizeof(T) == 2) {
+    if (t.high == 4 && t.ni == 2) return f(Shape<4, 2, 3>{});
+    if (t.high == 4) return f(Shape<4, 4, 4>{});
+  }
+  return f(Shape<2, 2, 4>{});
+}
+
+Tile pick_tile(const ExpertsArgs &a, Product p) {
+  const char *names[] = {"T_UP", "T_DOWN", "T_DH", "T_DX", "T_DW"};
+  if (const char *e = getenv(names[p])) { if (a.dtype == MOE_DTYPE_F32 && e[0] > '1') return {2, 2}; return {e[0] - '0', p == kUp && e[1] == '1' ? 2 : e[1] - '0'}; }
+  return {1, p == kUp ? 2 : 1};
+}
+
+// Calls f with the saved kind as a constant.
+template <class F>
+hipError_t with_kind(int kind, F f) {
+  if (kind == MOE_SAVE_MXFP8) return f(std::integral_constant<int, MOE_SAVE_MXFP8>{});
+  if (kind == MOE_SAVE_FULL) return f(std::integral_constant<int, MOE_SAVE_FULL>{});
+  return f(std::integral_constant<int, MOE_SAVE_NONE>{});
+}
+
+template <typename T>
+hipError_t run_up(const ExpertsArgs &a, T *h, hipStream_t s) {
   GroupedOp q = grouped_op(a, a.I);
   q.g.a[0] = {a.x, a.d, a.rows, a.d};
   q.g.b[0] = {a.w_gate, a.d, a.I, a.d};
   q.g.b_up = {a.w_up, a.d, a.I, a.d};
   q.b_expert = (int64_t)a.I * a.d * sizeof(T);
   q.g.kdim[0] = a.d;
-  const UpOut<T> up = {(T *)(ws + L.h), a.saved, 0, a.I, a.limit};
-  unsigned grid = rows_grid(q, {MI, NU}, true);
-  hipLaunchKernelGGL((up_kernel<T, MI, NU>), dim3(grid), dim3(256), 0, s, q, up);
-  hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return err;
-  q = grouped_op(a, a.d);
-  q.g.a[0] = {ws + L.h, a.I, a.rows, a.I};
+  return with_shape<T>(pick_tile(a, kUp), [&](auto sh) {
+    // two matrices share a tile
+    using SH = std::conditional_t<decltype(sh)::NI == 1, Shape<1, 2, 4>, decltype(sh)>;
+    const dim3 grid = rows_grid<SH>(q, true);
+    return with_kind(a.saved.kind, [&](auto kind) {
+      const UpOut<T, kind> o = {h, a.saved, a.I, a.limit};
+      hipLaunchKernelGGL((up_kernel<T, SH, kind>), grid, dim3(256), 0, s, q, o);
+      return hipGetLastError();
+    });
+  });
+}
+
+template <typename T>
+hipError_t run_down(const ExpertsArgs &a, const T *h, hipStream_t s) {
+  GroupedOp q = grouped_op(a, a.d);
+  q.g.a[0] = {h, a.I, a.rows, a.I};
   q.g.b[0] = {a.w_down, a.I, a.d, a.I};
   q.b_expert = (int64_t)a.I * a.d * sizeof(T);
   q.g.kdim[0] = a.I;
-  const RowsOut<T> down = {(T *)a.y, a.d};
-  grid = rows_grid(q, {MI, NI}, false);
-  hipLaunchKernelGGL((down_kernel<T, MI, NI>), dim3(grid), dim3(256), 0, s, q, down);
-  return hipGetLastError();
+  const SumsOut<T> o = {(T *)a.y, nullptr, a.d};
+  return with_shape<T>(pick_tile(a, kDown), [&](auto sh) {
+    using SH = decltype(sh);
+    const dim3 grid = rows_grid<SH>(q, false);
+    hipLaunchKernelGGL((down_kernel<T, SH>), grid, dim3(256), 0, s, q, o);
+    return hipGetLastError();
+  });
+}
+
+template <typename T>
+hipError_t run_dh(const ExpertsArgs &a, T *dz, T *du, T *h, hipStream_t s) {
+  GroupedOp q = grouped_op(a, a.I);
+  q.g.a[0] = {a.dy, a.d, a.rows, a.d};
+  q.g.b[0] = {a.w_down, a.I, a.d, a.I};
+  q.b_expert = (int64_t)a.I * a.d * sizeof(T);
+  q.g.kdim[0] = a.d;
+  return with_shape<T>(pick_tile(a, kDh), [&](auto sh) {
+    using SH = decltype(sh);
+    const dim3 grid = rows_grid<SH>(q, false);
+    if (a.saved.kind == MOE_SAVE_MXFP8) {
+      const SlopeOut<T, MOE_SAVE_MXFP8> o = {dz, du, h, a.saved, a.I, a.limit};
+      hipLaunchKernelGGL((dh_kernel<T, SH, MOE_SAVE_MXFP8>), grid, dim3(256), 0, s, q, o);
+    } else {
+      const SlopeOut<T, MOE_SAVE_FULL> o = {dz, du, h, a.saved, a.I, a.limit};
+      hipLaunchKernelGGL((dh_kernel<T, SH, MOE_SAVE_FULL>), grid, dim3(256), 0, s, q, o);
+    }
+    return hipGetLastError();
+  });
+}
+
+template <typename T>
+hipError_t run_dx(const ExpertsArgs &a, const T *dz, const T *du, hipStream_t s) {
+  GroupedOp q = grouped_op(a, a.d);
+  q.g.a[0] = {dz, a.I, a.rows, a.I};
+  q.g.a[1] = {du, a.I, a.rows, a.I};
+  q.g.b[0] = {a.w_gate, a.d, a.I, a.d};
+  q.g.b[1] = {a.w_up, a.d, a.I, a.d};
+  q.b_expert = (int64_t)a.I * a.d * sizeof(T);
+  q.g.kdim[0] = q.g.kdim[1] = a.I;
+  q.g.segments = 2;
+  const SumsOut<T> o = {(T *)a.dx, nullptr, a.d};
+  return with_shape<T>(pick_tile(a, kDx), [&](auto sh) {
+    using SH = decltype(sh);
+    const dim3 grid = rows_grid<SH>(q, false);
+    hipLaunchKernelGGL((dx_kernel<T, SH>), grid, dim3(256), 0, s, q, o);
+    return hipGetLastError();
+  });
 }
 
 // A weight gradient [N, K] of every expert: columns of A (and A_up), columns of B.
-template <typename T, int MI, int NI>
+template <typename T>
 hipError_t run_dw(const ExpertsArgs &a, const void *A, const void *A_up, int N, const void *B, int K,
                   void *dw, void *dw_up, hipStream_t s) {
   GroupedOp q = grouped_op(a, K);
@@ -409,68 +743,52 @@ hipError_t run_dw(const ExpertsArgs &a, const void *A, const void *A_up, int N, 
   q.g.b[0] = {B, K, a.rows, K};
   q.g.M = N;
   q.g.halves = A_up ? 2 : 1;
-  q.g.m_tiles = (N + 64 * MI - 1) / (64 * MI) * q.g.halves;
-  q.g.n_tiles = (K + 64 * NI - 1) / (64 * NI);
-  q.out_expert = (int64_t)N * K * sizeof(T);
-  const WeightOut<T> o = {(T *)dw, (T *)dw_up, K};
-  hipLaunchKernelGGL((dw_kernel<T, MI, NI>), dim3(grid_of(q.g.m_tiles * q.g.n_tiles * a.E)), dim3(256),
-                     0, s, q, o);
-  return hipGetLastError();
+  const SumsOut<T> o = {(T *)dw, (T *)dw_up, K};
+  return with_shape<T>(pick_tile(a, kDw), [&](auto sh) {
+    using SH = decltype(sh);
+    q.g.m_tiles = (N + 64 * SH::HIGH - 1) / (64 * SH::HIGH) * q.g.halves;
+    q.g.n_tiles = (K + 64 * SH::NI - 1) / (64 * SH::NI);
+    const dim3 grid = held_grid<SH>(q.g.m_tiles * q.g.n_tiles * a.E);
+    hipLaunchKernelGGL((dw_kernel<T, SH>), grid, dim3(256), 0, s, q, o);
+    return hipGetLastError();
+  });
 }
 
-template <typename T, int MI, int NI>
+template <typename T>
+hipError_t run_forward(const ExpertsArgs &a, char *ws, hipStream_t s) {
+  T *h = (T *)(ws + experts_space(a.rows, a.I, a.dtype, false).h);
+  const hipError_t err = run_up<T>(a, h, s);
+  return err != hipSuccess ? err : run_down<T>(a, h, s);
+}
+
+template <typename T>
 hipError_t run_backward(const ExpertsArgs &a, char *ws, hipStream_t s) {
   const ExpertsSpace L = experts_space(a.rows, a.I, a.dtype, true);
   T *h = (T *)(ws + L.h), *dz = (T *)(ws + L.dz), *du = (T *)(ws + L.du);
   hipError_t err;
-  if (a.rows > 0) {
-    GroupedOp q = grouped_op(a, a.I);
-    q.g.a[0] = {a.dy, a.d, a.rows, a.d};
-    q.g.b[0] = {a.w_down, a.I, a.d, a.I};
-    q.b_expert = (int64_t)a.I * a.d * sizeof(T);
-    q.g.kdim[0] = a.d;
-    const SlopeOut<T> o = {dz, du, h, a.saved, 0, a.I, a.limit};
-    unsigned grid = rows_grid(q, {MI, NI}, false);
-    hipLaunchKernelGGL((dh_kernel<T, MI, NI>), dim3(grid), dim3(256), 0, s, q, o);
-    if ((err = hipGetLastError()) != hipSuccess) return err;
-  }
+  if (a.rows > 0 && (err = run_dh<T>(a, dz, du, h, s)) != hipSuccess) return err;
   if (a.dw_down &&
-      (err = run_dw<T, MI, NI>(a, a.dy, nullptr, a.d, h, a.I, a.dw_down, nullptr, s)) != hipSuccess)
+      (err = run_dw<T>(a, a.dy, nullptr, a.d, h, a.I, a.dw_down, nullptr, s)) != hipSuccess)
     return err;
   if (a.dw_gate || a.dw_up) {
     // both in one launch, or the one that is wanted
     const bool both = a.dw_gate && a.dw_up;
-    if ((err = run_dw<T, MI, NI>(a, a.dw_gate ? dz : du, both ? du : nullptr, a.I, a.x, a.d,
-                                 a.dw_gate ? a.dw_gate : a.dw_up, a.dw_up, s)) != hipSuccess)
+    if ((err = run_dw<T>(a, a.dw_gate ? dz : du, both ? du : nullptr, a.I, a.x, a.d,
+                         a.dw_gate ? a.dw_gate : a.dw_up, a.dw_up, s)) != hipSuccess)
       return err;
   }
-  if (a.dx && a.rows > 0) {
-    GroupedOp q = grouped_op(a, a.d);
-    q.g.a[0] = {dz, a.I, a.rows, a.I};
-    q.g.a[1] = {du, a.I, a.rows, a.I};
-    q.g.b[0] = {a.w_gate, a.d, a.I, a.d};
-    q.g.b[1] = {a.w_up, a.d, a.I, a.d};
-    q.b_expert = (int64_t)a.I * a.d * sizeof(T);
-    q.g.kdim[0] = q.g.kdim[1] = a.I;
-    q.g.segments = 2;
-    const RowsOut<T> o = {(T *)a.dx, a.d};
-    unsigned grid = rows_grid(q, {MI, NI}, false);
-    hipLaunchKernelGGL((dx_kernel<T, MI, NI>), dim3(grid), dim3(256), 0, s, q, o);
-    if ((err = hipGetLastError()) != hipSuccess) return err;
-  }
+  if (a.dx && a.rows > 0) return run_dx<T>(a, dz, du, s);
   return hipSuccess;
 }
 
 }  // namespace
 
 hipError_t launch_experts(const ExpertsArgs &a, char *ws, hipStream_t s) {
-  return a.dtype == MOE_DTYPE_F32 ? run_forward<float, 1, 1>(a, ws, s)
-                                  : run_forward<bf16, 1, 1>(a, ws, s);
+  return a.dtype == MOE_DTYPE_F32 ? run_forward<float>(a, ws, s) : run_forward<bf16>(a, ws, s);
 }
 
 hipError_t launch_experts_backward(const ExpertsArgs &a, char *ws, hipStream_t s) {
-  return a.dtype == MOE_DTYPE_F32 ? run_backward<float, 1, 1>(a, ws, s)
-                                  : run_backward<bf16, 1, 1>(a, ws, s);
+  return a.dtype == MOE_DTYPE_F32 ? run_backward<float>(a, ws, s) : run_backward<bf16>(a, ws, s);
 }
 
 }  // namespace moe

@@ -23,10 +23,20 @@ namespace {
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
-// |v| for the block's maximum.
-__device__ __forceinline__ float keep_magnitude(float v) {
-  const float a = fabsf(v);
-  return a < __builtin_inff() ? a : 0.f;
+// Largest finite magnitude of eight values, whatever bits they have.
+__device__ __forceinline__ float keep_top(const float (&v)[8]) {
+  float m = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]) < __builtin_inff() ? fabsf(v[j]) : 0.f);
+  return m;
+}
+// The same of results of arithmetic, whose NaNs are quiet ones: a maximum with one is
+// the other operand, and infinities alone need the comparison.
+__device__ __forceinline__ float keep_top_of_sums(const float (&v)[8]) {
+  float m = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
+  return m == __builtin_inff() ? keep_top(v) : m;
 }
 
 // X of a block from its largest finite magnitude.
@@ -46,7 +56,7 @@ __device__ __forceinline__ void keep8(const float (&v)[8], int X, float limit, u
   const float to = keep_pow2(-X);
   float q[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) q[j] = fabsf(v[j]) < __builtin_inff() ? v[j] * to : __builtin_nanf("");
+  for (int j = 0; j < 8; ++j) q[j] = v[j] * to;              // the conversion makes NaN of infinities
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[4 * h], q[4 * h + 1], 0, false);

@@ -16,12 +16,142 @@
 namespace moe {
 namespace {
 
+// Work item of this workgroup: workgroups are dealt round-robin to the 8 XCDs,
+// each XCD takes a contiguous run of items; within a part, tiles run down
+// groups of 8 row tiles before the next column tile, so the tiles an XCD works
+// on at a time form a block that shares operand rows in its L2.
+__device__ __forceinline__ bool gemm_item(const GemmOp &g, int64_t *mt, int *nt, int *part) {
+  const int64_t tiles = g.m_tiles * g.n_tiles, items = tiles * g.parts;
+  const int64_t per = (items + 7) / 8;
+  const int64_t item = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if ((blockIdx.x >> 3) >= per || item >= items) return false;
+  *part = (int)(item / tiles);
+  const int64_t t = item - *part * tiles;
+  const int64_t group = t / (8 * g.n_tiles), first = group * 8;
+  const int64_t high = g.m_tiles - first < 8 ? g.m_tiles - first : 8;
+  const int64_t r = t - first * g.n_tiles;
+  *nt = (int)(r / high);
+  *mt = first + (r - *nt * high);
+  return true;
+}
+
 template <typename T, int MI, int NI, bool AC, bool BC, bool DUAL>
-__global__ __launch_bounds__(256, MI *NI >= 8 ? 1 : 2) void gemm_kernel(const GemmOp g) {
+__device__ __forceinline__ void gemm_tile(const GemmOp &g) {
+  constexpr int ES = sizeof(T), NS = 4;
+  constexpr int TM = 64 * MI, TN = 64 * NI, SLOT = kSlot<MI, NI>;
+  __shared__ __attribute__((aligned(1024))) uint8_t L0[SLOT];
+  __shared__ __attribute__((aligned(1024))) uint8_t L1[SLOT];
+  __shared__ __attribute__((aligned(1024))) uint8_t L2[SLOT];
+  __shared__ __attribute__((aligned(1024))) uint8_t L3[SLOT];
   int64_t mt;
   int nt, part;
-  if (gemm_item(g, &mt, &nt, &part))
-    gemm_tile<T, MI, NI, AC, BC, DUAL>(g, mt, nt, part, LinearOut{});
+  if (!gemm_item(g, &mt, &nt, &part)) return;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  constexpr int TO = DUAL ? TN / 2 : TN;       // output columns of a tile
+  int half = 0;
+  if constexpr (AC) {                          // dW
+    const int64_t per = g.m_tiles / g.halves;
+    half = mt >= per ? 1 : 0;
+    mt -= half * per;
+  }
+  const int64_t m0 = mt * TM, n0 = (int64_t)nt * TO;
+  f32x16 acc[MI][NI];
+  gemm_sums<T, MI, NI, AC, BC, DUAL, NS>(g, m0, n0, half, part, L0, L1, L2, L3, acc);
+
+  // Epilogue.  32 rows of the wave's quarter at a time go through the wave's own
+  // part of LDS (no barrier), so that a lane then has eight consecutive columns
+  // of a row and 16 or 8 lanes a whole line.  bf16: the whole tile's residual is
+  // asked for at once, into the registers that the operands have left (in 32-row
+  // pieces a read's latency bounded it: 10 % longer at 4096x2048->7168).
+  constexpr int NJ = DUAL ? NI / 2 : NI;       // output column blocks of the wave
+  constexpr int PC = NJ * 4;                   // pieces of 8 columns per row
+  constexpr int PPI = 32 * PC / 64;            // pieces per lane and 32 rows
+  constexpr int LD = NI * 32 + 4;              // floats per LDS row (padded)
+  constexpr bool RES = !AC && !BC;             // gradients have no residual
+  constexpr int AHEAD = RES && ES == 2 ? MI : 1;
+  static_assert(32 * LD * 4 <= SLOT, "a wave's rows fit a ring slot");
+  float *stage_f = (float *)(wave == 0 ? L0 : wave == 1 ? L1 : wave == 2 ? L2 : L3);
+  const bool plain = g.parts > 1;
+  // piece q of the wave's rows 32 i ..: row and piece in the block, place in the output
+  struct Place {
+    int r, pc;
+    int64_t m;
+    int n;
+  };
+  auto place = [&](int i, int q) {
+    const int idx = q * 64 + lane;
+    const int r = idx / PC, pc = idx - r * PC;
+    return Place{r, pc, m0 + (wm * MI + i) * 32 + r, (int)n0 + wn * NJ * 32 + pc * 8};
+  };
+  Raw8<T> res[PPI], ahead[AHEAD][PPI];
+  auto fetch = [&](int i, Raw8<T> (&to)[PPI]) {
+#pragma unroll
+    for (int q = 0; q < PPI; ++q) {
+      const Place o = place(i, q);
+      if (o.m < g.M && o.n < g.e.N)
+        fetch8<T>(to[q], (const T *)g.e.residual + o.m * g.e.ld_res + o.n, g.e.N - o.n,
+                  g.e.vec != 0);
+    }
+  };
+  const bool has_res = RES && g.e.residual && !plain;
+  Biases<T, DUAL> bias;                        // a lane's columns are the same in every piece
+  static_assert(64 % PC == 0, "they are");
+  __builtin_amdgcn_s_waitcnt(0);
+  if (RES && !plain) bias.fetch(g.e, place(0, 0).n);
+  if (AHEAD > 1 && has_res) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) fetch(i, ahead[i]);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_barrier();                // every wave is done with the ring
+  __builtin_amdgcn_sched_barrier(0);
+  for (int ci = 0; ci < MI; ++ci) {
+    if (AHEAD == 1 && has_res) fetch(ci, res);
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+      if (i == ci) {                           // uniform; the accumulators keep their registers
+#pragma unroll
+        for (int j = 0; j < NI; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *(f32x4 *)(stage_f + (lane & 31) * LD + j * 32 + 8 * e + 4 * (lane >> 5)) =
+                f32x4{acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2],
+                      acc[i][j][4 * e + 3]};
+        if constexpr (AHEAD > 1)
+#pragma unroll
+          for (int q = 0; q < PPI; ++q) res[q] = ahead[i][q];
+      }
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int q = 0; q < PPI; ++q) {
+      const Place o = place(ci, q);
+      float v[8], u[8], rs[8];
+      load8<float>(v, stage_f + o.r * LD + o.pc * 8, 8, true);
+      if constexpr (DUAL) load8<float>(u, stage_f + o.r * LD + NJ * 32 + o.pc * 8, 8, true);
+      if (o.m >= g.M || o.n >= g.e.N) continue;
+      if (plain) {
+        // rows of ldp, a multiple of 8: whole pieces
+        float *to =
+            g.part + (((int64_t)part * (DUAL ? 2 : g.halves) + half) * g.M + o.m) * g.ldp + o.n;
+        store8<float>(to, v, 8, true);
+        if constexpr (DUAL) store8<float>(to + g.M * g.ldp, u, 8, true);
+      } else if constexpr (!RES) {             // a gradient: no epilogue
+        store8<T>((T *)(half ? g.y_up : g.e.y) + o.m * g.e.ld_y + o.n, v, g.e.N - o.n,
+                  g.e.vec != 0);
+      } else {
+        if (has_res) widen8<T>(rs, res[q]);
+        finish8<T, DUAL>(g.e, v, u, bias, rs, o.m, o.n);
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+template <typename T, int MI, int NI, bool AC, bool BC, bool DUAL>
+__global__ __launch_bounds__(256, MI *NI >= 8 ? 1 : 2) void gemm_kernel(const GemmOp g) {
+  gemm_tile<T, MI, NI, AC, BC, DUAL>(g);
 }
 
 // Sum of the parts of a split product, in order, and the epilogue.

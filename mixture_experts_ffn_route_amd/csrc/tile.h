@@ -65,8 +65,11 @@ struct Operand {
   // 16-byte pieces of an LDS row are permuted so that a half-wave's reads take
   // distinct banks: by rows, row r's piece c sits at c ^ (r / 8 % 4) (eight
   // rows of 64 bytes cover address bits 6-8, the four pieces bits 4-5); by
-  // columns, the four rows of a transposed read sit 64 bytes apart modulo 256.
-  static __device__ __forceinline__ int swz(int k) { return ES == 2 && TC >= 128 ? (k & 3) << 2 : 0; }
+  // columns, the four rows of a transposed read sit 64 bytes apart modulo 256 (rows
+  // of an odd number of 128 bytes are 128 apart by themselves).
+  static __device__ __forceinline__ int swz(int k) {
+    return ES != 2 ? 0 : TC % 128 == 0 ? (k & 3) << 2 : (k & 2) << 1;
+  }
 
   // Byte offset, from the stage's origin, of what lane l copies to byte 16 l of
   // unit u.
@@ -136,25 +139,6 @@ __device__ __forceinline__ void mma(f32x16 &acc, const u32x4 &a, const u32x4 &b)
   }
 }
 
-// Work item of this workgroup: workgroups are dealt round-robin to the 8 XCDs,
-// each XCD takes a contiguous run of items; within a part, tiles run down
-// groups of 8 row tiles before the next column tile, so the tiles an XCD works
-// on at a time form a block that shares operand rows in its L2.
-__device__ __forceinline__ bool gemm_item(const GemmOp &g, int64_t *mt, int *nt, int *part) {
-  const int64_t tiles = g.m_tiles * g.n_tiles, items = tiles * g.parts;
-  const int64_t per = (items + 7) / 8;
-  const int64_t item = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  if ((blockIdx.x >> 3) >= per || item >= items) return false;
-  *part = (int)(item / tiles);
-  const int64_t t = item - *part * tiles;
-  const int64_t group = t / (8 * g.n_tiles), first = group * 8;
-  const int64_t high = g.m_tiles - first < 8 ? g.m_tiles - first : 8;
-  const int64_t r = t - first * g.n_tiles;
-  *nt = (int)(r / high);
-  *mt = first + (r - *nt * high);
-  return true;
-}
-
 // Where an operand's next stage starts: address, bytes from there to the end of
 // the matrix (a copy past it reads zeros), bytes to the stage after.
 struct Cursor {
@@ -175,6 +159,12 @@ __device__ __forceinline__ rsrc_t cursor_rsrc(const Cursor &c) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(c.p), 0, n, 0x00027000);
 }
 
+// 16 bytes a lane from the matrix to LDS, lane l's at to + 16 l, zeros where off is
+// past the end.
+__device__ __forceinline__ void copy16(rsrc_t r, uint8_t *to, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (MOE_LDS void *)to, 16, off, 0, 0, 0);
+}
+
 // The order a step's instructions are issued in: one LDS read (of DS) after
 // each of the first MFMAs (of N), the copies (of VM) spread over all of them.
 // The scheduler otherwise sinks the reads to their use in the next step and
@@ -193,46 +183,33 @@ __device__ __forceinline__ void interleave() {
   }
 }
 
-// What becomes of a tile's sums.  `plain`: the dense product's own endings (its
-// epilogue, a gradient, a part of a split contraction).  Otherwise the type says:
-// fetch() asks for what eight columns of a row need, put() takes their sums.
-struct LinearOut {
-  static constexpr bool plain = true;
-  struct Ahead {};
-};
+// Bytes of a ring slot.
+template <int MI, int NI>
+constexpr int kSlot = (64 * MI + 64 * NI) * 64;
 
-// One tile: row tile mt, column tile nt, share `part` of the contraction.
-template <typename T, int MI, int NI, bool AC, bool BC, bool DUAL, class OUT>
-__device__ __forceinline__ void gemm_tile(const GemmOp &g, int64_t mt, int nt, int part,
-                                          const OUT &out) {
-  constexpr int ES = sizeof(T), KB = 64 / ES, NS = 4;
+// The sums of one tile: 64 MI rows from m0 (of the second matrix: `half`) and 64 NI
+// columns from n0 (swiglu: half of them of each matrix), share `part` of the
+// contraction.  Wave w has the rows of quarter w / 2 and the columns of quarter w % 2
+// as MI x NI blocks (mma() says what a lane holds).  The ring has NS slots, one LDS
+// object each, so that a read of one does not wait for copies into another; they may
+// be larger than this tile's.  Copies past the end may still be under way at the end.
+template <typename T, int MI, int NI, bool AC, bool BC, bool DUAL, int NS>
+__device__ __forceinline__ void gemm_sums(const GemmOp &g, int64_t m0, int64_t n0, int half, int part,
+                                          uint8_t *L0, uint8_t *L1, uint8_t *L2, uint8_t *L3,
+                                          f32x16 (&acc)[MI][NI]) {
+  uint8_t *const ring[4] = {L0, L1, L2, L3};   // NS of them
+  constexpr int ES = sizeof(T), KB = 64 / ES;
   constexpr int TM = 64 * MI, TN = 64 * NI;
   constexpr int UA = TM / 16, UB = TN / 16;    // 1 KB copy units per stage
   constexpr int VA = UA / 4, VB = UB / 4, VM = VA + VB;          // per wave
-  constexpr int SLOT = (TM + TN) * 64;
   constexpr bool SEGS = !AC && BC;             // two contraction segments occur (dx of swiglu)
   static_assert(!DUAL || (!AC && !BC), "the two-matrix product is the forward one");
   static_assert(UA % 4 == 0 && UB % 4 == 0, "units split evenly");
   using OA = Operand<T, AC, TM>;
   using OB = Operand<T, BC, TN>;
-  // one LDS object per slot, so that a read of one does not wait for copies
-  // into another
-  __shared__ __attribute__((aligned(1024))) uint8_t L0[SLOT];
-  __shared__ __attribute__((aligned(1024))) uint8_t L1[SLOT];
-  __shared__ __attribute__((aligned(1024))) uint8_t L2[SLOT];
-  __shared__ __attribute__((aligned(1024))) uint8_t L3[SLOT];
-  uint8_t *const ring[4] = {L0, L1, L2, L3};
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1;
-  constexpr int TO = DUAL ? TN / 2 : TN;       // output columns of a tile
-  int half = 0;
-  if constexpr (AC) {                          // dW
-    const int64_t per = g.m_tiles / g.halves;
-    half = mt >= per ? 1 : 0;
-    mt -= half * per;
-  }
-  const int64_t m0 = mt * TM, n0 = (int64_t)nt * TO;
 
   const int st_seg0 = (int)((g.kdim[0] + KB - 1) / KB);
   const int st_all = SEGS && g.segments > 1 ? st_seg0 + (int)((g.kdim[1] + KB - 1) / KB) : st_seg0;
@@ -269,8 +246,7 @@ __device__ __forceinline__ void gemm_tile(const GemmOp &g, int64_t mt, int nt, i
     const uint32_t tail = (!AC && ka >= rest) || to_end <= 0 ? kOut : 0u;
 #pragma unroll
     for (int q = 0; q < VA; ++q)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (MOE_LDS void *)(ring[slot] + (wave + 4 * q) * 1024),
-                                               16, off_a[q] | tail, 0, 0, 0);
+      copy16(r, ring[slot] + (wave + 4 * q) * 1024, off_a[q] | tail);
     ca.p += ca.step; ca.left -= ca.step; rest -= KB; --to_end;
     if constexpr (SEGS) {
       const bool sw = --to_switch == 0;
@@ -284,8 +260,7 @@ __device__ __forceinline__ void gemm_tile(const GemmOp &g, int64_t mt, int nt, i
       const int u = wave + 4 * q;
       // units of the second half hold W_up's rows
       const bool up = DUAL && (UB >= 8 ? q >= VB / 2 : u >= UB / 2);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(cursor_rsrc(up ? cu : cb), (MOE_LDS void *)(ring[slot] + (UA + u) * 1024), 16,
-                                               off_b[q] | tail, 0, 0, 0);
+      copy16(cursor_rsrc(up ? cu : cb), ring[slot] + (UA + u) * 1024, off_b[q] | tail);
     }
     cb.p += cb.step; cb.left -= cb.step; rest_b -= KB; --to_end_b;
     if constexpr (DUAL) { cu.p += cb.step; cu.left -= cb.step; }
@@ -295,7 +270,6 @@ __device__ __forceinline__ void gemm_tile(const GemmOp &g, int64_t mt, int nt, i
     }
   };
 
-  f32x16 acc[MI][NI];
 #pragma unroll
   for (int i = 0; i < MI; ++i)
 #pragma unroll
@@ -328,12 +302,12 @@ __device__ __forceinline__ void gemm_tile(const GemmOp &g, int64_t mt, int nt, i
 
 #pragma unroll
   for (int p = 0; p < NS - 1; ++p) { copy_a(p); copy_b(p); }
-  __builtin_amdgcn_s_waitcnt(MOE_VMCNT(2 * VM));
+  __builtin_amdgcn_s_waitcnt(MOE_VMCNT((NS - 2) * VM));
   __builtin_amdgcn_s_barrier();
   read(0, 0, 0);
   // Stage st from slot p.  The second step's fragments are read while the first
   // step multiplies; then, with every read of this slot done and the next stage
-  // landed (younger: one stage and the A half of another), one barrier, and the
+  // landed (younger: NS - 3 stages and the A half of another), one barrier, and the
   // next stage's first fragments are read while the second step multiplies.
   // The slot the previous stage used (free since the previous barrier) is
   // refilled meanwhile, A in the first step, B in the second.  Stages past the
@@ -345,7 +319,7 @@ __device__ __forceinline__ void gemm_tile(const GemmOp &g, int64_t mt, int nt, i
     multiply(0);
     interleave<0, kMma, kReadsA + kReadsB, VA>();
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(MOE_VMCNT(VM + VA) & ~(15 << 8));   // and lgkmcnt(0)
+    __builtin_amdgcn_s_waitcnt(MOE_VMCNT((NS - 3) * VM + VA) & ~(15 << 8));   // and lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
     read(0, (p + 1) % NS, 0);
@@ -362,103 +336,6 @@ __device__ __forceinline__ void gemm_tile(const GemmOp &g, int64_t mt, int nt, i
 #pragma unroll
   for (int p = 0; p < NS - 1; ++p)
     if (st + p < nst) stage(p);
-  // Epilogue.  32 rows of the wave's quarter at a time go through the wave's own
-  // part of LDS (no barrier), so that a lane then has eight consecutive columns
-  // of a row and 16 or 8 lanes a whole line.  bf16: the whole tile's residual is
-  // asked for at once, into the registers that the operands have left (in 32-row
-  // pieces a read's latency bounded it: 10 % longer at 4096x2048->7168).
-  constexpr int NJ = DUAL ? NI / 2 : NI;       // output column blocks of the wave
-  constexpr int PC = NJ * 4;                   // pieces of 8 columns per row
-  constexpr int PPI = 32 * PC / 64;            // pieces per lane and 32 rows
-  constexpr int LD = NI * 32 + 4;              // floats per LDS row (padded)
-  constexpr bool RES = OUT::plain && !AC && !BC;   // gradients have no residual
-  constexpr int AHEAD = RES && ES == 2 ? MI : 1;
-  static_assert(32 * LD * 4 <= SLOT, "a wave's rows fit a ring slot");
-  float *stage_f = (float *)(wave == 0 ? L0 : wave == 1 ? L1 : wave == 2 ? L2 : L3);
-  const bool plain = OUT::plain && g.parts > 1;
-  // piece q of the wave's rows 32 i ..: row and piece in the block, place in the output
-  struct Place {
-    int r, pc;
-    int64_t m;
-    int n;
-  };
-  auto place = [&](int i, int q) {
-    const int idx = q * 64 + lane;
-    const int r = idx / PC, pc = idx - r * PC;
-    return Place{r, pc, m0 + (wm * MI + i) * 32 + r, (int)n0 + wn * NJ * 32 + pc * 8};
-  };
-  Raw8<T> res[PPI], ahead[AHEAD][PPI];
-  typename OUT::Ahead mine[PPI];
-  auto fetch = [&](int i, Raw8<T> (&to)[PPI]) {
-#pragma unroll
-    for (int q = 0; q < PPI; ++q) {
-      const Place o = place(i, q);
-      if (o.m < g.M && o.n < g.e.N)
-        fetch8<T>(to[q], (const T *)g.e.residual + o.m * g.e.ld_res + o.n, g.e.N - o.n,
-                  g.e.vec != 0);
-    }
-  };
-  const bool has_res = RES && g.e.residual && !plain;
-  Biases<T, DUAL> bias;                        // a lane's columns are the same in every piece
-  static_assert(64 % PC == 0, "they are");
-  __builtin_amdgcn_s_waitcnt(0);
-  if (RES && !plain) bias.fetch(g.e, place(0, 0).n);
-  if (AHEAD > 1 && has_res) {
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i) fetch(i, ahead[i]);
-  }
-  __builtin_amdgcn_sched_barrier(0);
-  __builtin_amdgcn_s_barrier();                // every wave is done with the ring
-  __builtin_amdgcn_sched_barrier(0);
-  for (int ci = 0; ci < MI; ++ci) {
-    if (AHEAD == 1 && has_res) fetch(ci, res);
-    if constexpr (!OUT::plain) {
-#pragma unroll
-      for (int q = 0; q < PPI; ++q) {
-        const Place o = place(ci, q);
-        if (o.m < g.M && o.n < g.e.N) out.fetch(mine[q], o.m, o.n);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
-      if (i == ci) {                           // uniform; the accumulators keep their registers
-#pragma unroll
-        for (int j = 0; j < NI; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            *(f32x4 *)(stage_f + (lane & 31) * LD + j * 32 + 8 * e + 4 * (lane >> 5)) =
-                f32x4{acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2],
-                      acc[i][j][4 * e + 3]};
-        if constexpr (AHEAD > 1)
-#pragma unroll
-          for (int q = 0; q < PPI; ++q) res[q] = ahead[i][q];
-      }
-    __builtin_amdgcn_wave_barrier();
-#pragma unroll
-    for (int q = 0; q < PPI; ++q) {
-      const Place o = place(ci, q);
-      float v[8], u[8], rs[8];
-      load8<float>(v, stage_f + o.r * LD + o.pc * 8, 8, true);
-      if constexpr (DUAL) load8<float>(u, stage_f + o.r * LD + NJ * 32 + o.pc * 8, 8, true);
-      if (o.m >= g.M || o.n >= g.e.N) continue;
-      if constexpr (!OUT::plain) {
-        out.put(mine[q], o.m, o.n, v, u, half);
-      } else if (plain) {
-        // rows of ldp, a multiple of 8: whole pieces
-        float *to =
-            g.part + (((int64_t)part * (DUAL ? 2 : g.halves) + half) * g.M + o.m) * g.ldp + o.n;
-        store8<float>(to, v, 8, true);
-        if constexpr (DUAL) store8<float>(to + g.M * g.ldp, u, 8, true);
-      } else if constexpr (!RES) {             // a gradient: no epilogue
-        store8<T>((T *)(half ? g.y_up : g.e.y) + o.m * g.e.ld_y + o.n, v, g.e.N - o.n,
-                  g.e.vec != 0);
-      } else {
-        if (has_res) widen8<T>(rs, res[q]);
-        finish8<T, DUAL>(g.e, v, u, bias, rs, o.m, o.n);
-      }
-    }
-    __builtin_amdgcn_wave_barrier();
-  }
 }
 
 }  // namespace
