@@ -57,7 +57,7 @@ __device__ __forceinline__ Span span_of(const GroupedOp &q, int e) {
 struct GroupedItem {
   int e, lo, n;                // expert, its first row and rows
   int m0, blocks;
-  int nt;
+  int nt, half;                // half: of the second matrix
 };
 
 // Tiles of up to HIGH blocks of 64 rows that cover n rows, of as equal heights as
@@ -129,45 +129,15 @@ __device__ __forceinline__ void move(Matrix &m, const GroupedItem &it) {
 // wait does not have to be one for all stores before it.
 
 // Rows that a tile reads or writes, from its first.
+__device__ __forceinline__ int height(int left, int high) { return left < high ? left : high; }
 __device__ __forceinline__ rsrc_t rows_rsrc(const void *p, int64_t first, int rows, int64_t row_bytes) {
   const uint8_t *at = (const uint8_t *)p + first * row_bytes;
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(at), 0, (uint32_t)(rows * row_bytes),
                                            0x00027000);
 }
 
-// Columns 16 (l / 32) .. of row l % 32 of a 32 x 32 block of sums: what mma() leaves a
-// lane, four columns in eight, against its partner's at distance 32.
-__device__ __forceinline__ void columns16(float (&v)[16], const f32x16 &a) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a[e]), __float_as_uint(a[e + 8]),
-                                                    false, false);
-    v[e < 4 ? e : e + 4] = __uint_as_float(r[0]);
-    v[e < 4 ? e + 4 : e + 8] = __uint_as_float(r[1]);
-  }
-}
-
-// 16 columns of type T at byte `off`, of which `left` are in the matrix (whole pieces
-// of 16 bytes).
-template <typename T>
-__device__ __forceinline__ void store16(rsrc_t r, uint32_t off, const float (&v)[16], int left) {
-  constexpr int P = 16 / sizeof(T);
-#pragma unroll
-  for (int p = 0; p < 16 / P; ++p) {
-    u32x4 w;
-    if constexpr (sizeof(T) == 2) {
-      bf16x8 b;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) b[j] = (bf16)v[8 * p + j];
-      w = __builtin_bit_cast(u32x4, b);
-    } else {
-      w = u32x4{__float_as_uint(v[4 * p]), __float_as_uint(v[4 * p + 1]), __float_as_uint(v[4 * p + 2]),
-                __float_as_uint(v[4 * p + 3])};
-    }
-    __builtin_amdgcn_raw_buffer_store_b128(w, r, p * P < left ? off + 16 * p : kOut, 0, 0);
-  }
-}
-// Eight columns, likewise.
+// Eight columns of type T at byte `off`, of which `left` are in the matrix (whole
+// pieces of 16 bytes).
 template <typename T>
 __device__ __forceinline__ void store_piece(rsrc_t r, uint32_t off, const float (&v)[8], int left) {
   if constexpr (sizeof(T) == 2) {
@@ -195,22 +165,22 @@ __device__ __forceinline__ void fetch_piece(Raw8<T> &a, rsrc_t r, uint32_t off, 
   }
 }
 
-// Rows of sums, rounded: y and dx; the weight gradients.  Straight from the
-// accumulators, 16 columns of a row a lane: a quarter fewer instructions than through
-// LDS, though a store's 64 lanes then lie on 32 rows.
+// Rows of sums, rounded: y and dx; the weight gradients.
 template <typename T>
 struct SumsOut {
-  static constexpr bool direct = true;
+  static constexpr bool sums = true;
   struct Tile {
     rsrc_t y;
   };
   T *y, *y_up;                 // y_up: of the second matrix
-  int N;
-  __device__ __forceinline__ Tile begin(int64_t first, int rows, int half) const {
-    return Tile{rows_rsrc(half ? y_up : y, first, rows, (int64_t)N * sizeof(T))};
+  int N, M;                    // M > 0: rows of every expert's matrix
+  __device__ __forceinline__ Tile begin(const GroupedItem &it, int high) const {
+    const int64_t first = (M ? (int64_t)it.e * M : it.lo) + it.m0;
+    return Tile{rows_rsrc(it.half ? y_up : y, first, height((M ? M : it.n) - it.m0, high),
+                          (int64_t)N * sizeof(T))};
   }
-  __device__ __forceinline__ void put(const Tile &t, int m, int n, const float (&v)[16]) const {
-    store16<T>(t.y, ((uint32_t)m * N + n) * sizeof(T), v, N - n);
+  __device__ __forceinline__ void put(const Tile &t, int m, int n, const u32x4 &piece) const {
+    __builtin_amdgcn_raw_buffer_store_b128(piece, t.y, n < N ? ((uint32_t)m * N + n) * sizeof(T) : kOut, 0, 0);
   }
 };
 
@@ -261,7 +231,7 @@ __device__ __forceinline__ Clamped clamped(float z, float u, float top) {
 // h, and z and u as they are saved.
 template <typename T, int KIND>
 struct UpOut {
-  static constexpr bool direct = false;
+  static constexpr bool sums = false;
   struct Ahead {};
   struct Tile {
     rsrc_t h;
@@ -271,7 +241,9 @@ struct UpOut {
   moe_experts_saved s;
   int N;
   float limit;
-  __device__ __forceinline__ Tile begin(int64_t first, int rows, int) const {
+  __device__ __forceinline__ Tile begin(const GroupedItem &it, int high) const {
+    const int64_t first = (int64_t)it.lo + it.m0;
+    const int rows = height(it.n - it.m0, high);
     return Tile{rows_rsrc(h, first, rows, (int64_t)N * sizeof(T)), SavedTile<T>(s, first, rows, N)};
   }
   __device__ __forceinline__ void fetch(const Tile &, Ahead &, int, int) const {}
@@ -304,7 +276,7 @@ struct UpOut {
 // dz, du and h from dh and the saved z and u.
 template <typename T, int KIND>
 struct SlopeOut {
-  static constexpr bool direct = false, MX = KIND == MOE_SAVE_MXFP8;
+  static constexpr bool sums = false, MX = KIND == MOE_SAVE_MXFP8;
   struct Ahead {
     Raw8<T> z, u;              // MXFP8: the codes in the first two words
     uint32_t zs, us;           // and the scales
@@ -317,8 +289,9 @@ struct SlopeOut {
   moe_experts_saved s;
   int N;
   float limit;
-  __device__ __forceinline__ Tile begin(int64_t first, int rows, int) const {
-    const int64_t b = (int64_t)N * sizeof(T);
+  __device__ __forceinline__ Tile begin(const GroupedItem &it, int high) const {
+    const int64_t b = (int64_t)N * sizeof(T), first = (int64_t)it.lo + it.m0;
+    const int rows = height(it.n - it.m0, high);
     return Tile{rows_rsrc(dz, first, rows, b), rows_rsrc(du, first, rows, b), rows_rsrc(h, first, rows, b),
                 SavedTile<T>(s, first, rows, N)};
   }
@@ -364,157 +337,418 @@ struct SlopeOut {
 };
 
 // ---------------------------------------------------------------------------
-// A launch's tiles: up to 64 HIGH rows, by the body of their height, 64 NI columns,
-// a ring of NS slots.
-template <int H, int N, int S>
+// A launch's tiles: up to 64 HIGH rows, by the body of their height, 64 NI columns.
+template <int H, int N>
 struct Shape {
-  static constexpr int HIGH = H, NI = N, NS = S;
-  static constexpr int PER_CU = 160 * 1024 / (S * kSlot<H, N>);  // workgroups by LDS
+  static constexpr int HIGH = H, NI = N;
+  static constexpr int SLOT = (64 * H + 64 * N) * 64;            // bytes of a stage
+  static constexpr int PER_CU = 160 * 1024 / (4 * SLOT);         // workgroups by LDS
 };
 constexpr int kCus = 256;
 
-template <typename T, int MI, class SH, bool AC, bool BC, bool DUAL, class OUT>
-__device__ __forceinline__ void tile(const GemmOp &g, const GroupedItem &it, int64_t first, int half,
-                                     const OUT &out, uint8_t *L0, uint8_t *L1, uint8_t *L2, uint8_t *L3) {
-  constexpr int NI = SH::NI, NJ = DUAL ? NI / 2 : NI;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave >> 1, wn = wave & 1;
-  const int n0 = it.nt * (64 * NJ);
-  f32x16 acc[MI][NI];
-  gemm_sums<T, MI, NI, AC, BC, DUAL, SH::NS>(g, it.m0, n0, 0, 0, L0, L1, L2, L3, acc);
-  // every wave is done with the ring, and the copies past the end have landed
-  __builtin_amdgcn_s_waitcnt(0);
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_sched_barrier(0);
-  const int left = (int)(g.M - it.m0), rows = left < 64 * MI ? left : 64 * MI;
-  const auto t = out.begin(first + it.m0, rows, half);
-  if constexpr (OUT::direct) {
+// The two operands' copies into the ring: four slots of a stage each, one LDS object
+// a slot, B's units first, so that a stage's place and the number of its copies do not
+// depend on the height of the tile it belongs to, and the first stages of a tile can
+// be asked for while the one before is being stored.
+template <typename T, class SH, bool AC, bool BC, bool DUAL>
+struct Feed {
+  static constexpr int ES = sizeof(T), KB = 64 / ES, HIGH = SH::HIGH, NI = SH::NI;
+  static constexpr bool SEGS = !AC && BC;      // two contraction segments (dx)
+  static constexpr int AT = 4 * NI * 1024;     // A in a slot
+  using OA = Operand<T, AC, 64 * HIGH>;
+  using OB = Operand<T, BC, 64 * NI>;
+  uint8_t *ring[4];
+  int lane, wave, ka;
+  uint32_t off_a[HIGH], off_b[NI];
+  Cursor ca, cb, cu, ca1, cb1;
+  int rest, rest_b, rest1, to_switch, to_switch_b, to_end, to_end_b, nst;
+
+  __device__ __forceinline__ Feed(const GemmOp &g, uint8_t *L0, uint8_t *L1, uint8_t *L2, uint8_t *L3)
+      : ring{L0, L1, L2, L3}, lane(threadIdx.x & 63),
+        wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) {
+    ka = OA::first_k(wave, lane);
+#pragma unroll
+    for (int q = 0; q < HIGH; ++q) off_a[q] = OA::source(wave + 4 * q, lane, g.a[0].ld);
+#pragma unroll
+    for (int q = 0; q < NI; ++q) {
+      int u = wave + 4 * q;
+      if (DUAL && u >= 2 * NI) u -= 2 * NI;
+      off_b[q] = OB::source(u, lane, g.b[0].ld);
+    }
+  }
+  // To the first stage of a tile's contraction.
+  __device__ __forceinline__ void aim(const GemmOp &g, int m0, int n0) {
+    const int st0 = (int)((g.kdim[0] + KB - 1) / KB);
+    nst = SEGS && g.segments > 1 ? st0 + (int)((g.kdim[1] + KB - 1) / KB) : st0;
+    ca = cursor<T, AC>(g.a[0], m0, 0);
+    cb = cursor<T, BC>(g.b[0], n0, 0);
+    cu = DUAL ? cursor<T, BC>(g.b_up, n0, 0) : cb;
+    ca1 = SEGS ? cursor<T, AC>(g.a[1], m0, 0) : ca;
+    cb1 = SEGS ? cursor<T, BC>(g.b[1], n0, 0) : cb;
+    to_switch = to_switch_b = SEGS && g.segments > 1 ? st0 : -1;
+    rest = rest_b = (int)g.kdim[0];
+    rest1 = (int)g.kdim[1];
+    to_end = to_end_b = nst;
+  }
+  template <int VA>
+  __device__ __forceinline__ void copy_a(int slot) {
+    const rsrc_t r = cursor_rsrc(ca);
+    const uint32_t tail = (!AC && ka >= rest) || to_end <= 0 ? kOut : 0u;
+#pragma unroll
+    for (int q = 0; q < VA; ++q) copy16(r, ring[slot] + AT + (wave + 4 * q) * 1024, off_a[q] | tail);
+    ca.p += ca.step; ca.left -= ca.step; rest -= KB; --to_end;
+    if constexpr (SEGS) {
+      const bool sw = --to_switch == 0;
+      ca.p = sw ? ca1.p : ca.p; ca.left = sw ? ca1.left : ca.left; rest = sw ? rest1 : rest;
+    }
+  }
+  __device__ __forceinline__ void copy_b(int slot) {
+    const uint32_t tail = (!BC && ka >= rest_b) || to_end_b <= 0 ? kOut : 0u;
+#pragma unroll
+    for (int q = 0; q < NI; ++q) {
+      const int u = wave + 4 * q;
+      // units of the second half hold W_up's rows
+      const bool up = DUAL && (NI >= 2 ? q >= NI / 2 : u >= 2 * NI);
+      copy16(cursor_rsrc(up ? cu : cb), ring[slot] + u * 1024, off_b[q] | tail);
+    }
+    cb.p += cb.step; cb.left -= cb.step; rest_b -= KB; --to_end_b;
+    if constexpr (DUAL) { cu.p += cb.step; cu.left -= cb.step; }
+    if constexpr (SEGS) {
+      const bool sw = --to_switch_b == 0;
+      cb.p = sw ? cb1.p : cb.p; cb.left = sw ? cb1.left : cb.left; rest_b = sw ? rest1 : rest_b;
+    }
+  }
+  template <int FIRST, int LAST>
+  __device__ __forceinline__ void start() {
+#pragma unroll
+    for (int p = FIRST; p < LAST; ++p) { copy_a<HIGH>(p); copy_b(p); }
+  }
+};
+
+constexpr int wait_for(int younger) { return MOE_VMCNT(younger < 63 ? younger : 63); }
+
+// The sums of a tile of MI x 64 rows whose first PRE stages are asked for.  STORES
+// stores, those of the tile before, stand between these copies and the next.  vmcnt
+// counts in order, so what a stage waits for leaves them out until a stage is needed
+// that was asked for after them.  The steps of a stage, and their order: linear.hip.
+// Each stage has one way in, from the stage before, so that the compiler can tell which
+// copies are under way; where a stage might be skipped it waits for all of them.
+template <int MI, int PRE, int STORES, typename T, class SH, bool AC, bool BC, bool DUAL>
+__device__ __forceinline__ void sums(Feed<T, SH, AC, BC, DUAL> &f, f32x16 (&acc)[MI][SH::NI]) {
+  using F = Feed<T, SH, AC, BC, DUAL>;
+  constexpr int NI = SH::NI, ES = sizeof(T);
+  // by columns the whole width is copied, whose stride in LDS is one for all heights
+  constexpr int VA = AC ? SH::HIGH : MI, VM = VA + NI, VM0 = SH::HIGH + NI;
+  const int lane = f.lane, wm = f.wave >> 1, wn = f.wave & 1;
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NI; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+  // swiglu: the first half of a wave's column blocks are gate columns, the rest the up
+  // columns that go with them
+  auto col_block = [&](int j) {
+    return DUAL ? (j < NI / 2 ? wn * (NI / 2) + j : NI + wn * (NI / 2) + j - NI / 2) : wn * NI + j;
+  };
+  u32x4 fa[2][MI], fb[2][NI];
+  auto read = [&](int buf, int slot, int s) {
+#pragma unroll
+    for (int j = 0; j < NI; ++j) fb[buf][j] = F::OB::fragment(f.ring[slot], 0, col_block(j) * 32, s, lane);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) fa[buf][i] = F::OA::fragment(f.ring[slot], F::AT, (wm * MI + i) * 32, s, lane);
+  };
+  auto multiply = [&](int buf) {
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int j = 0; j < NI; ++j) {
-        float v[16];
-        f32x16 a = acc[i][j];
-        asm volatile("" : "+v"(a));            // a block's exchange after the one before's stores
-        columns16(v, a);
-        out.put(t, (wm * MI + i) * 32 + (lane & 31), n0 + (wn * NI + j) * 32 + 16 * (lane >> 5), v);
-      }
-  } else {
-    // 32 rows of the wave's quarter at a time through the wave's own part of LDS, then
-    // a piece of eight columns a lane.  The pieces' loop stays one: unrolled, the code
-    // of these endings would not stay in the instruction cache.  What the next piece
-    // reads is asked for before this one's stores.
-    constexpr int PC = NJ * 4;                 // pieces of a row
-    constexpr int PPI = 32 * PC / 64;          // pieces of a lane in 32 rows
-    constexpr int LD = NI * 32 + 4;            // floats of an LDS row (padded)
-    static_assert(32 * LD * 4 * (SH::NS > 3 ? 1 : 2) <= kSlot<SH::HIGH, NI>, "they fit");
-    float *stage = (float *)(wave == 0 ? L0 : wave == 1 ? L1 : wave == 2 ? L2
-                             : SH::NS > 3 ? L3 : L0 + 32 * LD * 4);
-    const int r0 = lane / PC, c0 = (lane % PC) * 8;      // PC divides 64
-    const int m0 = wm * MI * 32 + r0, n = n0 + wn * NJ * 32 + c0;
-    constexpr int STEP = 64 / PC;              // rows from a lane's piece to its next
-    typename OUT::Ahead next, now;
-    out.fetch(t, next, m0, n);
-#pragma unroll 1
-    for (int ci = 0; ci < MI; ++ci) {
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-        if (i == ci) {                         // uniform; the accumulators keep their registers
-#pragma unroll
-          for (int j = 0; j < NI; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              *(f32x4 *)(stage + (lane & 31) * LD + j * 32 + 8 * e + 4 * (lane >> 5)) =
-                  f32x4{acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2],
-                        acc[i][j][4 * e + 3]};
-        }
-      __builtin_amdgcn_wave_barrier();
-#pragma unroll 1
-      for (int q = 0; q < PPI; ++q) {
-        const int m = m0 + ci * 32 + q * STEP;
-        now = next;
-        // the piece after: rows follow one another across the 32 of a pass
-        out.fetch(t, next, m + STEP, n);
-        float v[8], u[8];
-        const float *from = stage + (r0 + q * STEP) * LD + c0;
-        load8<float>(v, from, 8, true);
-        if constexpr (DUAL) load8<float>(u, from + NJ * 32, 8, true);
-        out.put(t, now, m, n, v, u);
-      }
-      __builtin_amdgcn_wave_barrier();
-    }
-    // the stage is part of the ring
-    __builtin_amdgcn_s_waitcnt(MOE_VMCNT(63) & ~(15 << 8));
+      for (int j = 0; j < NI; ++j) mma<T>(acc[i][j], fa[buf][i], fb[buf][j]);
+  };
+  constexpr int kMma = MI * NI * (ES == 2 ? 1 : 4);
+  constexpr int kReadsA = MI * (!AC ? 1 : ES == 2 ? 2 : 4);
+  constexpr int kReadsB = NI * (!BC ? 1 : ES == 2 ? 2 : 4);
+
+  f.template start<PRE, 3>();
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt(wait_for(2 * VM0 + STORES));
+  __builtin_amdgcn_s_barrier();
+  read(0, 0, 0);
+  auto stage = [&](int p, auto early) {
+    __builtin_amdgcn_sched_barrier(0);
+    read(1, p, 1);
+    f.template copy_a<VA>((p + 3) % 4);
+    multiply(0);
+    interleave<0, kMma, kReadsA + kReadsB, VA>();
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(wait_for(VM + VA + (early ? STORES : 0)) & ~(15 << 8));   // and lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
+    read(0, (p + 1) % 4, 0);
+    f.copy_b((p + 3) % 4);
+    multiply(1);
+    interleave<0, kMma, kReadsA + kReadsB, NI>();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  constexpr std::false_type later{};
+  constexpr std::bool_constant<(STORES > 0)> early{};
+  int left = f.nst;
+  if (STORES > 0 && left >= 4) {
+    stage(0, early);
+    stage(1, early);
+    stage(2, later);
+    stage(3, later);
+    left -= 4;
   }
+  for (; left >= 4; left -= 4) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p) stage(p, later);
+  }
+  if (left > 0) {
+    stage(0, later);
+    if (left > 1) {
+      stage(1, later);
+      if (left > 2) stage(2, later);
+    }
+  }
+  // the copies past the end have landed, and every wave is done with the ring
+  __builtin_amdgcn_s_waitcnt(0);
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
 }
 
-template <typename T, class SH, bool AC, bool BC, bool DUAL, class OUT>
-__device__ __forceinline__ void tile_of_height(const GemmOp &g, const GroupedItem &it, int64_t first,
-                                               int half, const OUT &out, uint8_t *L0, uint8_t *L1,
-                                               uint8_t *L2, uint8_t *L3) {
-#define MOE_BODY(MI)                                                                             \
-  if constexpr (MI <= SH::HIGH) {                                                                \
-    if (it.blocks == MI)                                                                         \
-      tile<T, MI, SH, AC, BC, DUAL>(g, it, first, half, out, L0, L1, L2, L3);                    \
+// A workgroup's tiles, one after another: next(it) finds its next one.
+template <typename T, class SH, bool AC, bool BC, bool DUAL, class OUT, class NEXT, class AIM>
+__device__ __forceinline__ void walk(const GemmOp &g, const OUT &out, NEXT next, AIM aim) {
+  __shared__ __attribute__((aligned(1024))) uint8_t L0[SH::SLOT];
+  __shared__ __attribute__((aligned(1024))) uint8_t L1[SH::SLOT];
+  __shared__ __attribute__((aligned(1024))) uint8_t L2[SH::SLOT];
+  __shared__ __attribute__((aligned(1024))) uint8_t L3[SH::SLOT];
+  constexpr int NI = SH::NI, NJ = DUAL ? NI / 2 : NI, HIGH = SH::HIGH;
+  // The end of a tile goes through LDS, so that a store's lanes write whole lines
+  // (straight from the accumulators, 32 bytes a row and store, 16384 rows of 64 experts
+  // took 271 us for dW of 2048 -> 2 x 1024, %%% through LDS: the L2 takes a request a
+  // piece).  Of the largest tiles through memory of its own beside the ring, so that
+  // the next one's first stages can be asked for before; of others the ring itself,
+  // where that would cost a CU a workgroup.
+  constexpr int PASS = NI >= 2 ? 2 : 1;        // blocks of a wave there at a time
+  constexpr int BYTES = PASS * 1024 * (OUT::sums ? (int)sizeof(T) : 4);
+  constexpr bool OWN = SH::PER_CU == 1;
+  constexpr int PRE = OWN ? 3 : 0;
+  __shared__ __attribute__((aligned(1024))) uint8_t ends[OWN ? 4 * BYTES : 16];
+  // Stores of a tile's end where they stand after copies, the same for every height and
+  // before the first tile.
+  constexpr int STORES = OWN && OUT::sums ? HIGH * NI * (int)sizeof(T) : 0;
+  auto no_stores = [](int n) {
+    const rsrc_t none = __builtin_amdgcn_make_buffer_rsrc(nullptr, 0, 0, 0x00027000);
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      __builtin_amdgcn_raw_buffer_store_b128(u32x4{0, 0, 0, 0}, none, kOut, 0, 0);
+      asm volatile("" ::: "memory");           // each one its own: they are counted
+    }
+  };
+  GroupedItem it, nx;
+  if (!next(&it)) return;
+  Feed<T, SH, AC, BC, DUAL> f(g, L0, L1, L2, L3);
+  const int lane = f.lane, wave = f.wave, wm = wave >> 1, wn = wave & 1;
+  aim(f, it, it.nt * 64 * NJ);
+  f.template start<0, PRE>();
+  __builtin_amdgcn_sched_barrier(0);
+  no_stores(STORES);
+  __builtin_amdgcn_sched_barrier(0);
+  auto body = [&](auto height) {
+    constexpr int MI = decltype(height)::value;
+    f32x16 acc[MI][NI];
+    sums<MI, PRE, STORES>(f, acc);
+    const bool more = next(&nx);
+    const int n0 = it.nt * 64 * NJ;
+    // The next tile's first stages; without one copies that read nothing, so that their
+    // number is known where a load's wait counts them.
+    auto ask = [&]() {
+      if (more) aim(f, nx, nx.nt * 64 * NJ);
+      else f.to_end = f.to_end_b = 0;
+      f.template start<0, PRE>();
+    };
+    const auto t = out.begin(it, MI * 64);
+    constexpr bool TWO = 2 * BYTES <= SH::SLOT;        // waves to a slot
+    static_assert(BYTES <= SH::SLOT, "they fit");
+    uint8_t *stage = OWN ? ends + wave * BYTES
+                     : TWO ? (wave < 2 ? L0 : L1) + (wave & 1) * BYTES
+                           : (wave == 0 ? L0 : wave == 1 ? L1 : wave == 2 ? L2 : L3);
+    // 16-byte chunk c of row r lies at chunk c ^ (r % 8) (of four to a row, r % 4): a
+    // column of chunks, which lanes write together, and a row of them, which they read,
+    // take all banks
+    constexpr int CHUNKS = BYTES / 32 / 16, SWAP = CHUNKS < 8 ? CHUNKS - 1 : 7;
+    auto chunk = [&](int r, int c) { return stage + r * (BYTES / 32) + ((c ^ (r & SWAP)) << 4); };
+    if constexpr (OUT::sums) {
+      constexpr int PC = CHUNKS;               // pieces of a row
+      constexpr int ROWS = 64 / PC;            // rows that the wave takes at once
+      if (OWN) ask();
+      __builtin_amdgcn_sched_barrier(0);       // sums() counts these copies before the stores
+      const int r0 = lane / PC, pc = lane % PC;
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NI; j += PASS) {
+#pragma unroll
+          for (int k = 0; k < PASS; ++k) {
+            f32x16 a = acc[i][j + k];
+            asm volatile("" : "+v"(a));        // rounded here, not all blocks ahead
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if constexpr (sizeof(T) == 2) {
+                typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+                *(bf16x4 *)(chunk(lane & 31, 4 * k + e) + 8 * (lane >> 5)) =
+                    bf16x4{(bf16)a[4 * e], (bf16)a[4 * e + 1], (bf16)a[4 * e + 2], (bf16)a[4 * e + 3]};
+              } else {
+                *(f32x4 *)chunk(lane & 31, 8 * k + 2 * e + (lane >> 5)) =
+                    f32x4{a[4 * e], a[4 * e + 1], a[4 * e + 2], a[4 * e + 3]};
+              }
+            }
+          }
+          __builtin_amdgcn_wave_barrier();
+#pragma unroll
+          for (int q = 0; q < 32 / ROWS; ++q)
+            out.put(t, (wm * MI + i) * 32 + r0 + q * ROWS,
+                    n0 + (wn * NI + j) * 32 + pc * (16 / (int)sizeof(T)),
+                    *(const u32x4 *)chunk(r0 + q * ROWS, pc));
+          __builtin_amdgcn_wave_barrier();
+          __builtin_amdgcn_sched_barrier(0);   // a pass's registers at a time
+        }
+      if (STORES > 0) no_stores((HIGH - MI) * NI * (int)sizeof(T));
+    } else {
+      // PASS blocks at a time (swiglu: one of the gate and the up one that goes with it)
+      // through the wave's part of LDS, then a piece of eight columns a lane.  The
+      // blocks' and the pieces' loops stay loops: unrolled, the code of these endings
+      // would not stay in the instruction cache.  What the next piece reads is asked for
+      // before this one's stores.
+      constexpr int COLS = DUAL ? 1 : PASS;    // blocks of output columns a pass
+      constexpr int PC = COLS * 4;             // pieces of a row
+      constexpr int PPL = 32 * PC / 64;        // pieces of a lane and pass
+      constexpr int ROWS = 64 / PC;            // rows that the wave takes at once
+      constexpr int PER_ROW = NJ / COLS;       // passes in 32 rows
+      static_assert(NJ % COLS == 0, "passes divide the columns");
+      const int r0 = lane / PC, pc = lane % PC;
+      const int m0 = wm * MI * 32 + r0, c0 = n0 + wn * NJ * 32 + pc * 8;
+      typename OUT::Ahead ahead, now;
+      out.fetch(t, ahead, m0, c0);
+      if (OWN) ask();
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll 1
+      for (int b = 0; b < MI * PER_ROW; ++b) {
+#pragma unroll
+        for (int k = 0; k < MI * PER_ROW; ++k)
+          if (k == b) {                        // uniform; the accumulators keep their registers
+#pragma unroll
+            for (int j = 0; j < PASS; ++j) {
+              const f32x16 &a = acc[k / PER_ROW][DUAL ? k % PER_ROW + j * NJ : k % PER_ROW * PASS + j];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                *(f32x4 *)chunk(lane & 31, j * 8 + 2 * e + (lane >> 5)) =
+                    f32x4{a[4 * e], a[4 * e + 1], a[4 * e + 2], a[4 * e + 3]};
+            }
+          }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+        for (int q = 0; q < PPL; ++q) {
+          auto at = [&](int pass, int piece, int *m, int *n) {
+            *m = m0 + pass / PER_ROW * 32 + piece * ROWS;
+            *n = c0 + pass % PER_ROW * COLS * 32;
+          };
+          int m, n, m1, n1;
+          at(b, q, &m, &n);
+          at(q + 1 < PPL ? b : b + 1, q + 1 < PPL ? q + 1 : 0, &m1, &n1);
+          now = ahead;
+          out.fetch(t, ahead, m1, n1);         // past the last: rows that are not there
+          const int r = r0 + q * ROWS;
+          float v[8], u[8];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const f32x4 x = *(const f32x4 *)chunk(r, 2 * pc + h);
+            f32x4 y = x;
+            if constexpr (DUAL) y = *(const f32x4 *)chunk(r, 8 + 2 * pc + h);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) { v[4 * h + j] = x[j]; u[4 * h + j] = y[j]; }
+          }
+          out.put(t, now, m, n, v, u);
+        }
+        __builtin_amdgcn_wave_barrier();
+      }
+    }
+    if constexpr (!OWN) {
+      // this part of the ring is the next tile's again
+      __builtin_amdgcn_s_waitcnt(MOE_VMCNT(63) & ~(15 << 8));
+      __builtin_amdgcn_s_barrier();
+      ask();
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    it = nx;
+    return more;
+  };
+  for (;;) {
+    bool more = false;
+    if (it.blocks == 1) more = body(std::integral_constant<int, 1>{});
+    if constexpr (HIGH >= 2) {
+      if (it.blocks == 2) more = body(std::integral_constant<int, 2>{});
+    }
+    if constexpr (HIGH >= 4) {
+      if (it.blocks == 3) more = body(std::integral_constant<int, 3>{});
+      if (it.blocks == 4) more = body(std::integral_constant<int, 4>{});
+    }
+    if (!more) break;
   }
-  MOE_BODY(4)
-  MOE_BODY(3)
-  MOE_BODY(2)
-  MOE_BODY(1)
-#undef MOE_BODY
+  __builtin_amdgcn_s_waitcnt(0);               // no copy into LDS outlives the workgroup
 }
 
-#define MOE_RING(SH)                                                                    \
-  constexpr int SLOT = kSlot<SH::HIGH, SH::NI>;                                         \
-  __shared__ __attribute__((aligned(1024))) uint8_t L0[SLOT];                           \
-  __shared__ __attribute__((aligned(1024))) uint8_t L1[SLOT];                           \
-  __shared__ __attribute__((aligned(1024))) uint8_t L2[SLOT];                           \
-  __shared__ __attribute__((aligned(1024))) uint8_t L3[SH::NS > 3 ? SLOT : 16];
-
-// Products over rows: a workgroup a tile.  Items go expert by expert, a column tile's
-// row tiles together, and each XCD takes a contiguous run of them: the rows of an
-// expert and the weights of a column tile are then read through one L2.
+// Products over rows.  Items go expert by expert, a column tile's row tiles together;
+// each XCD takes a contiguous run of them and its workgroups go through it side by
+// side: the rows of an expert and the weights of a column tile are then read through
+// one L2.  (Contiguous shares for the workgroups, all of one size, spread an XCD over
+// eight experts at a time: 16384 rows of 64 experts, 2048 -> 2 x 1024, 267 us where
+// this order took 217.)
 template <typename T, class SH, bool BC, bool DUAL, class OUT>
 __device__ __forceinline__ void rows_product(const GroupedOp &q, const OUT &out) {
-  MOE_RING(SH)
   const auto line = line_of<int>(q.E, [&](int e) { return tiles_of<SH::HIGH>(span_of(q, e).n); });
   const int nt = q.g.n_tiles, items = line.total() * nt, per = (items + 7) / 8;
   const int run = (int)(blockIdx.x & 7) * per, mine = items - run < per ? items - run : per;
   // Tiles of a last round that leave half of the XCD's places free are cut lower, into
-  // `cut` parts each (8192 rows of 48 experts, 5120 -> 1536, dh: 324 tiles on 256 CUs
-  // 283 us, cut %%% us).
-  constexpr int PLACES = kCus / 8 * SH::PER_CU;
-  const int last = mine % PLACES, whole = mine - last;
-  const int cut = last * 4 <= PLACES && SH::HIGH >= 4 ? 4 : last * 2 <= PLACES && SH::HIGH >= 2 ? 2 : 1;
-  const int slot = (int)(blockIdx.x >> 3), behind = slot - whole;
-  if (behind >= last * cut) return;
-  const int item = run + (behind < 0 ? slot : whole + behind / cut);
-  GroupedItem it;
-  int start;
-  it.e = line.at(item / nt, &start);
-  const Span s = span_of(q, it.e);
-  it.lo = __builtin_amdgcn_readfirstlane(s.lo);
-  it.n = __builtin_amdgcn_readfirstlane(s.n);
-  const int high = tiles_of<SH::HIGH>(it.n), local = item - start * nt;
-  it.nt = local / high;
-  height_of((it.n + 63) / 64, high, local - it.nt * high, &it);
-  if (behind >= 0 && cut > 1) {
-    const int m0 = it.m0;
-    height_of(it.blocks, cut, behind % cut, &it);
-    it.m0 += m0;
-    if (it.blocks == 0) return;
-  }
-  GemmOp g = q.g;
-  move<T>(g.a[0], it);
-  move<T>(g.a[1], it);
-  g.b[0].p = (const uint8_t *)g.b[0].p + it.e * q.b_expert;
-  g.b[1].p = (const uint8_t *)g.b[1].p + it.e * q.b_expert;
-  g.b_up.p = (const uint8_t *)g.b_up.p + it.e * q.b_expert;
-  g.M = it.n;
-  tile_of_height<T, SH, false, BC, DUAL>(g, it, it.lo, 0, out, L0, L1, L2, L3);
+  // `cut` parts each (8192 rows of 64 experts, 2048 -> 1024, dh: 117 us, cut 92).
+  const int places = (int)(gridDim.x >> 3);
+  const int last = mine > 0 ? mine % places : 0, whole = mine - last;
+  const int cut = SH::HIGH >= 4 && last * 4 <= places ? 4 : SH::HIGH >= 2 && last * 2 <= places ? 2 : 1;
+  int slot = (int)(blockIdx.x >> 3) - places;
+  auto next = [&](GroupedItem *it) {
+    for (;;) {
+      slot += places;
+      const int behind = slot - whole;
+      if (behind >= last * cut) return false;
+      const int item = run + (behind < 0 ? slot : whole + behind / cut);
+      int start;
+      it->e = line.at(item / nt, &start);
+      const Span s = span_of(q, it->e);
+      it->lo = __builtin_amdgcn_readfirstlane(s.lo);
+      it->n = __builtin_amdgcn_readfirstlane(s.n);
+      const int high = tiles_of<SH::HIGH>(it->n), local = item - start * nt;
+      it->nt = local / high;
+      it->half = 0;
+      height_of((it->n + 63) / 64, high, local - it->nt * high, it);
+      if (behind >= 0 && cut > 1) {
+        const int m0 = it->m0;
+        height_of(it->blocks, cut, behind % cut, it);
+        it->m0 += m0;
+        if (it->blocks == 0) continue;
+      }
+      return true;
+    }
+  };
+  walk<T, SH, false, BC, DUAL>(q.g, out, next, [&](auto &f, const GroupedItem &it, int n0) {
+    GemmOp g = q.g;
+    move<T>(g.a[0], it);
+    move<T>(g.a[1], it);
+    g.b[0].p = (const uint8_t *)g.b[0].p + it.e * q.b_expert;
+    g.b[1].p = (const uint8_t *)g.b[1].p + it.e * q.b_expert;
+    g.b_up.p = (const uint8_t *)g.b_up.p + it.e * q.b_expert;
+    f.aim(g, it.m0, n0);
+  });
 }
 
 template <typename T, class SH, int KIND>
@@ -541,7 +775,6 @@ __global__ __launch_bounds__(256, SH::PER_CU) void dx_kernel(const GroupedOp q, 
 constexpr int kTileStages = 8;
 template <typename T, class SH>
 __global__ __launch_bounds__(256, SH::PER_CU) void dw_kernel(const GroupedOp q, const SumsOut<T> o) {
-  MOE_RING(SH)
   constexpr int KB = 64 / sizeof(T);
   const int tiles = (int)q.g.m_tiles * q.g.n_tiles, per_half = (int)q.g.m_tiles / q.g.halves;
   auto cost = [&](int e) { return (span_of(q, e).n + KB - 1) / KB + kTileStages; };
@@ -552,27 +785,32 @@ __global__ __launch_bounds__(256, SH::PER_CU) void dw_kernel(const GroupedOp q, 
     const int e = line.at(pos, &start);
     return e * tiles + (int)((pos - start) / __builtin_amdgcn_readfirstlane(cost(e)));
   };
-  const int xcd = (int)(blockIdx.x & 7);
+  const int xcd = (int)(blockIdx.x & 7), places = (int)(gridDim.x >> 3);
   const int last = xcd == 7 ? tiles * q.E : first_of(xcd + 1);
-  for (int item = first_of(xcd) + (int)(blockIdx.x >> 3); item < last; item += (int)(gridDim.x >> 3)) {
-    GroupedItem it;
-    it.e = item / tiles;
-    const int local = item - it.e * tiles;
+  int item = first_of(xcd) + (int)(blockIdx.x >> 3) - places;
+  auto next = [&](GroupedItem *it) {
+    item += places;
+    if (item >= last) return false;
+    it->e = item / tiles;
+    const int local = item - it->e * tiles;
     int mt = local / q.g.n_tiles;
-    it.nt = local - mt * q.g.n_tiles;
-    const int half = mt >= per_half ? 1 : 0;
-    mt -= half * per_half;
-    height_of((int)((q.g.M + 63) / 64), per_half, mt, &it);
-    const Span s = span_of(q, it.e);
-    it.lo = __builtin_amdgcn_readfirstlane(s.lo);
-    it.n = __builtin_amdgcn_readfirstlane(s.n);
+    it->nt = local - mt * q.g.n_tiles;
+    it->half = mt >= per_half ? 1 : 0;
+    mt -= it->half * per_half;
+    height_of((int)((q.g.M + 63) / 64), per_half, mt, it);
+    const Span s = span_of(q, it->e);
+    it->lo = __builtin_amdgcn_readfirstlane(s.lo);
+    it->n = __builtin_amdgcn_readfirstlane(s.n);
+    return true;
+  };
+  walk<T, SH, true, true, false>(q.g, o, next, [&](auto &f, const GroupedItem &it, int n0) {
     GemmOp g = q.g;
-    if (half) g.a[0] = g.a_up;
+    if (it.half) g.a[0] = g.a_up;
     move<T>(g.a[0], it);
     move<T>(g.b[0], it);
     g.kdim[0] = it.n;
-    tile_of_height<T, SH, true, true, false>(g, it, it.e * g.M, half, o, L0, L1, L2, L3);
-  }
+    f.aim(g, it.m0, n0);
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -591,22 +829,19 @@ GroupedOp grouped_op(const ExpertsArgs &a, int N) {
   return q;
 }
 
-// Workgroups that walk their items: what the GPU holds, or fewer where there is less
-// to do.
+// Workgroups: what the GPU holds, or fewer where there is less to do.
 template <class SH>
 dim3 held_grid(int64_t items) {
   const int64_t most = kCus * SH::PER_CU, n = (items + 7) / 8 * 8;
   return dim3((unsigned)(n < most ? n : most));
 }
 
-// Sets a product's column tiles; workgroups for the most row tiles that there can be.
+// Sets a product's column tiles; its workgroups.
 template <class SH>
 dim3 rows_grid(GroupedOp &q, bool dual) {
   const int to = dual ? 32 * SH::NI : 64 * SH::NI;
   q.g.n_tiles = (q.g.e.N + to - 1) / to;
-  const int64_t tiles = q.rows / (64 * SH::HIGH) + (q.rows < q.E ? q.rows : q.E);
-  const int64_t per = (tiles * q.g.n_tiles + 7) / 8, places = kCus / 8 * SH::PER_CU;
-  return dim3((unsigned)(8 * ((per + places - 1) / places * places)));
+  return held_grid<SH>(most_blocks(q.rows, q.E) * q.g.n_tiles);
 }
 
 }  // namespace
@@ -628,12 +863,12 @@ ExpertsSpace experts_space(int64_t rows, int I, int dtype, bool backward) {
 }
 
 bool experts_launchable(const ExpertsArgs &a, bool backward) {
-  // fewer than 2^32 threads a launch; the smallest tiles are the most
+  // tiles are counted in 31 bits; the smallest are the most
   const int64_t wide = a.d > a.I ? a.d : a.I, cols = (wide + 31) / 32;
   const int64_t by_rows = most_blocks(a.rows, a.E) * cols;
   const int64_t by_expert =
       backward ? 2 * (int64_t)a.E * ((a.d + 63) / 64) * ((a.I + 63) / 64) : 0;
-  return by_rows * 256 + (1 << 20) < (int64_t)1 << 32 && by_expert < INT32_MAX;
+  return by_rows < INT32_MAX && by_expert < INT32_MAX;
 }
 
 namespace {
@@ -649,11 +884,11 @@ namespace {
 template <typename T, class N, class F>
 hipError_t with_shape(N tiles, F f) {
   if constexpr (sizeof(T) == 2) {
-    if (tiles(4, 4) >= 200) return f(Shape<4, 4, 4>{});
-    if (tiles(2, 2) >= 256) return f(Shape<2, 2, 4>{});
-    if (tiles(1, 2) >= 512) return f(Shape<1, 2, 4>{});
+    if (tiles(4, 4) >= 200) return f(Shape<4, 4>{});
+    if (tiles(2, 2) >= 256) return f(Shape<2, 2>{});
+    if (tiles(1, 2) >= 512) return f(Shape<1, 2>{});
   }
-  return f(Shape<1, 1, 4>{});
+  return f(Shape<1, 1>{});
 }
 
 // Tiles of a product over rows with N columns (a swiglu one's 64 are of both
@@ -685,7 +920,7 @@ hipError_t run_up(const ExpertsArgs &a, T *h, hipStream_t s) {
   q.g.kdim[0] = a.d;
   return with_shape<T>(RowTiles(a, 2 * (int64_t)a.I), [&](auto sh) {
     // two matrices share a tile
-    using SH = std::conditional_t<decltype(sh)::NI == 1, Shape<1, 2, 4>, decltype(sh)>;
+    using SH = std::conditional_t<decltype(sh)::NI == 1, Shape<1, 2>, decltype(sh)>;
     const dim3 grid = rows_grid<SH>(q, true);
     return with_kind(a.saved.kind, [&](auto kind) {
       const UpOut<T, kind> o = {h, a.saved, a.I, a.limit};
@@ -702,7 +937,7 @@ hipError_t run_down(const ExpertsArgs &a, const T *h, hipStream_t s) {
   q.g.b[0] = {a.w_down, a.I, a.d, a.I};
   q.b_expert = (int64_t)a.I * a.d * sizeof(T);
   q.g.kdim[0] = a.I;
-  const SumsOut<T> o = {(T *)a.y, nullptr, a.d};
+  const SumsOut<T> o = {(T *)a.y, nullptr, a.d, 0};
   return with_shape<T>(RowTiles(a, a.d), [&](auto sh) {
     using SH = decltype(sh);
     const dim3 grid = rows_grid<SH>(q, false);
@@ -742,7 +977,7 @@ hipError_t run_dx(const ExpertsArgs &a, const T *dz, const T *du, hipStream_t s)
   q.b_expert = (int64_t)a.I * a.d * sizeof(T);
   q.g.kdim[0] = q.g.kdim[1] = a.I;
   q.g.segments = 2;
-  const SumsOut<T> o = {(T *)a.dx, nullptr, a.d};
+  const SumsOut<T> o = {(T *)a.dx, nullptr, a.d, 0};
   return with_shape<T>(RowTiles(a, a.d), [&](auto sh) {
     using SH = decltype(sh);
     const dim3 grid = rows_grid<SH>(q, false);
@@ -761,7 +996,7 @@ hipError_t run_dw(const ExpertsArgs &a, const void *A, const void *A_up, int N, 
   q.g.b[0] = {B, K, a.rows, K};
   q.g.M = N;
   q.g.halves = A_up ? 2 : 1;
-  const SumsOut<T> o = {(T *)dw, (T *)dw_up, K};
+  const SumsOut<T> o = {(T *)dw, (T *)dw_up, K, N};
   auto tiles = [&](int high, int wide) {
     return q.g.halves * (int64_t)a.E * ((N + 64 * high - 1) / (64 * high)) * ((K + 64 * wide - 1) / (64 * wide));
   };

@@ -37,12 +37,23 @@ __device__ __forceinline__ bool gemm_item(const GemmOp &g, int64_t *mt, int *nt,
 
 template <typename T, int MI, int NI, bool AC, bool BC, bool DUAL>
 __device__ __forceinline__ void gemm_tile(const GemmOp &g) {
-  constexpr int ES = sizeof(T), NS = 4;
-  constexpr int TM = 64 * MI, TN = 64 * NI, SLOT = kSlot<MI, NI>;
+  constexpr int ES = sizeof(T), KB = 64 / ES, NS = 4;
+  constexpr int TM = 64 * MI, TN = 64 * NI;
+  constexpr int UA = TM / 16, UB = TN / 16;    // 1 KB copy units per stage
+  constexpr int VA = UA / 4, VB = UB / 4, VM = VA + VB;          // per wave
+  constexpr int SLOT = (TM + TN) * 64;
+  constexpr bool SEGS = !AC && BC;             // two contraction segments occur (dx of swiglu)
+  static_assert(!DUAL || (!AC && !BC), "the two-matrix product is the forward one");
+  static_assert(UA % 4 == 0 && UB % 4 == 0, "units split evenly");
+  using OA = Operand<T, AC, TM>;
+  using OB = Operand<T, BC, TN>;
+  // one LDS object per slot, so that a read of one does not wait for copies
+  // into another
   __shared__ __attribute__((aligned(1024))) uint8_t L0[SLOT];
   __shared__ __attribute__((aligned(1024))) uint8_t L1[SLOT];
   __shared__ __attribute__((aligned(1024))) uint8_t L2[SLOT];
   __shared__ __attribute__((aligned(1024))) uint8_t L3[SLOT];
+  uint8_t *const ring[4] = {L0, L1, L2, L3};
   int64_t mt;
   int nt, part;
   if (!gemm_item(g, &mt, &nt, &part)) return;
@@ -57,9 +68,135 @@ __device__ __forceinline__ void gemm_tile(const GemmOp &g) {
     mt -= half * per;
   }
   const int64_t m0 = mt * TM, n0 = (int64_t)nt * TO;
-  f32x16 acc[MI][NI];
-  gemm_sums<T, MI, NI, AC, BC, DUAL, NS>(g, m0, n0, half, part, L0, L1, L2, L3, acc);
 
+  const int st_seg0 = (int)((g.kdim[0] + KB - 1) / KB);
+  const int st_all = SEGS && g.segments > 1 ? st_seg0 + (int)((g.kdim[1] + KB - 1) / KB) : st_seg0;
+  const int st_first = (int)((int64_t)st_all * part / g.parts);
+  const int nst = (int)((int64_t)st_all * (part + 1) / g.parts) - st_first;
+
+  // sources of the next stage to copy; `rest` counts contraction elements left
+  // of its segment for the row operands' ragged ends
+  const bool second = SEGS && st_first >= st_seg0;
+  const int64_t k_first = (int64_t)(second ? st_first - st_seg0 : st_first) * KB;
+  Cursor ca = cursor<T, AC>(second ? g.a[1] : half ? g.a_up : g.a[0], m0, k_first);
+  Cursor cb = cursor<T, BC>(second ? g.b[1] : g.b[0], n0, k_first);
+  Cursor cu = DUAL ? cursor<T, BC>(g.b_up, n0, k_first) : cb;
+  const Cursor ca1 = SEGS ? cursor<T, AC>(g.a[1], m0, 0) : ca;
+  const Cursor cb1 = SEGS ? cursor<T, BC>(g.b[1], n0, 0) : cb;
+  int to_switch = SEGS && g.segments > 1 && !second ? st_seg0 - st_first : -1;
+  int rest = (int)((second ? g.kdim[1] : g.kdim[0]) - k_first), rest_b = rest;
+  int to_switch_b = to_switch;
+  const int rest1 = (int)g.kdim[1];
+  int to_end = nst, to_end_b = nst;            // stages left to copy
+
+  uint32_t off_a[VA], off_b[VB];
+#pragma unroll
+  for (int q = 0; q < VA; ++q) off_a[q] = OA::source(wave + 4 * q, lane, g.a[0].ld);
+#pragma unroll
+  for (int q = 0; q < VB; ++q) {
+    int u = wave + 4 * q;
+    if (DUAL && u >= UB / 2) u -= UB / 2;
+    off_b[q] = OB::source(u, lane, g.b[0].ld);
+  }
+  const int ka = OA::first_k(wave, lane);
+  auto copy_a = [&](int slot) {
+    rsrc_t r = cursor_rsrc(ca);
+    const uint32_t tail = (!AC && ka >= rest) || to_end <= 0 ? kOut : 0u;
+#pragma unroll
+    for (int q = 0; q < VA; ++q)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (MOE_LDS void *)(ring[slot] + (wave + 4 * q) * 1024),
+                                               16, off_a[q] | tail, 0, 0, 0);
+    ca.p += ca.step; ca.left -= ca.step; rest -= KB; --to_end;
+    if constexpr (SEGS) {
+      const bool sw = --to_switch == 0;
+      ca.p = sw ? ca1.p : ca.p; ca.left = sw ? ca1.left : ca.left; rest = sw ? rest1 : rest;
+    }
+  };
+  auto copy_b = [&](int slot) {
+    const uint32_t tail = (!BC && ka >= rest_b) || to_end_b <= 0 ? kOut : 0u;
+#pragma unroll
+    for (int q = 0; q < VB; ++q) {
+      const int u = wave + 4 * q;
+      // units of the second half hold W_up's rows
+      const bool up = DUAL && (UB >= 8 ? q >= VB / 2 : u >= UB / 2);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(cursor_rsrc(up ? cu : cb), (MOE_LDS void *)(ring[slot] + (UA + u) * 1024), 16,
+                                               off_b[q] | tail, 0, 0, 0);
+    }
+    cb.p += cb.step; cb.left -= cb.step; rest_b -= KB; --to_end_b;
+    if constexpr (DUAL) { cu.p += cb.step; cu.left -= cb.step; }
+    if constexpr (SEGS) {
+      const bool sw = --to_switch_b == 0;
+      cb.p = sw ? cb1.p : cb.p; cb.left = sw ? cb1.left : cb.left; rest_b = sw ? rest1 : rest_b;
+    }
+  };
+
+  f32x16 acc[MI][NI];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NI; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+
+  // 32-column block j of the wave; swiglu: the first half of a wave's blocks are
+  // gate columns, the rest the up columns that go with them
+  auto col_block = [&](int j) {
+    return DUAL ? (j < NI / 2 ? wn * (NI / 2) + j : NI + wn * (NI / 2) + j - NI / 2) : wn * NI + j;
+  };
+  u32x4 fa[2][MI], fb[2][NI];
+  auto read = [&](int buf, int slot, int s) {
+#pragma unroll
+    for (int j = 0; j < NI; ++j) fb[buf][j] = OB::fragment(ring[slot], UA * 1024, col_block(j) * 32, s, lane);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) fa[buf][i] = OA::fragment(ring[slot], 0, (wm * MI + i) * 32, s, lane);
+  };
+  auto multiply = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NI; ++j) mma<T>(acc[i][j], fa[buf][i], fb[buf][j]);
+  };
+  // instructions of a step
+  constexpr int kMma = MI * NI * (ES == 2 ? 1 : 4);
+  constexpr int kReadsA = MI * (!AC ? 1 : ES == 2 ? 2 : 4);
+  constexpr int kReadsB = NI * (!BC ? 1 : ES == 2 ? 2 : 4);
+
+#pragma unroll
+  for (int p = 0; p < NS - 1; ++p) { copy_a(p); copy_b(p); }
+  __builtin_amdgcn_s_waitcnt(MOE_VMCNT(2 * VM));
+  __builtin_amdgcn_s_barrier();
+  read(0, 0, 0);
+  // Stage st from slot p.  The second step's fragments are read while the first
+  // step multiplies; then, with every read of this slot done and the next stage
+  // landed (younger: one stage and the A half of another), one barrier, and the
+  // next stage's first fragments are read while the second step multiplies.
+  // The slot the previous stage used (free since the previous barrier) is
+  // refilled meanwhile, A in the first step, B in the second.  Stages past the
+  // end copy nothing.
+  auto stage = [&](int p) {
+    __builtin_amdgcn_sched_barrier(0);
+    read(1, p, 1);
+    copy_a((p + NS - 1) % NS);
+    multiply(0);
+    interleave<0, kMma, kReadsA + kReadsB, VA>();
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(MOE_VMCNT(VM + VA) & ~(15 << 8));   // and lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    read(0, (p + 1) % NS, 0);
+    copy_b((p + NS - 1) % NS);
+    multiply(1);
+    interleave<0, kMma, kReadsA + kReadsB, VB>();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  int st = 0;
+  for (; st + NS <= nst; st += NS) {
+#pragma unroll
+    for (int p = 0; p < NS; ++p) stage(p);
+  }
+#pragma unroll
+  for (int p = 0; p < NS - 1; ++p)
+    if (st + p < nst) stage(p);
   // Epilogue.  32 rows of the wave's quarter at a time go through the wave's own
   // part of LDS (no barrier), so that a lane then has eight consecutive columns
   // of a row and 16 or 8 lanes a whole line.  bf16: the whole tile's residual is
