@@ -128,6 +128,15 @@ __device__ __forceinline__ void move(Matrix &m, const GroupedItem &it) {
 // or the matrix's columns at an offset that drops them (reads zeros), so that a load's
 // wait does not have to be one for all stores before it.
 
+// The nontemporal policy: of results, and of weights that one or two row tiles read, by
+// columns (whole lines at a time), so that they leave the caches to the rows that tiles
+// share.  8192 rows of 48 experts, 5120 -> 2 x 1536: all six products 2267 us, the
+// results so 2136, the weights of dh and dx too 2015.  With 1024 rows an expert the
+// weights are read by four row tiles, and dh takes 117 us, so 129.  Weights read by
+// rows come half a line a stage, and such a line is gone before its other half is
+// needed (up 215, so 234).
+constexpr int kStream = 2;
+
 // Rows that a tile reads or writes, from its first.
 __device__ __forceinline__ int height(int left, int high) { return left < high ? left : high; }
 __device__ __forceinline__ rsrc_t rows_rsrc(const void *p, int64_t first, int rows, int64_t row_bytes) {
@@ -180,7 +189,8 @@ struct SumsOut {
                           (int64_t)N * sizeof(T))};
   }
   __device__ __forceinline__ void put(const Tile &t, int m, int n, const u32x4 &piece) const {
-    __builtin_amdgcn_raw_buffer_store_b128(piece, t.y, n < N ? ((uint32_t)m * N + n) * sizeof(T) : kOut, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(piece, t.y, n < N ? ((uint32_t)m * N + n) * sizeof(T) : kOut, 0,
+                                           kStream);
   }
 };
 
@@ -337,10 +347,12 @@ struct SlopeOut {
 };
 
 // ---------------------------------------------------------------------------
-// A launch's tiles: up to 64 HIGH rows, by the body of their height, 64 NI columns.
-template <int H, int N>
+// A launch's tiles: up to 64 HIGH rows, by the body of their height, 64 NI columns;
+// whether its weights are read once (kStream).
+template <int H, int N, bool S = false>
 struct Shape {
   static constexpr int HIGH = H, NI = N;
+  static constexpr bool STREAM = S;
   static constexpr int SLOT = (64 * H + 64 * N) * 64;            // bytes of a stage
   static constexpr int PER_CU = 160 * 1024 / (4 * SLOT);         // workgroups by LDS
 };
@@ -395,7 +407,7 @@ struct Feed {
     const rsrc_t r = cursor_rsrc(ca);
     const uint32_t tail = (!AC && ka >= rest) || to_end <= 0 ? kOut : 0u;
 #pragma unroll
-    for (int q = 0; q < VA; ++q) copy16(r, ring[slot] + AT + (wave + 4 * q) * 1024, off_a[q] | tail);
+    for (int q = 0; q < VA; ++q) copy16<0>(r, ring[slot] + AT + (wave + 4 * q) * 1024, off_a[q] | tail);
     ca.p += ca.step; ca.left -= ca.step; rest -= KB; --to_end;
     if constexpr (SEGS) {
       const bool sw = --to_switch == 0;
@@ -409,7 +421,7 @@ struct Feed {
       const int u = wave + 4 * q;
       // units of the second half hold W_up's rows
       const bool up = DUAL && (NI >= 2 ? q >= NI / 2 : u >= 2 * NI);
-      copy16(cursor_rsrc(up ? cu : cb), ring[slot] + u * 1024, off_b[q] | tail);
+      copy16<SH::STREAM ? kStream : 0>(cursor_rsrc(up ? cu : cb), ring[slot] + u * 1024, off_b[q] | tail);
     }
     cb.p += cb.step; cb.left -= cb.step; rest_b -= KB; --to_end_b;
     if constexpr (DUAL) { cu.p += cb.step; cu.left -= cb.step; }
@@ -881,14 +893,22 @@ namespace {
 // 1536, dx takes 444 and 575.  fp32, whose matrix cores are the bound at every shape,
 // has 64 rows alone (2048 rows of 16 experts, 1024 -> 512, all six: 315, with 128 x
 // 128 363).
-template <typename T, class N, class F>
+template <typename T, bool STREAM = false, class N, class F>
 hipError_t with_shape(N tiles, F f) {
   if constexpr (sizeof(T) == 2) {
-    if (tiles(4, 4) >= 200) return f(Shape<4, 4>{});
+    if (tiles(4, 4) >= 200) return f(Shape<4, 4, STREAM>{});
     if (tiles(2, 2) >= 256) return f(Shape<2, 2>{});
     if (tiles(1, 2) >= 512) return f(Shape<1, 2>{});
   }
   return f(Shape<1, 1>{});
+}
+
+// The same for a product whose weights are read by columns: streamed where an expert
+// has two row tiles of the largest on the mean, or fewer.
+template <typename T, class N, class F>
+hipError_t with_stream(const ExpertsArgs &a, N tiles, F f) {
+  if (a.rows <= 512 * (int64_t)a.E) return with_shape<T, true>(tiles, f);
+  return with_shape<T>(tiles, f);
 }
 
 // Tiles of a product over rows with N columns (a swiglu one's 64 are of both
@@ -953,7 +973,7 @@ hipError_t run_dh(const ExpertsArgs &a, T *dz, T *du, T *h, hipStream_t s) {
   q.g.b[0] = {a.w_down, a.I, a.d, a.I};
   q.b_expert = (int64_t)a.I * a.d * sizeof(T);
   q.g.kdim[0] = a.d;
-  return with_shape<T>(RowTiles(a, a.I), [&](auto sh) {
+  return with_stream<T>(a, RowTiles(a, a.I), [&](auto sh) {
     using SH = decltype(sh);
     const dim3 grid = rows_grid<SH>(q, false);
     if (a.saved.kind == MOE_SAVE_MXFP8) {
@@ -978,7 +998,7 @@ hipError_t run_dx(const ExpertsArgs &a, const T *dz, const T *du, hipStream_t s)
   q.g.kdim[0] = q.g.kdim[1] = a.I;
   q.g.segments = 2;
   const SumsOut<T> o = {(T *)a.dx, nullptr, a.d, 0};
-  return with_shape<T>(RowTiles(a, a.d), [&](auto sh) {
+  return with_stream<T>(a, RowTiles(a, a.d), [&](auto sh) {
     using SH = decltype(sh);
     const dim3 grid = rows_grid<SH>(q, false);
     hipLaunchKernelGGL((dx_kernel<T, SH>), grid, dim3(256), 0, s, q, o);

@@ -161,8 +161,9 @@ __device__ __forceinline__ rsrc_t cursor_rsrc(const Cursor &c) {
 
 // 16 bytes a lane from the matrix to LDS, lane l's at to + 16 l, zeros where off is
 // past the end.
+template <int POLICY = 0>
 __device__ __forceinline__ void copy16(rsrc_t r, uint8_t *to, uint32_t off) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (MOE_LDS void *)to, 16, off, 0, 0, 0);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (MOE_LDS void *)to, 16, off, 0, 0, POLICY);
 }
 
 // The order a step's instructions are issued in: one LDS read (of DS) after
