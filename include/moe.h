@@ -669,10 +669,9 @@ int moe_checkpoint_load(const uint8_t *codes, const uint8_t *scales, int32_t dty
  *             leaves) are neither read nor written, here and in the gradient
  *   offsets   [E + 1] int32 on the device, as moe_permute writes it.  Values outside
  *             [0, rows] or descending ones are clamped: no access is out of range
- *   saved     where z and u go for the gradient: kind FULL in the layer's type
- *             (never rounded across the clamp's border), kind MXFP8 as
- *             moe_checkpoint_save with limit L keeps them (I % 32 == 0).  NULL or
- *             kind NONE: not saved
+ *   saved     where z and u go for the gradient: kind FULL in fp32, as they are; kind
+ *             MXFP8 as moe_checkpoint_save with limit L keeps them, in a quarter of
+ *             the memory (I % 32 == 0).  NULL or kind NONE: not saved
  *   ws        moe_experts_workspace_size(cfg, rows, 0) bytes, 256-byte aligned;
  *             nothing in it needs to start at any value.  Calls that share one must
  *             be ordered on one stream
@@ -688,7 +687,7 @@ typedef enum {
 } moe_save_kind;
 typedef struct {
   int32_t kind;                /* moe_save_kind                                  */
-  void *gate, *up;             /* z, u: [rows, I] act_dtype, or bytes (codes)    */
+  void *gate, *up;             /* z, u: [rows, I] float, or bytes (codes)        */
   uint8_t *gate_scales;        /* MXFP8: [rows, I / 32]                          */
   uint8_t *up_scales;
 } moe_experts_saved;

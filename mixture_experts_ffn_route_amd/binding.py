@@ -735,7 +735,8 @@ def _experts_check(where, c: MoeConfigC, layer, offsets, rows, saved, row_tensor
     tensors += [(n, t, shapes[n[1:]], dt) for n, t in weight_grads]
     if saved is not None and saved["kind"] != "none":
         mx = saved["kind"] == "mxfp8"
-        tensors += [(n, saved[n], (rows, I), torch.uint8 if mx else dt) for n in ("gate", "up")]
+        tensors += [(n, saved[n], (rows, I), torch.uint8 if mx else torch.float32)
+                    for n in ("gate", "up")]
         if mx:
             tensors += [(n, saved[n], (rows, I // 32), torch.uint8)
                         for n in ("gate_scales", "up_scales")]
@@ -911,9 +912,8 @@ def alloc_experts_workspace(cfg, rows: int, backward=False, device="cuda"):
 
 def alloc_experts_saved(cfg, rows: int, kind="mxfp8", device="cuda") -> dict:
     """Where moe_experts saves the pre-activations of `rows` sorted rows: kind "full"
-    in the layer's type, "mxfp8" in 8 bits with a scale per 32."""
-    c = _as_config_c(cfg)
-    I, dt = c.moe_inter_dim, torch.uint8 if kind == "mxfp8" else _act_dtype(c)
+    in fp32, "mxfp8" in 8 bits with a scale per 32."""
+    I, dt = _as_config_c(cfg).moe_inter_dim, torch.uint8 if kind == "mxfp8" else torch.float32
     saved = {"kind": kind}
     if kind != "none":
         saved.update({n: torch.empty((rows, I), dtype=dt, device=device) for n in ("gate", "up")})

@@ -74,7 +74,7 @@ __global__ __launch_bounds__(256) void load_kernel(const CheckpointArgs a, uint3
     Eight<T> w;
 #pragma unroll
     for (int j = 0; j < 8; ++j) w[j] = (T)v[j];
-    *(Eight<T> *)dst = w;
+    __builtin_nontemporal_store(w, (Eight<T> *)dst);
   } else {
     uint32_t c[2] = {0u, 0u};
 #pragma unroll

@@ -208,11 +208,10 @@ __device__ __forceinline__ void keep_piece(const float (&v)[8], float limit, rsr
 }
 
 // Saved z and u of a tile's rows.
-template <typename T>
 struct SavedTile {
   rsrc_t z, u, zs, us;
   __device__ __forceinline__ SavedTile(const moe_experts_saved &s, int64_t first, int rows, int N) {
-    const int64_t bytes = s.kind == MOE_SAVE_NONE ? 0 : s.kind == MOE_SAVE_MXFP8 ? N : N * (int64_t)sizeof(T);
+    const int64_t bytes = s.kind == MOE_SAVE_NONE ? 0 : s.kind == MOE_SAVE_MXFP8 ? N : N * (int64_t)4;
     const int64_t scales = s.kind == MOE_SAVE_MXFP8 ? N / 32 : 0;
     z = rows_rsrc(s.gate, first, rows, bytes);
     u = rows_rsrc(s.up, first, rows, bytes);
@@ -245,7 +244,7 @@ struct UpOut {
   struct Ahead {};
   struct Tile {
     rsrc_t h;
-    SavedTile<T> s;
+    SavedTile s;
   };
   T *h;
   moe_experts_saved s;
@@ -254,7 +253,7 @@ struct UpOut {
   __device__ __forceinline__ Tile begin(const GroupedItem &it, int high) const {
     const int64_t first = (int64_t)it.lo + it.m0;
     const int rows = height(it.n - it.m0, high);
-    return Tile{rows_rsrc(h, first, rows, (int64_t)N * sizeof(T)), SavedTile<T>(s, first, rows, N)};
+    return Tile{rows_rsrc(h, first, rows, (int64_t)N * sizeof(T)), SavedTile(s, first, rows, N)};
   }
   __device__ __forceinline__ void fetch(const Tile &, Ahead &, int, int) const {}
   __device__ __forceinline__ void put(const Tile &t, const Ahead &, int m, int n, float (&v)[8],
@@ -265,13 +264,8 @@ struct UpOut {
       keep_piece(v, limit, t.s.z, t.s.zs, at, block, n < N, n % 32 == 0);
       keep_piece(u, limit, t.s.u, t.s.us, at, block, n < N, n % 32 == 0);
     } else if constexpr (KIND == MOE_SAVE_FULL) {
-      float k[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) k[j] = saved<T, false>(v[j], limit);
-      store_piece<T>(t.s.z, at * sizeof(T), k, N - n);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) k[j] = saved<T, true>(u[j], limit);
-      store_piece<T>(t.s.u, at * sizeof(T), k, N - n);
+      store_piece<float>(t.s.z, at * 4, v, N - n);
+      store_piece<float>(t.s.u, at * 4, u, N - n);
     }
     const float top = limit > 0.f ? limit : __builtin_inff();
 #pragma unroll
@@ -288,12 +282,12 @@ template <typename T, int KIND>
 struct SlopeOut {
   static constexpr bool sums = false, MX = KIND == MOE_SAVE_MXFP8;
   struct Ahead {
-    Raw8<T> z, u;              // MXFP8: the codes in the first two words
+    Raw8<float> z, u;          // MXFP8: the codes in the first two words
     uint32_t zs, us;           // and the scales
   };
   struct Tile {
     rsrc_t dz, du, h;
-    SavedTile<T> s;
+    SavedTile s;
   };
   T *dz, *du, *h;
   moe_experts_saved s;
@@ -303,7 +297,7 @@ struct SlopeOut {
     const int64_t b = (int64_t)N * sizeof(T), first = (int64_t)it.lo + it.m0;
     const int rows = height(it.n - it.m0, high);
     return Tile{rows_rsrc(dz, first, rows, b), rows_rsrc(du, first, rows, b), rows_rsrc(h, first, rows, b),
-                SavedTile<T>(s, first, rows, N)};
+                SavedTile(s, first, rows, N)};
   }
   __device__ __forceinline__ void fetch(const Tile &t, Ahead &a, int m, int n) const {
     const uint32_t at = (uint32_t)m * N + n;
@@ -316,8 +310,8 @@ struct SlopeOut {
       a.zs = __builtin_amdgcn_raw_buffer_load_b8(t.s.zs, block, 0, 0);
       a.us = __builtin_amdgcn_raw_buffer_load_b8(t.s.us, block, 0, 0);
     } else {
-      fetch_piece<T>(a.z, t.s.z, at * sizeof(T), N - n);
-      fetch_piece<T>(a.u, t.s.u, at * sizeof(T), N - n);
+      fetch_piece<float>(a.z, t.s.z, at * 4, N - n);
+      fetch_piece<float>(a.u, t.s.u, at * 4, N - n);
     }
   }
   __device__ __forceinline__ void put(const Tile &t, const Ahead &a, int m, int n, float (&v)[8],
@@ -327,8 +321,8 @@ struct SlopeOut {
       kept8(z, a.z.w[0], a.z.w[1], a.zs);
       kept8(u, a.u.w[0], a.u.w[1], a.us);
     } else {
-      widen8<T>(z, a.z);
-      widen8<T>(u, a.u);
+      widen8<float>(z, a.z);
+      widen8<float>(u, a.u);
     }
     const float top = limit > 0.f ? limit : __builtin_inff();
 #pragma unroll

@@ -10,7 +10,7 @@
 // in slot order in fp32 by one thread, so results do not depend on the launch.  A
 // pair whose row is outside [0, R) takes no part.
 //
-// A row is cut into 16-byte pieces, one a thread.  Vectors have the alignment of an
+// A row is cut into 16-byte pieces.  Vectors have the alignment of an
 // element, so any width is taken: the last piece of a row whose width is not a
 // whole number of pieces starts early enough to end with the row (and computes some
 // elements twice, alike).  Rows shorter than a piece go by elements.
@@ -24,24 +24,26 @@ namespace {
 template <typename T, int V>
 using Vec = T __attribute__((ext_vector_type(V), aligned(sizeof(T))));
 
+// Sorted rows are read and written past the caches (nontemporal): each once, and 8192
+// tokens' are larger than the L2.  4096 tokens of 8 rows of 7168 in bf16: combine 133 us,
+// so 119, dispatch 104 and 93, the gradient of combine 206 and 189.
+// (x, dy and what is added are not: dispatch 93, so 113.)
 template <typename T, int V>
-struct Bits {
+struct Piece {
   Vec<T, V> v;
+  __device__ __forceinline__ void load(const T *p) { v = *(const Vec<T, V> *)p; }
+  __device__ __forceinline__ void load_once(const T *p) {
+    v = __builtin_nontemporal_load((const Vec<T, V> *)p);
+  }
+  __device__ __forceinline__ float operator[](int i) const { return (float)v[i]; }
 };
 template <typename T>
-struct Bits<T, 1> {
+struct Piece<T, 1> {
   T v;
+  __device__ __forceinline__ void load(const T *p) { v = *p; }
+  __device__ __forceinline__ void load_once(const T *p) { v = *p; }
+  __device__ __forceinline__ float operator[](int) const { return (float)v; }
 };
-template <typename T, int V>
-__device__ __forceinline__ void widen(float (&f)[V], const T *p) {
-  if constexpr (V == 1) {
-    f[0] = (float)*p;
-  } else {
-    const Vec<T, V> w = *(const Vec<T, V> *)p;
-#pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = (float)w[i];
-  }
-}
 template <typename T, int V>
 __device__ __forceinline__ void narrow(T *p, const float (&f)[V]) {
   if constexpr (V == 1) {
@@ -50,62 +52,86 @@ __device__ __forceinline__ void narrow(T *p, const float (&f)[V]) {
     Vec<T, V> w;
 #pragma unroll
     for (int i = 0; i < V; ++i) w[i] = (T)f[i];
-    *(Vec<T, V> *)p = w;
+    __builtin_nontemporal_store(w, (Vec<T, V> *)p);
   }
 }
 
-// Token and first column of this thread's piece; false past the last token.
-template <int V>
-__device__ __forceinline__ bool place(const RowsArgs &a, uint32_t pieces, int64_t *t, int *c) {
-  const uint32_t i = blockIdx.x * 256u + threadIdx.x, tok = i / pieces;
-  const int at = (int)(i - tok * pieces) * V;
-  *t = tok;
-  *c = at < a.d - V ? at : a.d - V;
-  return tok < a.T;
+// Calls f(token)(first column) for this thread's pieces.  Rows of kTokenPieces and more
+// take a workgroup a token, whose indices are then scalars and whose waves read the
+// same rows at the same time (combine above 119 us, so 111); shorter ones have the
+// pieces of all tokens in one line (4096 tokens of 88 pieces 7.5 us, by tokens 8.9).
+constexpr uint32_t kTokenPieces = 192;
+template <int V, bool BY_TOKEN, class F>
+__device__ __forceinline__ void each_piece(const RowsArgs &a, uint32_t pieces, F f) {
+  auto column = [&](uint32_t p) {
+    const int at = (int)p * V;
+    return at < a.d - V ? at : a.d - V;
+  };
+  if constexpr (BY_TOKEN) {
+    const auto of_token = f((int64_t)blockIdx.x);
+    for (uint32_t p = threadIdx.x; p < pieces; p += 256) of_token(column(p));
+  } else {
+    const uint32_t i = blockIdx.x * 256u + threadIdx.x, t = i / pieces;
+    if (t < a.T) f((int64_t)t)(column(i - t * pieces));
+  }
 }
 
-template <typename T, int V>
+template <typename T, int V, bool BY_TOKEN>
 __global__ __launch_bounds__(256) void dispatch_kernel(const RowsArgs a, uint32_t pieces) {
-  int64_t t;
-  int c;
-  if (!place<V>(a, pieces, &t, &c)) return;
-  const auto v = *(const decltype(Bits<T, V>::v) *)((const T *)a.tokens + t * a.d + c);
+  each_piece<V, BY_TOKEN>(a, pieces, [&](int64_t t) {
+    return [&a, t](int c) {
+      Piece<T, V> x;
+      x.load((const T *)a.tokens + t * a.d + c);
+      float v[V];                              // and back: exact
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = x[i];
 #pragma unroll 4
-  for (int j = 0; j < a.k; ++j) {
-    const int64_t r = a.inverse[t * a.k + j];
-    if (r >= 0 && r < a.R) *(decltype(Bits<T, V>::v) *)((T *)a.out_rows + r * a.d + c) = v;
-  }
+      for (int j = 0; j < a.k; ++j) {
+        const int64_t r = a.inverse[t * a.k + j];
+        if (r >= 0 && r < a.R) narrow<T, V>((T *)a.out_rows + r * a.d + c, v);
+      }
+    };
+  });
 }
 
-template <typename T, int V, int K>
+template <int K>
+struct Sources {
+  int64_t row[K];              // of a token's slots; -1: none
+  float w[K];
+  __device__ __forceinline__ Sources(const RowsArgs &a, int64_t t) {
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      const int64_t r = j < a.k ? a.inverse[t * a.k + j] : -1;
+      row[j] = r >= 0 && r < a.R ? r : -1;
+      w[j] = row[j] < 0 ? 0.f : a.weights ? a.weights[t * a.k + j] : 1.f;
+    }
+  }
+};
+
+template <typename T, int V, int K, bool BY_TOKEN>
 __global__ __launch_bounds__(256) void combine_kernel(const RowsArgs a, uint32_t pieces) {
-  int64_t t;
-  int c;
-  if (!place<V>(a, pieces, &t, &c)) return;
-  float v[K][V], w[K];
+  each_piece<V, BY_TOKEN>(a, pieces, [&](int64_t t) {
+    const Sources<K> s(a, t);
+    return [&a, s, t](int c) {
+      Piece<T, V> v[K], add;                   // all asked for before the first is used
 #pragma unroll
-  for (int j = 0; j < K; ++j) {
-    const int64_t r = j < a.k ? a.inverse[t * a.k + j] : -1;
-    const bool on = r >= 0 && r < a.R;
-    w[j] = on ? (a.weights ? a.weights[t * a.k + j] : 1.f) : 0.f;
+      for (int j = 0; j < K; ++j)
+        if (s.row[j] >= 0) v[j].load_once((const T *)a.rows + s.row[j] * a.d + c);
+      if (a.tokens) add.load((const T *)a.tokens + t * a.d + c);
+      float sum[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[j][i] = 0.f;
-    if (on) widen<T, V>(v[j], (const T *)a.rows + r * a.d + c);
-  }
-  float sum[V];
+      for (int i = 0; i < V; ++i) sum[i] = 0.f;
 #pragma unroll
-  for (int i = 0; i < V; ++i) sum[i] = 0.f;
+      for (int j = 0; j < K; ++j)
+        if (s.row[j] >= 0)
 #pragma unroll
-  for (int j = 0; j < K; ++j)
+          for (int i = 0; i < V; ++i) sum[i] += s.w[j] * v[j][i];
+      if (a.tokens)
 #pragma unroll
-    for (int i = 0; i < V; ++i) sum[i] += w[j] * v[j][i];
-  if (a.tokens) {
-    float b[V];
-    widen<T, V>(b, (const T *)a.tokens + t * a.d + c);
-#pragma unroll
-    for (int i = 0; i < V; ++i) sum[i] += b[i];
-  }
-  narrow<T, V>((T *)a.out_tokens + t * a.d + c, sum);
+        for (int i = 0; i < V; ++i) sum[i] += add[i];
+      narrow<T, V>((T *)a.out_tokens + t * a.d + c, sum);
+    };
+  });
 }
 
 // A workgroup takes a token; a thread every blockDim-th piece of its row.
@@ -113,32 +139,31 @@ template <typename T, int V, int K>
 __global__ __launch_bounds__(256) void combine_backward_kernel(const RowsArgs a, uint32_t pieces) {
   __shared__ float red[4][K];
   const int64_t t = blockIdx.x;
-  int64_t r[K];
-  float w[K], dot[K];
+  const Sources<K> s(a, t);
+  float dot[K];
 #pragma unroll
-  for (int j = 0; j < K; ++j) {
-    const int64_t at = j < a.k ? a.inverse[t * a.k + j] : -1;
-    r[j] = at >= 0 && at < a.R ? at : -1;
-    w[j] = r[j] >= 0 && a.weights ? a.weights[t * a.k + j] : 0.f;
-    dot[j] = 0.f;
-  }
+  for (int j = 0; j < K; ++j) dot[j] = 0.f;
   for (uint32_t p = threadIdx.x; p < pieces; p += blockDim.x) {
     const int at = (int)p * V, c = at < a.d - V ? at : a.d - V;
-    float g[V], v[V];
-    widen<T, V>(g, (const T *)a.tokens + t * a.d + c);
+    Piece<T, V> g, v[K];
+    g.load((const T *)a.tokens + t * a.d + c);
+    if (a.dweights)
+#pragma unroll
+      for (int j = 0; j < K; ++j)
+        if (s.row[j] >= 0) v[j].load_once((const T *)a.rows + s.row[j] * a.d + c);
 #pragma unroll
     for (int j = 0; j < K; ++j) {
-      if (r[j] < 0) continue;
+      if (s.row[j] < 0) continue;
       if (a.dweights) {
-        widen<T, V>(v, (const T *)a.rows + r[j] * a.d + c);
 #pragma unroll
         for (int i = 0; i < V; ++i)
-          if (c + i >= at) dot[j] += v[i] * g[i];           // once each
+          if (c + i >= at) dot[j] += v[j][i] * g[i];        // once each
       }
       if (a.out_rows) {
+        float o[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = w[j] * g[i];
-        narrow<T, V>((T *)a.out_rows + r[j] * a.d + c, v);
+        for (int i = 0; i < V; ++i) o[i] = s.w[j] * g[i];
+        narrow<T, V>((T *)a.out_rows + s.row[j] * a.d + c, o);
       }
     }
   }
@@ -151,9 +176,9 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const RowsArgs a,
     for (int j = 0; j < K; ++j) red[wave][j] = dot[j];
   __syncthreads();
   if ((int)threadIdx.x < a.k) {
-    float s = 0.f;
-    for (int i = 0; i < waves; ++i) s += red[i][threadIdx.x];
-    a.dweights[t * a.k + threadIdx.x] = s;
+    float v = 0.f;
+    for (int i = 0; i < waves; ++i) v += red[i][threadIdx.x];
+    a.dweights[t * a.k + threadIdx.x] = v;
   }
 }
 
@@ -163,23 +188,28 @@ uint32_t pieces_of(int d, int V) { return (uint32_t)((d + V - 1) / V); }
 int waves_a_token(uint32_t pieces) { return pieces > 192 ? 4 : (int)((pieces + 63) / 64); }
 
 unsigned blocks_of(const RowsArgs &a, uint32_t pieces) {
-  return (unsigned)((a.T * pieces + 255) / 256);
+  return (unsigned)(pieces >= kTokenPieces ? a.T : (a.T * pieces + 255) / 256);
 }
 
 template <typename T, int V>
 hipError_t run_dispatch(const RowsArgs &a, hipStream_t s) {
   const uint32_t n = pieces_of(a.d, V);
-  hipLaunchKernelGGL((dispatch_kernel<T, V>), dim3(blocks_of(a, n)), dim3(256), 0, s, a, n);
+  const dim3 grid(blocks_of(a, n));
+  if (n >= kTokenPieces) hipLaunchKernelGGL((dispatch_kernel<T, V, true>), grid, dim3(256), 0, s, a, n);
+  else hipLaunchKernelGGL((dispatch_kernel<T, V, false>), grid, dim3(256), 0, s, a, n);
   return hipGetLastError();
 }
 template <typename T, int V, int K>
 hipError_t run_combine(const RowsArgs &a, bool backward, hipStream_t s) {
   const uint32_t n = pieces_of(a.d, V);
+  const dim3 grid(blocks_of(a, n));
   if (backward)
     hipLaunchKernelGGL((combine_backward_kernel<T, V, K>), dim3((unsigned)a.T),
                        dim3(64 * waves_a_token(n)), 0, s, a, n);
+  else if (n >= kTokenPieces)
+    hipLaunchKernelGGL((combine_kernel<T, V, K, true>), grid, dim3(256), 0, s, a, n);
   else
-    hipLaunchKernelGGL((combine_kernel<T, V, K>), dim3(blocks_of(a, n)), dim3(256), 0, s, a, n);
+    hipLaunchKernelGGL((combine_kernel<T, V, K, false>), grid, dim3(256), 0, s, a, n);
   return hipGetLastError();
 }
 template <typename T, int V>
@@ -201,7 +231,7 @@ hipError_t run_combine_of(const RowsArgs &a, bool backward, hipStream_t s) {
 int64_t rows_threads(const RowsArgs &a) {
   const int V = a.dtype == MOE_DTYPE_F32 ? 4 : 8;
   const uint32_t n = pieces_of(a.d, a.d >= V ? V : 1);
-  const int64_t by_token = a.T * 64 * waves_a_token(n), flat = a.T * (int64_t)n + 256;
+  const int64_t by_token = a.T * 256, flat = a.T * (int64_t)n + 256;
   return by_token > flat ? by_token : flat;
 }
 

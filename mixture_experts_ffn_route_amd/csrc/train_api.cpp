@@ -121,7 +121,7 @@ struct ExpertsMemory {
     rows = es * a.rows * a.d;
     weights = es * a.E * a.d * a.I;
     const bool mx = a.saved.kind == MOE_SAVE_MXFP8;
-    kept = a.saved.kind == MOE_SAVE_NONE ? 0 : (mx ? 1 : es) * a.rows * a.I;
+    kept = a.saved.kind == MOE_SAVE_NONE ? 0 : (size_t)(mx ? 1 : 4) * a.rows * a.I;
     scales = mx ? (size_t)a.rows * (a.I / 32) : 0;
   }
 };

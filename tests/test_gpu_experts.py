@@ -71,7 +71,7 @@ class Step:
                 H.decode(s["up"][part], s["up_scales"][part]))
 
     def check_forward(self):
-        limit, half = self.cfg.swiglu_limit, H.HALF[self.dt]
+        limit = self.cfg.swiglu_limit
         y = self.y.cpu()
         for e, n in enumerate(self.counts):
             part, w = self.expert(e)
@@ -84,11 +84,11 @@ class Step:
             for name, got in zip(("z", "u"), self.kept(part)):
                 want, tol = f[name]
                 size = want.abs() + tol
-                # a step instead of half of one where rounding would cross the limit
-                steps = 2 if limit > 0 else 1
                 if self.kind == "full":
-                    bound = tol + steps * half * size
+                    bound = tol + 2.0 ** -24 * size
                 else:
+                    # a step instead of half of one where rounding would cross the limit
+                    steps = 2 if limit > 0 else 1
                     unit = torch.exp2(self.saved[{"z": "gate", "u": "up"}[name] + "_scales"]
                                       .cpu()[part].double() - 127).repeat_interleave(32, 1)
                     bound = tol + steps * torch.maximum(size * 2.0 ** -4, unit * 2.0 ** -10)

@@ -169,7 +169,7 @@ def test_experts_workspace():
         B.alloc_experts_workspace(replace(CFG, dim=68), 10, True, "cpu")
     s = B.alloc_experts_saved(CFG, 10, "mxfp8", "cpu")
     assert s["gate"].shape == (10, 96) and s["up_scales"].shape == (10, 3)
-    assert B.alloc_experts_saved(CFG, 10, "full", "cpu")["up"].dtype is torch.bfloat16
+    assert B.alloc_experts_saved(CFG, 10, "full", "cpu")["up"].dtype is torch.float32
     with pytest.raises(ValueError):
         B.alloc_experts_saved(CFG, 10, "fp8", "cpu")
 
