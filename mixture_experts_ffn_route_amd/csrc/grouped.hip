@@ -202,7 +202,7 @@ __device__ __forceinline__ void keep_piece(const float (&v)[8], float limit, rsr
   m = fmaxf(m, xor_lane<2>(m));
   const int X = keep_exponent(m);
   uint32_t c[2];
-  keep8(v, X, limit, c);
+  keep<8>(v, X, limit, c);
   __builtin_amdgcn_raw_buffer_store_b64(u32x2{c[0], c[1]}, codes, on ? at : kOut, 0, 0);
   __builtin_amdgcn_raw_buffer_store_b8((uint8_t)(X + 127), scales, on && first ? block : kOut, 0, 0);
 }
@@ -318,8 +318,8 @@ struct SlopeOut {
                                       float (&)[8]) const {
     float z[8], u[8];
     if constexpr (MX) {
-      kept8(z, a.z.w[0], a.z.w[1], a.zs);
-      kept8(u, a.u.w[0], a.u.w[1], a.us);
+      kept<8>(z, {a.z.w[0], a.z.w[1]}, a.zs);
+      kept<8>(u, {a.u.w[0], a.u.w[1]}, a.us);
     } else {
       widen8<float>(z, a.z);
       widen8<float>(u, a.u);

@@ -23,11 +23,12 @@ namespace {
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
-// Largest finite magnitude of eight values, whatever bits they have.
-__device__ __forceinline__ float keep_top(const float (&v)[8]) {
+// Largest finite magnitude of N values, whatever bits they have.
+template <int N>
+__device__ __forceinline__ float keep_top(const float (&v)[N]) {
   float m = 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]) < __builtin_inff() ? fabsf(v[j]) : 0.f);
+  for (int j = 0; j < N; ++j) m = fmaxf(m, fabsf(v[j]) < __builtin_inff() ? fabsf(v[j]) : 0.f);
   return m;
 }
 // The same of results of arithmetic, whose NaNs are quiet ones: a maximum with one is
@@ -51,21 +52,22 @@ __device__ __forceinline__ float keep_pow2(int x) {
   return __uint_as_float(x > -127 ? (uint32_t)(x + 127) << 23 : 0x400000u);
 }
 
-// Codes of eight values of a block with exponent X.
-__device__ __forceinline__ void keep8(const float (&v)[8], int X, float limit, uint32_t (&out)[2]) {
+// Codes of N values of a block with exponent X, four to a word.
+template <int N>
+__device__ __forceinline__ void keep(const float (&v)[N], int X, float limit, uint32_t (&out)[N / 4]) {
   const float to = keep_pow2(-X);
-  float q[8];
+  float q[N];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) q[j] = v[j] * to;              // the conversion makes NaN of infinities
+  for (int j = 0; j < N; ++j) q[j] = v[j] * to;              // the conversion makes NaN of infinities
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+  for (int h = 0; h < N / 4; ++h) {
     int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[4 * h], q[4 * h + 1], 0, false);
     out[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[4 * h + 2], q[4 * h + 3], w, true);
   }
   if (limit > 0.f) {
     const float edge = limit * to;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < N / 4; ++h) {
       const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)out[h], false);
       const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8((int)out[h], true);
       const float r[4] = {a[0], a[1], b[0], b[1]};
@@ -81,15 +83,19 @@ __device__ __forceinline__ void keep8(const float (&v)[8], int X, float limit, u
   }
 }
 
-// Eight values from their codes and the block's scale byte.
-__device__ __forceinline__ void kept8(float (&v)[8], uint32_t lo, uint32_t hi, uint32_t scale) {
+// N values from their codes and the block's scale byte.
+template <int N>
+__device__ __forceinline__ void kept(float (&v)[N], const uint32_t (&codes)[N / 4], uint32_t scale) {
   const float unit = keep_pow2((int)scale - 127);
-  const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)lo, false);
-  const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8((int)lo, true);
-  const f32x2 c = __builtin_amdgcn_cvt_pk_f32_fp8((int)hi, false);
-  const f32x2 d = __builtin_amdgcn_cvt_pk_f32_fp8((int)hi, true);
-  v[0] = a[0] * unit; v[1] = a[1] * unit; v[2] = b[0] * unit; v[3] = b[1] * unit;
-  v[4] = c[0] * unit; v[5] = c[1] * unit; v[6] = d[0] * unit; v[7] = d[1] * unit;
+#pragma unroll
+  for (int h = 0; h < N / 4; ++h) {
+    const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)codes[h], false);
+    const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8((int)codes[h], true);
+    v[4 * h] = a[0] * unit;
+    v[4 * h + 1] = a[1] * unit;
+    v[4 * h + 2] = b[0] * unit;
+    v[4 * h + 3] = b[1] * unit;
+  }
 }
 
 }  // namespace
