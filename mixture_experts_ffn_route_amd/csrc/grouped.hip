@@ -220,20 +220,27 @@ struct SavedTile {
   }
 };
 
-// Clamped gate and up values and SiLU's factor; NaN passes.  `top` is infinite
-// without a clamp.
+// SiLU's factor.  bf16: the hardware's 2^x as it is, which makes zeros of results below
+// 2^-126 (1 + 2^-126 is 1 all the same), and its reciprocal.
+template <typename T>
+__device__ __forceinline__ float silu_factor(float v) {
+  if constexpr (sizeof(T) == 4) return sigmoid<T>(v);
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v * -1.4426950408889634f));
+}
+
+// Clamped gate and up values and SiLU's factor; NaN passes.
 struct Clamped {
   float g, w, s;
   bool off, off_up;
 };
-template <typename T>
+template <typename T, bool LIMIT>
 __device__ __forceinline__ Clamped clamped(float z, float u, float top) {
   Clamped c;
-  c.off = z > top;
-  c.off_up = fabsf(u) > top;
+  c.off = LIMIT && z > top;
+  c.off_up = LIMIT && fabsf(u) > top;
   c.g = c.off ? top : z;
   c.w = c.off_up ? copysignf(top, u) : u;
-  c.s = sigmoid<T>(c.g);
+  c.s = silu_factor<T>(c.g);
   return c;
 }
 
@@ -256,6 +263,14 @@ struct UpOut {
     return Tile{rows_rsrc(h, first, rows, (int64_t)N * sizeof(T)), SavedTile(s, first, rows, N)};
   }
   __device__ __forceinline__ void fetch(const Tile &, Ahead &, int, int) const {}
+  template <bool LIMIT>
+  __device__ __forceinline__ void glu(float (&v)[8], const float (&u)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const Clamped c = clamped<T, LIMIT>(v[j], u[j], limit);
+      v[j] = c.g * c.s * c.w;
+    }
+  }
   __device__ __forceinline__ void put(const Tile &t, const Ahead &, int m, int n, float (&v)[8],
                                       float (&u)[8]) const {
     const uint32_t at = (uint32_t)m * N + n;
@@ -267,12 +282,8 @@ struct UpOut {
       store_piece<float>(t.s.z, at * 4, v, N - n);
       store_piece<float>(t.s.u, at * 4, u, N - n);
     }
-    const float top = limit > 0.f ? limit : __builtin_inff();
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const Clamped c = clamped<T>(v[j], u[j], top);
-      v[j] = c.g * c.s * c.w;
-    }
+    if (limit > 0.f) glu<true>(v, u);
+    else glu<false>(v, u);
     store_piece<T>(t.h, at * sizeof(T), v, N - n);
   }
 };
@@ -314,6 +325,18 @@ struct SlopeOut {
       fetch_piece<float>(a.u, t.s.u, at * 4, N - n);
     }
   }
+  // v: dh, then h; z and u, then dz and du
+  template <bool LIMIT>
+  __device__ __forceinline__ void slopes(float (&v)[8], float (&z)[8], float (&u)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const Clamped c = clamped<T, LIMIT>(z[j], u[j], limit);
+      const float q = v[j] * c.s;              // dh SiLU's factor
+      z[j] = c.off ? 0.f : q * c.w * (1.f + c.g * (1.f - c.s));
+      u[j] = c.off_up ? 0.f : q * c.g;
+      v[j] = c.g * c.s * c.w;
+    }
+  }
   __device__ __forceinline__ void put(const Tile &t, const Ahead &a, int m, int n, float (&v)[8],
                                       float (&)[8]) const {
     float z[8], u[8];
@@ -324,15 +347,8 @@ struct SlopeOut {
       widen8<float>(z, a.z);
       widen8<float>(u, a.u);
     }
-    const float top = limit > 0.f ? limit : __builtin_inff();
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const Clamped c = clamped<T>(z[j], u[j], top);
-      const float q = v[j] * c.s;              // dh SiLU's factor
-      z[j] = c.off ? 0.f : q * c.w * (1.f + c.g * (1.f - c.s));
-      u[j] = c.off_up ? 0.f : q * c.g;
-      v[j] = c.g * c.s * c.w;
-    }
+    if (limit > 0.f) slopes<true>(v, z, u);
+    else slopes<false>(v, z, u);
     const uint32_t off = ((uint32_t)m * N + n) * sizeof(T);
     store_piece<T>(t.dz, off, z, N - n);
     store_piece<T>(t.du, off, u, N - n);
@@ -654,7 +670,7 @@ __device__ __forceinline__ void walk(const GemmOp &g, const OUT &out, NEXT next,
             }
           }
         __builtin_amdgcn_wave_barrier();
-#pragma unroll 1
+#pragma unroll 2
         for (int q = 0; q < PPL; ++q) {
           auto at = [&](int pass, int piece, int *m, int *n) {
             *m = m0 + pass / PER_ROW * 32 + piece * ROWS;
