@@ -714,6 +714,23 @@ int moe_experts_backward(const moe_config *cfg, const moe_weights *w, const void
                          const moe_experts_saved *saved, const moe_experts_grads *grads, void *ws,
                          size_t ws_bytes, void *stream);
 
+/* Tiles of the products of these calls (host-only, for tests and profiles): a choice by
+ * sizes and types alone. */
+typedef enum {
+  MOE_EXPERTS_UP = 0,          /* z and u, h                                     */
+  MOE_EXPERTS_DOWN = 1,        /* y                                              */
+  MOE_EXPERTS_DH = 2,          /* dh; dz, du and h                               */
+  MOE_EXPERTS_DX = 3,
+  MOE_EXPERTS_DW_DOWN = 4,
+  MOE_EXPERTS_DW = 5           /* dw_gate and dw_up                              */
+} moe_experts_product;
+typedef struct {
+  int32_t tile_rows;           /* at most: lower ones for what is left           */
+  int32_t tile_cols;           /* (UP: columns of both matrices)                 */
+  int32_t streamed;            /* the weights pass the caches by                 */
+} moe_experts_path_info;
+int moe_experts_path(const moe_config *cfg, int64_t rows, int32_t product, moe_experts_path_info *info);
+
 /* Roofline probes: the achievable HBM read rate and bf16 / FP8 MFMA rates of
  * the GPU, measured with the instruction forms the layer kernels use (16-byte
  * nontemporal vector loads; v_mfma_f32_16x16x32_bf16, v_mfma_f32_32x32x16_bf16,

@@ -38,7 +38,7 @@ EXPORTED_SYMBOLS = (
     "moe_linear_workspace_size", "moe_linear", "moe_linear_backward", "moe_linear_path",
     "moe_dispatch", "moe_dispatch_backward", "moe_combine", "moe_combine_backward",
     "moe_checkpoint_save", "moe_checkpoint_load", "moe_experts_workspace_size", "moe_experts",
-    "moe_experts_backward",
+    "moe_experts_backward", "moe_experts_path",
 )
 MOE_STAGES = ("route", "permute", "gemm1", "gemm2", "combine")
 
@@ -104,6 +104,10 @@ class MoeExpertsSavedC(ctypes.Structure):
         "gate", "up", "gate_scales", "up_scales")]
 
 
+class MoeExpertsPathC(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("tile_rows", "tile_cols", "streamed")]
+
+
 class MoeExpertsGradsC(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("dx", "dw_gate", "dw_up", "dw_down")]
 
@@ -159,7 +163,9 @@ def _load():
     lib.moe_experts.argtypes = [cfgp, wp, vp, vp, i64, vp, sp, vp, size, vp]
     lib.moe_experts_backward.argtypes = [cfgp, wp, vp, vp, i64, vp, sp,
                                          ctypes.POINTER(MoeExpertsGradsC), vp, size, vp]
+    lib.moe_experts_path.argtypes = [cfgp, i64, i32, ctypes.POINTER(MoeExpertsPathC)]
     for f in ("moe_dispatch", "moe_dispatch_backward", "moe_combine", "moe_combine_backward",
+              "moe_experts_path",
               "moe_checkpoint_save", "moe_checkpoint_load", "moe_experts", "moe_experts_backward"):
         getattr(lib, f).restype = ctypes.c_int
     for f in ("moe_few_workspace_layout", "moe_forward_few", "moe_linear", "moe_linear_backward",
@@ -752,6 +758,17 @@ def _saved_c(saved):
 
 def moe_experts_workspace_size(cfg, rows: int, backward=False) -> int:
     return _lib.moe_experts_workspace_size(_config_ref(cfg), rows, int(bool(backward)))
+
+
+EXPERTS_PRODUCT = {"up": 0, "down": 1, "dh": 2, "dx": 3, "dw_down": 4, "dw": 5}
+
+
+def moe_experts_path(cfg, rows: int, product: str) -> tuple:
+    """(most tile rows, tile columns, whether the weights are streamed) of a product."""
+    info = MoeExpertsPathC()
+    _check(_lib.moe_experts_path(_config_ref(cfg), rows, EXPERTS_PRODUCT[product],
+                                 ctypes.byref(info)), "moe_experts_path")
+    return info.tile_rows, info.tile_cols, bool(info.streamed)
 
 
 def moe_experts(cfg, layer, x, offsets, y, ws, saved=None, stream=None):

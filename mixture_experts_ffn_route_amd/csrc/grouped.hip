@@ -548,7 +548,7 @@ __device__ __forceinline__ void walk(const GemmOp &g, const OUT &out, NEXT next,
   constexpr int NI = SH::NI, NJ = DUAL ? NI / 2 : NI, HIGH = SH::HIGH;
   // The end of a tile goes through LDS, so that a store's lanes write whole lines
   // (straight from the accumulators, 32 bytes a row and store, 16384 rows of 64 experts
-  // took 271 us for dW of 2048 -> 2 x 1024, %%% through LDS: the L2 takes a request a
+  // took 271 us for dW of 2048 -> 2 x 1024, through LDS 245: the L2 takes a request a
   // piece).  Of the largest tiles through memory of its own beside the ring, so that
   // the next one's first stages can be asked for before; of others the ring itself,
   // where that would cost a CU a workgroup.
@@ -895,42 +895,54 @@ bool experts_launchable(const ExpertsArgs &a, bool backward) {
 
 namespace {
 
-// Calls f with the shape of a product that has `tiles(high, wide)` tiles of 64 high x
-// 64 wide: the largest of which there are about as many as CUs.  bf16, microseconds,
-// each shape forced on 14 problems (90 products): the rule loses 2.5 % on the mean to
-// the best of them, 21 % at most; on 4096 rows of one expert, 2048 -> 1024, the 64
-// tiles of 256 x 256 of dh take 63, 128 x 128 32; on 8192 rows of 48 experts, 5120 ->
-// 1536, dx takes 444 and 575.  fp32, whose matrix cores are the bound at every shape,
-// has 64 rows alone (2048 rows of 16 experts, 1024 -> 512, all six: 315, with 128 x
-// 128 363).
-template <typename T, bool STREAM = false, class N, class F>
-hipError_t with_shape(N tiles, F f) {
-  if constexpr (sizeof(T) == 2) {
-    if (tiles(4, 4) >= 200) return f(Shape<4, 4, STREAM>{});
-    if (tiles(2, 2) >= 256) return f(Shape<2, 2>{});
-    if (tiles(1, 2) >= 512) return f(Shape<1, 2>{});
-  }
-  return f(Shape<1, 1>{});
-}
-
-// The same for a product whose weights are read by columns: streamed where an expert
-// has two row tiles of the largest on the mean, or fewer.
-template <typename T, class N, class F>
-hipError_t with_stream(const ExpertsArgs &a, N tiles, F f) {
-  if (a.rows <= 512 * (int64_t)a.E) return with_shape<T, true>(tiles, f);
-  return with_shape<T>(tiles, f);
-}
-
-// Tiles of a product over rows with N columns (a swiglu one's 64 are of both
-// matrices): experts with the mean's rows, half a tile each left over.
-struct RowTiles {
-  int64_t rows, experts, cols;
-  RowTiles(const ExpertsArgs &a, int64_t n) : rows(a.rows), experts(a.rows < a.E ? a.rows : a.E), cols(n) {}
-  int64_t operator()(int high, int wide) const {
-    const int64_t by_rows = rows / (64 * high) + experts / 2;
-    return (by_rows > experts ? by_rows : experts) * ((cols + 64 * wide - 1) / (64 * wide));
-  }
+// Tile shape of a product: the largest tiles of which there are about as many as CUs,
+// counting for a product over rows experts with the mean's rows and half a tile each
+// left over.  bf16, microseconds, each shape forced on 14 problems (90 products): the
+// rule loses 2.5 % on the mean to the best of them, 21 % at most; on 4096 rows of one
+// expert, 2048 -> 1024, the 64 tiles of 256 x 256 of dh take 63, 128 x 128 32; on 8192
+// rows of 48 experts, 5120 -> 1536, dx takes 444 and 575.  fp32, whose matrix cores are
+// the bound at every shape, has 64 x 64 alone (2048 rows of 16 experts, 1024 -> 512, all
+// six: 315, with 128 x 128 363).  up has two matrices in a tile, 64 x 128 at least.
+//
+// Weights by columns are streamed where an expert has two row tiles of the largest on
+// the mean, or fewer.
+struct Pick {
+  int high, ni;
+  bool stream;
 };
+Pick pick(const ExpertsArgs &a, int product) {
+  const bool rows_product = product <= MOE_EXPERTS_DX, dw = product == MOE_EXPERTS_DW;
+  const int64_t d = a.d, I = a.I, experts = a.rows < a.E ? a.rows : a.E;
+  const int64_t cols = product == MOE_EXPERTS_UP ? 2 * I
+                       : product == MOE_EXPERTS_DOWN || product == MOE_EXPERTS_DX || dw ? d : I;
+  auto tiles = [&](int high, int wide) {
+    const int64_t across = (cols + 64 * wide - 1) / (64 * wide);
+    if (!rows_product) return a.E * (((dw ? 2 * I : d) + 64 * high - 1) / (64 * high)) * across;
+    const int64_t by_rows = a.rows / (64 * high) + experts / 2;
+    return (by_rows > experts ? by_rows : experts) * across;
+  };
+  if (a.dtype == MOE_DTYPE_BF16) {
+    if (tiles(4, 4) >= 200) {
+      const bool by_columns = product == MOE_EXPERTS_DH || product == MOE_EXPERTS_DX;
+      return {4, 4, by_columns && a.rows <= 512 * (int64_t)a.E};
+    }
+    if (tiles(2, 2) >= 256) return {2, 2, false};
+  }
+  return {1, product == MOE_EXPERTS_UP ? 2 : 1, false};
+}
+
+// Calls f with the shape that is picked.
+template <typename T, int PRODUCT, class F>
+hipError_t with_shape(const ExpertsArgs &a, F f) {
+  const Pick t = pick(a, PRODUCT);
+  if constexpr (sizeof(T) == 2) {
+    if constexpr (PRODUCT == MOE_EXPERTS_DH || PRODUCT == MOE_EXPERTS_DX)
+      if (t.stream) return f(Shape<4, 4, true>{});
+    if (t.high == 4) return f(Shape<4, 4>{});
+    if (t.high == 2) return f(Shape<2, 2>{});
+  }
+  return f(Shape<1, PRODUCT == MOE_EXPERTS_UP ? 2 : 1>{});
+}
 
 // Calls f with the saved kind as a constant.
 template <class F>
@@ -948,9 +960,8 @@ hipError_t run_up(const ExpertsArgs &a, T *h, hipStream_t s) {
   q.g.b_up = {a.w_up, a.d, a.I, a.d};
   q.b_expert = (int64_t)a.I * a.d * sizeof(T);
   q.g.kdim[0] = a.d;
-  return with_shape<T>(RowTiles(a, 2 * (int64_t)a.I), [&](auto sh) {
-    // two matrices share a tile
-    using SH = std::conditional_t<decltype(sh)::NI == 1, Shape<1, 2>, decltype(sh)>;
+  return with_shape<T, MOE_EXPERTS_UP>(a, [&](auto sh) {
+    using SH = decltype(sh);
     const dim3 grid = rows_grid<SH>(q, true);
     return with_kind(a.saved.kind, [&](auto kind) {
       const UpOut<T, kind> o = {h, a.saved, a.I, a.limit};
@@ -968,7 +979,7 @@ hipError_t run_down(const ExpertsArgs &a, const T *h, hipStream_t s) {
   q.b_expert = (int64_t)a.I * a.d * sizeof(T);
   q.g.kdim[0] = a.I;
   const SumsOut<T> o = {(T *)a.y, nullptr, a.d, 0};
-  return with_shape<T>(RowTiles(a, a.d), [&](auto sh) {
+  return with_shape<T, MOE_EXPERTS_DOWN>(a, [&](auto sh) {
     using SH = decltype(sh);
     const dim3 grid = rows_grid<SH>(q, false);
     hipLaunchKernelGGL((down_kernel<T, SH>), grid, dim3(256), 0, s, q, o);
@@ -983,7 +994,7 @@ hipError_t run_dh(const ExpertsArgs &a, T *dz, T *du, T *h, hipStream_t s) {
   q.g.b[0] = {a.w_down, a.I, a.d, a.I};
   q.b_expert = (int64_t)a.I * a.d * sizeof(T);
   q.g.kdim[0] = a.d;
-  return with_stream<T>(a, RowTiles(a, a.I), [&](auto sh) {
+  return with_shape<T, MOE_EXPERTS_DH>(a, [&](auto sh) {
     using SH = decltype(sh);
     const dim3 grid = rows_grid<SH>(q, false);
     if (a.saved.kind == MOE_SAVE_MXFP8) {
@@ -1008,7 +1019,7 @@ hipError_t run_dx(const ExpertsArgs &a, const T *dz, const T *du, hipStream_t s)
   q.g.kdim[0] = q.g.kdim[1] = a.I;
   q.g.segments = 2;
   const SumsOut<T> o = {(T *)a.dx, nullptr, a.d, 0};
-  return with_stream<T>(a, RowTiles(a, a.d), [&](auto sh) {
+  return with_shape<T, MOE_EXPERTS_DX>(a, [&](auto sh) {
     using SH = decltype(sh);
     const dim3 grid = rows_grid<SH>(q, false);
     hipLaunchKernelGGL((dx_kernel<T, SH>), grid, dim3(256), 0, s, q, o);
@@ -1017,7 +1028,7 @@ hipError_t run_dx(const ExpertsArgs &a, const T *dz, const T *du, hipStream_t s)
 }
 
 // A weight gradient [N, K] of every expert: columns of A (and A_up), columns of B.
-template <typename T>
+template <typename T, bool DOWN>
 hipError_t run_dw(const ExpertsArgs &a, const void *A, const void *A_up, int N, const void *B, int K,
                   void *dw, void *dw_up, hipStream_t s) {
   GroupedOp q = grouped_op(a, K);
@@ -1027,17 +1038,16 @@ hipError_t run_dw(const ExpertsArgs &a, const void *A, const void *A_up, int N, 
   q.g.M = N;
   q.g.halves = A_up ? 2 : 1;
   const SumsOut<T> o = {(T *)dw, (T *)dw_up, K, N};
-  auto tiles = [&](int high, int wide) {
-    return q.g.halves * (int64_t)a.E * ((N + 64 * high - 1) / (64 * high)) * ((K + 64 * wide - 1) / (64 * wide));
-  };
-  return with_shape<T>(tiles, [&](auto sh) {
+  auto run = [&](auto sh) {
     using SH = decltype(sh);
     q.g.m_tiles = (N + 64 * SH::HIGH - 1) / (64 * SH::HIGH) * q.g.halves;
     q.g.n_tiles = (K + 64 * SH::NI - 1) / (64 * SH::NI);
     const dim3 grid = held_grid<SH>(q.g.m_tiles * q.g.n_tiles * a.E);
     hipLaunchKernelGGL((dw_kernel<T, SH>), grid, dim3(256), 0, s, q, o);
     return hipGetLastError();
-  });
+  };
+  // one of gate and up alone takes the tiles of both, and comes out the same
+  return DOWN ? with_shape<T, MOE_EXPERTS_DW_DOWN>(a, run) : with_shape<T, MOE_EXPERTS_DW>(a, run);
 }
 
 template <typename T>
@@ -1054,12 +1064,12 @@ hipError_t run_backward(const ExpertsArgs &a, char *ws, hipStream_t s) {
   hipError_t err;
   if (a.rows > 0 && (err = run_dh<T>(a, dz, du, h, s)) != hipSuccess) return err;
   if (a.dw_down &&
-      (err = run_dw<T>(a, a.dy, nullptr, a.d, h, a.I, a.dw_down, nullptr, s)) != hipSuccess)
+      (err = run_dw<T, true>(a, a.dy, nullptr, a.d, h, a.I, a.dw_down, nullptr, s)) != hipSuccess)
     return err;
   if (a.dw_gate || a.dw_up) {
     // both in one launch, or the one that is wanted
     const bool both = a.dw_gate && a.dw_up;
-    if ((err = run_dw<T>(a, a.dw_gate ? dz : du, both ? du : nullptr, a.I, a.x, a.d,
+    if ((err = run_dw<T, false>(a, a.dw_gate ? dz : du, both ? du : nullptr, a.I, a.x, a.d,
                          a.dw_gate ? a.dw_gate : a.dw_up, a.dw_up, s)) != hipSuccess)
       return err;
   }
@@ -1068,6 +1078,11 @@ hipError_t run_backward(const ExpertsArgs &a, char *ws, hipStream_t s) {
 }
 
 }  // namespace
+
+moe_experts_path_info experts_path(const ExpertsArgs &a, int product) {
+  const Pick t = pick(a, product);
+  return {64 * t.high, 64 * t.ni, t.stream};
+}
 
 hipError_t launch_experts(const ExpertsArgs &a, char *ws, hipStream_t s) {
   return a.dtype == MOE_DTYPE_F32 ? run_forward<float>(a, ws, s) : run_forward<bf16>(a, ws, s);

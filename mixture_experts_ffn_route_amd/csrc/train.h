@@ -55,6 +55,7 @@ struct ExpertsSpace {
 ExpertsSpace experts_space(int64_t rows, int I, int dtype, bool backward);
 // Whether each launch of a call has fewer than 2^32 threads.
 bool experts_launchable(const ExpertsArgs &a, bool backward);
+moe_experts_path_info experts_path(const ExpertsArgs &a, int product);
 hipError_t launch_experts(const ExpertsArgs &a, char *ws, hipStream_t s);
 hipError_t launch_experts_backward(const ExpertsArgs &a, char *ws, hipStream_t s);
 

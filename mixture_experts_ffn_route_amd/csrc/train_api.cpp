@@ -281,4 +281,13 @@ int moe_experts_backward(const moe_config *cfg, const moe_weights *w, const void
   return hip_status(moe::launch_experts_backward(a, (char *)ws, (hipStream_t)stream));
 }
 
+int moe_experts_path(const moe_config *cfg, int64_t rows, int32_t product, moe_experts_path_info *info) {
+  moe::ExpertsArgs a;
+  const int st = check_experts(cfg, rows, nullptr, &a);
+  if (st != MOE_OK) return st;
+  if (!info || product < MOE_EXPERTS_UP || product > MOE_EXPERTS_DW) return MOE_ERR_INVALID_ARG;
+  *info = moe::experts_path(a, product);
+  return MOE_OK;
+}
+
 }  // extern "C"
