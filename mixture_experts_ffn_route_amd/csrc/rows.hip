@@ -56,11 +56,11 @@ __device__ __forceinline__ void narrow(T *p, const float (&f)[V]) {
   }
 }
 
-// Calls f(token)(first column) for this thread's pieces.  Rows of kTokenPieces and more
-// take a workgroup a token, whose indices are then scalars and whose waves read the
-// same rows at the same time (combine above 119 us, so 111); shorter ones have the
-// pieces of all tokens in one line (4096 tokens of 88 pieces 7.5 us, by tokens 8.9).
-constexpr uint32_t kTokenPieces = 192;
+// Calls f(token)(first column) for this thread's pieces.  Long rows of many tokens take
+// a workgroup a token, whose indices are then scalars and whose waves read the same
+// rows at the same time (combine above 119 us, so 111); otherwise the pieces of all
+// tokens stand in one line (4096 tokens of 88 pieces 7.5 us, by tokens 8.9; 64 tokens of
+// 896, dispatch, 6.4 and 8.0).
 template <int V, bool BY_TOKEN, class F>
 __device__ __forceinline__ void each_piece(const RowsArgs &a, uint32_t pieces, F f) {
   auto column = [&](uint32_t p) {
@@ -187,15 +187,16 @@ uint32_t pieces_of(int d, int V) { return (uint32_t)((d + V - 1) / V); }
 
 int waves_a_token(uint32_t pieces) { return pieces > 192 ? 4 : (int)((pieces + 63) / 64); }
 
+bool by_token(const RowsArgs &a, uint32_t pieces) { return pieces >= 192 && a.T >= 1024; }
 unsigned blocks_of(const RowsArgs &a, uint32_t pieces) {
-  return (unsigned)(pieces >= kTokenPieces ? a.T : (a.T * pieces + 255) / 256);
+  return (unsigned)(by_token(a, pieces) ? a.T : (a.T * pieces + 255) / 256);
 }
 
 template <typename T, int V>
 hipError_t run_dispatch(const RowsArgs &a, hipStream_t s) {
   const uint32_t n = pieces_of(a.d, V);
   const dim3 grid(blocks_of(a, n));
-  if (n >= kTokenPieces) hipLaunchKernelGGL((dispatch_kernel<T, V, true>), grid, dim3(256), 0, s, a, n);
+  if (by_token(a, n)) hipLaunchKernelGGL((dispatch_kernel<T, V, true>), grid, dim3(256), 0, s, a, n);
   else hipLaunchKernelGGL((dispatch_kernel<T, V, false>), grid, dim3(256), 0, s, a, n);
   return hipGetLastError();
 }
@@ -206,7 +207,7 @@ hipError_t run_combine(const RowsArgs &a, bool backward, hipStream_t s) {
   if (backward)
     hipLaunchKernelGGL((combine_backward_kernel<T, V, K>), dim3((unsigned)a.T),
                        dim3(64 * waves_a_token(n)), 0, s, a, n);
-  else if (n >= kTokenPieces)
+  else if (by_token(a, n))
     hipLaunchKernelGGL((combine_kernel<T, V, K, true>), grid, dim3(256), 0, s, a, n);
   else
     hipLaunchKernelGGL((combine_kernel<T, V, K, false>), grid, dim3(256), 0, s, a, n);
