@@ -698,17 +698,23 @@ def _checkpoint_check(where, name, m, codes, scales):
         raise ValueError(f"{where}: {name} is {tuple(m.shape)} {m.dtype}, "
                          f"expected a matrix in float32 or bfloat16")
     rows, cols = m.shape
-    if m.numel() and (m.stride(1) != 1 and cols > 1 or m.stride(0) < cols and rows > 1):
-        raise ValueError(f"{where}: {name}'s rows are not contiguous or overlap")
-    _tensors_check(where, (("codes", codes, (rows, cols), torch.uint8),
-                           ("scales", scales, (rows, -(-cols // 32)), torch.uint8)),
-                   launches=False)
-    for other, t in (("codes", codes), ("scales", scales)):
-        if t.device != m.device:
-            raise ValueError(f"{where}: {other} is on {t.device}, others on {m.device}")
+    ld, device = 0, m.device
+    if not m.is_contiguous():
+        ld, step = m.stride()
+        if step != 1 and cols > 1 or ld < cols and rows > 1:
+            raise ValueError(f"{where}: {name}'s rows are not contiguous or overlap")
+        ld = 0 if rows < 2 else ld
+    for other, t, shape in (("codes", codes, (rows, cols)), ("scales", scales, (rows, -(-cols // 32)))):
+        if t.dtype is not torch.uint8 or t.shape != shape:
+            raise ValueError(f"{where}: {other} is {tuple(t.shape)} {t.dtype}, "
+                             f"expected {shape} {torch.uint8}")
+        if not t.is_contiguous():
+            raise ValueError(f"{where}: {other} is not contiguous")
+        if t.device != device:
+            raise ValueError(f"{where}: {other} is on {t.device}, others on {device}")
     if rows:
-        _device_check(where, m.device)
-    return rows, cols, 0 if rows < 2 else m.stride(0)
+        _device_check(where, device)
+    return rows, cols, ld
 
 
 def moe_checkpoint_save(src, codes, scales, limit: float = 0.0, stream=None):
