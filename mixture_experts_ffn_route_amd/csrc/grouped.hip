@@ -65,9 +65,9 @@ struct GroupedItem {
 template <int HIGH>
 __device__ __forceinline__ int tiles_of(int n) { return ((n + 63) / 64 + HIGH - 1) / HIGH; }
 __device__ __forceinline__ void height_of(int blocks, int tiles, int i, GroupedItem *out) {
-  const int first = blocks * i / tiles;
-  out->m0 = first * 64;
-  out->blocks = blocks * (i + 1) / tiles - first;
+  const int low = blocks / tiles, higher = blocks - low * tiles;
+  out->m0 = (i * low + (i < higher ? i : higher)) * 64;
+  out->blocks = low + (i < higher ? 1 : 0);
 }
 
 // What the experts before each lane's own amount to (a lane has E / 64 of them, one
@@ -885,9 +885,10 @@ ExpertsSpace experts_space(int64_t rows, int I, int dtype, bool backward) {
 }
 
 bool experts_launchable(const ExpertsArgs &a, bool backward) {
-  // tiles are counted in 31 bits; the smallest are the most
-  const int64_t wide = a.d > a.I ? a.d : a.I, cols = (wide + 31) / 32;
-  const int64_t by_rows = most_blocks(a.rows, a.E) * cols;
+  // tiles are counted in 31 bits; the smallest are the most.  Offsets that are not
+  // ascending can give every second expert all rows.
+  const int64_t down = (a.d + 63) / 64, up = (a.I + 31) / 32;
+  const int64_t by_rows = (a.E + 1) / 2 * ((a.rows + 63) / 64) * (down > up ? down : up);
   const int64_t by_expert =
       backward ? 2 * (int64_t)a.E * ((a.d + 63) / 64) * ((a.I + 63) / 64) : 0;
   return by_rows < INT32_MAX && by_expert < INT32_MAX;

@@ -53,7 +53,7 @@ struct ExpertsSpace {
   size_t dz, du;               // backward: gradients of the gate and up products
 };
 ExpertsSpace experts_space(int64_t rows, int I, int dtype, bool backward);
-// Whether each launch of a call has fewer than 2^32 threads.
+// Whether the tiles of each launch can be counted, whatever the offsets hold.
 bool experts_launchable(const ExpertsArgs &a, bool backward);
 moe_experts_path_info experts_path(const ExpertsArgs &a, int product);
 hipError_t launch_experts(const ExpertsArgs &a, char *ws, hipStream_t s);

@@ -9,6 +9,7 @@
 namespace {
 
 constexpr size_t kAlign = 256;
+constexpr int32_t kMostColumns = INT32_MAX - 31;  // rounded up to whole pieces and blocks: 31 bits
 
 bool misaligned(const void *p, size_t n) { return (uintptr_t)p % n != 0; }
 int hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
@@ -40,7 +41,8 @@ int check_rows(const moe_config *c, int64_t T, int64_t R, const int32_t *inverse
   if (!c || c->dim < 1 || c->n_activated_experts < 1) return MOE_ERR_INVALID_ARG;
   if (c->act_dtype != MOE_DTYPE_F32 && c->act_dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
   if (T < 0 || R < 0) return MOE_ERR_INVALID_ARG;
-  if (c->n_activated_experts > 16 || T > INT32_MAX / c->n_activated_experts || R > INT32_MAX)
+  if (c->n_activated_experts > 16 || T > INT32_MAX / c->n_activated_experts || R > INT32_MAX ||
+      c->dim > kMostColumns)
     return MOE_ERR_UNSUPPORTED;
   *a = {};
   a->inverse = inverse;
@@ -66,7 +68,7 @@ int check_checkpoint(const void *m, int32_t dtype, int64_t rows, int32_t cols, i
   if (rows < 0 || cols < 1) return MOE_ERR_INVALID_ARG;
   if (ld == 0) ld = cols;
   if (ld < cols) return MOE_ERR_INVALID_ARG;
-  if (rows > INT32_MAX || ld > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if (rows > INT32_MAX || ld > INT32_MAX || cols > kMostColumns) return MOE_ERR_UNSUPPORTED;
   *a = {};
   a->rows = rows; a->cols = cols; a->ld = ld; a->dtype = dtype;
   if (rows == 0) return MOE_OK;
@@ -97,7 +99,7 @@ int check_experts(const moe_config *c, int64_t rows, const moe_experts_saved *sa
   if (c->dim % piece || c->moe_inter_dim % piece) return MOE_ERR_UNSUPPORTED;
   // a tile's rows are addressed with 32-bit byte offsets
   if (c->n_routed_experts > 1024 || c->dim > MOE_LINEAR_MAX_LD ||
-      c->moe_inter_dim > MOE_LINEAR_MAX_LD || rows > INT32_MAX)
+      c->moe_inter_dim > MOE_LINEAR_MAX_LD || rows > INT32_MAX - 1024)
     return MOE_ERR_UNSUPPORTED;
   if (saved && saved->kind == MOE_SAVE_MXFP8 && c->moe_inter_dim % 32) return MOE_ERR_UNSUPPORTED;
   *a = {};

@@ -161,6 +161,15 @@ def test_widths_of_whole_pieces(gpu, d, I):
         s.check_backward()
 
 
+def test_many_rows_of_one_expert(gpu):
+    """46879 blocks of 64 rows: a block's number times the tiles' passes 31 bits."""
+    s = Step([3_000_201, 7], 4, 4, "f32").to(gpu, "full")
+    s.forward()
+    s.backward()
+    s.check_forward()
+    s.check_backward()
+
+
 def test_without_saving(gpu):
     s = Step([30, 2, 0, 70], 64, 96, "bf16", spare=4).to(gpu, "none")
     s.forward()

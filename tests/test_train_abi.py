@@ -45,6 +45,7 @@ def test_rows_refuse_before_any_launch():
         assert call(T=1 << 30) == UNSUP                      # T k past 31 bits
         assert call(wide, T=1 << 16) == UNSUP                # 2^33 pieces of 16 bytes
         assert call(R=1 << 31) == UNSUP
+        assert call(replace(CFG, dim=(1 << 31) - 1), T=1) == UNSUP
         assert call(inv=None) == BAD and call(inv=at(2) + 2) == BAD
         assert call(T=0) == OK
     assert dispatch(x=None) == BAD and dispatch(rows=None) == BAD
@@ -78,6 +79,7 @@ def test_checkpoints_refuse_before_any_launch():
         assert call(dtype=2) == BAD and call(rows=-1) == BAD and call(cols=0) == BAD
         assert call(ld=39) == BAD
         assert call(rows=1 << 31) == UNSUP and call(rows=1 << 28, cols=1 << 10) == UNSUP
+        assert call(rows=1, cols=(1 << 31) - 1) == UNSUP and call(rows=1, cols=(1 << 31) - 31) == UNSUP
         assert call(codes=None) == BAD and call(scales=None) == BAD
         assert call(rows=0) == OK
     assert save(src=None) == BAD and load(dst=None) == BAD
@@ -120,6 +122,9 @@ def back(cfg=CFG, rows=10, x=at(1), off=at(2), dy=at(3), saved=(), ws=at(4), ws_
 @pytest.mark.parametrize("call", [experts, back])
 def test_experts_refuse_before_any_launch(call):
     assert call(rows=-1) == BAD and call(rows=1 << 31) == UNSUP
+    assert call(replace(CFG, n_routed_experts=1), rows=(1 << 31) - 64) == UNSUP
+    # offsets [0, rows, 0, rows, ..] would make more tiles than 31 bits count
+    assert call(replace(CFG, n_routed_experts=1024), rows=1 << 29) == UNSUP
     for change in (dict(dim=0), dict(n_routed_experts=0), dict(moe_inter_dim=0),
                    dict(swiglu_limit=-1.0), dict(swiglu_limit=float("inf")),
                    dict(swiglu_limit=float("nan")), dict(act_dtype="fp8")):
