@@ -906,6 +906,11 @@ namespace {
 // the bound at every shape, has 64 x 64 alone (2048 rows of 16 experts, 1024 -> 512, all
 // six: 315, with 128 x 128 363).  up has two matrices in a tile, 64 x 128 at least.
 //
+// The products forward of a few rows an expert are a stream of weights, and take 64 x 256,
+// of which two workgroups fit a CU: up and down of 64 rows of 32 experts, 7168 -> 2 x 2048,
+// 319 and 141 with 256 x 256, so 303 and 134; 512 rows of 48, 5120 -> 2 x 1536, 340 and 152,
+// so 319 and 144.
+//
 // Weights by columns are streamed where an expert has two row tiles of the largest on
 // the mean, or fewer.
 struct Pick {
@@ -924,6 +929,8 @@ Pick pick(const ExpertsArgs &a, int product) {
     return (by_rows > experts ? by_rows : experts) * across;
   };
   if (a.dtype == MOE_DTYPE_BF16) {
+    if (product <= MOE_EXPERTS_DOWN && a.rows <= 16 * (int64_t)a.E && tiles(1, 4) >= 200)
+      return {1, 4, false};
     if (tiles(4, 4) >= 200) {
       const bool by_columns = product == MOE_EXPERTS_DH || product == MOE_EXPERTS_DX;
       return {4, 4, by_columns && a.rows <= 512 * (int64_t)a.E};
@@ -940,6 +947,8 @@ hipError_t with_shape(const ExpertsArgs &a, F f) {
   if constexpr (sizeof(T) == 2) {
     if constexpr (PRODUCT == MOE_EXPERTS_DH || PRODUCT == MOE_EXPERTS_DX)
       if (t.stream) return f(Shape<4, 4, true>{});
+    if constexpr (PRODUCT <= MOE_EXPERTS_DOWN)
+      if (t.high == 1 && t.ni == 4) return f(Shape<1, 4>{});
     if (t.high == 4) return f(Shape<4, 4>{});
     if (t.high == 2) return f(Shape<2, 2>{});
   }

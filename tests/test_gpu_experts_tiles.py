@@ -12,11 +12,15 @@ from tests.test_gpu_experts import GRADS, Step
 pytestmark = pytest.mark.gpu
 
 LARGE, STREAMED, MIDDLE, SMALL = (256, 256, False), (256, 256, True), (128, 128, False), (64, 64, False)
+FLAT = (64, 256, False)
+FEW = [(i * 5) % 9 for i in range(62)] + [130, 65]
 MANY = [(i * 37) % 90 for i in range(66)] + [330, 256, 257, 193]
 
 CASES = [
     # every height, most experts with little; 210 to 1050 tiles on 256 CUs
     (MANY, 520, 544, dict(up=LARGE, down=LARGE, dh=STREAMED, dx=STREAMED, dw_down=LARGE, dw=LARGE)),
+    # a few rows an expert: 64 x 256, 320 and more tiles; two experts with several
+    (FEW, 1032, 544, dict(up=FLAT, down=FLAT, dh=MIDDLE)),
     # one expert: weights read by five row tiles; 275 tiles, the last rounds cut in four
     ([1100], 14080, 32, dict(down=LARGE, dx=LARGE, up=(64, 128, False))),
     ([1100], 32, 14080, dict(up=LARGE, dh=LARGE, down=SMALL)),
