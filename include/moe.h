@@ -1,7 +1,8 @@
 /*
  * moe.h -- C ABI of the MI355X (gfx950) mixture-of-experts feed-forward layer.
  *
- * The library computes the forward pass of a DeepSeek-style MoE FFN layer:
+ * The library computes the forward pass of a DeepSeek-style MoE FFN layer, and has the
+ * operators that train one (moe_dispatch, moe_experts, moe_combine and their gradients):
  *
  *   y[t] = cast( sum_j w[t,j] * FFN_{idx[t,j]}(x[t]) + FFN_shared(x[t]) )
  *   FFN(u) = W_down( SiLU(min(W_gate u, L)) * clamp(W_up u, -L, L) )

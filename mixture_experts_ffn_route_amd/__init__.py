@@ -1,4 +1,5 @@
-"""MI355X-native (gfx950) DeepSeek-style MoE feed-forward layer forward pass.
+"""MI355X-native (gfx950) DeepSeek-style MoE feed-forward layer: its forward pass and
+the operators that train it.
 
 The compute path is the HIP library ``libmoe_mi355x.so`` (C ABI in
 ``include/moe.h``); ``binding`` is its thin Python binding.  ``config`` holds
