@@ -14,8 +14,8 @@
 //   dWg, dWu  A = dz, du by columns, B = x by columns, one launch
 //
 // Where an expert's rows begin is known on the device alone: every workgroup scans
-// the offsets once (one wave's prefix sum over the experts' 64-row blocks) and takes
-// an equal share of the blocks, so nothing waits for a list.  Offsets are clamped to
+// the offsets once (a wave's prefix sum over the experts' tiles) and finds its tiles by
+// that, so nothing waits for a list.  Offsets are clamped to
 // [0, rows] and to ascending ones, so whatever they hold no access is out of range.
 //
 // Workgroups are as many as the GPU holds at once and walk their tiles one after
