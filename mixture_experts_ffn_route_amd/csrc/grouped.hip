@@ -28,6 +28,7 @@
 #include "keep.h"
 #include "tile.h"
 #include "train.h"
+#include "walk.h"
 
 namespace moe {
 namespace {
@@ -568,16 +569,16 @@ __device__ __forceinline__ void walk(const GemmOp &g, const OUT &out, NEXT next,
       asm volatile("" ::: "memory");           // each one its own: they are counted
     }
   };
-  GroupedItem it, nx;
-  if (!next(&it)) return;
+  GroupedItem first;
+  if (!next(&first)) return;
   Feed<T, SH, AC, BC, DUAL> f(g, L0, L1, L2, L3);
   const int lane = f.lane, wave = f.wave, wm = wave >> 1, wn = wave & 1;
-  aim(f, it, it.nt * 64 * NJ);
+  aim(f, first, first.nt * 64 * NJ);
   f.template start<0, PRE>();
   __builtin_amdgcn_sched_barrier(0);
   no_stores(STORES);
   __builtin_amdgcn_sched_barrier(0);
-  auto body = [&](auto height) {
+  walk_tiles<HIGH>(first, [&](auto height, const GroupedItem &it, GroupedItem &nx) {
     constexpr int MI = decltype(height)::value;
     f32x16 acc[MI][NI];
     sums<MI, PRE, STORES>(f, acc);
@@ -703,21 +704,8 @@ __device__ __forceinline__ void walk(const GemmOp &g, const OUT &out, NEXT next,
       ask();
     }
     __builtin_amdgcn_sched_barrier(0);
-    it = nx;
     return more;
-  };
-  for (;;) {
-    bool more = false;
-    if (it.blocks == 1) more = body(std::integral_constant<int, 1>{});
-    if constexpr (HIGH >= 2) {
-      if (it.blocks == 2) more = body(std::integral_constant<int, 2>{});
-    }
-    if constexpr (HIGH >= 4) {
-      if (it.blocks == 3) more = body(std::integral_constant<int, 3>{});
-      if (it.blocks == 4) more = body(std::integral_constant<int, 4>{});
-    }
-    if (!more) break;
-  }
+  });
   __builtin_amdgcn_s_waitcnt(0);               // no copy into LDS outlives the workgroup
 }
 
