@@ -672,7 +672,7 @@ int moe_checkpoint_load(const uint8_t *codes, const uint8_t *scales, int32_t dty
  *             leaves) are neither read nor written, here and in the gradient
  *   offsets   [E + 1] int32 on the device, as moe_permute writes it.  Values outside
  *             [0, rows] or descending ones are clamped: no access is out of range
- *             (2^31 - 1024 rows and more, and sizes that could come to 2^31
+ *             (2^31 - 1024 rows and more, and sizes that could come near 2^31
  *             tiles, are MOE_ERR_UNSUPPORTED)
  *   saved     where z and u go for the gradient: kind FULL in fp32, as they are; kind
  *             MXFP8 as moe_checkpoint_save with limit L keeps them, in a quarter of

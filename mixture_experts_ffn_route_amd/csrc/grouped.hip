@@ -874,13 +874,14 @@ ExpertsSpace experts_space(int64_t rows, int I, int dtype, bool backward) {
 }
 
 bool experts_launchable(const ExpertsArgs &a, bool backward) {
-  // tiles are counted in 31 bits; the smallest are the most.  Offsets that are not
-  // ascending can give every second expert all rows.
-  const int64_t down = (a.d + 63) / 64, up = (a.I + 31) / 32;
-  const int64_t by_rows = (a.E + 1) / 2 * ((a.rows + 63) / 64) * (down > up ? down : up);
+  // Tiles are counted in 31 bits, by workgroups that step past the last; the smallest are
+  // the most.  Offsets that are not ascending can give every second expert all rows, and
+  // where experts follow one another each can have a block that is not whole.
+  const int64_t down = (a.d + 63) / 64, up = (a.I + 31) / 32, most = INT32_MAX - 1024;
+  const int64_t by_rows = ((a.E + 1) / 2 * (a.rows / 64) + a.E) * (down > up ? down : up);
   const int64_t by_expert =
       backward ? 2 * (int64_t)a.E * ((a.d + 63) / 64) * ((a.I + 63) / 64) : 0;
-  return by_rows < INT32_MAX && by_expert < INT32_MAX;
+  return by_rows < most && by_expert < most;
 }
 
 namespace {

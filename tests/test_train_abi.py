@@ -150,6 +150,25 @@ def test_experts_refuse_before_any_launch(call):
     assert call(ws=at(1) + 256) == BAD                       # inside x
 
 
+@pytest.mark.parametrize("E,d,I", [(2, 64, 1 << 20), (4, 64, 1 << 20), (1024, 64, 1 << 20),
+                                   (1024, 1 << 20, 64), (1, 64, 1 << 20), (7, 1 << 20, 64)])
+def test_experts_tiles_can_be_counted(E, d, I):
+    """Of the largest sizes that are taken the tiles stay below 2^31, whatever the offsets:
+    expert after expert all rows and none, two neighbours with a block of 64 rows
+    more than their rows make, and room for workgroups that step past the last."""
+    cfg, lo, hi = replace(CFG, n_routed_experts=E, dim=d, moe_inter_dim=I), 0, 1 << 25
+    while hi - lo > 1:                                       # blocks of 64 rows
+        mid = (lo + hi) // 2
+        lo, hi = (mid, hi) if B.moe_experts_workspace_size(cfg, 64 * mid) else (lo, mid)
+    rows = 64 * lo
+    assert lo > 100 and B.moe_experts_workspace_size(cfg, rows + 64) == 0
+    offsets = [0] if E % 2 else [0, 1]
+    while len(offsets) <= E:
+        offsets.append(0 if offsets[-1] == rows else rows)
+    blocks = sum(-(-max(b - a, 0) // 64) for a, b in zip(offsets, offsets[1:]))
+    assert blocks * max(-(-d // 64), -(-I // 32)) < (1 << 31) - 1024
+
+
 def test_experts_overlaps():
     assert experts(y=at(1)) == BAD and experts(y=at(1) + 64) == BAD and experts(y=at(12) + 16) == BAD
     assert experts(saved=kept(up=at(20) + 32)) == BAD        # z's codes run into u's
