@@ -635,7 +635,8 @@ int moe_combine(const moe_config *cfg, const void *rows, const int32_t *inverse,
                 const void *add, int64_t T, int64_t R, void *y, void *stream);
 /* drows[inverse[t, j]] = weights[t, j] dy[t] (other rows are left alone) and
  * dweights[t, j] = rows[inverse[t, j]] . dy[t] (0 where a pair has no row).  Either
- * may be NULL: not wanted; rows is read for dweights alone, weights for drows. */
+ * may be NULL: not wanted (both: only where T or R is 0); rows is read for dweights
+ * alone, weights for drows. */
 int moe_combine_backward(const moe_config *cfg, const void *dy, const void *rows,
                          const int32_t *inverse, const float *weights, int64_t T, int64_t R,
                          void *drows, float *dweights, void *stream);
@@ -713,7 +714,8 @@ int moe_experts(const moe_config *cfg, const moe_weights *w, const void *x, cons
  * rows gets zeros.  w_down is always read, w_gate and w_up for dx, x for dw_gate and
  * dw_up; w's others may be NULL.  dz, du and h are rounded to the type once, as the
  * products take them.  ws: moe_experts_workspace_size(cfg, rows, 1) bytes.
- * rows == 0 writes zeros to the weight gradients. */
+ * rows == 0 writes zeros to the weight gradients that are wanted, and dx, empty, may be
+ * NULL. */
 int moe_experts_backward(const moe_config *cfg, const moe_weights *w, const void *x,
                          const int32_t *offsets, int64_t rows, const void *dy,
                          const moe_experts_saved *saved, const moe_experts_grads *grads, void *ws,

@@ -179,8 +179,8 @@ int moe_combine_backward(const moe_config *cfg, const void *dy, const void *rows
   moe::RowsArgs a;
   const int st = check_rows(cfg, T, R, inverse, &a);
   if (st != MOE_OK) return st;
-  if (!drows && !dweights) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
+  if (!drows && !dweights) return R > 0 ? MOE_ERR_INVALID_ARG : MOE_OK;   // drows is empty
   const RowsMemory m(a);
   if (!dy || misaligned(dy, m.es) || (drows && !weights) || (dweights && !rows && R > 0))
     return MOE_ERR_INVALID_ARG;
@@ -257,7 +257,8 @@ int moe_experts_backward(const moe_config *cfg, const moe_weights *w, const void
   int st = check_experts(cfg, rows, saved, &a);
   if (st != MOE_OK) return st;
   if (!w || !g || !offsets || misaligned(offsets, 4)) return MOE_ERR_INVALID_ARG;
-  if (!g->dx && !g->dw_gate && !g->dw_up && !g->dw_down) return MOE_ERR_INVALID_ARG;
+  if (!g->dx && !g->dw_gate && !g->dw_up && !g->dw_down)
+    return rows > 0 ? MOE_ERR_INVALID_ARG : MOE_OK;                       // dx is empty
   const bool up = g->dw_gate || g->dw_up;
   if (rows > 0) {
     if (!saved || saved->kind == MOE_SAVE_NONE || !dy || !w->w_down) return MOE_ERR_INVALID_ARG;

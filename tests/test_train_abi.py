@@ -182,6 +182,20 @@ def test_experts_overlaps():
     assert back(dw_gate=at(31) + 8) == BAD and back(dy=at(3) + 8) == BAD
 
 
+def test_gradients_of_nothing():
+    """Outputs without elements have no address: a rank without tokens, or without a row,
+    makes the same calls."""
+    assert combine_back(T=0, R=0, drows=None, dw=None) == OK
+    assert combine_back(T=0, dw=None) == OK and combine_back(T=0, R=0, dy=None, rows=None) == OK
+    assert combine_back(R=0, rows=None, drows=None, dw=None) == OK
+    assert combine_back(T=0, drows=None, dw=None, inv=None, w=None) == OK
+    assert combine_back(T=-1, drows=None, dw=None) == BAD
+    none, inv, w = bf(0, 64), torch.zeros((0, 2), dtype=torch.int32), torch.zeros((0, 2))
+    B.moe_combine_backward(CFG, none, none, inv, w, 0, drows=none.clone(), dweights=w.clone(), stream=0)
+    assert back(rows=0, dx=None, dw_gate=None, dw_up=None, dw_down=None) == OK
+    assert back(rows=0, off=None, dx=None, dw_gate=None, dw_up=None, dw_down=None) == BAD
+
+
 def test_experts_workspace():
     one = B.moe_experts_workspace_size(CFG, 1000)
     assert one >= 1000 * 96 * 2 and one % 256 == 0
