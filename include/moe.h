@@ -646,10 +646,13 @@ int moe_combine_backward(const moe_config *cfg, const void *dy, const void *rows
  * consecutive columns of a row (fewer at its end) one E8M0 scale byte X + 127 and
  * E4M3 codes of v / 2^X, nearest value, ties to even; X is the least integer >= -127
  * with max|v| <= 448 2^X, 0 for a block of zeros: nothing saturates, a value is off
- * by 2^-4 of itself at most (below 2^-6 2^X: by 2^-10 2^X).
+ * by 2^-4 of itself at most (below 2^-6 2^X: by 2^-10 2^X; at the top of the range see
+ * below).
  * limit > 0: no value is carried across +-limit (the next code on the value's side
  * is taken), because the gradient of a clamp goes by the saved value; 0: no clamp.
- * NaN and infinities are kept as NaN and do not count for X.
+ * NaN and infinities are kept as NaN and do not count for X.  Finite values from
+ * 1.9375 2^127 on in magnitude, and those above a limit that is 1.875 2^127 or more, take
+ * the code of 2^128 and come back as infinities of their sign.
  *   src, dst  [rows, cols] dtype (F32 or BF16), row stride ld elements (0: cols)
  *   codes     [rows, cols] bytes;   scales  [rows, ceil(cols / 32)] bytes
  * Any sizes (to 2^31 - 32 columns, and below 2^32 pieces of 16 bytes) and strides;

@@ -14,6 +14,9 @@
 // value above L is below or at 448 2^X.
 //
 // NaN and infinities take the NaN code, and amax is that of the other values.
+//
+// The largest X is 120.  There the nearest code of values from 248 2^120 = 1.9375 2^127 on
+// is 256, whose value 2^128 no float holds: they come back as infinities.
 #pragma once
 
 #include "common.h"

@@ -83,6 +83,31 @@ def test_no_value_is_carried_across_the_limit(gpu, limit):
         assert ((back.double().abs() > limit) == (src.double().abs() > limit)).all()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_the_top_of_the_range(gpu, dtype):
+    """From 1.9375 2^127 on the nearest code is that of 2^128, an infinity; below, finite
+    values stay finite, on their side of the limit."""
+    dt, top = H.TDT[dtype], 1.9375 * 2.0 ** 127
+    below = top * (1 - torch.finfo(dt).eps / 2)               # the value before it: halfway in its binade
+    src = torch.tensor([[below, -below, 1.875 * 2.0 ** 127, 1.8125 * 2.0 ** 127, 2.0 ** 127, -1.0],
+                        [top, -top, torch.finfo(dt).max, torch.finfo(dt).min, 0.0, below]],
+                       dtype=torch.float64).to(dt)
+    assert ((src.double().abs() >= top).sum(1) == torch.tensor([0, 4])).all()
+    compare(src, 0.0, gpu)
+    back = run(src, 0.0, gpu)[2]
+    assert (back.isinf() == (src.double().abs() >= top)).all()
+    for limit in (2.0 ** 127, 1.8125 * 2.0 ** 127, 1.85 * 2.0 ** 127, 1.9 * 2.0 ** 127, top):
+        limit = torch.tensor(limit, dtype=torch.float32).item()
+        compare(src, limit, gpu)
+        back = run(src, limit, gpu)[2].double()
+        over = src.double().abs() > limit
+        assert ((back.abs() > limit) == over).all()
+        if limit < 1.875 * 2.0 ** 127:
+            assert (back.isinf() == (src.double().abs() >= top)).all()
+        else:
+            assert (back.isinf() == over).all()
+
+
 def test_nothing_is_written_past_the_last_row(gpu):
     codes = torch.full((11 * 40 + 64,), 0xEE, dtype=torch.uint8, device=gpu)
     scales = torch.full((11 * 2 + 64,), 0xEE, dtype=torch.uint8, device=gpu)

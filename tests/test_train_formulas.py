@@ -62,3 +62,16 @@ def test_permutation_is_one():
     inverse, R = H.permutation(20, 3, 8, H.gen(1), 0.2)
     rows = inverse[inverse >= 0].sort()[0]
     assert R < 60 and rows.tolist() == list(range(R))
+
+
+def test_encode_at_the_top_of_the_range():
+    top, step = 1.9375 * 2.0 ** 127, 2.0 ** 104               # fp32's step there
+    src = torch.tensor([[top - step, -(top - step), 1.0, 0.0], [top, -top, 2.0 ** 127, 3.0],
+                        [torch.finfo(torch.float32).max, 0.0, 0.0, 0.0]])
+    codes, scales = H.encode(src)
+    assert (scales == 247).all()
+    back = H.decode(codes, scales).float()
+    inf = src.abs() >= top
+    assert (back.isinf() == inf).all() and (back[inf].sign() == src[inf].sign()).all()
+    err = (back.double() - src.double()).abs()[~inf]
+    assert (err <= torch.maximum(src.double().abs()[~inf] / 16, torch.tensor(2.0 ** 110))).all()
