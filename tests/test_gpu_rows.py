@@ -79,6 +79,21 @@ def test_rows(gpu, T, d, k, E, dropped, dtype):
         assert torch.equal(t.cpu(), h)
 
 
+# 1024 tokens and rows of 192 pieces of 16 bytes (1529 columns in bf16, 765 in fp32) take
+# a workgroup a token: both sides of either border, odd widths, every number of slots
+MANY = [(1024, 1529, 1, 4, 0.0), (1024, 1528, 2, 4, 0.1), (1023, 1601, 3, 8, 0.1),
+        (1024, 1601, 3, 8, 0.1), (1027, 765, 4, 8, 0.0), (1024, 764, 4, 8, 0.1),
+        (1025, 801, 5, 8, 0.3), (1024, 4099, 2, 8, 0.0), (1031, 1601, 8, 16, 0.5),
+        (1024, 1537, 7, 9, 0.02), (1100, 2048, 9, 16, 0.1), (1040, 1544, 16, 24, 0.3),
+        (2000, 1600, 6, 12, 1.0)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,d,k,E,dropped", MANY)
+def test_rows_of_many_tokens(gpu, T, d, k, E, dropped, dtype):
+    test_rows(gpu, T, d, k, E, dropped, dtype)
+
+
 def test_rows_out_of_range_take_no_part(gpu):
     cfg = config(24, 3, 8, "bf16")
     inverse, R, x, rows, w, _ = inputs(50, 24, 3, 8, 0.0, "bf16", spare=0)
