@@ -53,6 +53,22 @@ def test_tiles(gpu, case, kind):
     assert all(torch.equal(a, b) for a, b in zip(first, [s.y] + [s.grads[n] for n in GRADS]))
 
 
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_tiles_without_saving(gpu, case):
+    """Nothing saved: kernels of their own for every tile of up, the same y."""
+    counts, d, I, paths = CASES[case]
+    print(f"[tiles] rows={sum(counts)} E={len(counts)} d={d} I={I} none", flush=True)
+    s = Step(counts, d, I, "bf16", spare=3, limit=1.5 if case % 2 else 0.0).to(gpu, "full")
+    s.forward()
+    s.check_forward()
+    want = s.y.clone()
+    s.kind = "none"
+    s.y.fill_(-7.0)
+    s.ws.fill_(0xFF)
+    s.forward()
+    assert torch.equal(s.y, want)
+
+
 def test_1024_experts(gpu):
     """More experts than lanes: each lane scans sixteen."""
     counts = [(i * 7) % 5 if i % 3 else 0 for i in range(1024)]
