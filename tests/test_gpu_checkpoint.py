@@ -125,6 +125,37 @@ def test_empty(gpu):
     B.moe_checkpoint_load(u8, u8[:, :2].contiguous(), none)
 
 
+# from 2^22 pieces of 16 bytes on (whole blocks of 32 columns) a thread takes four; none
+# of these fills its last workgroup
+@pytest.mark.parametrize("limit", [0.0, 7.0])
+@pytest.mark.parametrize("rows,cols,pad,dtype", [
+    (5003, 3361, 3, "f32"), (9905, 3361, 5, "bf16"), (524_289, 6, 0, "f32"), (1_048_577, 27, 2, "bf16"),
+    (1, 16_777_250, 0, "f32"), (3, 11_184_850, 1, "bf16")])
+def test_large_matrices(gpu, rows, cols, pad, dtype, limit):
+    pieces = rows * -(-cols // 32) * (8 if dtype == "f32" else 4)
+    assert 1 << 22 <= pieces < 5 << 20 and pieces % 1024
+    print(f"[checkpoint] {rows}x{cols}+{pad} {dtype} limit {limit}", flush=True)
+    g = torch.Generator(device=gpu)
+    g.manual_seed(rows + cols)
+    dt = H.TDT[dtype]
+    wide = torch.full((rows, cols + pad), 123.0, dtype=dt, device=gpu)
+    std = torch.exp2(torch.randint(-3, 5, (rows, 1), device=gpu, generator=g).float())
+    wide[:, :cols] = torch.randn((rows, cols), device=gpu, generator=g) * std
+    codes = torch.full((rows * cols + 64,), 0xEE, dtype=torch.uint8, device=gpu)
+    scales = torch.full((rows * -(-cols // 32) + 64,), 0xEE, dtype=torch.uint8, device=gpu)
+    c, s = codes[:-64].view(rows, cols), scales[:-64].view(rows, -1)
+    B.moe_checkpoint_save(wide[:, :cols], c, s, limit=limit)
+    assert (codes[-64:] == 0xEE).all() and (scales[-64:] == 0xEE).all()
+    want, want_scales = H.encode_whole(wide[:, :cols], limit)
+    assert torch.equal(s, want_scales) and torch.equal(c, want)
+    back = torch.full((rows + 1, cols + pad), 123.0, dtype=dt, device=gpu)
+    B.moe_checkpoint_load(c, s, back[:rows, :cols])
+    values = H.VALUES.to(gpu)[want.long()]
+    unit = torch.exp2(want_scales.double() - 127).repeat_interleave(32, dim=1)[:, :cols]
+    assert torch.equal(back[:rows, :cols], (values * unit).to(dt))
+    assert (back[rows] == 123).all() and (back[:, cols:] == 123).all()
+
+
 def test_positions_past_32_bits(gpu):
     rows, cols = 70_000, 65_536                              # 4.6e9 values
     src = torch.zeros((rows, cols), dtype=torch.bfloat16, device=gpu)

@@ -64,6 +64,17 @@ def test_permutation_is_one():
     assert R < 60 and rows.tolist() == list(range(R))
 
 
+@pytest.mark.parametrize("limit", [0.0, 7.0])
+def test_encode_of_whole_blocks(limit):
+    g = H.gen(6)
+    src = torch.randn((40, 101), generator=g) * torch.exp2(torch.randint(-140, 100, (40, 1), generator=g))
+    src[3] = 0.0
+    src[::2] = torch.randn((20, 101), generator=g) * 7
+    for dt in (torch.float32, torch.bfloat16):
+        for a, b in zip(H.encode(src.to(dt), limit), H.encode_whole(src.to(dt), limit)):
+            assert torch.equal(a, b)
+
+
 def test_encode_at_the_top_of_the_range():
     top, step = 1.9375 * 2.0 ** 127, 2.0 ** 104               # fp32's step there
     src = torch.tensor([[top - step, -(top - step), 1.0, 0.0], [top, -top, 2.0 ** 127, 3.0],

@@ -94,6 +94,28 @@ def encode(src, limit=0.0):
     return codes, scales
 
 
+def encode_whole(src, limit=0.0):
+    """encode() of finite values in whole blocks at once, where the matrix is."""
+    rows, cols = src.shape
+    v = torch.zeros((rows, -(-cols // 32) * 32), dtype=torch.float64, device=src.device)
+    v[:, :cols] = src
+    v = v.reshape(rows, -1, 32)
+    m, e = torch.frexp(v.abs().amax(dim=2))
+    x = torch.where(m > 0, (e - 9 + (m > 0.875)).clamp(min=-127), 0)
+    unit = torch.exp2(x.double()).unsqueeze(2)
+    mags, a = VALUES[:127].to(src.device), v.abs() / unit
+    hi = torch.searchsorted(mags, a.contiguous()).clamp(max=126)
+    lo = (hi - 1).clamp(min=0)
+    below, above = a - mags[lo], mags[hi] - a
+    code = torch.where((above < below) | ((above == below) & (hi % 2 == 0)), hi, lo)
+    if limit > 0:
+        edge = limit / unit
+        code = torch.where((a > edge) & (mags[code] <= edge), hi, code)
+        code = torch.where((a <= edge) & (mags[code] > edge), lo, code)
+    code = (code + 128 * torch.signbit(v)).to(torch.uint8).reshape(rows, -1)[:, :cols]
+    return code.contiguous(), (x + 127).to(torch.uint8)
+
+
 def decode(codes, scales):
     unit = torch.exp2(scales.double() - 127).repeat_interleave(32, dim=1)[:, :codes.shape[1]]
     return VALUES[codes.long()] * unit
