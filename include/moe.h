@@ -619,9 +619,9 @@ int moe_linear_path(const moe_linear_config *cfg, int32_t product, moe_linear_pa
  * Sums are fp32, over the slots in order; results are rounded once and do not
  * depend on what else runs.  Alignment: an element's size.  No output may overlap
  * an input or another output.  T == 0 is a no-op.  Sizes whose launch would have 2^32
- * threads (a thread takes 16 bytes of a token's row), or with dim past 2^31 - 32, are
- * MOE_ERR_UNSUPPORTED.  Only kernels are enqueued, so the calls can be captured in a
- * HIP graph.
+ * threads (a thread takes 16 bytes of a token's row, and 2^24 tokens can have as many), or
+ * with dim past 2^31 - 32, are MOE_ERR_UNSUPPORTED.  Only kernels are enqueued, so the
+ * calls can be captured in a HIP graph.
  *
  * rows[inverse[t, j]] = x[t]; sorted rows that stand in no pair are left alone. */
 int moe_dispatch(const moe_config *cfg, const void *x, const int32_t *inverse, int64_t T, int64_t R,
@@ -675,9 +675,10 @@ int moe_checkpoint_load(const uint8_t *codes, const uint8_t *scales, int32_t dty
  *   x, y      [rows, dim]; rows of no expert (rows >= offsets[E]: room that a batch
  *             leaves) are neither read nor written, here and in the gradient
  *   offsets   [E + 1] int32 on the device, as moe_permute writes it.  Values outside
- *             [0, rows] or descending ones are clamped: no access is out of range
- *             (2^31 - 1024 rows and more, and sizes that could come near 2^31
- *             tiles, are MOE_ERR_UNSUPPORTED)
+ *             [0, rows] are clamped, and an expert that ends before it starts has no
+ *             rows: no access is out of range, but rows that two experts then share
+ *             have either's result (2^31 - 1024 rows and more, and sizes that could
+ *             come near 2^31 tiles, are MOE_ERR_UNSUPPORTED)
  *   saved     where z and u go for the gradient: kind FULL in fp32, as they are; kind
  *             MXFP8 as moe_checkpoint_save with limit L keeps them, in a quarter of
  *             the memory (I % 32 == 0).  NULL or kind NONE: not saved

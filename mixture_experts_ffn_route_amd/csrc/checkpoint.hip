@@ -41,9 +41,8 @@ __device__ __forceinline__ int64_t scale_of(const CheckpointArgs &a, const Piece
   return p.row * ((a.cols + 31) / 32) + p.col / 32;
 }
 
-// U pieces a thread, a workgroup's width apart, all read before the first is written:
-// with one, what the waves that fit a CU have under way does not cover the memory's
-// latency.
+// U pieces a thread, a workgroup's width apart, all read before the first is written, so
+// that the waves that fit a CU have more under way.
 template <typename T, int U>
 __global__ __launch_bounds__(256) void save_kernel(const CheckpointArgs a, uint32_t per_row) {
   constexpr int N = kN<T>;
@@ -134,7 +133,15 @@ uint32_t pieces_per_row(const CheckpointArgs &a) {
   return (uint32_t)((a.cols + 31) / 32 * (a.dtype == MOE_DTYPE_F32 ? 8 : 4));
 }
 
-// Pieces a thread: four where that leaves every CU sixteen workgroups.
+// Pieces a thread: four where that leaves every CU sixteen workgroups.  us with one and with
+// four, the same matrix again and again, so that what fits the last cache stays there:
+//   1536 columns in bf16   save             load
+//        16384 rows        15.1 and 19.0     8.9 and 9.7
+//        21900             17.7 and 20.2    16.0 and 15.5      (from here on four)
+//        65536             59.3 and 60.1    44.6 and 43.6
+//       262144              234 and 221      202 and 205
+//   65536 x 2048 in fp32   saved and loaded in turn 234 and 226
+// so load gains little from the border on, save from where the matrix passes that cache.
 template <typename T, class F1, class F4>
 hipError_t run(const CheckpointArgs &a, F1 one, F4 four, hipStream_t s) {
   const uint32_t per = pieces_per_row(a);

@@ -15,8 +15,9 @@
 //
 // Where an expert's rows begin is known on the device alone: every workgroup scans
 // the offsets once (a wave's prefix sum over the experts' tiles) and finds its tiles by
-// that, so nothing waits for a list.  Offsets are clamped to
-// [0, rows] and to ascending ones, so whatever they hold no access is out of range.
+// that, so nothing waits for a list.  Offsets are clamped to [0, rows], and an expert that
+// ends before it starts has no rows, so whatever they hold no access is out of range.
+// (After such a descent an expert's rows can be another's too, and its results either's.)
 //
 // Workgroups are as many as the GPU holds at once and walk their tiles one after
 // another: starting a workgroup for every tile left 2.6 us between one's end and the
@@ -132,10 +133,8 @@ __device__ __forceinline__ void move(Matrix &m, const GroupedItem &it) {
 // The nontemporal policy: of results, and of weights that one or two row tiles read, by
 // columns (whole lines at a time), so that they leave the caches to the rows that tiles
 // share.  8192 rows of 48 experts, 5120 -> 2 x 1536: all six products 2267 us, the
-// results so 2136, the weights of dh and dx too 2015.  With 1024 rows an expert the
-// weights are read by four row tiles, and dh takes 117 us, so 129.  Weights read by
-// rows come half a line a stage, and such a line is gone before its other half is
-// needed (up 215, so 234).
+// results so 2136, the weights of dh and dx too 2015.  Weights read by rows come half a line
+// a stage, and such a line is gone before its other half is needed (up 215, so 234).
 constexpr int kStream = 2;
 
 // Rows that a tile reads or writes, from its first.
@@ -888,20 +887,47 @@ namespace {
 
 // Tile shape of a product: the largest tiles of which there are about as many as CUs,
 // counting for a product over rows experts with the mean's rows and half a tile each
-// left over.  bf16, microseconds, each shape forced on 14 problems (90 products): the
-// rule loses 2.5 % on the mean to the best of them, 21 % at most; on 4096 rows of one
-// expert, 2048 -> 1024, the 64 tiles of 256 x 256 of dh take 63, 128 x 128 32; on 8192
-// rows of 48 experts, 5120 -> 1536, dx takes 444 and 575.  fp32, whose matrix cores are
-// the bound at every shape, has 64 x 64 alone (2048 rows of 16 experts, 1024 -> 512, all
-// six: 315, with 128 x 128 363).  up has two matrices in a tile, 64 x 128 at least.
+// left over.  bf16, microseconds, each shape forced on 20 problems (120 products), 256 x
+// 256 against 128 x 128:
+//   256 tiles: 4096 rows of one expert, 4096 -> 2 x 2048, up 126 and 188, down 65 and 95, dx
+//   112 and 159; 240: 8192 of 16, 1024 -> 2 x 768, up 46 and 49; 192: 4096 of 16, 2048 -> 2 x
+//   1024, up 64 and 61, dx 52 and 55; 144: 8192 of 8, 2048 -> 2 x 1024, dh 67 and 56
+// and 128 x 128 against 64 x 64:
+//   288 tiles: 4096 of 8, 2048 -> 2 x 1024, dh 39 and 45; 272: 4096 of 4, 1024 -> 2 x 1024,
+//   down 21 and 26; 160: 8192 of 33, 512 -> 2 x 256, dh 16.0 and 14.9, but 2048 of 8, 1024 ->
+//   2 x 1024, down 13.3 and 16.3; 92: 2000 of 16, 512 -> 2 x 512, down 7.9 and 7.5
+// Products over rows lose 3 % on the mean to the best shape, 26 % at most (dx of those 2048
+// rows: 25.8, 128 x 128 20.5).  Weight gradients lose 8 % and up to 48 %: the endings of 256 x
+// 256 weigh on a few hundred rows an expert, where 128 x 128 is the faster to some 500 tiles
+// (256 tiles: dWd of 4096 of 8, 2048 -> 2 x 1024, 36 and 26; but dWg and dWu of one expert's 4096
+// rows, 4096 -> 2 x 2048, 109 and 159; 512: dWg and dWu of the former 50 and 47).
+// up has two matrices in a tile, 64 x 128 at least.  fp32 has 64 x 64 alone: 2048 rows of 16
+// experts, 1024 -> 2 x 512, all six 315, with 128 x 128 363, where the matrix cores' rate
+// would allow 128: the contractions are short, and nothing runs beside the one or two tiles'
+// first copies and endings.
 //
 // The products forward of a few rows an expert are a stream of weights, and take 64 x 256,
-// of which two workgroups fit a CU: up and down of 64 rows of 32 experts, 7168 -> 2 x 2048,
-// 319 and 141 with 256 x 256, so 303 and 134; 512 rows of 48, 5120 -> 2 x 1536, 340 and 152,
-// so 319 and 144.
+// of which two workgroups fit a CU.  up and down, 64 x 256 against 256 x 256:
+//    2 rows an expert  32 experts, 7168 -> 2 x 2048  296, 134 and 312, 137
+//   16                                               360, 189 and 366, 196
+//   20                                               360, 189 and 365, 194
+//   24                                               467, 189 and 374, 195
+//   16                 64 experts, 2048 -> 2 x 1024  137, 59 and 144, 61
+//   20                                               156, 68 and 141, 60
+//   24                 48 experts, 5120 -> 2 x 1536  352, 161 and 371, 168
+//   32                                               356, 184 and 376, 169
+// (from where the fullest experts have more than 64 rows they take a second tile).
 //
 // Weights by columns are streamed where an expert has two row tiles of the largest on
-// the mean, or fewer.
+// the mean, or fewer.  dh and dx streamed, and not:
+//   rows an expert   64 experts, 2048 -> 2 x 1024    48 experts, 5120 -> 2 x 1536
+//        64           77, 110 and  88, 120           212, 323 and 229, 337
+//       128          106, 142 and 119, 146           247, 372 and 252, 384
+//       256          141, 175 and 135, 171           324, 519 and 322, 484
+//       512          256, 305 and 229, 285           536, 861 and 501, 777
+//       640          293, 376 and 282, 373           673, 1042 and 560, 918
+//      1024          422, 536 and 377, 501          1010, 1522 and 842, 1354
+// so of one row tile it gains up to some 200 rows an expert, and of two it loses.
 struct Pick {
   int high, ni;
   bool stream;

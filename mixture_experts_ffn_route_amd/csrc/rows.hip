@@ -58,9 +58,16 @@ __device__ __forceinline__ void narrow(T *p, const float (&f)[V]) {
 
 // Calls f(token)(first column) for this thread's pieces.  Long rows of many tokens take
 // a workgroup a token, whose indices are then scalars and whose waves read the same
-// rows at the same time (combine above 119 us, so 111); otherwise the pieces of all
-// tokens stand in one line (4096 tokens of 88 pieces 7.5 us, by tokens 8.9; 64 tokens of
-// 896, dispatch, 6.4 and 8.0).
+// rows at the same time; otherwise the pieces of all tokens stand in one line (4096 tokens
+// of 88 pieces 7.5 us, by tokens 8.9; 64 tokens of 896, dispatch, 6.4 and 8.0).  By tokens and in
+// line, us a call:
+//   combine, 4096 tokens of 4 rows of 256 pieces 12.6 and 13.4, of 8 of 192 20.2 and 21.2
+//   dispatch of the same 12.8 and 12.7, 20.5 and 19.9
+//   1024 of 8 of 192: 7.2 and 7.1 (the call from Python), of 896 24.4 and 23.8
+//   4096 of 8 of 896: combine 94 and 85, with an added row 97 and 90, dispatch 92 and 90
+//   16384 of 6 of 640: combine 207 and 188, dispatch 192 and 189
+// so combine gains to 256 pieces; of longer rows the line is the faster since a piece's
+// loads are all asked for ahead.
 template <int V, bool BY_TOKEN, class F>
 __device__ __forceinline__ void each_piece(const RowsArgs &a, uint32_t pieces, F f) {
   auto column = [&](uint32_t p) {

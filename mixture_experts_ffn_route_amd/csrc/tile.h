@@ -66,7 +66,9 @@ struct Operand {
   // distinct banks: by rows, row r's piece c sits at c ^ (r / 8 % 4) (eight
   // rows of 64 bytes cover address bits 6-8, the four pieces bits 4-5); by
   // columns, the four rows of a transposed read sit 64 bytes apart modulo 256 (rows
-  // of an odd number of 128 bytes are 128 apart by themselves).
+  // of an odd number of 128 bytes are 128 apart by themselves; of 64 columns, dense
+  // products without and with it: dx of 1000 rows, 1024 -> 1024, 9.5 us and 9.5, dW 8.8 and
+  // 8.4, dW of 512 rows, 2048 -> 512, 6.7 and 6.4).
   static __device__ __forceinline__ int swz(int k) {
     return ES != 2 ? 0 : TC % 128 == 0 ? (k & 3) << 2 : (k & 2) << 1;
   }
